@@ -502,6 +502,50 @@ tl_status tiled_linear_forward_static(int64_t T, int64_t K, int64_t M, int32_t N
                                       const void *w_host, const void *x_dev, void *y_dev,
                                       int32_t *status_host, void *stream);
 
+/* --- operators around the product ------------------------------------------
+ * What one pre-norm linear layer's training step needs next to the streamed
+ * product, on device-resident matrices: layer norm, the product in 8-bit
+ * floating point, and the orthogonalised update of a weight.  They take no
+ * handle.  Every call enqueues on `stream` of the current device and returns;
+ * the message of a refused call is tiled_linear_last_error(NULL) in the
+ * calling thread.  Rows and columns are element counts, leading dimensions
+ * (ld*) elements between the starts of two rows.  Workspaces belong to the
+ * caller and are in use until the call's work has completed: calls that may
+ * overlap (other streams) need their own. */
+enum { TL_TYPE_BF16 = 0, TL_TYPE_F16 = 1, TL_TYPE_F32 = 2 };  /* tl_type */
+
+/* Layer norm over the columns of each row.
+ *   mean[r] = sum(x[r]) / cols, rstd[r] = 1 / sqrt(sum((x[r] - mean)^2) / cols + eps)
+ *   y[r, c] = (x[r, c] - mean[r]) rstd[r] weight[c] + bias[c]
+ *  x, y: [rows, cols] of `type`; y may be x.  weight, bias: [cols] of
+ *  `param_type`, NULL for ones / zeros.  mean, rstd: fp32 [rows].
+ *  cols is 1..131072.  Any leading dimension >= cols and any alignment of the
+ *  element type is taken; rows that all start on 16-byte boundaries (and a
+ *  cols of whole 16-byte vectors) are read and written 16 bytes at a time.
+ *  Statistics are fp32.  rows = 0 is a no-op.
+ * Errors: TL_ERR_INVALID, TL_ERR_CUDA. */
+tl_status tiled_linear_norm_forward(int64_t rows, int64_t cols, int32_t type, const void *x_dev, int64_t ldx,
+                                    int32_t param_type, const void *weight_dev, const void *bias_dev, float eps,
+                                    void *y_dev, int64_t ldy, float *mean_dev, float *rstd_dev, void *stream);
+
+/* Bytes of workspace that the backward needs (0 if the arguments are invalid). */
+size_t tiled_linear_norm_backward_workspace_bytes(int64_t rows, int64_t cols);
+
+/* Layer norm's gradients, with the forward's mean and rstd, xh = (x - mean) rstd
+ * and g = dy weight:
+ *   dx[r, c]   = rstd[r] (g[r, c] - mean_c(g[r]) - xh[r, c] mean_c(g[r] xh[r]))
+ *   dweight[c] = sum_r dy[r, c] xh[r, c],   dbias[c] = sum_r dy[r, c]
+ *  dy, dx: [rows, cols] of `type`; dx may be dy or x.  dweight, dbias: fp32
+ *  [cols], overwritten, NULL where not wanted.  The sums over rows have a fixed
+ *  order for given sizes: no atomics, the same bits every time.  rows = 0
+ *  writes zeros to dweight and dbias.  workspace: 16-byte aligned.
+ * Errors: TL_ERR_INVALID, TL_ERR_WORKSPACE, TL_ERR_CUDA. */
+tl_status tiled_linear_norm_backward(int64_t rows, int64_t cols, int32_t type, const void *dy_dev, int64_t lddy,
+                                     const void *x_dev, int64_t ldx, const float *mean_dev, const float *rstd_dev,
+                                     int32_t param_type, const void *weight_dev, void *dx_dev, int64_t lddx,
+                                     float *dweight_dev, float *dbias_dev, void *workspace_dev,
+                                     size_t workspace_bytes, void *stream);
+
 /* --- pinned host memory helpers ------------------------------------------ */
 /* Page-locked host allocation (cudaHostAlloc, portable); *out = NULL on
  * failure.  Free with tiled_linear_host_free. */

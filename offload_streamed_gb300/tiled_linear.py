@@ -164,6 +164,14 @@ def load():
         L.tiled_linear_selftest_timeout.restype = st
         L.tiled_linear_forward_static.argtypes = [i64, i64, i64, i32, vp, vp, vp, vp, vp]
         L.tiled_linear_forward_static.restype = st
+        L.tiled_linear_norm_forward.argtypes = [i64, i64, i32, vp, i64, i32, vp, vp, ctypes.c_float, vp, i64, vp,
+                                                vp, vp]
+        L.tiled_linear_norm_forward.restype = st
+        L.tiled_linear_norm_backward_workspace_bytes.argtypes = [i64, i64]
+        L.tiled_linear_norm_backward_workspace_bytes.restype = sz
+        L.tiled_linear_norm_backward.argtypes = [i64, i64, i32, vp, i64, vp, i64, vp, vp, i32, vp, vp, i64, vp, vp,
+                                                 vp, sz, vp]
+        L.tiled_linear_norm_backward.restype = st
         L.tiled_linear_host_alloc.argtypes = [sz, ctypes.POINTER(vp)]
         L.tiled_linear_host_alloc.restype = st
         L.tiled_linear_host_free.argtypes = [vp]
@@ -387,6 +395,23 @@ def tiled_linear_forward_static(T, K, M, N, w_host, x_dev, y_dev, status_host, s
     st = load().tiled_linear_forward_static(T, K, M, N, w_host, x_dev, y_dev, status_host, stream)
     if st != TL_OK:
         raise TiledLinearError(st, "tiled_linear_forward_static")
+
+
+def tiled_linear_norm_forward(rows, cols, type, x, ldx, param_type, weight, bias, eps, y, ldy, mean, rstd,
+                              stream) -> None:
+    _check(load().tiled_linear_norm_forward(rows, cols, type, x, ldx, param_type, weight, bias, eps, y, ldy, mean,
+                                            rstd, stream), "tiled_linear_norm_forward")
+
+
+def tiled_linear_norm_backward_workspace_bytes(rows: int, cols: int) -> int:
+    return int(load().tiled_linear_norm_backward_workspace_bytes(rows, cols))
+
+
+def tiled_linear_norm_backward(rows, cols, type, dy, lddy, x, ldx, mean, rstd, param_type, weight, dx, lddx, dweight,
+                               dbias, workspace, workspace_bytes, stream) -> None:
+    _check(load().tiled_linear_norm_backward(rows, cols, type, dy, lddy, x, ldx, mean, rstd, param_type, weight, dx,
+                                             lddx, dweight, dbias, workspace, workspace_bytes, stream),
+           "tiled_linear_norm_backward")
 
 
 def tiled_linear_host_alloc(nbytes: int) -> int:
@@ -707,3 +732,110 @@ class HostAdam:
             self.close()
         except Exception:
             pass
+
+
+# --- operators around the product ---------------------------------------------
+# Functions of torch tensors: device-resident, enqueued on the current stream,
+# with outputs and workspaces from torch's allocator on that stream.  They take
+# no gradient through autograd: each backward is a function of its own.
+
+TL_TYPE_BF16, TL_TYPE_F16, TL_TYPE_F32 = range(3)
+_types = None
+
+
+def _type_of(t, where: str) -> int:
+    global _types
+    if _types is None:
+        import torch
+        _types = {torch.bfloat16: TL_TYPE_BF16, torch.float16: TL_TYPE_F16, torch.float32: TL_TYPE_F32}
+    got = _types.get(t.dtype)
+    if got is None:
+        raise TiledLinearError(TL_ERR_INVALID, where, f"dtype {t.dtype}: bfloat16, float16 or float32 is wanted")
+    return got
+
+
+def _refuse(where: str, why: str):
+    raise TiledLinearError(TL_ERR_INVALID, where, why)
+
+
+def _matrix(t, where: str, name: str) -> None:
+    """A device matrix whose rows are contiguous."""
+    if not t.is_cuda:
+        _refuse(where, f"{name} is not on a CUDA device")
+    if t.dim() != 2:
+        _refuse(where, f"{name} has {t.dim()} dimensions: a matrix is wanted")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        _refuse(where, f"the rows of {name} are not contiguous")
+
+
+def _ld(t) -> int:
+    """Leading dimension of a matrix (any value will do for a single row)."""
+    return max(t.stride(0), t.shape[1]) if t.shape[0] > 1 else t.shape[1]
+
+
+def _vector(t, n: int, like, where: str, name: str) -> None:
+    if t.shape != (n,) or (n > 1 and t.stride(0) != 1) or t.device != like.device:
+        _refuse(where, f"{name} must be a contiguous vector of {n} on the matrix's device")
+
+
+def _current_stream(t) -> int:
+    import torch
+    if torch.cuda.current_device() != t.device.index:
+        raise TiledLinearError(TL_ERR_INVALID, "current device", f"the tensors are on {t.device}: make it current")
+    return torch.cuda.current_stream().cuda_stream
+
+
+def layer_norm(x, weight=None, bias=None, eps: float = 1e-5):
+    """(y, mean, rstd): layer norm over the columns of x [rows, cols] (bf16, fp16 or
+    fp32; any row stride).  weight, bias: [cols], both of one of those types, or
+    None for ones / zeros.  mean and rstd are fp32 [rows], for the backward."""
+    import torch
+    where = "layer_norm"
+    _matrix(x, where, "x")
+    rows, cols = x.shape
+    ptype = TL_TYPE_F32
+    for v, name in ((weight, "weight"), (bias, "bias")):
+        if v is not None:
+            _vector(v, cols, x, where, name)
+            ptype = _type_of(v, where)
+    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+        _refuse(where, "weight and bias differ in dtype")
+    kind, stream = _type_of(x, where), _current_stream(x)
+    y = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
+    stat = torch.empty((2, rows), dtype=torch.float32, device=x.device)
+    mean, rstd = stat[0], stat[1]
+    tiled_linear_norm_forward(rows, cols, kind, x.data_ptr(), _ld(x), ptype,
+                              weight.data_ptr() if weight is not None else None,
+                              bias.data_ptr() if bias is not None else None, eps, y.data_ptr(), cols,
+                              mean.data_ptr(), rstd.data_ptr(), stream)
+    return y, mean, rstd
+
+
+def layer_norm_backward(dy, x, mean, rstd, weight=None):
+    """(dx, dweight, dbias) of ``layer_norm``: dx like x, dweight and dbias fp32
+    [cols] (the derivative by a weight of ones where there is none)."""
+    import torch
+    where = "layer_norm_backward"
+    _matrix(x, where, "x")
+    _matrix(dy, where, "dy")
+    if dy.shape != x.shape or dy.dtype != x.dtype or dy.device != x.device:
+        _refuse(where, "dy and x differ in shape, dtype or device")
+    rows, cols = x.shape
+    ptype = TL_TYPE_F32
+    if weight is not None:
+        _vector(weight, cols, x, where, "weight")
+        ptype = _type_of(weight, where)
+    for v, name in ((mean, "mean"), (rstd, "rstd")):
+        _vector(v, rows, x, where, name)
+        if v.dtype != torch.float32:
+            _refuse(where, f"{name} must be float32")
+    kind, stream = _type_of(x, where), _current_stream(x)
+    dx = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
+    grads = torch.empty((2, cols), dtype=torch.float32, device=x.device)
+    dweight, dbias = grads[0], grads[1]
+    need = tiled_linear_norm_backward_workspace_bytes(rows, cols)
+    ws = torch.empty(need, dtype=torch.uint8, device=x.device)
+    tiled_linear_norm_backward(rows, cols, kind, dy.data_ptr(), _ld(dy), x.data_ptr(), _ld(x), mean.data_ptr(),
+                               rstd.data_ptr(), ptype, weight.data_ptr() if weight is not None else None,
+                               dx.data_ptr(), cols, dweight.data_ptr(), dbias.data_ptr(), ws.data_ptr(), need, stream)
+    return dx, dweight, dbias
