@@ -23,10 +23,11 @@
 //    of row i + 1's sums is under way while row i is written, so one barrier
 //    a row is all there is, and its wait is mostly hidden.
 // All statistics and sums are fp32.  A row's variance is joined from the
-// threads' sums of squares about their own means, which loses nothing to
+// warps' sums of squares about their own means, which loses nothing to
 // cancellation, whatever the row's mean.  Every order of summation is fixed by
 // the sizes alone.
 #include "tl_norm.h"
+#include "tl_launch.h"
 #include "tl_types.cuh"
 
 #include <algorithm>
@@ -38,7 +39,7 @@ constexpr int kMaxRing = 4;         // rows in flight per thread
 constexpr int kWarpRowWarps = 8;    // rows of a CTA at a time where a warp has a row
 constexpr int kMaxWarps = 16;       // of a CTA that shares a row
 constexpr int kMaxCluster = 8;
-constexpr size_t kSmemBudget = 200 * 1024;
+constexpr size_t kSmemBudget = 220 * 1024;  // of an SM, for its CTAs
 constexpr int kMaxSms = 152, kCtasPerSm = 4;  // bound the grid, and with it the partial sums
 
 struct NormArgs {
@@ -96,32 +97,36 @@ __device__ __forceinline__ void cluster_wait() {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// Count, sum and sum of squares about the mean of a set of values, and the
-// union of two such sets.
+// Count, mean and sum of squares about the mean of a set of values.
 struct Moments {
-    float n, sum, m2;
+    float n, mean, m2;
 };
-__device__ __forceinline__ Moments join(const Moments& a, const Moments& b) {
-    const float n = a.n + b.n;
-    if (b.n == 0.0f) return a;
-    if (a.n == 0.0f) return b;
-    const float d = b.sum / b.n - a.sum / a.n;
-    return Moments{n, a.sum + b.sum, a.m2 + b.m2 + d * d * (a.n * b.n / n)};
-}
-__device__ __forceinline__ Moments warp_join(Moments v) {
-#pragma unroll
-    for (int s = 16; s; s >>= 1) {
-        const Moments o{__shfl_xor_sync(~0u, v.n, s), __shfl_xor_sync(~0u, v.sum, s), __shfl_xor_sync(~0u, v.m2, s)};
-        // both partners join in the same order, so that all lanes agree
-        const bool low = (threadIdx.x & s) == 0;
-        v = low ? join(v, o) : join(o, v);
-    }
-    return v;
-}
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int s = 16; s; s >>= 1) v += __shfl_xor_sync(~0u, v, s);
     return v;
+}
+
+// Sums over the n entries that a row's warps left: up to 16 are had by both
+// halves of the warp, which saves a step.
+template <typename F>
+__device__ __forceinline__ void for_entries(int lane, int n, F&& f) {
+    if (n <= kMaxWarps) {
+        if ((lane & 15) < n) f(lane & 15);
+    } else {
+        for (int i = lane; i < n; i += 32) f(i);
+    }
+}
+__device__ __forceinline__ float set_sum(float v, int n) {
+    if (n > kMaxWarps) v += __shfl_xor_sync(~0u, v, 16);
+#pragma unroll
+    for (int s = 8; s; s >>= 1) v += __shfl_xor_sync(~0u, v, s);
+    return v;
+}
+__device__ __forceinline__ float lane_of(const float (&v)[1], int) { return v[0]; }
+template <int N>
+__device__ __forceinline__ float lane_of(const float2 (&v)[N], int e) {
+    return e & 1 ? v[e / 2].y : v[e / 2].x;
 }
 
 // The columns of one thread: ITEMS vectors of VEC elements, `step` vectors
@@ -155,6 +160,37 @@ __device__ __forceinline__ void fetch(const Cols<T, VEC, ITEMS>& c, const T* row
     }
 }
 
+// A parameter (weight or bias) at the thread's columns, as fp32 in the thread's
+// own shared memory, in 16-byte chunks a thread apart.
+template <int VEC>
+struct Param {
+    static constexpr int kChunk = VEC > 1 ? 4 : 1;
+    using C = Vec<float, kChunk>;
+    C* at;
+    int threads;
+    __device__ __forceinline__ Param(float* base, int threads_) : at(reinterpret_cast<C*>(base) + threadIdx.x), threads(threads_) {}
+    template <typename T, int ITEMS>
+    __device__ __forceinline__ void fill(const Cols<T, VEC, ITEMS>& c, const void* p, int32_t type, float none) {
+#pragma unroll
+        for (int k = 0; k < ITEMS; ++k)
+            if (c.has(k))
+#pragma unroll
+                for (int e = 0; e < VEC; ++e)
+                    at[(k * (VEC / kChunk) + e / kChunk) * threads].v[e % kChunk] =
+                        p ? load_as_f32(p, type, c.col(k) + e) : none;
+    }
+    __device__ __forceinline__ void get(int k, float (&v)[1]) const { v[0] = at[k * threads].v[0]; }
+    template <int N>
+    __device__ __forceinline__ void get(int k, float2 (&v)[N]) const {
+#pragma unroll
+        for (int q = 0; q < N / 2; ++q) {
+            const C u = at[(k * (VEC / kChunk) + q) * threads];
+            v[2 * q] = make_float2(u.v[0], u.v[1]);
+            v[2 * q + 1] = make_float2(u.v[2], u.v[3]);
+        }
+    }
+};
+
 // Which rows and columns a thread works on.
 template <typename T, int VEC, int ITEMS, bool WARP_ROW>
 struct Place {
@@ -186,12 +222,13 @@ struct Place {
 
 // ---- forward -----------------------------------------------------------------
 template <typename T, int VEC, int ITEMS, bool WARP_ROW>
-__global__ void __launch_bounds__(WARP_ROW ? kWarpRowWarps * 32 : kMaxWarps * 32)
+__global__ void __launch_bounds__(WARP_ROW ? kWarpRowWarps * 32 : kMaxWarps * 32, WARP_ROW || VEC * ITEMS > 16 ? 1 : 2)
     norm_forward_kernel(const NormArgs p) {
-    constexpr int E = VEC * ITEMS;
+    constexpr int E = VEC * ITEMS, NL = VEC > 1 ? VEC / 2 : 1;
     using V = Vec<T, VEC>;
+    using L = Lanes<VEC>;
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ Moments red[3][kMaxCluster][kMaxWarps];
+    __shared__ Moments red[3][kMaxCluster * kMaxWarps];  // by CTA of the cluster, then by warp
     const Place<T, VEC, ITEMS, WARP_ROW> at(p);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = at.threads / 32;
     V* ring = reinterpret_cast<V*>(smem) + threadIdx.x;
@@ -199,61 +236,67 @@ __global__ void __launch_bounds__(WARP_ROW ? kWarpRowWarps * 32 : kMaxWarps * 32
     const T* x = static_cast<const T*>(p.x);
     T* y = static_cast<T*>(p.out);
 
-    int64_t next = at.row;
-    int filled = 0;
-    for (int s = 0; s < p.ring; ++s, next += at.stride, ++filled) {
-        if (next < p.rows) fetch(at.c, x + next * p.ldx, ring + s * slot_vecs, at.threads);
+    int64_t next = at.row;  // the next row to fetch, and where it is
+    const T* next_x = x + next * p.ldx;
+    const int64_t step_x = at.stride * p.ldx;
+    auto refill = [&](int slot) {
+        if (next < p.rows) fetch(at.c, next_x, ring + slot * slot_vecs, at.threads);
+        next += at.stride;
+        next_x += step_x;
         cp_async_commit();
-    }
-    float w[E], b[E];
+    };
+    for (int s = 0; s < p.ring; ++s) refill(s);
+    float* params = reinterpret_cast<float*>(smem + size_t(p.ring) * slot_vecs * sizeof(V));
+    Param<VEC> weight(params, at.threads), bias(params + E * at.threads, at.threads);
+    weight.fill(at.c, p.weight, p.param_type, 1.0f);
+    bias.fill(at.c, p.bias, p.param_type, 0.0f);
+    const float inv_c = 1.0f / float(p.cols);
+    float n_warp = 0;  // columns of the warp
 #pragma unroll
-    for (int k = 0; k < ITEMS; ++k)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            const bool in = at.c.has(k);
-            w[k * VEC + e] = in && p.weight ? load_as_f32(p.weight, p.param_type, at.c.col(k) + e) : 1.0f;
-            b[k * VEC + e] = in && p.bias ? load_as_f32(p.bias, p.param_type, at.c.col(k) + e) : 0.0f;
-        }
+    for (int k = 0; k < ITEMS; ++k) n_warp += at.c.has(k) ? VEC : 0;
+    n_warp = warp_sum(n_warp);
+    const float inv_n = n_warp > 0 ? 1.0f / n_warp : 0.0f;
 
-    // Moments of the thread's own columns of the row in ring slot `slot`.
+    // Moments of the warp's columns of the row in ring slot `slot`.
     auto own = [&](int slot) {
         const V* src = ring + slot * slot_vecs;
-        float v[E], n = 0, sum = 0, m2 = 0;
+        L v[ITEMS][NL], sum = splat<L>(0), m2 = splat<L>(0);
 #pragma unroll
         for (int k = 0; k < ITEMS; ++k)
             if (at.c.has(k)) {
-                const V u = src[k * at.threads];
+                unpack(src[k * at.threads], v[k]);
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    v[k * VEC + e] = to_f32(u.v[e]);
-                    sum += v[k * VEC + e];
-                }
-                n += VEC;
+                for (int i = 0; i < NL; ++i) sum = add(sum, v[k][i]);
             }
-        const float m = n > 0 ? sum / n : 0.0f;
+        const float m = warp_sum(total(sum)) * inv_n;
+        const L minus_m = splat<L>(-m);
 #pragma unroll
         for (int k = 0; k < ITEMS; ++k)
             if (at.c.has(k))
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    const float d = v[k * VEC + e] - m;
-                    m2 += d * d;
+                for (int i = 0; i < NL; ++i) {
+                    const L d = add(v[k][i], minus_m);
+                    m2 = fma(d, d, m2);
                 }
-        return warp_join(Moments{n, sum, m2});
+        return Moments{n_warp, m, warp_sum(total(m2))};
     };
     auto apply = [&](int64_t row, int slot, const Moments& s) {
-        const float mean = s.sum / float(p.cols);
-        const float rstd = rsqrtf(s.m2 / float(p.cols) + p.eps);
+        const float mean = s.mean;
+        const float rstd = rsqrtf(s.m2 * inv_c + p.eps);
         const V* src = ring + slot * slot_vecs;
         T* dst = y + row * p.ldout;
+        const L minus_m = splat<L>(-mean), r = splat<L>(rstd);
 #pragma unroll
         for (int k = 0; k < ITEMS; ++k)
             if (at.c.has(k)) {
-                const V u = src[k * at.threads];
-                V o;
+                L v[NL], w[NL], b[NL];
+                unpack(src[k * at.threads], v);
+                weight.get(k, w);
+                bias.get(k, b);
 #pragma unroll
-                for (int e = 0; e < VEC; ++e)
-                    o.v[e] = from_f32<T>((to_f32(u.v[e]) - mean) * rstd * w[k * VEC + e] + b[k * VEC + e]);
+                for (int i = 0; i < NL; ++i) v[i] = fma(mul(add(v[i], minus_m), r), w[i], b[i]);
+                V o;
+                pack(v, o);
                 *reinterpret_cast<V*>(dst + at.c.col(k)) = o;
             }
         const bool writes = WARP_ROW ? lane == 0 : threadIdx.x == 0 && at.rank == 0;
@@ -261,11 +304,6 @@ __global__ void __launch_bounds__(WARP_ROW ? kWarpRowWarps * 32 : kMaxWarps * 32
             p.mean[row] = mean;
             p.rstd[row] = rstd;
         }
-    };
-    auto refill = [&](int slot) {
-        if (next < p.rows) fetch(at.c, x + next * p.ldx, ring + slot * slot_vecs, at.threads);
-        next += at.stride;
-        cp_async_commit();
     };
 
     if constexpr (WARP_ROW) {
@@ -282,21 +320,36 @@ __global__ void __launch_bounds__(WARP_ROW ? kWarpRowWarps * 32 : kMaxWarps * 32
         // another's last read.
         auto send = [&](int buf, const Moments& s) {
             if (p.cluster == 1) {
-                if (lane == 0) red[buf][0][warp] = s;
+                if (lane == 0) red[buf][warp] = s;
             } else {
                 if (lane < p.cluster) {
-                    const uint32_t a = saddr(&red[buf][at.rank][warp]);
+                    const uint32_t a = saddr(&red[buf][int(at.rank) * warps + warp]);
                     st_cluster_f32(a, uint32_t(lane), s.n);
-                    st_cluster_f32(a + 4, uint32_t(lane), s.sum);
+                    st_cluster_f32(a + 4, uint32_t(lane), s.mean);
                     st_cluster_f32(a + 8, uint32_t(lane), s.m2);
                 }
                 cluster_arrive();
             }
         };
         auto receive = [&](int buf) {
-            Moments s{0, 0, 0};
-            for (int i = lane; i < p.cluster * warps; i += 32) s = join(s, red[buf][i / warps][i % warps]);
-            return warp_join(s);
+            // The union of the warps' sets, in one pass about the first set's
+            // mean.  That mean is off the row's by no more than the first
+            // set's share of the squares lets it be, so that little cancels.
+            const float first = red[buf][0].mean, pivot = isfinite(first) ? first : 0.0f;
+            float sum = 0, sq = 0;
+            auto take = [&](const Moments& w) {
+                const float d = w.mean - pivot, nd = w.n * d;
+                if (w.n > 0) {
+                    sum += nd;
+                    sq += w.m2 + nd * d;
+                }
+            };
+            for_entries(lane, p.cluster * warps, [&](int i) { take(red[buf][i]); });
+            sum = set_sum(sum, p.cluster * warps);
+            sq = set_sum(sq, p.cluster * warps);
+            const float off = sum * inv_c;
+            const float m2 = sq - sum * off;
+            return Moments{float(p.cols), pivot + off, m2 < 0.0f ? 0.0f : m2};  // (a NaN stays one)
         };
         if (p.cluster > 1) {  // every CTA of the cluster runs before its memory is written
             cluster_arrive();
@@ -333,45 +386,45 @@ __global__ void __launch_bounds__(WARP_ROW ? kWarpRowWarps * 32 : kMaxWarps * 32
 
 // ---- backward ----------------------------------------------------------------
 template <typename T, int VEC, int ITEMS, bool WARP_ROW>
-__global__ void __launch_bounds__(WARP_ROW ? kWarpRowWarps * 32 : kMaxWarps * 32)
+__global__ void __launch_bounds__(WARP_ROW ? kWarpRowWarps * 32 : kMaxWarps * 32, WARP_ROW || VEC * ITEMS > 16 ? 1 : 2)
     norm_backward_kernel(const NormArgs p) {
-    constexpr int E = VEC * ITEMS;
+    constexpr int E = VEC * ITEMS, NL = VEC > 1 ? VEC / 2 : 1;
     using V = Vec<T, VEC>;
+    using L = Lanes<VEC>;
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ float2 red[3][kMaxCluster][kMaxWarps];
+    __shared__ float2 red[3][kMaxCluster * kMaxWarps];  // as in the forward
     const Place<T, VEC, ITEMS, WARP_ROW> at(p);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = at.threads / 32;
     const int slot_vecs = ITEMS * at.threads;
     V* ring_x = reinterpret_cast<V*>(smem) + threadIdx.x;
     V* ring_dy = ring_x + p.ring * slot_vecs;
-    float* wsm = reinterpret_cast<float*>(smem + size_t(2 * p.ring) * slot_vecs * sizeof(V)) + threadIdx.x;
     const T* x = static_cast<const T*>(p.x);
     const T* dy = static_cast<const T*>(p.dy);
     T* dx = static_cast<T*>(p.out);
     const float inv_c = 1.0f / float(p.cols);
 
     int64_t next = at.row;
-    for (int s = 0; s < p.ring; ++s, next += at.stride) {
+    const T *next_x = x + next * p.ldx, *next_dy = dy + next * p.lddy;
+    const int64_t step_x = at.stride * p.ldx, step_dy = at.stride * p.lddy;
+    auto refill = [&](int slot) {
         if (next < p.rows) {
-            fetch(at.c, x + next * p.ldx, ring_x + s * slot_vecs, at.threads);
-            fetch(at.c, dy + next * p.lddy, ring_dy + s * slot_vecs, at.threads);
+            fetch(at.c, next_x, ring_x + slot * slot_vecs, at.threads);
+            fetch(at.c, next_dy, ring_dy + slot * slot_vecs, at.threads);
         }
+        next += at.stride;
+        next_x += step_x;
+        next_dy += step_dy;
         cp_async_commit();
-    }
-    // the weight as fp32 in the thread's own shared memory: registers go to
-    // the two sums
-    if (p.weight) {
+    };
+    for (int s = 0; s < p.ring; ++s) refill(s);
+    // the weight goes to shared memory: registers go to the two sums
+    Param<VEC> weight(reinterpret_cast<float*>(smem + size_t(2 * p.ring) * slot_vecs * sizeof(V)), at.threads);
+    weight.fill(at.c, p.weight, p.param_type, 1.0f);
+    L aw[ITEMS][NL], ab[ITEMS][NL];
 #pragma unroll
-        for (int k = 0; k < ITEMS; ++k)
+    for (int k = 0; k < ITEMS; ++k)
 #pragma unroll
-            for (int e = 0; e < VEC; ++e)
-                wsm[(k * VEC + e) * at.threads] =
-                    at.c.has(k) ? load_as_f32(p.weight, p.param_type, at.c.col(k) + e) : 0.0f;
-    }
-    auto weight = [&](int i) { return p.weight ? wsm[i * at.threads] : 1.0f; };
-    float aw[E], ab[E];
-#pragma unroll
-    for (int i = 0; i < E; ++i) aw[i] = ab[i] = 0.0f;
+        for (int i = 0; i < NL; ++i) aw[k][i] = ab[k][i] = splat<L>(0);
 
     struct Stat {
         float mean, rstd;
@@ -383,47 +436,48 @@ __global__ void __launch_bounds__(WARP_ROW ? kWarpRowWarps * 32 : kMaxWarps * 32
     auto own = [&](int slot, const Stat& st) {
         const V* sx = ring_x + slot * slot_vecs;
         const V* sd = ring_dy + slot * slot_vecs;
-        float s1 = 0, s2 = 0;
+        L s1 = splat<L>(0), s2 = splat<L>(0);
+        const L minus_m = splat<L>(-st.mean), r = splat<L>(st.rstd);
 #pragma unroll
         for (int k = 0; k < ITEMS; ++k)
             if (at.c.has(k)) {
-                const V u = sx[k * at.threads], g = sd[k * at.threads];
+                L v[NL], d[NL], w[NL];
+                unpack(sx[k * at.threads], v);
+                unpack(sd[k * at.threads], d);
+                weight.get(k, w);
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    const float gw = to_f32(g.v[e]) * weight(k * VEC + e);
-                    s1 += gw;
-                    s2 += gw * ((to_f32(u.v[e]) - st.mean) * st.rstd);
+                for (int i = 0; i < NL; ++i) {
+                    const L g = mul(d[i], w[i]);
+                    s1 = add(s1, g);
+                    s2 = fma(g, mul(add(v[i], minus_m), r), s2);
                 }
             }
-        return make_float2(warp_sum(s1), warp_sum(s2));
+        return make_float2(warp_sum(total(s1)), warp_sum(total(s2)));
     };
     auto apply = [&](int64_t row, int slot, const Stat& st, float2 s) {
-        const float c1 = s.x * inv_c, c2 = s.y * inv_c;
         const V* sx = ring_x + slot * slot_vecs;
         const V* sd = ring_dy + slot * slot_vecs;
         T* dst = dx + row * p.ldout;
+        const L minus_m = splat<L>(-st.mean), r = splat<L>(st.rstd);
+        const L minus_c1 = splat<L>(-s.x * inv_c), minus_c2 = splat<L>(-s.y * inv_c);
 #pragma unroll
         for (int k = 0; k < ITEMS; ++k)
             if (at.c.has(k)) {
-                const V u = sx[k * at.threads], g = sd[k * at.threads];
-                V o;
+                L v[NL], d[NL], w[NL];
+                unpack(sx[k * at.threads], v);
+                unpack(sd[k * at.threads], d);
+                weight.get(k, w);
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    const float d = to_f32(g.v[e]), xh = (to_f32(u.v[e]) - st.mean) * st.rstd;
-                    o.v[e] = from_f32<T>(st.rstd * (d * weight(k * VEC + e) - c1 - xh * c2));
-                    aw[k * VEC + e] += d * xh;
-                    ab[k * VEC + e] += d;
+                for (int i = 0; i < NL; ++i) {
+                    const L xh = mul(add(v[i], minus_m), r);
+                    aw[k][i] = fma(d[i], xh, aw[k][i]);
+                    ab[k][i] = add(ab[k][i], d[i]);
+                    v[i] = mul(r, fma(xh, minus_c2, fma(d[i], w[i], minus_c1)));
                 }
+                V o;
+                pack(v, o);
                 *reinterpret_cast<V*>(dst + at.c.col(k)) = o;
             }
-    };
-    auto refill = [&](int slot) {
-        if (next < p.rows) {
-            fetch(at.c, x + next * p.ldx, ring_x + slot * slot_vecs, at.threads);
-            fetch(at.c, dy + next * p.lddy, ring_dy + slot * slot_vecs, at.threads);
-        }
-        next += at.stride;
-        cp_async_commit();
     };
 
     Stat st = stat(at.row);
@@ -440,10 +494,10 @@ __global__ void __launch_bounds__(WARP_ROW ? kWarpRowWarps * 32 : kMaxWarps * 32
     } else {
         auto send = [&](int buf, float2 s) {  // as in the forward
             if (p.cluster == 1) {
-                if (lane == 0) red[buf][0][warp] = s;
+                if (lane == 0) red[buf][warp] = s;
             } else {
                 if (lane < p.cluster) {
-                    const uint32_t a = saddr(&red[buf][at.rank][warp]);
+                    const uint32_t a = saddr(&red[buf][int(at.rank) * warps + warp]);
                     st_cluster_f32(a, uint32_t(lane), s.x);
                     st_cluster_f32(a + 4, uint32_t(lane), s.y);
                 }
@@ -452,12 +506,8 @@ __global__ void __launch_bounds__(WARP_ROW ? kWarpRowWarps * 32 : kMaxWarps * 32
         };
         auto receive = [&](int buf) {
             float2 s = make_float2(0.0f, 0.0f);
-            for (int i = lane; i < p.cluster * warps; i += 32) {
-                const float2 v = red[buf][i / warps][i % warps];
-                s.x += v.x;
-                s.y += v.y;
-            }
-            return make_float2(warp_sum(s.x), warp_sum(s.y));
+            for_entries(lane, p.cluster * warps, [&](int i) { s = add(s, red[buf][i]); });
+            return make_float2(set_sum(s.x, p.cluster * warps), set_sum(s.y, p.cluster * warps));
         };
         if (p.cluster > 1) {
             cluster_arrive();
@@ -506,8 +556,8 @@ __global__ void __launch_bounds__(WARP_ROW ? kWarpRowWarps * 32 : kMaxWarps * 32
 #pragma unroll
                         for (int e = 0; e < VEC; ++e) {
                             const int c = at.c.col(k) + e;
-                            acc[c] = (w ? acc[c] : 0.0f) + aw[k * VEC + e];
-                            acc[p.cols + c] = (w ? acc[p.cols + c] : 0.0f) + ab[k * VEC + e];
+                            acc[c] = (w ? acc[c] : 0.0f) + lane_of(aw[k], e);
+                            acc[p.cols + c] = (w ? acc[p.cols + c] : 0.0f) + lane_of(ab[k], e);
                         }
             }
             __syncthreads();
@@ -531,8 +581,8 @@ __global__ void __launch_bounds__(WARP_ROW ? kWarpRowWarps * 32 : kMaxWarps * 32
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
                     const int c = at.c.col(k) + e;
-                    if (to_w) to_w[c] = aw[k * VEC + e];
-                    if (to_b) to_b[c] = ab[k * VEC + e];
+                    if (to_w) to_w[c] = lane_of(aw[k], e);
+                    if (to_b) to_b[c] = lane_of(ab[k], e);
                 }
     }
 }
@@ -549,6 +599,7 @@ __global__ void __launch_bounds__(kReduceWarps * 32)
     if (!out) return;
     float s = 0;
     if (c < cols)
+#pragma unroll 8
         for (int i = warp; i < n; i += kReduceWarps) s += partials[(int64_t(i) * 2 + blockIdx.y) * cols + c];
     acc[warp][lane] = s;
     __syncthreads();
@@ -614,10 +665,11 @@ cudaError_t make_plan(const NormDesc& d, bool backward, int num_sms, Plan* out) 
         p.threads = int(((p.seg + e - 1) / e + 31) / 32 * 32);
     }
     const size_t row_bytes = size_t(p.threads) * e * esize * (backward ? 2 : 1);
-    const size_t fixed = backward && d.weight ? size_t(p.threads) * e * 4 : 0;
+    const size_t fixed = size_t(p.threads) * e * 4 * (backward ? 1 : 2);
     // only the vector copies are asynchronous: without them a longer ring
     // hides nothing
-    p.ring = vec == 1 ? 1 : int(std::max<size_t>(1, std::min<size_t>(kMaxRing, (kSmemBudget - fixed) / row_bytes)));
+    auto fits = [&](size_t budget) { return budget < fixed ? 0 : int(std::min<size_t>(kMaxRing, (budget - fixed) / row_bytes)); };
+    p.ring = vec == 1 ? 1 : fits(kSmemBudget / 2) >= 2 ? fits(kSmemBudget / 2) : std::max(1, fits(kSmemBudget));
     p.smem = p.ring * row_bytes + fixed;
     if (backward && p.warp_row) p.smem = std::max(p.smem, size_t(d.cols) * 8);
     if (d.type == TL_TYPE_BF16)
@@ -626,10 +678,8 @@ cudaError_t make_plan(const NormDesc& d, bool backward, int num_sms, Plan* out) 
         p.kernel = vec > 1 ? pick<__half, 8>(backward, p.warp_row, e) : pick<__half, 1>(backward, p.warp_row, e);
     else
         p.kernel = vec > 1 ? pick<float, 4>(backward, p.warp_row, e) : pick<float, 1>(backward, p.warp_row, e);
-    cudaError_t err = cudaFuncSetAttribute(p.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(p.smem));
-    if (err != cudaSuccess) return err;
     int per_sm = 1;
-    err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, p.kernel, p.threads, p.smem);
+    const cudaError_t err = ctas_per_sm(reinterpret_cast<const void*>(p.kernel), p.threads, p.smem, &per_sm);
     if (err != cudaSuccess) return err;
     if (per_sm < 1) return cudaErrorInvalidConfiguration;
     per_sm = std::min(per_sm, kCtasPerSm);

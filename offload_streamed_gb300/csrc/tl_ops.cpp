@@ -2,6 +2,7 @@
 // norm, 8-bit product, orthogonalised update): argument checks, workspaces
 // and launches.  The kernels are in tl_norm.cu, tl_fp8.cu and tl_ortho.cu.
 #include "tiled_linear.h"
+#include "tl_launch.h"
 #include "tl_norm.h"
 #include "tl_unbound_error.h"
 
@@ -19,15 +20,6 @@ tl_status refuse(tl_status st, const std::string& why) {
 tl_status done(cudaError_t e, const char* what) {
     if (e == cudaSuccess) return TL_OK;
     return refuse(TL_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
-}
-
-// SMs of the current device; 0 if it cannot be told.
-int sm_count() {
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return 0;
-    return sms;
 }
 
 // Nothing is thrown across the ABI.
@@ -66,7 +58,7 @@ tl_status tiled_linear_norm_forward(int64_t rows, int64_t cols, int32_t type, co
         d.rstd = rstd_dev;
         const std::string bad = norm_check(d, false);
         if (!bad.empty()) return refuse(TL_ERR_INVALID, bad);
-        const int sms = sm_count();
+        const int sms = device_sms();
         if (sms < 1) return refuse(TL_ERR_CUDA, "no current device");
         return done(norm_forward_launch(d, sms, static_cast<cudaStream_t>(stream)), "layer norm");
     });
@@ -106,7 +98,7 @@ tl_status tiled_linear_norm_backward(int64_t rows, int64_t cols, int32_t type, c
                          workspace_bytes < tiled_linear_norm_backward_workspace_bytes(rows, cols)))
             return refuse(TL_ERR_WORKSPACE, "workspace is null, not 16-byte aligned or smaller than "
                                             "tiled_linear_norm_backward_workspace_bytes");
-        const int sms = sm_count();
+        const int sms = device_sms();
         if (sms < 1) return refuse(TL_ERR_CUDA, "no current device");
         return done(norm_backward_launch(d, sms, static_cast<cudaStream_t>(stream)), "layer norm backward");
     });

@@ -740,73 +740,79 @@ class HostAdam:
 # no gradient through autograd: each backward is a function of its own.
 
 TL_TYPE_BF16, TL_TYPE_F16, TL_TYPE_F32 = range(3)
-_types = None
+_torch = None
+_types = {}
 
 
-def _type_of(t, where: str) -> int:
-    global _types
-    if _types is None:
+def _t():
+    """torch, imported by the first call that needs it."""
+    global _torch
+    if _torch is None:
         import torch
-        _types = {torch.bfloat16: TL_TYPE_BF16, torch.float16: TL_TYPE_F16, torch.float32: TL_TYPE_F32}
-    got = _types.get(t.dtype)
-    if got is None:
-        raise TiledLinearError(TL_ERR_INVALID, where, f"dtype {t.dtype}: bfloat16, float16 or float32 is wanted")
-    return got
+        _types.update({torch.bfloat16: TL_TYPE_BF16, torch.float16: TL_TYPE_F16, torch.float32: TL_TYPE_F32})
+        _torch = torch
+    return _torch
 
 
 def _refuse(where: str, why: str):
     raise TiledLinearError(TL_ERR_INVALID, where, why)
 
 
-def _matrix(t, where: str, name: str) -> None:
-    """A device matrix whose rows are contiguous."""
+def _type_of(t, where: str) -> int:
+    got = _types.get(t.dtype)
+    if got is None:
+        _refuse(where, f"dtype {t.dtype}: bfloat16, float16 or float32 is wanted")
+    return got
+
+
+def _ld(t, where: str, name: str) -> int:
+    """Leading dimension of a device matrix whose rows are contiguous (that of
+    a single row is its length)."""
     if not t.is_cuda:
         _refuse(where, f"{name} is not on a CUDA device")
     if t.dim() != 2:
         _refuse(where, f"{name} has {t.dim()} dimensions: a matrix is wanted")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    rows, cols = t.shape
+    ld, step = t.stride()
+    if cols > 1 and step != 1:
         _refuse(where, f"the rows of {name} are not contiguous")
+    if rows > 1 and ld < cols:
+        _refuse(where, f"the rows of {name} overlap")
+    return ld if rows > 1 else cols
 
 
-def _ld(t) -> int:
-    """Leading dimension of a matrix (any value will do for a single row)."""
-    return max(t.stride(0), t.shape[1]) if t.shape[0] > 1 else t.shape[1]
-
-
-def _vector(t, n: int, like, where: str, name: str) -> None:
-    if t.shape != (n,) or (n > 1 and t.stride(0) != 1) or t.device != like.device:
+def _vector(t, n: int, device, where: str, name: str) -> None:
+    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1) or t.device != device:
         _refuse(where, f"{name} must be a contiguous vector of {n} on the matrix's device")
 
 
-def _current_stream(t) -> int:
-    import torch
-    if torch.cuda.current_device() != t.device.index:
-        raise TiledLinearError(TL_ERR_INVALID, "current device", f"the tensors are on {t.device}: make it current")
-    return torch.cuda.current_stream().cuda_stream
+def _stream_of(device, where: str) -> int:
+    """The current stream, which is one of `device`."""
+    torch = _torch
+    if torch.cuda.current_device() != device.index:
+        _refuse(where, f"the tensors are on {device}: make it the current device")
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-5):
     """(y, mean, rstd): layer norm over the columns of x [rows, cols] (bf16, fp16 or
     fp32; any row stride).  weight, bias: [cols], both of one of those types, or
     None for ones / zeros.  mean and rstd are fp32 [rows], for the backward."""
-    import torch
-    where = "layer_norm"
-    _matrix(x, where, "x")
-    rows, cols = x.shape
-    ptype = TL_TYPE_F32
-    for v, name in ((weight, "weight"), (bias, "bias")):
-        if v is not None:
-            _vector(v, cols, x, where, name)
-            ptype = _type_of(v, where)
-    if weight is not None and bias is not None and weight.dtype != bias.dtype:
-        _refuse(where, "weight and bias differ in dtype")
-    kind, stream = _type_of(x, where), _current_stream(x)
-    y = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
-    stat = torch.empty((2, rows), dtype=torch.float32, device=x.device)
-    mean, rstd = stat[0], stat[1]
-    tiled_linear_norm_forward(rows, cols, kind, x.data_ptr(), _ld(x), ptype,
-                              weight.data_ptr() if weight is not None else None,
-                              bias.data_ptr() if bias is not None else None, eps, y.data_ptr(), cols,
+    torch, where = _t(), "layer_norm"
+    ldx, (rows, cols), device = _ld(x, where, "x"), x.shape, x.device
+    ptype, wp, bp = TL_TYPE_F32, None, None
+    if weight is not None:
+        _vector(weight, cols, device, where, "weight")
+        ptype, wp = _type_of(weight, where), weight.data_ptr()
+    if bias is not None:
+        _vector(bias, cols, device, where, "bias")
+        if weight is not None and weight.dtype != bias.dtype:
+            _refuse(where, "weight and bias differ in dtype")
+        ptype, bp = _type_of(bias, where), bias.data_ptr()
+    kind, stream = _type_of(x, where), _stream_of(device, where)
+    y = x.new_empty((rows, cols))
+    mean, rstd = x.new_empty(rows, dtype=torch.float32), x.new_empty(rows, dtype=torch.float32)
+    tiled_linear_norm_forward(rows, cols, kind, x.data_ptr(), ldx, ptype, wp, bp, eps, y.data_ptr(), cols,
                               mean.data_ptr(), rstd.data_ptr(), stream)
     return y, mean, rstd
 
@@ -814,28 +820,25 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5):
 def layer_norm_backward(dy, x, mean, rstd, weight=None):
     """(dx, dweight, dbias) of ``layer_norm``: dx like x, dweight and dbias fp32
     [cols] (the derivative by a weight of ones where there is none)."""
-    import torch
-    where = "layer_norm_backward"
-    _matrix(x, where, "x")
-    _matrix(dy, where, "dy")
-    if dy.shape != x.shape or dy.dtype != x.dtype or dy.device != x.device:
+    torch, where = _t(), "layer_norm_backward"
+    ldx, (rows, cols), device = _ld(x, where, "x"), x.shape, x.device
+    lddy = _ld(dy, where, "dy")
+    if dy.shape != x.shape or dy.dtype != x.dtype or dy.device != device:
         _refuse(where, "dy and x differ in shape, dtype or device")
-    rows, cols = x.shape
-    ptype = TL_TYPE_F32
+    ptype, wp = TL_TYPE_F32, None
     if weight is not None:
-        _vector(weight, cols, x, where, "weight")
-        ptype = _type_of(weight, where)
+        _vector(weight, cols, device, where, "weight")
+        ptype, wp = _type_of(weight, where), weight.data_ptr()
     for v, name in ((mean, "mean"), (rstd, "rstd")):
-        _vector(v, rows, x, where, name)
+        _vector(v, rows, device, where, name)
         if v.dtype != torch.float32:
             _refuse(where, f"{name} must be float32")
-    kind, stream = _type_of(x, where), _current_stream(x)
-    dx = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
-    grads = torch.empty((2, cols), dtype=torch.float32, device=x.device)
-    dweight, dbias = grads[0], grads[1]
+    kind, stream = _type_of(x, where), _stream_of(device, where)
+    dx = x.new_empty((rows, cols))
+    dweight, dbias = x.new_empty(cols, dtype=torch.float32), x.new_empty(cols, dtype=torch.float32)
     need = tiled_linear_norm_backward_workspace_bytes(rows, cols)
-    ws = torch.empty(need, dtype=torch.uint8, device=x.device)
-    tiled_linear_norm_backward(rows, cols, kind, dy.data_ptr(), _ld(dy), x.data_ptr(), _ld(x), mean.data_ptr(),
-                               rstd.data_ptr(), ptype, weight.data_ptr() if weight is not None else None,
-                               dx.data_ptr(), cols, dweight.data_ptr(), dbias.data_ptr(), ws.data_ptr(), need, stream)
+    ws = x.new_empty(need, dtype=torch.uint8)
+    tiled_linear_norm_backward(rows, cols, kind, dy.data_ptr(), lddy, x.data_ptr(), ldx, mean.data_ptr(),
+                               rstd.data_ptr(), ptype, wp, dx.data_ptr(), cols, dweight.data_ptr(), dbias.data_ptr(),
+                               ws.data_ptr(), need, stream)
     return dx, dweight, dbias

@@ -163,11 +163,12 @@ def test_norm_nan_and_inf_stay_in_their_rows(tl, cols):
     x, dy, w, b = make(6, cols, torch.float32, 9)
     x[1, cols // 2] = float("nan")
     x[3, cols - 1] = float("inf")
-    good = [0, 2, 4, 5]
+    x[5, 0] = float("-inf")
+    good = [0, 2, 4]
     y, mean, rstd = tl.layer_norm(x.cuda(), w.cuda(), b.cuda())
     y64, m64, r64, _ = forward64(x[good], w, b, 1e-5)
-    assert torch.isnan(y[1]).all() and torch.isnan(y[3]).all()
-    assert torch.isnan(mean[1]) and torch.isinf(mean[3])
+    assert torch.isnan(y[1]).all() and torch.isnan(y[3]).all() and torch.isnan(y[5]).all()
+    assert torch.isnan(mean[1]) and mean[3] == float("inf") and mean[5] == float("-inf")
     assert torch.allclose(y[good].double().cpu(), y64, rtol=1e-5, atol=1e-5)
     dx, _, _ = tl.layer_norm_backward(dy.cuda(), x.cuda(), mean, rstd, w.cuda())
     assert torch.isnan(dx[1]).all() and torch.isfinite(dx[good]).all()
