@@ -511,7 +511,10 @@ tl_status tiled_linear_forward_static(int64_t T, int64_t K, int64_t M, int32_t N
  * calling thread.  Rows and columns are element counts, leading dimensions
  * (ld*) elements between the starts of two rows.  Workspaces belong to the
  * caller and are in use until the call's work has completed: calls that may
- * overlap (other streams) need their own. */
+ * overlap (other streams) need their own.  err_dev is a device int32, zeroed
+ * by the caller before first use, that is only ever OR-ed into: non-zero once
+ * a bounded wait has given up, and the results of that call are then not
+ * valid.  Calls may share one, on any stream. */
 enum { TL_TYPE_BF16 = 0, TL_TYPE_F16 = 1, TL_TYPE_F32 = 2 };  /* tl_type */
 
 /* Layer norm over the columns of each row.
@@ -526,7 +529,8 @@ enum { TL_TYPE_BF16 = 0, TL_TYPE_F16 = 1, TL_TYPE_F32 = 2 };  /* tl_type */
  * Errors: TL_ERR_INVALID, TL_ERR_CUDA. */
 tl_status tiled_linear_norm_forward(int64_t rows, int64_t cols, int32_t type, const void *x_dev, int64_t ldx,
                                     int32_t param_type, const void *weight_dev, const void *bias_dev, float eps,
-                                    void *y_dev, int64_t ldy, float *mean_dev, float *rstd_dev, void *stream);
+                                    void *y_dev, int64_t ldy, float *mean_dev, float *rstd_dev, int32_t *err_dev,
+                                    void *stream);
 
 /* Bytes of workspace that the backward needs (0 if the arguments are invalid). */
 size_t tiled_linear_norm_backward_workspace_bytes(int64_t rows, int64_t cols);
@@ -544,7 +548,7 @@ tl_status tiled_linear_norm_backward(int64_t rows, int64_t cols, int32_t type, c
                                      const void *x_dev, int64_t ldx, const float *mean_dev, const float *rstd_dev,
                                      int32_t param_type, const void *weight_dev, void *dx_dev, int64_t lddx,
                                      float *dweight_dev, float *dbias_dev, void *workspace_dev,
-                                     size_t workspace_bytes, void *stream);
+                                     size_t workspace_bytes, int32_t *err_dev, void *stream);
 
 /* --- pinned host memory helpers ------------------------------------------ */
 /* Page-locked host allocation (cudaHostAlloc, portable); *out = NULL on

@@ -22,6 +22,7 @@ struct NormDesc {
     int64_t ldout = 0;
     float* mean = nullptr;
     float* rstd = nullptr;
+    int32_t* err = nullptr;  // device word that a bounded wait sets
     // backward only
     const void* dy = nullptr;
     int64_t lddy = 0;

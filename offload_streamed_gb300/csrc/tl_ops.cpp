@@ -40,13 +40,15 @@ extern "C" {
 
 tl_status tiled_linear_norm_forward(int64_t rows, int64_t cols, int32_t type, const void* x_dev, int64_t ldx,
                                     int32_t param_type, const void* weight_dev, const void* bias_dev, float eps,
-                                    void* y_dev, int64_t ldy, float* mean_dev, float* rstd_dev, void* stream) {
+                                    void* y_dev, int64_t ldy, float* mean_dev, float* rstd_dev,
+                                    int32_t* err_dev, void* stream) {
     return guarded([&]() -> tl_status {
         NormDesc d;
         d.rows = rows;
         d.cols = cols;
         d.type = type;
         d.param_type = param_type;
+        d.err = err_dev;
         d.x = x_dev;
         d.ldx = ldx;
         d.weight = weight_dev;
@@ -73,7 +75,7 @@ tl_status tiled_linear_norm_backward(int64_t rows, int64_t cols, int32_t type, c
                                      const void* x_dev, int64_t ldx, const float* mean_dev, const float* rstd_dev,
                                      int32_t param_type, const void* weight_dev, void* dx_dev, int64_t lddx,
                                      float* dweight_dev, float* dbias_dev, void* workspace_dev,
-                                     size_t workspace_bytes, void* stream) {
+                                     size_t workspace_bytes, int32_t* err_dev, void* stream) {
     return guarded([&]() -> tl_status {
         NormDesc d;
         d.rows = rows;
@@ -82,6 +84,7 @@ tl_status tiled_linear_norm_backward(int64_t rows, int64_t cols, int32_t type, c
         d.param_type = param_type;
         d.dy = dy_dev;
         d.lddy = lddy;
+        d.err = err_dev;
         d.x = x_dev;
         d.ldx = ldx;
         d.mean = const_cast<float*>(mean_dev);

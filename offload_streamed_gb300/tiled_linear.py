@@ -165,12 +165,12 @@ def load():
         L.tiled_linear_forward_static.argtypes = [i64, i64, i64, i32, vp, vp, vp, vp, vp]
         L.tiled_linear_forward_static.restype = st
         L.tiled_linear_norm_forward.argtypes = [i64, i64, i32, vp, i64, i32, vp, vp, ctypes.c_float, vp, i64, vp,
-                                                vp, vp]
+                                                vp, vp, vp]
         L.tiled_linear_norm_forward.restype = st
         L.tiled_linear_norm_backward_workspace_bytes.argtypes = [i64, i64]
         L.tiled_linear_norm_backward_workspace_bytes.restype = sz
         L.tiled_linear_norm_backward.argtypes = [i64, i64, i32, vp, i64, vp, i64, vp, vp, i32, vp, vp, i64, vp, vp,
-                                                 vp, sz, vp]
+                                                 vp, sz, vp, vp]
         L.tiled_linear_norm_backward.restype = st
         L.tiled_linear_host_alloc.argtypes = [sz, ctypes.POINTER(vp)]
         L.tiled_linear_host_alloc.restype = st
@@ -397,10 +397,10 @@ def tiled_linear_forward_static(T, K, M, N, w_host, x_dev, y_dev, status_host, s
         raise TiledLinearError(st, "tiled_linear_forward_static")
 
 
-def tiled_linear_norm_forward(rows, cols, type, x, ldx, param_type, weight, bias, eps, y, ldy, mean, rstd,
+def tiled_linear_norm_forward(rows, cols, type, x, ldx, param_type, weight, bias, eps, y, ldy, mean, rstd, err,
                               stream) -> None:
     _check(load().tiled_linear_norm_forward(rows, cols, type, x, ldx, param_type, weight, bias, eps, y, ldy, mean,
-                                            rstd, stream), "tiled_linear_norm_forward")
+                                            rstd, err, stream), "tiled_linear_norm_forward")
 
 
 def tiled_linear_norm_backward_workspace_bytes(rows: int, cols: int) -> int:
@@ -408,9 +408,9 @@ def tiled_linear_norm_backward_workspace_bytes(rows: int, cols: int) -> int:
 
 
 def tiled_linear_norm_backward(rows, cols, type, dy, lddy, x, ldx, mean, rstd, param_type, weight, dx, lddx, dweight,
-                               dbias, workspace, workspace_bytes, stream) -> None:
+                               dbias, workspace, workspace_bytes, err, stream) -> None:
     _check(load().tiled_linear_norm_backward(rows, cols, type, dy, lddy, x, ldx, mean, rstd, param_type, weight, dx,
-                                             lddx, dweight, dbias, workspace, workspace_bytes, stream),
+                                             lddx, dweight, dbias, workspace, workspace_bytes, err, stream),
            "tiled_linear_norm_backward")
 
 
@@ -794,6 +794,32 @@ def _stream_of(device, where: str) -> int:
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
+_err_words = {}
+
+
+def _err_word(device) -> int:
+    """Device address of the error word that this process's calls on `device` share."""
+    got = _err_words.get(device.index)
+    if got is None:
+        word = _torch.zeros(4, dtype=_torch.int32, device=device)
+        _torch.cuda.synchronize(device)  # zero before any stream's first call
+        got = _err_words.setdefault(device.index, (word, word.data_ptr()))
+    return got[1]
+
+
+def check_operators(device=None) -> None:
+    """Wait for the device and raise TL_ERR_TIMEOUT if a kernel of the functions
+    below has given up one of its bounded waits since the last check."""
+    torch = _t()
+    index = torch.cuda.current_device() if device is None else torch.device(device).index or 0
+    if index in _err_words:
+        torch.cuda.synchronize(index)
+        bits = int(_err_words[index][0][0])
+        if bits:
+            _err_words[index][0].zero_()
+            raise TiledLinearError(TL_ERR_TIMEOUT, "check_operators", f"error word {bits:#x}")
+
+
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-5):
     """(y, mean, rstd): layer norm over the columns of x [rows, cols] (bf16, fp16 or
     fp32; any row stride).  weight, bias: [cols], both of one of those types, or
@@ -813,7 +839,7 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5):
     y = x.new_empty((rows, cols))
     mean, rstd = x.new_empty(rows, dtype=torch.float32), x.new_empty(rows, dtype=torch.float32)
     tiled_linear_norm_forward(rows, cols, kind, x.data_ptr(), ldx, ptype, wp, bp, eps, y.data_ptr(), cols,
-                              mean.data_ptr(), rstd.data_ptr(), stream)
+                              mean.data_ptr(), rstd.data_ptr(), _err_word(device), stream)
     return y, mean, rstd
 
 
@@ -840,5 +866,5 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None):
     ws = x.new_empty(need, dtype=torch.uint8)
     tiled_linear_norm_backward(rows, cols, kind, dy.data_ptr(), lddy, x.data_ptr(), ldx, mean.data_ptr(),
                                rstd.data_ptr(), ptype, wp, dx.data_ptr(), cols, dweight.data_ptr(), dbias.data_ptr(),
-                               ws.data_ptr(), need, stream)
+                               ws.data_ptr(), need, _err_word(device), stream)
     return dx, dweight, dbias

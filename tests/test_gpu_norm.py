@@ -207,15 +207,17 @@ def test_norm_in_place_and_same_bits(tl):
     s = torch.cuda.current_stream().cuda_stream
     x2, dy2 = xd.clone(), dyd.clone()
     m2, r2 = torch.empty_like(mean), torch.empty_like(rstd)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
     tl.tiled_linear_norm_forward(700, 1544, tl.TL_TYPE_BF16, x2.data_ptr(), 1544, tl.TL_TYPE_BF16, wd.data_ptr(),
-                                 bd.data_ptr(), 1e-5, x2.data_ptr(), 1544, m2.data_ptr(), r2.data_ptr(), s)
+                                 bd.data_ptr(), 1e-5, x2.data_ptr(), 1544, m2.data_ptr(), r2.data_ptr(), err.data_ptr(), s)
     assert torch.equal(x2, y)
     need = tl.tiled_linear_norm_backward_workspace_bytes(700, 1544)
     ws = torch.empty(need, dtype=torch.uint8, device="cuda")
     tl.tiled_linear_norm_backward(700, 1544, tl.TL_TYPE_BF16, dy2.data_ptr(), 1544, xd.data_ptr(), 1544,
                                   mean.data_ptr(), rstd.data_ptr(), tl.TL_TYPE_BF16, wd.data_ptr(), dy2.data_ptr(),
-                                  1544, None, None, ws.data_ptr(), need, s)
-    assert torch.equal(dy2, a[0])
+                                  1544, None, None, ws.data_ptr(), need, err.data_ptr(), s)
+    assert torch.equal(dy2, a[0]) and not err.any()
+    tl.check_operators()
 
 
 def test_norm_no_rows(tl):
