@@ -1,0 +1,428 @@
+// tl_fp8.cu -- the three products of a linear layer on 8-bit operands with a
+// power-of-two scale for each block of 128 along the reduction:
+//
+//   D[i, j] = bf16( sum_b 2^(sa[i, b] + sb[j, b] - 254) sum_{k in block b} A[i, k] B[j, k] )
+//
+// The scales go to the tensor core with the operands: tcgen05.mma's
+// block-scaled form multiplies each 32 products by the two scales' powers of
+// two and adds them in fp32, so there is nothing to do between the blocks and
+// the accumulator stays in tensor memory for the whole reduction.  (A scale of
+// 128 elements is the same byte in four consecutive MMAs.)
+//
+// gemm (many rows): CTA pairs, 256 x 256 output tiles, K-blocks of 128 bytes:
+//   warp 0      TMA producer: 128-row slices of A and B into a shared ring
+//   warp 1      MMA issuer (first CTA): scales shared -> tensor memory once in
+//               four K-blocks, then four MMAs of K = 32 a K-block
+//   warp 2      allocates the tensor memory
+//   warp 3      gathers the scales of four K-blocks (a 32-bit word for each
+//               row) into the layout that the copy to tensor memory takes
+//   warps 4..7  epilogue: fp32 accumulator -> bf16 -> TMA store
+// Two 256-column accumulators and the scales need more than the 512 columns of
+// tensor memory, so the accumulators share 24: the epilogue reads those first,
+// and the next tile's MMAs wait for no more than that.
+//
+// Every wait is bounded; see tl_gemm.cu, whose error protocol this shares.
+#include "tl_fp8.h"
+#include "tl_gemm.h"
+#include "tl_kernel_common.cuh"
+#include "tl_launch.h"
+#include "tl_tmap.h"
+
+#include "tiled_linear.h"
+
+#include <algorithm>
+#include <climits>
+
+namespace tl {
+namespace {
+
+using namespace kc;
+
+constexpr int kFp8BlockK = 128;     // one K-block: one scale block, one 128-byte swizzle row
+constexpr int kChunkBlocks = 4;     // K-blocks whose scales share a 32-bit word
+constexpr int kStagesPair = 5;
+constexpr uint32_t kStageHalf = 128 * 128;  // 128 rows (or reduction indices) of 128 bytes
+constexpr int kSfSlots = 4;
+constexpr uint32_t kSfA = 512, kSfB = 1024, kSfSlot = kSfA + kSfB;
+constexpr uint32_t kAcc1 = 232;     // columns: accumulators at 0 and 232, 256 each,
+constexpr uint32_t kSfCols = 488;   // then two sets of 4 + 8 scale columns
+constexpr uint32_t kSfSet = 12;
+
+// tcgen05.mma, 8-bit operands with one scale byte per 32 reduction elements.
+template <bool PAIR>
+__device__ __forceinline__ void umma_fp8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                         uint32_t accumulate) {
+    if constexpr (PAIR)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
+}
+// 32 lanes x 16 bytes of shared memory to 4 tensor-memory columns, the same in
+// all four quarters of the lanes.
+template <bool PAIR>
+__device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint32_t saddr) {
+    // no swizzle: 8-row groups of 16-byte rows, 128 bytes apart
+    const uint64_t desc = uint64_t((saddr >> 4) & 0x3fffu) | (uint64_t(128 >> 4) << 32) | (uint64_t(1) << 46);
+    if constexpr (PAIR)
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+    else
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+// Instruction descriptor of kind::mxf8f6f4: scale id of B (bits 4-5), formats
+// of A (7-9) and B (10-12; 0 = e4m3, 1 = e5m2), majors (15, 16; 1 = MN),
+// N >> 3 (17-22), scale type (23; 1 = a power of two in 8 bits), M >> 4 at
+// 24-28, scale id of A (29-30).
+__host__ __device__ constexpr uint32_t idesc_fp8(int m, int n, bool a_mn, bool b_mn, int fa, int fb) {
+    return (uint32_t(fa) << 7) | (uint32_t(fb) << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+           (uint32_t(n >> 3) << 17) | (1u << 23) | (uint32_t(m >> 4) << 24);
+}
+__device__ __forceinline__ uint32_t with_scale_id(uint32_t idesc, uint32_t id) { return idesc | (id << 4) | (id << 29); }
+
+// Step j (32 reduction elements) of a 128 x 128-byte operand.
+__device__ __forceinline__ uint64_t fp8_desc(bool mn, uint32_t base, int j) {
+    return mn ? smem_desc_sw128(base + uint32_t(j) * 4096u, 16384, 1024) : smem_desc_sw128(base + uint32_t(j) * 32u, 16, 1024);
+}
+
+struct Scales {
+    const uint8_t* p;
+    int64_t i_step, k_step;
+    int32_t i_shift, words;  // words: the four blocks of a word are adjacent and 4-byte aligned
+};
+
+struct Fp8Params {
+    int32_t m_dim, n_dim, k_dim;
+    int32_t num_m, num_n, num_k, num_tiles;
+    int32_t raster, group, stream_shared;
+    uint32_t idesc;
+    Scales a, b;
+    int32_t* err;
+    uint64_t timeout_ns;
+};
+
+// The scale bytes of four K-blocks from kb on, for index i: 1.0 (127) outside.
+__device__ __forceinline__ uint32_t scale_word(const Scales& s, int i, int dim, int kb, int num_k) {
+    if (i >= dim) return 0x7f7f7f7fu;
+    const uint8_t* at = s.p + int64_t(i >> s.i_shift) * s.i_step + int64_t(kb) * s.k_step;
+    if (s.words && kb + kChunkBlocks <= num_k) return __ldg(reinterpret_cast<const uint32_t*>(at));
+    uint32_t w = 0;
+#pragma unroll
+    for (int j = 0; j < kChunkBlocks; ++j)
+        w |= (kb + j < num_k ? uint32_t(__ldg(at + j * s.k_step)) : 127u) << (8 * j);
+    return w;
+}
+
+constexpr size_t kSmemPair = size_t(kStagesPair) * 2 * kStageHalf + 4 * 2 * kEpiBuf + kSfSlots * kSfSlot + kBarBytes + 1024;
+static_assert(kSmemPair <= 232448, "shared memory budget");
+
+template <bool A_MN, bool B_MN>
+__global__ void __launch_bounds__(kThreads, 1)
+    fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                    const __grid_constant__ CUtensorMap map_d, const Fp8Params p) {
+    const WaitCtx wc{p.err, p.timeout_ns};
+    constexpr int S = kStagesPair;
+    constexpr uint32_t kStage = 2 * kStageHalf;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t smem0 = smem_addr(smem);
+    const uint32_t epi_base = smem0 + S * kStage, sf0 = epi_base + 8 * kEpiBuf;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S * kStage + 8 * kEpiBuf + kSfSlots * kSfSlot);
+    const uint32_t bar0 = smem_addr(bars);
+    // full[s], empty[s], sf_full[q], sf_empty[q], tmem_full[a], shared columns
+    // read, drain.  full, sf_full and the shared columns' barrier are used in
+    // the first CTA only.
+    auto full_bar = [&](uint32_t s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](uint32_t s) { return bar0 + 8u * (S + s); };
+    auto sf_full_bar = [&](uint32_t q) { return bar0 + 8u * (2 * S + q); };
+    auto sf_empty_bar = [&](uint32_t q) { return bar0 + 8u * (2 * S + kSfSlots + q); };
+    auto tfull_bar = [&](uint32_t a) { return bar0 + 8u * (2 * S + 2 * kSfSlots + a); };
+    const uint32_t tread_bar = bar0 + 8u * (2 * S + 2 * kSfSlots + 2);
+    const uint32_t drain_bar = bar0 + 8u * (2 * S + 2 * kSfSlots + 3);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 2 * kSfSlots + 4);
+    static_assert((2 * S + 2 * kSfSlots + 4) * 8 + 4 <= int(kBarBytes), "barrier area");
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+    const int first_tile = int(cluster_id_x()), tile_step = int(cluster_count_x());
+    const int chunks = (p.num_k + kChunkBlocks - 1) / kChunkBlocks;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(full_bar(s), 1);
+            mbar_init(empty_bar(s), 1);
+        }
+        for (int q = 0; q < kSfSlots; ++q) {
+            mbar_init(sf_full_bar(q), 2);  // the scale warps of both CTAs
+            mbar_init(sf_empty_bar(q), 1);
+        }
+        for (int a = 0; a < 2; ++a) mbar_init(tfull_bar(a), 1);
+        mbar_init(tread_bar, 8);  // the epilogue warps of both CTAs
+        mbar_init(drain_bar, 1);
+        mbar_init_fence();
+    }
+    if (warp == 2) {
+        tmem_alloc<true>(smem_addr(tmem_slot), 512);
+        tmem_relinquish<true>();
+    }
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            tma_prefetch_map(&map_a);
+            tma_prefetch_map(&map_b);
+            const uint64_t pol_s = p.stream_shared ? l2_policy_evict_normal() : l2_policy_evict_first();
+            const uint64_t pol_a = p.raster == 0 ? l2_policy_evict_last() : pol_s;
+            const uint64_t pol_b = p.raster == 0 ? pol_s : l2_policy_evict_last();
+            uint32_t fills = 0;
+            bool ok = true;
+            for (int tile = first_tile; ok && tile < p.num_tiles; tile += tile_step) {
+                int mb, nb;
+                tile_coords(tile, p.num_m, p.num_n, p.raster, p.group, mb, nb);
+                const int m0 = mb * 256 + int(rank) * 128, n0 = nb * 256 + int(rank) * 128;
+                for (int kb = 0; kb < p.num_k; ++kb, ++fills) {
+                    const uint32_t s = fills % S;
+                    if (!wait_bounded(empty_bar(s), ((fills / S) & 1u) ^ 1u, wc, kErrProducerWait)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t sa = smem0 + s * kStage, sb = sa + kStageHalf;
+                    const int k0 = kb * kFp8BlockK;
+                    if (leader) mbar_arrive_expect_tx(full_bar(s), 2 * kStage);
+                    const uint32_t fb = map_to_rank(full_bar(s), 0);
+                    if (A_MN) tma_load_2d_pair_hint(sa, &map_a, fb, m0, k0, pol_a);
+                    else tma_load_2d_pair_hint(sa, &map_a, fb, k0, m0, pol_a);
+                    if (B_MN) tma_load_2d_pair_hint(sb, &map_b, fb, n0, k0, pol_b);
+                    else tma_load_2d_pair_hint(sb, &map_b, fb, k0, n0, pol_b);
+                }
+            }
+            if (leader) {  // loads must land before the CTAs may exit
+                const uint32_t outstanding = fills < uint32_t(S) ? fills : uint32_t(S);
+                for (uint32_t j = 0; j < outstanding; ++j) {
+                    const uint32_t f = fills - 1 - j;
+                    wait_bounded(full_bar(f % S), (f / S) & 1u, wc, kErrDrainWait, false);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && leader) {
+            uint32_t fills = 0, chunk = 0;
+            bool ok = true;
+            int it = 0;
+            for (int tile = first_tile; ok && tile < p.num_tiles; tile += tile_step, ++it) {
+                // the other accumulator's tile has left the shared columns
+                // (and the tile before that, all of this accumulator)
+                if (it > 0 && !wait_bounded(tread_bar, uint32_t(it - 1) & 1u, wc, kErrMmaWaitTmem)) break;
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + (it & 1 ? kAcc1 : 0u);
+                for (int kb = 0; kb < p.num_k; ++kb, ++fills) {
+                    const uint32_t q = chunk % kSfSlots, set = tmem_base + kSfCols + (chunk & 1u) * kSfSet;
+                    const uint32_t id = uint32_t(kb) % kChunkBlocks;
+                    if (id == 0) {
+                        // the MMAs that last read this set of columns are done
+                        if (chunk >= 2 && !wait_bounded(sf_empty_bar((chunk - 2) % kSfSlots), ((chunk - 2) / kSfSlots) & 1u,
+                                                        wc, kErrMmaWaitTmem))
+                            ok = false;
+                        if (ok && !wait_bounded_cluster(sf_full_bar(q), (chunk / kSfSlots) & 1u, wc, kErrMmaWaitFull)) ok = false;
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t src = sf0 + q * kSfSlot;
+                        tmem_copy_scales<true>(set, src);
+                        tmem_copy_scales<true>(set + 4, src + kSfA);
+                        tmem_copy_scales<true>(set + 8, src + kSfA + 512);
+                    }
+                    const uint32_t s = fills % S;
+                    if (!wait_bounded(full_bar(s), (fills / S) & 1u, wc, kErrMmaWaitFull)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sa = smem0 + s * kStage, sb = sa + kStageHalf;
+                    const uint32_t idesc = with_scale_id(p.idesc, id);
+#pragma unroll
+                    for (int j = 0; j < kFp8BlockK / 32; ++j)
+                        umma_fp8<true>(d_tmem, fp8_desc(A_MN, sa, j), fp8_desc(B_MN, sb, j), idesc, set, set + 4,
+                                       (kb | j) != 0 ? 1u : 0u);
+                    umma_commit_pair(empty_bar(s), 0x3);
+                    if (id == kChunkBlocks - 1 || kb == p.num_k - 1) {
+                        umma_commit_pair(sf_empty_bar(q), 0x3);
+                        ++chunk;
+                    }
+                }
+                if (ok) umma_commit_pair(tfull_bar(it & 1), 0x3);
+            }
+            umma_commit_pair(drain_bar, 0x3);
+            wait_bounded(drain_bar, 0, wc, kErrDrainWait, false);
+        }
+    } else if (warp == 3) {
+        // ---------------- scales: this CTA's 128 rows of A, all 256 of B ----------------
+        uint32_t chunk = 0;
+        bool ok = true;
+        for (int tile = first_tile; ok && tile < p.num_tiles; tile += tile_step) {
+            int mb, nb;
+            tile_coords(tile, p.num_m, p.num_n, p.raster, p.group, mb, nb);
+            const int m0 = mb * 256 + int(rank) * 128, n0 = nb * 256;
+            uint32_t w[12];
+            auto load = [&](int c) {
+                const int kb = c * kChunkBlocks;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[j] = scale_word(p.a, m0 + 32 * j + lane, p.m_dim, kb, p.num_k);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[4 + j] = scale_word(p.b, n0 + 32 * j + lane, p.n_dim, kb, p.num_k);
+            };
+            load(0);
+            for (int c = 0; c < chunks; ++c, ++chunk) {
+                const uint32_t q = chunk % kSfSlots;
+                if (!warp_wait(sf_empty_bar(q), ((chunk / kSfSlots) & 1u) ^ 1u, wc, kErrProducerWait, lane)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t dst = sf0 + q * kSfSlot + uint32_t(lane) * 16;
+                st_shared_v4(dst, w[0], w[1], w[2], w[3]);
+                st_shared_v4(dst + kSfA, w[4], w[5], w[6], w[7]);
+                st_shared_v4(dst + kSfA + 512, w[8], w[9], w[10], w[11]);
+                fence_proxy_async_shared();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(map_to_rank(sf_full_bar(q), 0));
+                if (c + 1 < chunks) load(c + 1);
+            }
+        }
+    } else if (warp >= kFirstEpilogueWarp) {
+        const int q = warp & 3;
+        const uint32_t epi0 = epi_base + uint32_t(q) * 2u * kEpiBuf;
+        if (lane == 0) tma_prefetch_map(&map_d);
+        uint32_t buf = 0;
+        int it = 0;
+        for (int tile = first_tile; tile < p.num_tiles; tile += tile_step, ++it) {
+            const uint32_t acc = it & 1;
+            int mb, nb;
+            tile_coords(tile, p.num_m, p.num_n, p.raster, p.group, mb, nb);
+            const int row0 = mb * 256 + int(rank) * 128 + q * 32, n0 = nb * 256;
+            const int have = row0 < p.m_dim ? min(4, (p.n_dim - n0 + 63) / 64) : 0;
+            if (!warp_wait(tfull_bar(acc), uint32_t(it >> 1) & 1u, wc, kErrEpilogueWait, lane)) break;
+            tc_fence_after();
+            const uint32_t t_row = tmem_base + (uint32_t(q * 32) << 16) + (acc ? kAcc1 : 0u);
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i) {
+                const int c = acc ? i : 3 - i;  // the shared columns first
+                if (c < have)
+                    epi_bf16_tma(&map_d, t_row + uint32_t(c) * 64u, epi0, buf, 1, n0 + c * 64, row0, lane);
+                if (i == 0) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (leader) mbar_arrive(tread_bar);
+                        else mbar_arrive_cluster(map_to_rank(tread_bar, 0));
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+        }
+        if (lane == 0) bulk_wait_group_all();
+        __syncwarp();
+    }
+
+    tc_fence_before();
+    cluster_sync();
+    if (warp == 2) {
+        tc_fence_after();
+        if (!leader) wait_bounded(drain_bar, 0, wc, kErrDrainWait, false);
+        tmem_dealloc<true>(tmem_base, 512);
+    }
+}
+
+bool map_operand(CUtensorMap* map, const Fp8Operand& o, int64_t dim, int64_t k, uint32_t box_rows, std::string* why) {
+    return o.mn_major ? swizzled_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, o.q, uint64_t(dim), uint64_t(k), uint64_t(o.ld), 128, why)
+                      : swizzled_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, o.q, uint64_t(k), uint64_t(dim), uint64_t(o.ld), box_rows, why);
+}
+
+Scales scales_of(const Fp8Operand& o) {
+    Scales s{o.scale, o.i_step, o.k_step, o.i_shift, 0};
+    s.words = o.k_step == 1 && o.i_step % 4 == 0 && (reinterpret_cast<uintptr_t>(o.scale) & 3) == 0;
+    return s;
+}
+
+template <typename K>
+cudaError_t launch_clusters(K kern, int grid, int cluster, int threads, size_t smem, cudaStream_t stream, const CUtensorMap& ma,
+                            const CUtensorMap& mb, const CUtensorMap& md, const Fp8Params& p) {
+    int per_sm = 0;
+    const cudaError_t e = ctas_per_sm(reinterpret_cast<const void*>(kern), threads, smem, &per_sm);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(unsigned(grid), 1, 1);
+    cfg.blockDim = dim3(unsigned(threads), 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = unsigned(cluster);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, ma, mb, md, p);
+}
+
+}  // namespace
+
+std::string fp8_gemm_check(const Fp8GemmDesc& g) {
+    if (g.m_dim < 1 || g.n_dim < 1 || g.k_dim < 1) return "sizes must be >= 1";
+    if (g.m_dim > INT32_MAX / 2 || g.n_dim > INT32_MAX / 2 || g.k_dim > INT32_MAX / 2) return "size too large";
+    if (!g.a.q || !g.b.q || !g.a.scale || !g.b.scale || !g.d || !g.err) return "null pointer";
+    auto off = [](const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; };
+    if (off(g.a.q, 16) || off(g.b.q, 16) || off(g.d, 16)) return "operand pointers must be 16-byte aligned";
+    if (off(g.err, 4)) return "err must be 4-byte aligned";
+    if (g.a.ld % 16 || g.b.ld % 16) return "leading dimensions of 8-bit matrices must be multiples of 16";
+    if (g.ldd % 8) return "the result's leading dimension must be a multiple of 8";
+    if (g.a.ld < (g.a.mn_major ? g.m_dim : g.k_dim) || g.b.ld < (g.b.mn_major ? g.n_dim : g.k_dim) || g.ldd < g.n_dim)
+        return "a leading dimension is smaller than a row";
+    for (const auto* o : {&g.a, &g.b})
+        if (o->format != TL_FP8_E4M3 && o->format != TL_FP8_E5M2) return "unknown tl_fp8_format";
+    if (((g.m_dim + 255) / 256) * ((g.n_dim + 255) / 256) > INT32_MAX) return "too many output tiles";
+    return {};
+}
+
+cudaError_t fp8_gemm_launch(const Fp8GemmDesc& g, int num_sms, cudaStream_t stream, std::string* why) {
+    CUtensorMap ma, mb, md;
+    if (!map_operand(&ma, g.a, g.m_dim, g.k_dim, 128, why) || !map_operand(&mb, g.b, g.n_dim, g.k_dim, 128, why) ||
+        !swizzled_map(&md, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, g.d, uint64_t(g.n_dim), uint64_t(g.m_dim), uint64_t(g.ldd), 32, why))
+        return cudaErrorInvalidValue;
+    Fp8Params p{};
+    p.m_dim = int32_t(g.m_dim);
+    p.n_dim = int32_t(g.n_dim);
+    p.k_dim = int32_t(g.k_dim);
+    p.num_m = int32_t((g.m_dim + 255) / 256);
+    p.num_n = int32_t((g.n_dim + 255) / 256);
+    p.num_k = int32_t((g.k_dim + kFp8BlockK - 1) / kFp8BlockK);
+    p.num_tiles = p.num_m * p.num_n;
+    const int slots = std::max(1, num_sms / 2);
+    // the order is chosen by the blocks' bytes: an 8-bit reduction of k counts as a bf16 one of k / 2
+    choose_tile_order(std::max<int64_t>(1, g.k_dim / 2), 256, p.num_m, p.num_n, slots, &p.raster, &p.group, &p.stream_shared);
+    p.a = scales_of(g.a);
+    p.b = scales_of(g.b);
+    p.err = g.err;
+    p.timeout_ns = 2000000000ull;
+    p.idesc = idesc_fp8(256, 256, g.a.mn_major, g.b.mn_major, g.a.format, g.b.format);
+    const int grid = 2 * std::min(p.num_tiles, slots);
+    auto run = [&](auto kern) { return launch_clusters(kern, grid, 2, kThreads, kSmemPair, stream, ma, mb, md, p); };
+    cudaError_t e;
+    if (g.a.mn_major) e = g.b.mn_major ? run(fp8_gemm_kernel<true, true>) : cudaErrorInvalidValue;
+    else e = g.b.mn_major ? run(fp8_gemm_kernel<false, true>) : run(fp8_gemm_kernel<false, false>);
+    if (e != cudaSuccess && why) *why = std::string("kernel launch: ") + cudaGetErrorString(e);
+    return e;
+}
+
+}  // namespace tl

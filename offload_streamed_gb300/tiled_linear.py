@@ -172,6 +172,11 @@ def load():
         L.tiled_linear_norm_backward.argtypes = [i64, i64, i32, vp, i64, vp, i64, vp, vp, i32, vp, vp, i64, vp, vp,
                                                  vp, sz, vp, vp]
         L.tiled_linear_norm_backward.restype = st
+        L.tiled_linear_fp8_quantize.argtypes = [i64, i64, i32, vp, i64, i32] + [vp, i64, vp, i64] * 3 + [vp]
+        L.tiled_linear_fp8_quantize.restype = st
+        for name in ("tiled_linear_fp8_gemm_forward", "tiled_linear_fp8_gemm_dx", "tiled_linear_fp8_gemm_dw"):
+            getattr(L, name).argtypes = [i64, i64, i64] + [i32, vp, i64, vp, i64] * 2 + [vp, i64, vp, vp]
+            getattr(L, name).restype = st
         L.tiled_linear_host_alloc.argtypes = [sz, ctypes.POINTER(vp)]
         L.tiled_linear_host_alloc.restype = st
         L.tiled_linear_host_free.argtypes = [vp]
@@ -412,6 +417,32 @@ def tiled_linear_norm_backward(rows, cols, type, dy, lddy, x, ldx, mean, rstd, p
     _check(load().tiled_linear_norm_backward(rows, cols, type, dy, lddy, x, ldx, mean, rstd, param_type, weight, dx,
                                              lddx, dweight, dbias, workspace, workspace_bytes, err, stream),
            "tiled_linear_norm_backward")
+
+
+def tiled_linear_fp8_quantize(rows, cols, type, x, ldx, format, row_q, ld_row, row_scale, ld_row_scale, col_q, ld_col,
+                              col_scale, ld_col_scale, tile_q, ld_tile, tile_scale, ld_tile_scale, stream) -> None:
+    _check(load().tiled_linear_fp8_quantize(rows, cols, type, x, ldx, format, row_q, ld_row, row_scale, ld_row_scale,
+                                            col_q, ld_col, col_scale, ld_col_scale, tile_q, ld_tile, tile_scale,
+                                            ld_tile_scale, stream), "tiled_linear_fp8_quantize")
+
+
+def tiled_linear_fp8_gemm_forward(T, K, n, x_format, x_q, ldx, x_scale, ld_x_scale, w_format, w_q, ldw, w_scale,
+                                  ld_w_scale, y, ldy, err, stream) -> None:
+    _check(load().tiled_linear_fp8_gemm_forward(T, K, n, x_format, x_q, ldx, x_scale, ld_x_scale, w_format, w_q, ldw,
+                                                w_scale, ld_w_scale, y, ldy, err, stream),
+           "tiled_linear_fp8_gemm_forward")
+
+
+def tiled_linear_fp8_gemm_dx(T, K, n, dy_format, dy_q, lddy, dy_scale, ld_dy_scale, w_format, w_q, ldw, w_scale,
+                             ld_w_scale, dx, lddx, err, stream) -> None:
+    _check(load().tiled_linear_fp8_gemm_dx(T, K, n, dy_format, dy_q, lddy, dy_scale, ld_dy_scale, w_format, w_q, ldw,
+                                           w_scale, ld_w_scale, dx, lddx, err, stream), "tiled_linear_fp8_gemm_dx")
+
+
+def tiled_linear_fp8_gemm_dw(T, K, n, x_format, x_q, ldx, x_scale, ld_x_scale, dy_format, dy_q, lddy, dy_scale,
+                             ld_dy_scale, dw, lddw, err, stream) -> None:
+    _check(load().tiled_linear_fp8_gemm_dw(T, K, n, x_format, x_q, ldx, x_scale, ld_x_scale, dy_format, dy_q, lddy,
+                                           dy_scale, ld_dy_scale, dw, lddw, err, stream), "tiled_linear_fp8_gemm_dw")
 
 
 def tiled_linear_host_alloc(nbytes: int) -> int:
@@ -868,3 +899,145 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None):
                                rstd.data_ptr(), ptype, wp, dx.data_ptr(), cols, dweight.data_ptr(), dbias.data_ptr(),
                                ws.data_ptr(), need, _err_word(device), stream)
     return dx, dweight, dbias
+
+
+TL_FP8_E4M3, TL_FP8_E5M2 = range(2)
+FP8_BLOCK = 128
+
+
+def _up(n: int, to: int) -> int:
+    return -(-n // to) * to
+
+
+def _fp8_format(t, where: str, name: str) -> int:
+    torch = _torch
+    if t.dtype == torch.float8_e4m3fn:
+        return TL_FP8_E4M3
+    if t.dtype == torch.float8_e5m2:
+        return TL_FP8_E5M2
+    _refuse(where, f"{name} has dtype {t.dtype}: float8_e4m3fn or float8_e5m2 is wanted")
+
+
+def _fp8_forms(rows: int, cols: int, form: str):
+    """(shape of the scales, their leading dimension) of a form."""
+    rb, cb = -(-rows // FP8_BLOCK), -(-cols // FP8_BLOCK)
+    if form == "row":
+        return (rows, cb), _up(cb, 4)
+    if form == "col":
+        return (rb, cols), cols
+    if form == "tile":
+        return (rb, cb), cb
+    _refuse("fp8_quantize", f"form {form!r}: 'row', 'col' or 'tile' is wanted")
+
+
+def fp8_quantize(x, *forms: str, format: str = "e4m3"):
+    """x [rows, cols] (bf16, fp16 or fp32) in 8 bits: (q, scale) for one form, a
+    tuple of such pairs for several, all from one reading of x.
+
+    forms: "row" (a scale for 128 columns of a row), "col" (128 rows of a column),
+    "tile" (128 x 128).  q: float8_e4m3fn or (format="e5m2") float8_e5m2
+    [rows, cols], rows on 16-byte boundaries; scale: uint8, q stands for
+    q * 2^(scale - 127)."""
+    torch, where = _t(), "fp8_quantize"
+    ldx, (rows, cols), device = _ld(x, where, "x"), x.shape, x.device
+    kind, stream = _type_of(x, where), _stream_of(device, where)
+    if cols < 1 or not forms or len(set(forms)) < len(forms):
+        _refuse(where, "x needs a column, and at least one form, each named once")
+    if format not in ("e4m3", "e5m2"):
+        _refuse(where, f"format {format!r}: 'e4m3' or 'e5m2' is wanted")
+    dtype = torch.float8_e4m3fn if format == "e4m3" else torch.float8_e5m2
+    ldq, out, args = _up(cols, 16), [], {}
+    for form in forms:
+        shape, lds = _fp8_forms(rows, cols, form)
+        q = x.new_empty((rows, ldq), dtype=dtype)
+        scale = x.new_empty((shape[0], lds), dtype=torch.uint8)
+        args[form] = (q.data_ptr(), ldq, scale.data_ptr(), lds)
+        out.append((q if ldq == cols else q[:, :cols], scale if lds == shape[1] else scale[:, :shape[1]]))
+    none = (None, 0, None, 0)
+    tiled_linear_fp8_quantize(rows, cols, kind, x.data_ptr(), ldx, 0 if format == "e4m3" else 1,
+                              *args.get("row", none), *args.get("col", none), *args.get("tile", none), stream)
+    return out[0] if len(forms) == 1 else tuple(out)
+
+
+def _fp8_operand(q, scale, form: str, where: str, name: str):
+    """(format, pointer, ld, scale pointer, ld of scales) of a matrix in 8 bits."""
+    fmt, ld = _fp8_format(q, where, name), _ld(q, where, name)
+    rows, cols = q.shape
+    shape, _ = _fp8_forms(rows, cols, form)
+    if scale.dtype != _torch.uint8 or tuple(scale.shape) != shape or scale.device != q.device:
+        _refuse(where, f"the scales of {name} must be uint8 {list(shape)} on its device")
+    lds = _ld(scale, where, f"the scales of {name}")
+    if rows == 1:
+        ld = _up(cols, 16)  # one row: there is no second for it to lead to
+    return fmt, q.data_ptr(), ld, scale.data_ptr(), lds
+
+
+def _fp8_result(x, rows: int, cols: int):
+    ld = _up(cols, 8)
+    out = x.new_empty((rows, ld), dtype=_torch.bfloat16)
+    return (out if ld == cols else out[:, :cols]), ld
+
+
+def _weight_shape(q, where: str):
+    if q.dim() != 2 or 0 in q.shape:
+        _refuse(where, "the weight must be a matrix [K, n] with K, n >= 1")
+    return q.shape
+
+
+def fp8_matmul(x, w):
+    """y [T, n] bf16 = x [T, K] . w [K, n], x = (q, scale) in the row form and
+    w = (q, scale) in the tile form."""
+    _t()
+    where, (xq, xs), (wq, ws) = "fp8_matmul", x, w
+    (K, n), T = _weight_shape(wq, where), xq.shape[0]
+    if xq.dim() != 2 or xq.shape[1] != K or xq.device != wq.device:
+        _refuse(where, "x and the weight do not fit each other")
+    y, ldy = _fp8_result(xq, T, n)
+    tiled_linear_fp8_gemm_forward(T, K, n, *_fp8_operand(xq, xs, "row", where, "x"),
+                                  *_fp8_operand(wq, ws, "tile", where, "the weight"), y.data_ptr(), ldy,
+                                  _err_word(xq.device), _stream_of(xq.device, where))
+    return y
+
+
+def fp8_matmul_dx(dy, w):
+    """dx [T, K] bf16 = dy [T, n] . w [K, n]^T, dy in the row form, w in the tile form."""
+    _t()
+    where, (dyq, dys), (wq, ws) = "fp8_matmul_dx", dy, w
+    (K, n), T = _weight_shape(wq, where), dyq.shape[0]
+    if dyq.dim() != 2 or dyq.shape[1] != n or dyq.device != wq.device:
+        _refuse(where, "dy and the weight do not fit each other")
+    dx, lddx = _fp8_result(dyq, T, K)
+    tiled_linear_fp8_gemm_dx(T, K, n, *_fp8_operand(dyq, dys, "row", where, "dy"),
+                             *_fp8_operand(wq, ws, "tile", where, "the weight"), dx.data_ptr(), lddx,
+                             _err_word(dyq.device), _stream_of(dyq.device, where))
+    return dx
+
+
+def fp8_matmul_dw(x, dy):
+    """dw [K, n] bf16 = x [T, K]^T . dy [T, n], both in the col form."""
+    _t()
+    where, (xq, xs), (dyq, dys) = "fp8_matmul_dw", x, dy
+    if xq.dim() != 2 or dyq.dim() != 2 or xq.shape[0] != dyq.shape[0] or xq.device != dyq.device \
+            or 0 in (xq.shape[1], dyq.shape[1]):
+        _refuse(where, "x and dy do not fit each other")
+    (T, K), n = xq.shape, dyq.shape[1]
+    dw, lddw = _fp8_result(xq, K, n)
+    tiled_linear_fp8_gemm_dw(T, K, n, *_fp8_operand(xq, xs, "col", where, "x"),
+                             *_fp8_operand(dyq, dys, "col", where, "dy"), dw.data_ptr(), lddw, _err_word(xq.device),
+                             _stream_of(xq.device, where))
+    return dw
+
+
+def fp8_linear(x, wq, ws):
+    """y [T, n] bf16 = x [T, K] . w with w in 8 bits (``fp8_quantize(w, "tile")``);
+    x (bf16, fp16 or fp32) is quantised on the way, with a scale for each 128
+    columns of a row."""
+    return fp8_matmul(fp8_quantize(x, "row"), (wq, ws))
+
+
+def fp8_linear_backward(x, dy, wq, ws):
+    """(dx [T, K], dw [K, n]) bf16 of ``fp8_linear`` for dy [T, n], as products in 8
+    bits: dy . w^T with dy's rows in blocks of 128, x^T . dy with blocks of 128
+    tokens.  (The derivative passes through the rounding to 8 bits.)"""
+    dy_row, dy_col = fp8_quantize(dy, "row", "col")
+    return fp8_matmul_dx(dy_row, (wq, ws)), fp8_matmul_dw(fp8_quantize(x, "col"), dy_col)
