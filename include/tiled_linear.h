@@ -554,10 +554,13 @@ tl_status tiled_linear_norm_backward(int64_t rows, int64_t cols, int32_t type, c
  * A matrix in 8 bits is one byte an element (e4m3 or e5m2) and one scale byte
  * for each block of 128: the element stands for q 2^(scale - 127).  Forms, for
  * a [rows, cols] matrix (values always [rows, cols], row-major):
- *   row : blocks of 128 columns of a row,  scales [rows, ceil(cols / 128)]
- *   col : blocks of 128 rows of a column,  scales [ceil(rows / 128), cols]
- *   tile: blocks of 128 x 128,             scales [ceil(rows / 128), ceil(cols / 128)]
- * Blocks at the edges are smaller.  A linear layer Y = X.W keeps W in the tile
+ *   row : blocks of 128 columns of a row,  scales [ceil(cols / 512)][rows][4]
+ *   col : blocks of 128 rows of a column,  scales [ceil(rows / 512)][cols][4]
+ *   tile: blocks of 128 x 128,             scales [ceil(rows / 128)][ceil(cols / 128)]
+ * Blocks at the edges are smaller.  In the row and col forms four blocks that
+ * follow each other along a row (column) are one 32-bit word, lowest byte first,
+ * and the words of neighbouring rows (columns) are adjacent, as the products
+ * take them; bytes past the last block are 127.  A linear layer Y = X.W keeps W in the tile
  * form, which serves the forward and dX; it takes X and dY in the row form
  * there, and both in the col form for dW, since the blocks run along each
  * product's reduction. */
@@ -568,15 +571,14 @@ enum { TL_FP8_E4M3 = 0, TL_FP8_E5M2 = 1 };  /* tl_fp8_format */
  *   scale = 2^e, e the least whole number >= -127 with amax <= top 2^e (top = 448
  *   for e4m3, 57344 for e5m2), 1 for a block of zeros; q = x / scale to nearest
  *   even.  A block that holds an infinity or NaN has the NaN scale, 255.
- * Leading dimensions of q and of scales are in bytes.  The products below want
- * 16-byte aligned values with leading dimensions that are multiples of 16, and
- * read row scales four at a time where those are 4-byte aligned with a leading
- * dimension that is a multiple of 4.  rows = 0 is a no-op.
+ * Leading dimensions of q are in bytes.  Scales are contiguous, those of the row
+ * and col forms 4-byte aligned.  The products below want 16-byte aligned values
+ * with leading dimensions that are multiples of 16.  rows = 0 is a no-op.
  * Errors: TL_ERR_INVALID, TL_ERR_CUDA. */
 tl_status tiled_linear_fp8_quantize(int64_t rows, int64_t cols, int32_t type, const void *x_dev, int64_t ldx,
-                                    int32_t format, void *row_q, int64_t ld_row, void *row_scale, int64_t ld_row_scale,
-                                    void *col_q, int64_t ld_col, void *col_scale, int64_t ld_col_scale, void *tile_q,
-                                    int64_t ld_tile, void *tile_scale, int64_t ld_tile_scale, void *stream);
+                                    int32_t format, void *row_q, int64_t ld_row, void *row_scale, void *col_q,
+                                    int64_t ld_col, void *col_scale, void *tile_q, int64_t ld_tile, void *tile_scale,
+                                    void *stream);
 
 /* y[T, n] (bf16, ld ldy) = x[T, K] . w[K, n]: x in the row form, w in the tile
  * form.  Products are summed in fp32 over the whole reduction and rounded to
@@ -584,23 +586,20 @@ tl_status tiled_linear_fp8_quantize(int64_t rows, int64_t cols, int32_t type, co
  * ldy is a multiple of 8, y 16-byte aligned.  T = 0 is a no-op.
  * Errors: TL_ERR_INVALID, TL_ERR_CUDA. */
 tl_status tiled_linear_fp8_gemm_forward(int64_t T, int64_t K, int64_t n, int32_t x_format, const void *x_q, int64_t ldx,
-                                        const void *x_scale, int64_t ld_x_scale, int32_t w_format, const void *w_q,
-                                        int64_t ldw, const void *w_scale, int64_t ld_w_scale, void *y_dev, int64_t ldy,
-                                        int32_t *err_dev, void *stream);
+                                        const void *x_scale, int32_t w_format, const void *w_q, int64_t ldw,
+                                        const void *w_scale, void *y_dev, int64_t ldy, int32_t *err_dev, void *stream);
 
 /* dx[T, K] (bf16, ld lddx) = dy[T, n] . w[K, n]^T: dy in the row form, w in the
  * tile form.  Otherwise as the forward. */
 tl_status tiled_linear_fp8_gemm_dx(int64_t T, int64_t K, int64_t n, int32_t dy_format, const void *dy_q, int64_t lddy,
-                                   const void *dy_scale, int64_t ld_dy_scale, int32_t w_format, const void *w_q,
-                                   int64_t ldw, const void *w_scale, int64_t ld_w_scale, void *dx_dev, int64_t lddx,
-                                   int32_t *err_dev, void *stream);
+                                   const void *dy_scale, int32_t w_format, const void *w_q, int64_t ldw,
+                                   const void *w_scale, void *dx_dev, int64_t lddx, int32_t *err_dev, void *stream);
 
 /* dw[K, n] (bf16, ld lddw) = x[T, K]^T . dy[T, n]: both in the col form.  T = 0
  * writes zeros.  Otherwise as the forward. */
 tl_status tiled_linear_fp8_gemm_dw(int64_t T, int64_t K, int64_t n, int32_t x_format, const void *x_q, int64_t ldx,
-                                   const void *x_scale, int64_t ld_x_scale, int32_t dy_format, const void *dy_q,
-                                   int64_t lddy, const void *dy_scale, int64_t ld_dy_scale, void *dw_dev, int64_t lddw,
-                                   int32_t *err_dev, void *stream);
+                                   const void *x_scale, int32_t dy_format, const void *dy_q, int64_t lddy,
+                                   const void *dy_scale, void *dw_dev, int64_t lddw, int32_t *err_dev, void *stream);
 
 /* --- pinned host memory helpers ------------------------------------------ */
 /* Page-locked host allocation (cudaHostAlloc, portable); *out = NULL on

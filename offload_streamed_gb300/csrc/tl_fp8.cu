@@ -93,10 +93,12 @@ __device__ __forceinline__ uint64_t fp8_desc(bool mn, uint32_t base, int j) {
     return mn ? smem_desc_sw128(base + uint32_t(j) * 4096u, 16384, 1024) : smem_desc_sw128(base + uint32_t(j) * 32u, 16, 1024);
 }
 
+// Scales of an operand, as words of four K-blocks' bytes: [chunk][dim] words
+// for vectors, bytes at (i / 128) * i_step + (k / 128) * k_step for tiles.
 struct Scales {
-    const uint8_t* p;
+    const void* p;
     int64_t i_step, k_step;
-    int32_t i_shift, words;  // words: the four blocks of a word are adjacent and 4-byte aligned
+    int32_t dim, tiles;
 };
 
 struct Fp8Params {
@@ -109,16 +111,29 @@ struct Fp8Params {
     uint64_t timeout_ns;
 };
 
-// The scale bytes of four K-blocks from kb on, for index i: 1.0 (127) outside.
-__device__ __forceinline__ uint32_t scale_word(const Scales& s, int i, int dim, int kb, int num_k) {
-    if (i >= dim) return 0x7f7f7f7fu;
-    const uint8_t* at = s.p + int64_t(i >> s.i_shift) * s.i_step + int64_t(kb) * s.k_step;
-    if (s.words && kb + kChunkBlocks <= num_k) return __ldg(reinterpret_cast<const uint32_t*>(at));
-    uint32_t w = 0;
+// The words of ROWS indices from i0 on, 32 apart (lane l has i0 + l, i0 + 32 + l,
+// ...), for chunk c: 1.0 (127) outside the matrix.
+template <int ROWS>
+__device__ __forceinline__ void scale_words(const Scales& s, int i0, int c, int num_k, int lane, uint32_t* w) {
+    if (s.tiles) {  // one word for 128 indices, the same in all lanes
 #pragma unroll
-    for (int j = 0; j < kChunkBlocks; ++j)
-        w |= (kb + j < num_k ? uint32_t(__ldg(at + j * s.k_step)) : 127u) << (8 * j);
-    return w;
+        for (int t = 0; t < ROWS / 4; ++t) {
+            uint32_t v = 0x7f7f7f7fu;
+            if (i0 + 128 * t < s.dim) {
+                const uint8_t* at = static_cast<const uint8_t*>(s.p) + int64_t(i0 / 128 + t) * s.i_step + int64_t(c) * kChunkBlocks * s.k_step;
+                const int have = num_k - c * kChunkBlocks;
+                v = 0;
+#pragma unroll
+                for (int j = 0; j < kChunkBlocks; ++j) v |= (j < have ? uint32_t(__ldg(at + j * s.k_step)) : 127u) << (8 * j);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[4 * t + j] = v;
+        }
+    } else {
+        const uint32_t* at = static_cast<const uint32_t*>(s.p) + int64_t(c) * s.dim + i0 + lane;
+#pragma unroll
+        for (int j = 0; j < ROWS; ++j) w[j] = i0 + 32 * j + lane < s.dim ? __ldg(at + 32 * j) : 0x7f7f7f7fu;
+    }
 }
 
 constexpr size_t kSmemPair = size_t(kStagesPair) * 2 * kStageHalf + 4 * 2 * kEpiBuf + kSfSlots * kSfSlot + kBarBytes + 1024;
@@ -276,11 +291,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int m0 = mb * 256 + int(rank) * 128, n0 = nb * 256;
             uint32_t w[12];
             auto load = [&](int c) {
-                const int kb = c * kChunkBlocks;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) w[j] = scale_word(p.a, m0 + 32 * j + lane, p.m_dim, kb, p.num_k);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) w[4 + j] = scale_word(p.b, n0 + 32 * j + lane, p.n_dim, kb, p.num_k);
+                scale_words<4>(p.a, m0, c, p.num_k, lane, w);
+                scale_words<8>(p.b, n0, c, p.num_k, lane, w + 4);
             };
             load(0);
             for (int c = 0; c < chunks; ++c, ++chunk) {
@@ -349,10 +361,8 @@ bool map_operand(CUtensorMap* map, const Fp8Operand& o, int64_t dim, int64_t k, 
                       : swizzled_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, o.q, uint64_t(k), uint64_t(dim), uint64_t(o.ld), box_rows, why);
 }
 
-Scales scales_of(const Fp8Operand& o) {
-    Scales s{o.scale, o.i_step, o.k_step, o.i_shift, 0};
-    s.words = o.k_step == 1 && o.i_step % 4 == 0 && (reinterpret_cast<uintptr_t>(o.scale) & 3) == 0;
-    return s;
+Scales scales_of(const Fp8Operand& o, int64_t dim) {
+    return Scales{o.scale, o.mn_major ? 1 : o.tile_cols, o.mn_major ? o.tile_cols : 1, int32_t(dim), o.tiles ? 1 : 0};
 }
 
 template <typename K>
@@ -390,6 +400,8 @@ std::string fp8_gemm_check(const Fp8GemmDesc& g) {
     if (g.a.ld < (g.a.mn_major ? g.m_dim : g.k_dim) || g.b.ld < (g.b.mn_major ? g.n_dim : g.k_dim) || g.ldd < g.n_dim)
         return "a leading dimension is smaller than a row";
     for (const auto* o : {&g.a, &g.b})
+        if (!o->tiles && off(o->scale, 4)) return "scales of the row and col forms must be 4-byte aligned";
+    for (const auto* o : {&g.a, &g.b})
         if (o->format != TL_FP8_E4M3 && o->format != TL_FP8_E5M2) return "unknown tl_fp8_format";
     if (((g.m_dim + 255) / 256) * ((g.n_dim + 255) / 256) > INT32_MAX) return "too many output tiles";
     return {};
@@ -411,8 +423,8 @@ cudaError_t fp8_gemm_launch(const Fp8GemmDesc& g, int num_sms, cudaStream_t stre
     const int slots = std::max(1, num_sms / 2);
     // the order is chosen by the blocks' bytes: an 8-bit reduction of k counts as a bf16 one of k / 2
     choose_tile_order(std::max<int64_t>(1, g.k_dim / 2), 256, p.num_m, p.num_n, slots, &p.raster, &p.group, &p.stream_shared);
-    p.a = scales_of(g.a);
-    p.b = scales_of(g.b);
+    p.a = scales_of(g.a, g.m_dim);
+    p.b = scales_of(g.b, g.n_dim);
     p.err = g.err;
     p.timeout_ns = 2000000000ull;
     p.idesc = idesc_fp8(256, 256, g.a.mn_major, g.b.mn_major, g.a.format, g.b.format);

@@ -24,8 +24,7 @@ struct Fp8QuantDesc {
         uint8_t* q = nullptr;  // [rows, cols], ld ldq; nullptr: not wanted
         int64_t ldq = 0;
         uint8_t* scale = nullptr;
-        int64_t lds = 0;
-    } row, col, tile;  // scales [rows, cols/128], [rows/128, cols], [rows/128, cols/128]
+    } row, col, tile;  // scales [cols/512][rows][4], [rows/512][cols][4], [rows/128][cols/128]
 };
 std::string fp8_quantize_check(const Fp8QuantDesc& d);
 cudaError_t fp8_quantize_launch(const Fp8QuantDesc& d, cudaStream_t stream);
@@ -37,10 +36,12 @@ struct Fp8Operand {
     int64_t ld = 0;
     bool mn_major = false;  // (i, k) at q[k * ld + i]; else at q[i * ld + k]
     int32_t format = 0;
-    // scale of (i, k): scale[(i >> i_shift) * i_step + (k / 128) * k_step]
-    const uint8_t* scale = nullptr;
-    int64_t i_step = 0, k_step = 0;
-    int32_t i_shift = 0;
+    // Vectors: byte k / 128 % 4 of the word [k / 512][i].  Tiles: byte
+    // [i / 128][k / 128] or, where the reduction runs down the rows (mn_major),
+    // [k / 128][i / 128] of a matrix of tile_cols columns.
+    const void* scale = nullptr;
+    bool tiles = false;
+    int64_t tile_cols = 0;
 };
 // D [m, n] (bf16, ld ldd) = sum over k of A (i, k) B (j, k)
 struct Fp8GemmDesc {

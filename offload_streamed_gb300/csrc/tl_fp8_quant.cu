@@ -30,7 +30,7 @@ struct QuantArgs {
     int64_t rows, cols;
     Fp8QuantDesc::Form row, col, tile;
     int32_t emax;  // exponent of the format's largest power of two
-    int32_t vec_in;
+    int32_t vec;   // rows of x start on 16-byte boundaries, rows of the results on 8-byte ones
 };
 
 // The scale's byte for a block's largest magnitude (NaN: not finite).
@@ -62,119 +62,166 @@ __device__ __forceinline__ uint32_t quant4(float a, float b, float c, float d) {
     return lo | (hi << 16);
 }
 
-__device__ __forceinline__ void store8(const Fp8QuantDesc::Form& f, int64_t r, int64_t c, int64_t cols, uint32_t lo,
-                                       uint32_t hi) {
-    uint8_t* dst = f.q + r * f.ldq + c;
-    if (c + 8 <= cols && (reinterpret_cast<uintptr_t>(dst) & 7) == 0) {
-        *reinterpret_cast<uint2*>(dst) = make_uint2(lo, hi);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (c + i < cols) dst[i] = uint8_t((i < 4 ? lo >> (8 * i) : hi >> (8 * i - 32)) & 255u);
-    }
+// The scale of block b of `blocks` of vector i of n: a byte of the word
+// [b / 4][i]; the last block writes the bytes that follow it, too.
+__device__ __forceinline__ void store_scale(uint8_t* scale, uint32_t b, uint32_t blocks, int64_t i, int64_t n, uint32_t byte) {
+    uint8_t* word = scale + (int64_t(b / 4) * n + i) * 4;
+    word[b % 4] = uint8_t(byte);
+    if (b == blocks - 1)
+        for (uint32_t j = b % 4 + 1; j < 4; ++j) word[j] = 127;
 }
 
-template <typename T, bool E5M2>
-__global__ void __launch_bounds__(kThreads) fp8_quantize_kernel(const QuantArgs p) {
-    __shared__ float part[16][kFp8Block];  // column maxima of the 16 threads that share a column
-    __shared__ float warp_max[kThreads / 32];
+// Eight elements of a row as they were read, and what is done with them.
+template <typename T>
+struct Eight {
+    static constexpr int N = 16 / sizeof(T), kVecs = 8 / N;
+    Vec<T, N> u[kVecs];
+    __device__ __forceinline__ float at(int i) const { return to_f32(u[i / N].v[i % N]); }
+};
+// The largest magnitude; a NaN stays.  16-bit types in pairs.
+__device__ __forceinline__ float amax8(const Eight<float>& e) {
+    float m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max_nan(m, fabsf(e.at(i)));
+    return m;
+}
+__device__ __forceinline__ float amax8(const Eight<__half>& e) {
+    const __half2* h = reinterpret_cast<const __half2*>(e.u[0].v);
+    const __half2 m = __hmax2_nan(__hmax2_nan(__habs2(h[0]), __habs2(h[1])), __hmax2_nan(__habs2(h[2]), __habs2(h[3])));
+    return __half2float(__hmax_nan(__low2half(m), __high2half(m)));
+}
+__device__ __forceinline__ float amax8(const Eight<__nv_bfloat16>& e) {
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(e.u[0].v);
+    const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(__habs2(h[0]), __habs2(h[1])), __hmax2_nan(__habs2(h[2]), __habs2(h[3])));
+    return __bfloat162float(__hmax_nan(__low2bfloat16(m), __high2bfloat16(m)));
+}
+
+// FORMS: which of the forms are made (bit 0 rows, 1 columns, 2 tiles).
+// WHOLE: the tile lies inside the matrix, on 16-byte (values) and 8-byte
+// (results) boundaries, so that nothing is asked of its elements.
+template <typename T, bool E5M2, int FORMS, bool WHOLE>
+__device__ __forceinline__ void quantize_tile(const QuantArgs& p, float (*part)[kFp8Block], float* warp_max) {
     const int lane16 = threadIdx.x & 15, r16 = threadIdx.x >> 4;
     const int64_t c0 = int64_t(blockIdx.x) * kFp8Block, c = c0 + lane16 * 8;
     const int64_t r0 = int64_t(blockIdx.y) * kFp8Block;
-    float v[kRowsPer][8];
-    const T* x = static_cast<const T*>(p.x);
+    Eight<T> v[kRowsPer];
+    const T* x = static_cast<const T*>(p.x) + (r0 + r16) * p.ldx + c;
 #pragma unroll
     for (int k = 0; k < kRowsPer; ++k) {
-        const int64_t r = r0 + r16 + 16 * k;
-        if (r < p.rows && p.vec_in && c + 8 <= p.cols) {
-            constexpr int N = 16 / sizeof(T);
-            const Vec<T, N>* src = reinterpret_cast<const Vec<T, N>*>(x + r * p.ldx + c);
+        const T* src = x + int64_t(16 * k) * p.ldx;
+        if constexpr (WHOLE) {
 #pragma unroll
-            for (int q = 0; q < 8 / N; ++q) {
-                const Vec<T, N> u = src[q];
-#pragma unroll
-                for (int i = 0; i < N; ++i) v[k][q * N + i] = to_f32(u.v[i]);
-            }
+            for (int q = 0; q < Eight<T>::kVecs; ++q)
+                v[k].u[q] = reinterpret_cast<const Vec<T, Eight<T>::N>*>(src)[q];
         } else {
+            const bool in = r0 + r16 + 16 * k < p.rows;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[k][i] = r < p.rows && c + i < p.cols ? to_f32(x[r * p.ldx + c + i]) : 0.0f;
+            for (int i = 0; i < 8; ++i) v[k].u[i / Eight<T>::N].v[i % Eight<T>::N] = in && c + i < p.cols ? src[i] : from_f32<T>(0.0f);
         }
     }
-    // rows: the 16 threads of a row are half a warp
-    float all = 0;
-#pragma unroll
-    for (int k = 0; k < kRowsPer; ++k) {
-        float m = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m = max_nan(m, fabsf(v[k][i]));
-        all = max_nan(all, m);
-        if (!p.row.q) continue;
-#pragma unroll
-        for (int s = 8; s; s >>= 1) m = max_nan(m, __shfl_xor_sync(~0u, m, s));
+    // write a row's eight, each times the power of two for its column
+    auto store = [&](const Fp8QuantDesc::Form& f, int k, const float (&by)[8]) {
         const int64_t r = r0 + r16 + 16 * k;
-        const uint32_t byte = scale_byte(m, p.emax);
-        const float f = unscale(byte);
-        if (r < p.rows) {
-            store8(p.row, r, c, p.cols, quant4<E5M2>(v[k][0] * f, v[k][1] * f, v[k][2] * f, v[k][3] * f),
-                   quant4<E5M2>(v[k][4] * f, v[k][5] * f, v[k][6] * f, v[k][7] * f));
-            if (lane16 == 0) p.row.scale[r * p.row.lds + blockIdx.x] = uint8_t(byte);
-        }
-    }
-    if (p.tile.q) {
-        all = max_nan(all, __shfl_xor_sync(~0u, all, 16));
+        const uint32_t lo = quant4<E5M2>(v[k].at(0) * by[0], v[k].at(1) * by[1], v[k].at(2) * by[2], v[k].at(3) * by[3]);
+        const uint32_t hi = quant4<E5M2>(v[k].at(4) * by[4], v[k].at(5) * by[5], v[k].at(6) * by[6], v[k].at(7) * by[7]);
+        uint8_t* dst = f.q + r * f.ldq + c;
+        if constexpr (WHOLE) {
+            *reinterpret_cast<uint2*>(dst) = make_uint2(lo, hi);
+        } else if (r < p.rows) {
 #pragma unroll
-        for (int s = 8; s; s >>= 1) all = max_nan(all, __shfl_xor_sync(~0u, all, s));
+            for (int i = 0; i < 8; ++i)
+                if (c + i < p.cols) dst[i] = uint8_t((i < 4 ? lo >> (8 * i) : hi >> (8 * i - 32)) & 255u);
+        }
+    };
+    auto all8 = [](float f, float (&by)[8]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) by[i] = f;
+    };
+    float m[kRowsPer], by[8];
+    if constexpr ((FORMS & 5) != 0) {
+#pragma unroll
+        for (int k = 0; k < kRowsPer; ++k) m[k] = amax8(v[k]);
+    }
+    if constexpr ((FORMS & 4) != 0) {
+        float all = m[0];
+#pragma unroll
+        for (int k = 1; k < kRowsPer; ++k) all = max_nan(all, m[k]);
+#pragma unroll
+        for (int s = 16; s; s >>= 1) all = max_nan(all, __shfl_xor_sync(~0u, all, s));
         if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = all;
         __syncthreads();
-        float m = 0;
 #pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) m = max_nan(m, warp_max[w]);
-        const uint32_t byte = scale_byte(m, p.emax);
-        const float f = unscale(byte);
+        for (int w = 0; w < kThreads / 32; ++w) all = max_nan(all, warp_max[w]);
+        const uint32_t byte = scale_byte(all, p.emax);
+        all8(unscale(byte), by);
+#pragma unroll
+        for (int k = 0; k < kRowsPer; ++k) store(p.tile, k, by);
+        if (threadIdx.x == 0) p.tile.scale[int64_t(blockIdx.y) * gridDim.x + blockIdx.x] = uint8_t(byte);
+    }
+    if constexpr ((FORMS & 1) != 0) {  // the 16 threads of a row are half a warp
+#pragma unroll
+        for (int s = 8; s; s >>= 1)
+#pragma unroll
+            for (int k = 0; k < kRowsPer; ++k) m[k] = max_nan(m[k], __shfl_xor_sync(~0u, m[k], s));
 #pragma unroll
         for (int k = 0; k < kRowsPer; ++k) {
             const int64_t r = r0 + r16 + 16 * k;
-            if (r < p.rows)
-                store8(p.tile, r, c, p.cols, quant4<E5M2>(v[k][0] * f, v[k][1] * f, v[k][2] * f, v[k][3] * f),
-                       quant4<E5M2>(v[k][4] * f, v[k][5] * f, v[k][6] * f, v[k][7] * f));
+            const uint32_t byte = scale_byte(m[k], p.emax);
+            all8(unscale(byte), by);
+            store(p.row, k, by);
+            if (lane16 == 0 && (WHOLE || r < p.rows)) store_scale(p.row.scale, blockIdx.x, gridDim.x, r, p.rows, byte);
         }
-        if (threadIdx.x == 0) p.tile.scale[int64_t(blockIdx.y) * p.tile.lds + blockIdx.x] = uint8_t(byte);
     }
-    if (p.col.q) {
+    if constexpr ((FORMS & 2) != 0) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            float m = 0;
+            float mc = fabsf(v[0].at(i));
 #pragma unroll
-            for (int k = 0; k < kRowsPer; ++k) m = max_nan(m, fabsf(v[k][i]));
-            part[r16][lane16 * 8 + i] = m;
+            for (int k = 1; k < kRowsPer; ++k) mc = max_nan(mc, fabsf(v[k].at(i)));
+            by[i] = max_nan(mc, __shfl_xor_sync(~0u, mc, 16));  // the two rows of a warp
+        }
+        if ((threadIdx.x & 31) < 16) {
+            float4* dst = reinterpret_cast<float4*>(&part[threadIdx.x >> 5][lane16 * 8]);
+            dst[0] = make_float4(by[0], by[1], by[2], by[3]);
+            dst[1] = make_float4(by[4], by[5], by[6], by[7]);
         }
         __syncthreads();
         if (threadIdx.x < kFp8Block) {
-            float m = 0;
+            float mc = 0;
 #pragma unroll
-            for (int w = 0; w < 16; ++w) m = max_nan(m, part[w][threadIdx.x]);
-            const uint32_t byte = scale_byte(m, p.emax);
+            for (int w = 0; w < kThreads / 32; ++w) mc = max_nan(mc, part[w][threadIdx.x]);
+            const uint32_t byte = scale_byte(mc, p.emax);
             part[0][threadIdx.x] = unscale(byte);
-            if (c0 + threadIdx.x < p.cols) p.col.scale[int64_t(blockIdx.y) * p.col.lds + c0 + threadIdx.x] = uint8_t(byte);
+            if (c0 + threadIdx.x < p.cols) store_scale(p.col.scale, blockIdx.y, gridDim.y, c0 + threadIdx.x, p.cols, byte);
         }
         __syncthreads();
-        float f[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = part[0][lane16 * 8 + i];
+        for (int i = 0; i < 8; ++i) by[i] = part[0][lane16 * 8 + i];
 #pragma unroll
-        for (int k = 0; k < kRowsPer; ++k) {
-            const int64_t r = r0 + r16 + 16 * k;
-            if (r < p.rows)
-                store8(p.col, r, c, p.cols, quant4<E5M2>(v[k][0] * f[0], v[k][1] * f[1], v[k][2] * f[2], v[k][3] * f[3]),
-                       quant4<E5M2>(v[k][4] * f[4], v[k][5] * f[5], v[k][6] * f[6], v[k][7] * f[7]));
-        }
+        for (int k = 0; k < kRowsPer; ++k) store(p.col, k, by);
     }
 }
 
-template <typename T>
-void launch(const QuantArgs& a, bool e5m2, dim3 grid, cudaStream_t stream) {
-    if (e5m2) fp8_quantize_kernel<T, true><<<grid, kThreads, 0, stream>>>(a);
-    else fp8_quantize_kernel<T, false><<<grid, kThreads, 0, stream>>>(a);
+template <typename T, bool E5M2, int FORMS>
+__global__ void __launch_bounds__(kThreads) fp8_quantize_kernel(const QuantArgs p) {
+    __shared__ __align__(16) float part[kThreads / 32][kFp8Block];  // column maxima, by warp
+    __shared__ float warp_max[kThreads / 32];
+    const bool whole = p.vec && int64_t(blockIdx.x + 1) * kFp8Block <= p.cols && int64_t(blockIdx.y + 1) * kFp8Block <= p.rows;
+    if (whole) quantize_tile<T, E5M2, FORMS, true>(p, part, warp_max);
+    else quantize_tile<T, E5M2, FORMS, false>(p, part, warp_max);
+}
+
+template <typename T, bool E5M2>
+void launch(const QuantArgs& a, int forms, dim3 grid, cudaStream_t stream) {
+    switch (forms) {
+        case 1: fp8_quantize_kernel<T, E5M2, 1><<<grid, kThreads, 0, stream>>>(a); break;
+        case 2: fp8_quantize_kernel<T, E5M2, 2><<<grid, kThreads, 0, stream>>>(a); break;
+        case 3: fp8_quantize_kernel<T, E5M2, 3><<<grid, kThreads, 0, stream>>>(a); break;
+        case 4: fp8_quantize_kernel<T, E5M2, 4><<<grid, kThreads, 0, stream>>>(a); break;
+        case 5: fp8_quantize_kernel<T, E5M2, 5><<<grid, kThreads, 0, stream>>>(a); break;
+        case 6: fp8_quantize_kernel<T, E5M2, 6><<<grid, kThreads, 0, stream>>>(a); break;
+        default: fp8_quantize_kernel<T, E5M2, 7><<<grid, kThreads, 0, stream>>>(a); break;
+    }
 }
 
 }  // namespace
@@ -188,11 +235,10 @@ std::string fp8_quantize_check(const Fp8QuantDesc& d) {
     if (!d.row.q && !d.col.q && !d.tile.q) return "no form is wanted";
     if (!d.x || reinterpret_cast<uintptr_t>(d.x) % type_bytes(d.type)) return "x is null or not aligned to its type";
     if (d.ldx < d.cols) return "the leading dimension of x is smaller than cols";
-    const int64_t cb = (d.cols + kFp8Block - 1) / kFp8Block;
     for (const auto& f : {d.row, d.col, d.tile})
         if (f.q && (!f.scale || f.ldq < d.cols)) return "a form has no scales, or a leading dimension smaller than cols";
-    if ((d.row.q && d.row.lds < cb) || (d.col.q && d.col.lds < d.cols) || (d.tile.q && d.tile.lds < cb))
-        return "a leading dimension of scales is too small";
+    for (const auto& f : {d.row, d.col})
+        if (f.q && (reinterpret_cast<uintptr_t>(f.scale) & 3)) return "scales of the row and col forms must be 4-byte aligned";
     return {};
 }
 
@@ -209,11 +255,24 @@ cudaError_t fp8_quantize_launch(const Fp8QuantDesc& d, cudaStream_t stream) {
     const bool e5m2 = d.format == TL_FP8_E5M2;
     a.emax = e5m2 ? 15 : 8;
     const int64_t vec = int64_t(16 / type_bytes(d.type));
-    a.vec_in = (reinterpret_cast<uintptr_t>(d.x) & 15) == 0 && d.ldx % vec == 0;
+    a.vec = (reinterpret_cast<uintptr_t>(d.x) & 15) == 0 && d.ldx % vec == 0;
+    int forms = 0, bit = 1;
+    for (const auto* f : {&d.row, &d.col, &d.tile}) {
+        if (f->q) {
+            forms |= bit;
+            a.vec = a.vec && (reinterpret_cast<uintptr_t>(f->q) & 7) == 0 && f->ldq % 8 == 0;
+        }
+        bit *= 2;
+    }
     const dim3 grid(unsigned((d.cols + kFp8Block - 1) / kFp8Block), unsigned((d.rows + kFp8Block - 1) / kFp8Block));
-    if (d.type == TL_TYPE_BF16) launch<__nv_bfloat16>(a, e5m2, grid, stream);
-    else if (d.type == TL_TYPE_F16) launch<__half>(a, e5m2, grid, stream);
-    else launch<float>(a, e5m2, grid, stream);
+    auto run = [&](auto zero) {
+        using T = decltype(zero);
+        if (e5m2) launch<T, true>(a, forms, grid, stream);
+        else launch<T, false>(a, forms, grid, stream);
+    };
+    if (d.type == TL_TYPE_BF16) run(__nv_bfloat16{});
+    else if (d.type == TL_TYPE_F16) run(__half{});
+    else run(float{});
     return cudaGetLastError();
 }
 

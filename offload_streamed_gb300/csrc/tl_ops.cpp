@@ -109,9 +109,9 @@ tl_status tiled_linear_norm_backward(int64_t rows, int64_t cols, int32_t type, c
 }
 
 tl_status tiled_linear_fp8_quantize(int64_t rows, int64_t cols, int32_t type, const void* x_dev, int64_t ldx,
-                                    int32_t format, void* row_q, int64_t ld_row, void* row_scale, int64_t ld_row_scale,
-                                    void* col_q, int64_t ld_col, void* col_scale, int64_t ld_col_scale, void* tile_q,
-                                    int64_t ld_tile, void* tile_scale, int64_t ld_tile_scale, void* stream) {
+                                    int32_t format, void* row_q, int64_t ld_row, void* row_scale, void* col_q,
+                                    int64_t ld_col, void* col_scale, void* tile_q, int64_t ld_tile, void* tile_scale,
+                                    void* stream) {
     return guarded([&]() -> tl_status {
         Fp8QuantDesc d;
         d.rows = rows;
@@ -120,9 +120,9 @@ tl_status tiled_linear_fp8_quantize(int64_t rows, int64_t cols, int32_t type, co
         d.x = x_dev;
         d.ldx = ldx;
         d.format = format;
-        d.row = {static_cast<uint8_t*>(row_q), ld_row, static_cast<uint8_t*>(row_scale), ld_row_scale};
-        d.col = {static_cast<uint8_t*>(col_q), ld_col, static_cast<uint8_t*>(col_scale), ld_col_scale};
-        d.tile = {static_cast<uint8_t*>(tile_q), ld_tile, static_cast<uint8_t*>(tile_scale), ld_tile_scale};
+        d.row = {static_cast<uint8_t*>(row_q), ld_row, static_cast<uint8_t*>(row_scale)};
+        d.col = {static_cast<uint8_t*>(col_q), ld_col, static_cast<uint8_t*>(col_scale)};
+        d.tile = {static_cast<uint8_t*>(tile_q), ld_tile, static_cast<uint8_t*>(tile_scale)};
         const std::string bad = fp8_quantize_check(d);
         if (!bad.empty()) return refuse(TL_ERR_INVALID, bad);
         return done(fp8_quantize_launch(d, static_cast<cudaStream_t>(stream)), "fp8 quantise");
@@ -133,24 +133,20 @@ tl_status tiled_linear_fp8_quantize(int64_t rows, int64_t cols, int32_t type, co
 
 namespace {
 
-// An operand whose blocks run along its rows (row form, the row index its
-// own), down its columns (col form, the column index its own), or the tile
-// form with either index its own.
-enum class Own { RowOfRow, ColOfCol, RowOfTile, ColOfTile };
-Fp8Operand operand(Own own, const void* q, int64_t ld, const void* scale, int64_t lds, int32_t format) {
+// An operand and the matrix that holds it: its own index runs down the rows or
+// along the columns, and its scales are of the vectors along the reduction
+// (row and col forms) or of tiles.
+Fp8Operand operand(bool own_is_row, bool tiles, int64_t cols, const void* q, int64_t ld, const void* scale, int32_t format) {
     Fp8Operand o;
     o.q = q;
     o.ld = ld;
+    o.mn_major = !own_is_row;
     o.format = format;
-    o.scale = static_cast<const uint8_t*>(scale);
-    o.mn_major = own == Own::ColOfCol || own == Own::ColOfTile;
-    o.i_step = o.mn_major ? 1 : lds;
-    o.k_step = o.mn_major ? lds : 1;
-    o.i_shift = own == Own::RowOfTile || own == Own::ColOfTile ? 7 : 0;
+    o.scale = scale;
+    o.tiles = tiles;
+    o.tile_cols = (cols + kFp8Block - 1) / kFp8Block;
     return o;
 }
-
-int64_t blocks(int64_t n) { return (n + kFp8Block - 1) / kFp8Block; }
 
 tl_status fp8_product(int64_t m, int64_t n, int64_t k, const Fp8Operand& a, const Fp8Operand& b, void* d, int64_t ldd,
                       int32_t* err, void* stream) {
@@ -177,48 +173,39 @@ tl_status fp8_product(int64_t m, int64_t n, int64_t k, const Fp8Operand& a, cons
 extern "C" {
 
 tl_status tiled_linear_fp8_gemm_forward(int64_t T, int64_t K, int64_t n, int32_t x_format, const void* x_q, int64_t ldx,
-                                        const void* x_scale, int64_t ld_x_scale, int32_t w_format, const void* w_q,
-                                        int64_t ldw, const void* w_scale, int64_t ld_w_scale, void* y_dev, int64_t ldy,
-                                        int32_t* err_dev, void* stream) {
+                                        const void* x_scale, int32_t w_format, const void* w_q, int64_t ldw,
+                                        const void* w_scale, void* y_dev, int64_t ldy, int32_t* err_dev, void* stream) {
     return guarded([&]() -> tl_status {
         if (T < 0 || K < 1 || n < 1) return refuse(TL_ERR_INVALID, "T must be >= 0, K and n >= 1");
-        if (ld_x_scale < blocks(K) || ld_w_scale < blocks(n))
-            return refuse(TL_ERR_INVALID, "a leading dimension of scales is too small");
         if (T == 0) return TL_OK;
-        return fp8_product(T, n, K, operand(Own::RowOfRow, x_q, ldx, x_scale, ld_x_scale, x_format),
-                           operand(Own::ColOfTile, w_q, ldw, w_scale, ld_w_scale, w_format), y_dev, ldy, err_dev, stream);
+        return fp8_product(T, n, K, operand(true, false, K, x_q, ldx, x_scale, x_format),
+                           operand(false, true, n, w_q, ldw, w_scale, w_format), y_dev, ldy, err_dev, stream);
     });
 }
 
 tl_status tiled_linear_fp8_gemm_dx(int64_t T, int64_t K, int64_t n, int32_t dy_format, const void* dy_q, int64_t lddy,
-                                   const void* dy_scale, int64_t ld_dy_scale, int32_t w_format, const void* w_q,
-                                   int64_t ldw, const void* w_scale, int64_t ld_w_scale, void* dx_dev, int64_t lddx,
-                                   int32_t* err_dev, void* stream) {
+                                   const void* dy_scale, int32_t w_format, const void* w_q, int64_t ldw,
+                                   const void* w_scale, void* dx_dev, int64_t lddx, int32_t* err_dev, void* stream) {
     return guarded([&]() -> tl_status {
         if (T < 0 || K < 1 || n < 1) return refuse(TL_ERR_INVALID, "T must be >= 0, K and n >= 1");
-        if (ld_dy_scale < blocks(n) || ld_w_scale < blocks(n))
-            return refuse(TL_ERR_INVALID, "a leading dimension of scales is too small");
         if (T == 0) return TL_OK;
-        return fp8_product(T, K, n, operand(Own::RowOfRow, dy_q, lddy, dy_scale, ld_dy_scale, dy_format),
-                           operand(Own::RowOfTile, w_q, ldw, w_scale, ld_w_scale, w_format), dx_dev, lddx, err_dev, stream);
+        return fp8_product(T, K, n, operand(true, false, n, dy_q, lddy, dy_scale, dy_format),
+                           operand(true, true, n, w_q, ldw, w_scale, w_format), dx_dev, lddx, err_dev, stream);
     });
 }
 
 tl_status tiled_linear_fp8_gemm_dw(int64_t T, int64_t K, int64_t n, int32_t x_format, const void* x_q, int64_t ldx,
-                                   const void* x_scale, int64_t ld_x_scale, int32_t dy_format, const void* dy_q,
-                                   int64_t lddy, const void* dy_scale, int64_t ld_dy_scale, void* dw_dev, int64_t lddw,
-                                   int32_t* err_dev, void* stream) {
+                                   const void* x_scale, int32_t dy_format, const void* dy_q, int64_t lddy,
+                                   const void* dy_scale, void* dw_dev, int64_t lddw, int32_t* err_dev, void* stream) {
     return guarded([&]() -> tl_status {
         if (T < 0 || K < 1 || n < 1) return refuse(TL_ERR_INVALID, "T must be >= 0, K and n >= 1");
-        if (ld_x_scale < K || ld_dy_scale < n)
-            return refuse(TL_ERR_INVALID, "a leading dimension of scales is too small");
         if (T == 0) {
             if (!dw_dev || lddw < n) return refuse(TL_ERR_INVALID, "dw is null or its leading dimension smaller than n");
             return done(cudaMemset2DAsync(dw_dev, size_t(lddw) * 2, 0, size_t(n) * 2, size_t(K),
                                           static_cast<cudaStream_t>(stream)), "fp8 dw");
         }
-        return fp8_product(K, n, T, operand(Own::ColOfCol, x_q, ldx, x_scale, ld_x_scale, x_format),
-                           operand(Own::ColOfCol, dy_q, lddy, dy_scale, ld_dy_scale, dy_format), dw_dev, lddw, err_dev,
+        return fp8_product(K, n, T, operand(false, false, K, x_q, ldx, x_scale, x_format),
+                           operand(false, false, n, dy_q, lddy, dy_scale, dy_format), dw_dev, lddw, err_dev,
                            stream);
     });
 }

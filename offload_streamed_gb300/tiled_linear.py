@@ -172,10 +172,10 @@ def load():
         L.tiled_linear_norm_backward.argtypes = [i64, i64, i32, vp, i64, vp, i64, vp, vp, i32, vp, vp, i64, vp, vp,
                                                  vp, sz, vp, vp]
         L.tiled_linear_norm_backward.restype = st
-        L.tiled_linear_fp8_quantize.argtypes = [i64, i64, i32, vp, i64, i32] + [vp, i64, vp, i64] * 3 + [vp]
+        L.tiled_linear_fp8_quantize.argtypes = [i64, i64, i32, vp, i64, i32] + [vp, i64, vp] * 3 + [vp]
         L.tiled_linear_fp8_quantize.restype = st
         for name in ("tiled_linear_fp8_gemm_forward", "tiled_linear_fp8_gemm_dx", "tiled_linear_fp8_gemm_dw"):
-            getattr(L, name).argtypes = [i64, i64, i64] + [i32, vp, i64, vp, i64] * 2 + [vp, i64, vp, vp]
+            getattr(L, name).argtypes = [i64, i64, i64] + [i32, vp, i64, vp] * 2 + [vp, i64, vp, vp]
             getattr(L, name).restype = st
         L.tiled_linear_host_alloc.argtypes = [sz, ctypes.POINTER(vp)]
         L.tiled_linear_host_alloc.restype = st
@@ -419,30 +419,29 @@ def tiled_linear_norm_backward(rows, cols, type, dy, lddy, x, ldx, mean, rstd, p
            "tiled_linear_norm_backward")
 
 
-def tiled_linear_fp8_quantize(rows, cols, type, x, ldx, format, row_q, ld_row, row_scale, ld_row_scale, col_q, ld_col,
-                              col_scale, ld_col_scale, tile_q, ld_tile, tile_scale, ld_tile_scale, stream) -> None:
-    _check(load().tiled_linear_fp8_quantize(rows, cols, type, x, ldx, format, row_q, ld_row, row_scale, ld_row_scale,
-                                            col_q, ld_col, col_scale, ld_col_scale, tile_q, ld_tile, tile_scale,
-                                            ld_tile_scale, stream), "tiled_linear_fp8_quantize")
+def tiled_linear_fp8_quantize(rows, cols, type, x, ldx, format, row_q, ld_row, row_scale, col_q, ld_col, col_scale,
+                              tile_q, ld_tile, tile_scale, stream) -> None:
+    _check(load().tiled_linear_fp8_quantize(rows, cols, type, x, ldx, format, row_q, ld_row, row_scale, col_q, ld_col,
+                                            col_scale, tile_q, ld_tile, tile_scale, stream),
+           "tiled_linear_fp8_quantize")
 
 
-def tiled_linear_fp8_gemm_forward(T, K, n, x_format, x_q, ldx, x_scale, ld_x_scale, w_format, w_q, ldw, w_scale,
-                                  ld_w_scale, y, ldy, err, stream) -> None:
-    _check(load().tiled_linear_fp8_gemm_forward(T, K, n, x_format, x_q, ldx, x_scale, ld_x_scale, w_format, w_q, ldw,
-                                                w_scale, ld_w_scale, y, ldy, err, stream),
-           "tiled_linear_fp8_gemm_forward")
+def tiled_linear_fp8_gemm_forward(T, K, n, x_format, x_q, ldx, x_scale, w_format, w_q, ldw, w_scale, y, ldy, err,
+                                  stream) -> None:
+    _check(load().tiled_linear_fp8_gemm_forward(T, K, n, x_format, x_q, ldx, x_scale, w_format, w_q, ldw, w_scale, y,
+                                                ldy, err, stream), "tiled_linear_fp8_gemm_forward")
 
 
-def tiled_linear_fp8_gemm_dx(T, K, n, dy_format, dy_q, lddy, dy_scale, ld_dy_scale, w_format, w_q, ldw, w_scale,
-                             ld_w_scale, dx, lddx, err, stream) -> None:
-    _check(load().tiled_linear_fp8_gemm_dx(T, K, n, dy_format, dy_q, lddy, dy_scale, ld_dy_scale, w_format, w_q, ldw,
-                                           w_scale, ld_w_scale, dx, lddx, err, stream), "tiled_linear_fp8_gemm_dx")
+def tiled_linear_fp8_gemm_dx(T, K, n, dy_format, dy_q, lddy, dy_scale, w_format, w_q, ldw, w_scale, dx, lddx, err,
+                             stream) -> None:
+    _check(load().tiled_linear_fp8_gemm_dx(T, K, n, dy_format, dy_q, lddy, dy_scale, w_format, w_q, ldw, w_scale, dx,
+                                           lddx, err, stream), "tiled_linear_fp8_gemm_dx")
 
 
-def tiled_linear_fp8_gemm_dw(T, K, n, x_format, x_q, ldx, x_scale, ld_x_scale, dy_format, dy_q, lddy, dy_scale,
-                             ld_dy_scale, dw, lddw, err, stream) -> None:
-    _check(load().tiled_linear_fp8_gemm_dw(T, K, n, x_format, x_q, ldx, x_scale, ld_x_scale, dy_format, dy_q, lddy,
-                                           dy_scale, ld_dy_scale, dw, lddw, err, stream), "tiled_linear_fp8_gemm_dw")
+def tiled_linear_fp8_gemm_dw(T, K, n, x_format, x_q, ldx, x_scale, dy_format, dy_q, lddy, dy_scale, dw, lddw, err,
+                             stream) -> None:
+    _check(load().tiled_linear_fp8_gemm_dw(T, K, n, x_format, x_q, ldx, x_scale, dy_format, dy_q, lddy, dy_scale, dw,
+                                           lddw, err, stream), "tiled_linear_fp8_gemm_dw")
 
 
 def tiled_linear_host_alloc(nbytes: int) -> int:
@@ -918,15 +917,14 @@ def _fp8_format(t, where: str, name: str) -> int:
     _refuse(where, f"{name} has dtype {t.dtype}: float8_e4m3fn or float8_e5m2 is wanted")
 
 
-def _fp8_forms(rows: int, cols: int, form: str):
-    """(shape of the scales, their leading dimension) of a form."""
-    rb, cb = -(-rows // FP8_BLOCK), -(-cols // FP8_BLOCK)
+def _fp8_scales(rows: int, cols: int, form: str) -> tuple:
+    """Shape of a form's scales."""
     if form == "row":
-        return (rows, cb), _up(cb, 4)
+        return -(-cols // (4 * FP8_BLOCK)), rows, 4
     if form == "col":
-        return (rb, cols), cols
+        return -(-rows // (4 * FP8_BLOCK)), cols, 4
     if form == "tile":
-        return (rb, cb), cb
+        return -(-rows // FP8_BLOCK), -(-cols // FP8_BLOCK)
     _refuse("fp8_quantize", f"form {form!r}: 'row', 'col' or 'tile' is wanted")
 
 
@@ -937,7 +935,9 @@ def fp8_quantize(x, *forms: str, format: str = "e4m3"):
     forms: "row" (a scale for 128 columns of a row), "col" (128 rows of a column),
     "tile" (128 x 128).  q: float8_e4m3fn or (format="e5m2") float8_e5m2
     [rows, cols], rows on 16-byte boundaries; scale: uint8, q stands for
-    q * 2^(scale - 127)."""
+    q * 2^(scale - 127).  A tile's scale is scale[row // 128, col // 128]; the row
+    form's is scale[col // 512, row, col // 128 % 4] and the col form's
+    scale[row // 512, col, row // 128 % 4], as the products take them."""
     torch, where = _t(), "fp8_quantize"
     ldx, (rows, cols), device = _ld(x, where, "x"), x.shape, x.device
     kind, stream = _type_of(x, where), _stream_of(device, where)
@@ -948,28 +948,26 @@ def fp8_quantize(x, *forms: str, format: str = "e4m3"):
     dtype = torch.float8_e4m3fn if format == "e4m3" else torch.float8_e5m2
     ldq, out, args = _up(cols, 16), [], {}
     for form in forms:
-        shape, lds = _fp8_forms(rows, cols, form)
+        scale = x.new_empty(_fp8_scales(rows, cols, form), dtype=torch.uint8)
         q = x.new_empty((rows, ldq), dtype=dtype)
-        scale = x.new_empty((shape[0], lds), dtype=torch.uint8)
-        args[form] = (q.data_ptr(), ldq, scale.data_ptr(), lds)
-        out.append((q if ldq == cols else q[:, :cols], scale if lds == shape[1] else scale[:, :shape[1]]))
-    none = (None, 0, None, 0)
+        args[form] = (q.data_ptr(), ldq, scale.data_ptr())
+        out.append((q if ldq == cols else q[:, :cols], scale))
+    none = (None, 0, None)
     tiled_linear_fp8_quantize(rows, cols, kind, x.data_ptr(), ldx, 0 if format == "e4m3" else 1,
                               *args.get("row", none), *args.get("col", none), *args.get("tile", none), stream)
     return out[0] if len(forms) == 1 else tuple(out)
 
 
 def _fp8_operand(q, scale, form: str, where: str, name: str):
-    """(format, pointer, ld, scale pointer, ld of scales) of a matrix in 8 bits."""
+    """(format, pointer, ld, scale pointer) of a matrix in 8 bits."""
     fmt, ld = _fp8_format(q, where, name), _ld(q, where, name)
     rows, cols = q.shape
-    shape, _ = _fp8_forms(rows, cols, form)
-    if scale.dtype != _torch.uint8 or tuple(scale.shape) != shape or scale.device != q.device:
-        _refuse(where, f"the scales of {name} must be uint8 {list(shape)} on its device")
-    lds = _ld(scale, where, f"the scales of {name}")
+    shape = _fp8_scales(rows, cols, form)
+    if scale.dtype != _torch.uint8 or scale.shape != shape or scale.device != q.device or not scale.is_contiguous():
+        _refuse(where, f"the scales of {name} must be contiguous uint8 {list(shape)} on its device")
     if rows == 1:
         ld = _up(cols, 16)  # one row: there is no second for it to lead to
-    return fmt, q.data_ptr(), ld, scale.data_ptr(), lds
+    return fmt, q.data_ptr(), ld, scale.data_ptr()
 
 
 def _fp8_result(x, rows: int, cols: int):

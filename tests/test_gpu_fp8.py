@@ -56,10 +56,29 @@ def reference(x: np.ndarray, form: str, fmt: str):
     return out, scale
 
 
+def plain_scales(scale, rows, cols, form):
+    """The bytes as [rows, cols / 128], [rows / 128, cols] or [rows / 128, cols / 128]; those past
+    the last block of a word have to be 127."""
+    s = scale.cpu().numpy()
+    if form == "tile":
+        return s
+    s = s.transpose(1, 0, 2).reshape(s.shape[1], -1)  # [vector, block]
+    have = -(-(cols if form == "row" else rows) // 128)
+    assert (s[:, have:] == 127).all()
+    return s[:, :have] if form == "row" else s[:, :have].T
+
+
+def packed(s, form):
+    """The inverse, as a device tensor."""
+    v = s.numpy() if form == "row" else s.numpy().T
+    v = np.pad(v, ((0, 0), (0, -v.shape[1] % 4)), constant_values=127)
+    return torch.from_numpy(np.ascontiguousarray(v.reshape(v.shape[0], -1, 4).transpose(1, 0, 2))).cuda()
+
+
 def values(q, scale, form):
     br, bc = BLOCKS[form]
     rows, cols = q.shape
-    e = scale.cpu().numpy().astype(np.int64)
+    e = plain_scales(scale, rows, cols, form).astype(np.int64)
     s = np.where(e == 255, np.nan, 2.0 ** (e - 127.0))
     s = np.repeat(np.repeat(s, br, 0)[:rows], bc, 1)[:, :cols]
     return q.cpu().float().numpy().astype(np.float64) * s
@@ -80,7 +99,7 @@ def test_forms_are_exact(tl, rows, cols, dtype, fmt):
     got = tl.fp8_quantize(x.cuda(), "tile", "row", "col", format=fmt)
     for (q, s), form in zip(got, ("tile", "row", "col")):
         ref, sref = reference(x.double().numpy(), form, fmt)
-        assert np.array_equal(s.cpu().numpy(), sref), form
+        assert np.array_equal(plain_scales(s, rows, cols, form), sref), form
         assert np.array_equal(values(q, s, form), ref, equal_nan=True), form
         one, sone = tl.fp8_quantize(x.cuda(), form, format=fmt)  # a form alone is the same
         assert torch.equal(sone, s) and torch.equal(one.view(torch.uint8), q.view(torch.uint8))
@@ -102,7 +121,7 @@ def test_forms_at_the_edges(tl):
         y = x if form == "row" else x.T.contiguous()
         q, s = tl.fp8_quantize(y.cuda(), form)
         ref, sref = reference(y.numpy(), form, "e4m3")
-        assert np.array_equal(s.cpu().numpy(), sref)
+        assert np.array_equal(plain_scales(s, *y.shape, form), sref)
         assert np.array_equal(values(q, s, form), ref, equal_nan=True)
 
 
@@ -114,7 +133,7 @@ def test_forms_of_strided_rows(tl, ld, off):
     xd.copy_(x)
     q, s = tl.fp8_quantize(xd, "row")
     ref, sref = reference(x.double().numpy(), "row", "e4m3")
-    assert np.array_equal(s.cpu().numpy(), sref) and np.array_equal(values(q, s, "row"), ref)
+    assert np.array_equal(plain_scales(s, 70, 200, "row"), sref) and np.array_equal(values(q, s, "row"), ref)
 
 
 def compare(name, got, a, b, K):
@@ -167,17 +186,17 @@ def test_every_scale_is_applied(tl, T):
     xs = torch.randint(120, 132, (T, K // 128), generator=g, dtype=torch.uint8)
     ws = torch.randint(122, 130, (K // 128, n // 128), generator=g, dtype=torch.uint8)
     one = lambda r, c: torch.ones(r, c).to(torch.float8_e4m3fn).cuda()  # noqa: E731
-    y = tl.fp8_matmul((one(T, K), xs.cuda()), (one(K, n), ws.cuda()))
+    y = tl.fp8_matmul((one(T, K), packed(xs, "row")), (one(K, n), ws.cuda()))
     ref = (2.0 ** (xs.double() - 127)) @ (2.0 ** (ws.double() - 127)) * 128
     assert torch.equal(y.cpu(), ref.repeat_interleave(128, 1).bfloat16())
     gs = torch.randint(120, 132, (T, n // 128), generator=g, dtype=torch.uint8)
-    dx = tl.fp8_matmul_dx((one(T, n), gs.cuda()), (one(K, n), ws.cuda()))
+    dx = tl.fp8_matmul_dx((one(T, n), packed(gs, "row")), (one(K, n), ws.cuda()))
     ref = (2.0 ** (gs.double() - 127)) @ (2.0 ** (ws.double().T - 127)) * 128
     assert torch.equal(dx.cpu(), ref.repeat_interleave(128, 1).bfloat16())
     tb = -(-T // 128)
     xc = torch.randint(120, 132, (tb, K), generator=g, dtype=torch.uint8)
     gc = torch.randint(122, 130, (tb, n), generator=g, dtype=torch.uint8)
-    dw = tl.fp8_matmul_dw((one(T, K), xc.cuda()), (one(T, n), gc.cuda()))
+    dw = tl.fp8_matmul_dw((one(T, K), packed(xc, "col")), (one(T, n), packed(gc, "col")))
     count = torch.tensor([min(128, T - 128 * i) for i in range(tb)], dtype=torch.float64)
     ref = (2.0 ** (xc.double().T - 127) * count) @ (2.0 ** (gc.double() - 127))
     assert torch.equal(dw.cpu(), ref.bfloat16())
