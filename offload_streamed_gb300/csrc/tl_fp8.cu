@@ -18,7 +18,7 @@
 //               row) into the layout that the copy to tensor memory takes
 //   warps 4..7  epilogue: fp32 accumulator -> bf16 -> TMA store
 // Two 256-column accumulators and the scales need more than the 512 columns of
-// tensor memory, so the accumulators share 24: the epilogue reads those first,
+// tensor memory, so the accumulators share 36: the epilogue reads those first,
 // and the next tile's MMAs wait for no more than that.
 //
 // Every wait is bounded; see tl_gemm.cu, whose error protocol this shares.
@@ -42,11 +42,12 @@ constexpr int kFp8BlockK = 128;     // one K-block: one scale block, one 128-byt
 constexpr int kChunkBlocks = 4;     // K-blocks whose scales share a 32-bit word
 constexpr int kStagesPair = 5;
 constexpr uint32_t kStageHalf = 128 * 128;  // 128 rows (or reduction indices) of 128 bytes
-constexpr int kSfSlots = 4;
-constexpr uint32_t kSfA = 512, kSfB = 1024, kSfSlot = kSfA + kSfB;
-constexpr uint32_t kAcc1 = 232;     // columns: accumulators at 0 and 232, 256 each,
-constexpr uint32_t kSfCols = 488;   // then two sets of 4 + 8 scale columns
-constexpr uint32_t kSfSet = 12;
+constexpr int kBatch = 4;           // chunks whose scales are handed over at once,
+constexpr int kSfSlots = 2;         // and how many batches shared memory holds
+constexpr uint32_t kSfA = 512, kSfB = 1024, kSfChunk = kSfA + kSfB, kSfSlot = kBatch * kSfChunk;
+constexpr uint32_t kAcc1 = 220;     // columns: accumulators at 0 and 220, 256 each,
+constexpr uint32_t kSfCols = 476;   // then three sets of 4 + 8 scale columns
+constexpr uint32_t kSfSet = 12, kSfSets = 3;
 
 // tcgen05.mma, 8-bit operands with one scale byte per 32 reduction elements.
 template <bool PAIR>
@@ -87,6 +88,12 @@ __host__ __device__ constexpr uint32_t idesc_fp8(int m, int n, bool a_mn, bool b
            (uint32_t(n >> 3) << 17) | (1u << 23) | (uint32_t(m >> 4) << 24);
 }
 __device__ __forceinline__ uint32_t with_scale_id(uint32_t idesc, uint32_t id) { return idesc | (id << 4) | (id << 29); }
+
+// wait_bounded_cluster, without its reading of the clock where the phase is
+// over already: that takes longer than four K-blocks' MMAs.
+__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, const WaitCtx& w, int32_t code) {
+    return mbar_try_wait_cluster(bar, parity) || wait_bounded_cluster(bar, parity, w, code);
+}
 
 // Step j (32 reduction elements) of a 128 x 128-byte operand.
 __device__ __forceinline__ uint64_t fp8_desc(bool mn, uint32_t base, int j) {
@@ -162,8 +169,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto tfull_bar = [&](uint32_t a) { return bar0 + 8u * (2 * S + 2 * kSfSlots + a); };
     const uint32_t tread_bar = bar0 + 8u * (2 * S + 2 * kSfSlots + 2);
     const uint32_t drain_bar = bar0 + 8u * (2 * S + 2 * kSfSlots + 3);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 2 * kSfSlots + 4);
-    static_assert((2 * S + 2 * kSfSlots + 4) * 8 + 4 <= int(kBarBytes), "barrier area");
+    auto set_free_bar = [&](uint32_t i) { return bar0 + 8u * (2 * S + 2 * kSfSlots + 4 + i); };  // first CTA's MMA thread alone
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 2 * kSfSlots + 4 + kSfSets);
+    static_assert((2 * S + 2 * kSfSlots + 4 + kSfSets) * 8 + 4 <= int(kBarBytes), "barrier area");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
@@ -183,6 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int a = 0; a < 2; ++a) mbar_init(tfull_bar(a), 1);
         mbar_init(tread_bar, 8);  // the epilogue warps of both CTAs
         mbar_init(drain_bar, 1);
+        for (uint32_t i = 0; i < kSfSets; ++i) mbar_init(set_free_bar(i), 1);
         mbar_init_fence();
     }
     if (warp == 2) {
@@ -234,7 +243,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
         if (lane == 0 && leader) {
             uint32_t fills = 0, chunk = 0;
-            bool ok = true;
+            const int tiles = first_tile < p.num_tiles ? (p.num_tiles - 1 - first_tile) / tile_step + 1 : 0;
+            const uint32_t all_chunks = uint32_t(tiles) * uint32_t(chunks);
+            // The next chunk's scales to their columns, in the middle of the
+            // MMAs of the chunk before it: the copy runs in the tensor pipe's
+            // order, and placed directly before its own MMAs it holds them up.
+            uint32_t copied = 0, batch = 0;
+            int c = 0;  // the chunk's place in its tile
+            auto copy_scales = [&] {
+                if (copied >= all_chunks) return true;
+                const uint32_t set = copied % kSfSets;
+                // the MMAs that last read this set of columns are done
+                if (copied >= kSfSets && !wait_bounded(set_free_bar(set), (copied / kSfSets - 1) & 1u, wc, kErrMmaWaitTmem)) return false;
+                if (c % kBatch == 0 && !wait_cluster(sf_full_bar(batch % kSfSlots), (batch / kSfSlots) & 1u, wc, kErrMmaWaitFull))
+                    return false;
+                tc_fence_after();
+                const uint32_t to = tmem_base + kSfCols + set * kSfSet;
+                const uint32_t src = sf0 + (batch % kSfSlots) * kSfSlot + uint32_t(c % kBatch) * kSfChunk;
+                tmem_copy_scales<true>(to, src);
+                tmem_copy_scales<true>(to + 4, src + kSfA);
+                tmem_copy_scales<true>(to + 8, src + kSfA + 512);
+                ++copied;
+                if (++c == chunks || c % kBatch == 0) {
+                    umma_commit_pair(sf_empty_bar(batch % kSfSlots), 0x3);
+                    ++batch;
+                    if (c == chunks) c = 0;
+                }
+                return true;
+            };
+            bool ok = copy_scales();
             int it = 0;
             for (int tile = first_tile; ok && tile < p.num_tiles; tile += tile_step, ++it) {
                 // the other accumulator's tile has left the shared columns
@@ -243,21 +280,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + (it & 1 ? kAcc1 : 0u);
                 for (int kb = 0; kb < p.num_k; ++kb, ++fills) {
-                    const uint32_t q = chunk % kSfSlots, set = tmem_base + kSfCols + (chunk & 1u) * kSfSet;
+                    const uint32_t set = tmem_base + kSfCols + (chunk % kSfSets) * kSfSet;
                     const uint32_t id = uint32_t(kb) % kChunkBlocks;
-                    if (id == 0) {
-                        // the MMAs that last read this set of columns are done
-                        if (chunk >= 2 && !wait_bounded(sf_empty_bar((chunk - 2) % kSfSlots), ((chunk - 2) / kSfSlots) & 1u,
-                                                        wc, kErrMmaWaitTmem))
-                            ok = false;
-                        if (ok && !wait_bounded_cluster(sf_full_bar(q), (chunk / kSfSlots) & 1u, wc, kErrMmaWaitFull)) ok = false;
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint32_t src = sf0 + q * kSfSlot;
-                        tmem_copy_scales<true>(set, src);
-                        tmem_copy_scales<true>(set + 4, src + kSfA);
-                        tmem_copy_scales<true>(set + 8, src + kSfA + 512);
-                    }
                     const uint32_t s = fills % S;
                     if (!wait_bounded(full_bar(s), (fills / S) & 1u, wc, kErrMmaWaitFull)) {
                         ok = false;
@@ -271,10 +295,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         umma_fp8<true>(d_tmem, fp8_desc(A_MN, sa, j), fp8_desc(B_MN, sb, j), idesc, set, set + 4,
                                        (kb | j) != 0 ? 1u : 0u);
                     umma_commit_pair(empty_bar(s), 0x3);
-                    if (id == kChunkBlocks - 1 || kb == p.num_k - 1) {
-                        umma_commit_pair(sf_empty_bar(q), 0x3);
-                        ++chunk;
+                    const bool last = id == kChunkBlocks - 1 || kb == p.num_k - 1;
+                    if ((id == 1 || (last && id == 0)) && !copy_scales()) {
+                        ok = false;
+                        break;
                     }
+                    if (last) umma_commit_pair(set_free_bar(chunk++ % kSfSets), 0x1);
                 }
                 if (ok) umma_commit_pair(tfull_bar(it & 1), 0x3);
             }
@@ -283,32 +309,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == 3) {
         // ---------------- scales: this CTA's 128 rows of A, all 256 of B ----------------
-        uint32_t chunk = 0;
+        // A batch at a time: the loads of four chunks are in flight together,
+        // and one proxy fence and one arrival hand all of them over.
+        uint32_t batch = 0;
         bool ok = true;
         for (int tile = first_tile; ok && tile < p.num_tiles; tile += tile_step) {
             int mb, nb;
             tile_coords(tile, p.num_m, p.num_n, p.raster, p.group, mb, nb);
             const int m0 = mb * 256 + int(rank) * 128, n0 = nb * 256;
-            uint32_t w[12];
-            auto load = [&](int c) {
-                scale_words<4>(p.a, m0, c, p.num_k, lane, w);
-                scale_words<8>(p.b, n0, c, p.num_k, lane, w + 4);
-            };
-            load(0);
-            for (int c = 0; c < chunks; ++c, ++chunk) {
-                const uint32_t q = chunk % kSfSlots;
-                if (!warp_wait(sf_empty_bar(q), ((chunk / kSfSlots) & 1u) ^ 1u, wc, kErrProducerWait, lane)) {
+            for (int c0 = 0; c0 < chunks; c0 += kBatch, ++batch) {
+                uint32_t w[kBatch][12];
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    if (c0 + i >= chunks) break;
+                    scale_words<4>(p.a, m0, c0 + i, p.num_k, lane, w[i]);
+                    scale_words<8>(p.b, n0, c0 + i, p.num_k, lane, w[i] + 4);
+                }
+                const uint32_t q = batch % kSfSlots;
+                if (!warp_wait(sf_empty_bar(q), ((batch / kSfSlots) & 1u) ^ 1u, wc, kErrProducerWait, lane)) {
                     ok = false;
                     break;
                 }
-                const uint32_t dst = sf0 + q * kSfSlot + uint32_t(lane) * 16;
-                st_shared_v4(dst, w[0], w[1], w[2], w[3]);
-                st_shared_v4(dst + kSfA, w[4], w[5], w[6], w[7]);
-                st_shared_v4(dst + kSfA + 512, w[8], w[9], w[10], w[11]);
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    if (c0 + i >= chunks) break;
+                    const uint32_t dst = sf0 + q * kSfSlot + uint32_t(i) * kSfChunk + uint32_t(lane) * 16;
+                    st_shared_v4(dst, w[i][0], w[i][1], w[i][2], w[i][3]);
+                    st_shared_v4(dst + kSfA, w[i][4], w[i][5], w[i][6], w[i][7]);
+                    st_shared_v4(dst + kSfA + 512, w[i][8], w[i][9], w[i][10], w[i][11]);
+                }
                 fence_proxy_async_shared();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(map_to_rank(sf_full_bar(q), 0));
-                if (c + 1 < chunks) load(c + 1);
             }
         }
     } else if (warp >= kFirstEpilogueWarp) {

@@ -21,6 +21,9 @@
 namespace tl {
 namespace {
 
+#ifndef QB
+#define QB 3
+#endif
 constexpr int kThreads = 256;
 constexpr int kRowsPer = 8;  // rows of a thread, 16 apart
 
@@ -203,7 +206,7 @@ __device__ __forceinline__ void quantize_tile(const QuantArgs& p, float (*part)[
 }
 
 template <typename T, bool E5M2, int FORMS>
-__global__ void __launch_bounds__(kThreads) fp8_quantize_kernel(const QuantArgs p) {
+__global__ void __launch_bounds__(kThreads, QB) fp8_quantize_kernel(const QuantArgs p) {
     __shared__ __align__(16) float part[kThreads / 32][kFp8Block];  // column maxima, by warp
     __shared__ float warp_max[kThreads / 32];
     const bool whole = p.vec && int64_t(blockIdx.x + 1) * kFp8Block <= p.cols && int64_t(blockIdx.y + 1) * kFp8Block <= p.rows;
