@@ -10,15 +10,18 @@
 // 128 elements is the same byte in four consecutive MMAs.)
 //
 // gemm (many rows): CTA pairs, 256 x 256 output tiles, K-blocks of 128 bytes:
-//   warp 0      TMA producer: 128-row slices of A and B into a shared ring
+//   warp 0      TMA producer: 128-row slices of A and B into a shared ring of
+//               three stages of two K-blocks
 //   warp 1      MMA issuer (first CTA): scales shared -> tensor memory once in
-//               four K-blocks, then four MMAs of K = 32 a K-block
+//               four K-blocks, then four MMAs of K = 32 a K-block.  At this
+//               rate the issuing thread's own time counts: a commit takes it
+//               about 150 ns, half of a K-block's MMAs, so a stage holds two
 //   warp 2      allocates the tensor memory
 //   warp 3      gathers the scales of four K-blocks (a 32-bit word for each
 //               row) into the layout that the copy to tensor memory takes
 //   warps 4..7  epilogue: fp32 accumulator -> bf16 -> TMA store
 // Two 256-column accumulators and the scales need more than the 512 columns of
-// tensor memory, so the accumulators share 36: the epilogue reads those first,
+// tensor memory, so the accumulators share 48: the epilogue reads those first,
 // and the next tile's MMAs wait for no more than that.
 //
 // Every wait is bounded; see tl_gemm.cu, whose error protocol this shares.
@@ -40,14 +43,15 @@ using namespace kc;
 
 constexpr int kFp8BlockK = 128;     // one K-block: one scale block, one 128-byte swizzle row
 constexpr int kChunkBlocks = 4;     // K-blocks whose scales share a 32-bit word
-constexpr int kStagesPair = 5;
-constexpr uint32_t kStageHalf = 128 * 128;  // 128 rows (or reduction indices) of 128 bytes
+constexpr int kStageBlocks = 2;      // K-blocks of a stage
+constexpr int kStagesPair = 3;
+constexpr uint32_t kStageHalf = 128 * 128;  // one operand's K-block of a CTA: 128 rows (or reduction indices) of 128 bytes
 constexpr int kBatch = 4;           // chunks whose scales are handed over at once,
 constexpr int kSfSlots = 2;         // and how many batches shared memory holds
 constexpr uint32_t kSfA = 512, kSfB = 1024, kSfChunk = kSfA + kSfB, kSfSlot = kBatch * kSfChunk;
-constexpr uint32_t kAcc1 = 220;     // columns: accumulators at 0 and 220, 256 each,
-constexpr uint32_t kSfCols = 476;   // then three sets of 4 + 8 scale columns
-constexpr uint32_t kSfSet = 12, kSfSets = 3;
+constexpr uint32_t kAcc1 = 208;     // columns: accumulators at 0 and 208, 256 each,
+constexpr uint32_t kSfCols = 464;   // then four sets of 4 + 8 scale columns
+constexpr uint32_t kSfSet = 12, kSfSets = 4;
 
 // tcgen05.mma, 8-bit operands with one scale byte per 32 reduction elements.
 template <bool PAIR>
@@ -143,8 +147,33 @@ __device__ __forceinline__ void scale_words(const Scales& s, int i0, int c, int 
     }
 }
 
-constexpr size_t kSmemPair = size_t(kStagesPair) * 2 * kStageHalf + 4 * 2 * kEpiBuf + kSfSlots * kSfSlot + kBarBytes + 1024;
+constexpr size_t kSmemPair = size_t(kStagesPair) * 2 * kStageBlocks * kStageHalf + 4 * kEpiBuf + kSfSlots * kSfSlot + kBarBytes + 1024;
 static_assert(kSmemPair <= 232448, "shared memory budget");
+
+// The lane's row of 64 accumulator columns, as bf16 pairs.
+__device__ __forceinline__ void read_bf16(uint32_t taddr, uint32_t (&w)[32]) {
+    uint32_t v[2][32];
+    tmem_ld_32cols(taddr, v[0]);
+    tmem_ld_32cols(taddr + 32u, v[1]);
+    tmem_ld_wait();
+#pragma unroll
+    for (int j = 0; j < 32; ++j) w[j] = pack_bf16x2(__uint_as_float(v[j / 16][2 * j % 32]), __uint_as_float(v[j / 16][2 * j % 32 + 1]));
+}
+// The warp's 32 rows of them through its staging box (128B-swizzled) to the result.
+__device__ __forceinline__ void store_box(const CUtensorMap* map, uint32_t box, const uint32_t (&w)[32], int col, int row, int lane) {
+    if (lane == 0) bulk_wait_group_read<0>();  // the box's last store has read it
+    __syncwarp();
+    const uint32_t row_addr = box + uint32_t(lane) * 128u;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        st_shared_v4(row_addr + ((uint32_t(j) ^ (uint32_t(lane) & 7u)) << 4), w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+    fence_proxy_async_shared();
+    __syncwarp();
+    if (lane == 0) {
+        tma_store_2d(map, box, col, row);
+        bulk_commit_group();
+    }
+}
 
 template <bool A_MN, bool B_MN>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -152,12 +181,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const __grid_constant__ CUtensorMap map_d, const Fp8Params p) {
     const WaitCtx wc{p.err, p.timeout_ns};
     constexpr int S = kStagesPair;
-    constexpr uint32_t kStage = 2 * kStageHalf;
+    constexpr uint32_t kStage = 2 * kStageBlocks * kStageHalf;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t smem0 = smem_addr(smem);
-    const uint32_t epi_base = smem0 + S * kStage, sf0 = epi_base + 8 * kEpiBuf;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S * kStage + 8 * kEpiBuf + kSfSlots * kSfSlot);
+    const uint32_t epi_base = smem0 + S * kStage, sf0 = epi_base + 4 * kEpiBuf;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S * kStage + 4 * kEpiBuf + kSfSlots * kSfSlot);
     const uint32_t bar0 = smem_addr(bars);
     // full[s], empty[s], sf_full[q], sf_empty[q], tmem_full[a], shared columns
     // read, drain.  full, sf_full and the shared columns' barrier are used in
@@ -169,9 +198,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto tfull_bar = [&](uint32_t a) { return bar0 + 8u * (2 * S + 2 * kSfSlots + a); };
     const uint32_t tread_bar = bar0 + 8u * (2 * S + 2 * kSfSlots + 2);
     const uint32_t drain_bar = bar0 + 8u * (2 * S + 2 * kSfSlots + 3);
-    auto set_free_bar = [&](uint32_t i) { return bar0 + 8u * (2 * S + 2 * kSfSlots + 4 + i); };  // first CTA's MMA thread alone
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 2 * kSfSlots + 4 + kSfSets);
-    static_assert((2 * S + 2 * kSfSlots + 4 + kSfSets) * 8 + 4 <= int(kBarBytes), "barrier area");
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 2 * kSfSlots + 4);
+    static_assert((2 * S + 2 * kSfSlots + 4) * 8 + 4 <= int(kBarBytes), "barrier area");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
@@ -191,7 +219,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int a = 0; a < 2; ++a) mbar_init(tfull_bar(a), 1);
         mbar_init(tread_bar, 8);  // the epilogue warps of both CTAs
         mbar_init(drain_bar, 1);
-        for (uint32_t i = 0; i < kSfSets; ++i) mbar_init(set_free_bar(i), 1);
         mbar_init_fence();
     }
     if (warp == 2) {
@@ -216,20 +243,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 int mb, nb;
                 tile_coords(tile, p.num_m, p.num_n, p.raster, p.group, mb, nb);
                 const int m0 = mb * 256 + int(rank) * 128, n0 = nb * 256 + int(rank) * 128;
-                for (int kb = 0; kb < p.num_k; ++kb, ++fills) {
+                for (int kb = 0; kb < p.num_k; kb += kStageBlocks, ++fills) {
                     const uint32_t s = fills % S;
                     if (!wait_bounded(empty_bar(s), ((fills / S) & 1u) ^ 1u, wc, kErrProducerWait)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t sa = smem0 + s * kStage, sb = sa + kStageHalf;
-                    const int k0 = kb * kFp8BlockK;
                     if (leader) mbar_arrive_expect_tx(full_bar(s), 2 * kStage);
                     const uint32_t fb = map_to_rank(full_bar(s), 0);
-                    if (A_MN) tma_load_2d_pair_hint(sa, &map_a, fb, m0, k0, pol_a);
-                    else tma_load_2d_pair_hint(sa, &map_a, fb, k0, m0, pol_a);
-                    if (B_MN) tma_load_2d_pair_hint(sb, &map_b, fb, n0, k0, pol_b);
-                    else tma_load_2d_pair_hint(sb, &map_b, fb, k0, n0, pol_b);
+#pragma unroll
+                    for (int j = 0; j < kStageBlocks; ++j) {  // a K-block past the end loads zeros
+                        const uint32_t sa = smem0 + s * kStage + uint32_t(2 * j) * kStageHalf, sb = sa + kStageHalf;
+                        const int k0 = (kb + j) * kFp8BlockK;
+                        if (A_MN) tma_load_2d_pair_hint(sa, &map_a, fb, m0, k0, pol_a);
+                        else tma_load_2d_pair_hint(sa, &map_a, fb, k0, m0, pol_a);
+                        if (B_MN) tma_load_2d_pair_hint(sb, &map_b, fb, n0, k0, pol_b);
+                        else tma_load_2d_pair_hint(sb, &map_b, fb, k0, n0, pol_b);
+                    }
                 }
             }
             if (leader) {  // loads must land before the CTAs may exit
@@ -252,9 +282,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             int c = 0;  // the chunk's place in its tile
             auto copy_scales = [&] {
                 if (copied >= all_chunks) return true;
+                // The MMAs that last read this set of columns are done: they
+                // are three chunks and more back, so at least three stages,
+                // and this thread has just seen the stage full that those
+                // three stages' ring slot was given back for.
+                static_assert(kSfSets >= S + 1, "a set outlives the stages in flight");
                 const uint32_t set = copied % kSfSets;
-                // the MMAs that last read this set of columns are done
-                if (copied >= kSfSets && !wait_bounded(set_free_bar(set), (copied / kSfSets - 1) & 1u, wc, kErrMmaWaitTmem)) return false;
                 if (c % kBatch == 0 && !wait_cluster(sf_full_bar(batch % kSfSlots), (batch / kSfSlots) & 1u, wc, kErrMmaWaitFull))
                     return false;
                 tc_fence_after();
@@ -279,28 +312,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (it > 0 && !wait_bounded(tread_bar, uint32_t(it - 1) & 1u, wc, kErrMmaWaitTmem)) break;
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + (it & 1 ? kAcc1 : 0u);
-                for (int kb = 0; kb < p.num_k; ++kb, ++fills) {
+                for (int kb = 0; kb < p.num_k; kb += kStageBlocks, ++fills) {
                     const uint32_t set = tmem_base + kSfCols + (chunk % kSfSets) * kSfSet;
-                    const uint32_t id = uint32_t(kb) % kChunkBlocks;
                     const uint32_t s = fills % S;
                     if (!wait_bounded(full_bar(s), (fills / S) & 1u, wc, kErrMmaWaitFull)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t sa = smem0 + s * kStage, sb = sa + kStageHalf;
-                    const uint32_t idesc = with_scale_id(p.idesc, id);
+                    const bool first = kb % kChunkBlocks == 0;  // stage of its chunk
 #pragma unroll
-                    for (int j = 0; j < kFp8BlockK / 32; ++j)
-                        umma_fp8<true>(d_tmem, fp8_desc(A_MN, sa, j), fp8_desc(B_MN, sb, j), idesc, set, set + 4,
-                                       (kb | j) != 0 ? 1u : 0u);
+                    for (int i = 0; i < kStageBlocks; ++i) {
+                        const uint32_t sa = smem0 + s * kStage + uint32_t(2 * i) * kStageHalf, sb = sa + kStageHalf;
+                        const uint32_t idesc = with_scale_id(p.idesc, uint32_t(i) + (first ? 0u : uint32_t(kStageBlocks)));
+#pragma unroll
+                        for (int j = 0; j < kFp8BlockK / 32; ++j)
+                            umma_fp8<true>(d_tmem, fp8_desc(A_MN, sa, j), fp8_desc(B_MN, sb, j), idesc, set, set + 4,
+                                           (kb | i | j) != 0 ? 1u : 0u);
+                    }
                     umma_commit_pair(empty_bar(s), 0x3);
-                    const bool last = id == kChunkBlocks - 1 || kb == p.num_k - 1;
-                    if ((id == 1 || (last && id == 0)) && !copy_scales()) {
+                    if (first && !copy_scales()) {
                         ok = false;
                         break;
                     }
-                    if (last) umma_commit_pair(set_free_bar(chunk++ % kSfSets), 0x1);
+                    if (!first || kb + kStageBlocks >= p.num_k) ++chunk;
                 }
                 if (ok) umma_commit_pair(tfull_bar(it & 1), 0x3);
             }
@@ -345,9 +380,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp >= kFirstEpilogueWarp) {
         const int q = warp & 3;
-        const uint32_t epi0 = epi_base + uint32_t(q) * 2u * kEpiBuf;
+        const uint32_t box = epi_base + uint32_t(q) * kEpiBuf;
         if (lane == 0) tma_prefetch_map(&map_d);
-        uint32_t buf = 0;
         int it = 0;
         for (int tile = first_tile; tile < p.num_tiles; tile += tile_step, ++it) {
             const uint32_t acc = it & 1;
@@ -361,8 +395,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int i = 0; i < 4; ++i) {
                 const int c = acc ? i : 3 - i;  // the shared columns first
-                if (c < have)
-                    epi_bf16_tma(&map_d, t_row + uint32_t(c) * 64u, epi0, buf, 1, n0 + c * 64, row0, lane);
+                uint32_t w[32];
+                if (c < have) read_bf16(t_row + uint32_t(c) * 64u, w);
                 if (i == 0) {
                     tc_fence_before();
                     __syncwarp();
@@ -371,6 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         else mbar_arrive_cluster(map_to_rank(tread_bar, 0));
                     }
                 }
+                if (c < have) store_box(&map_d, box, w, n0 + c * 64, row0, lane);
             }
             tc_fence_before();
             __syncwarp();
