@@ -601,6 +601,29 @@ tl_status tiled_linear_fp8_gemm_dw(int64_t T, int64_t K, int64_t n, int32_t x_fo
                                    const void *x_scale, int32_t dy_format, const void *dy_q, int64_t lddy,
                                    const void *dy_scale, void *dw_dev, int64_t lddw, int32_t *err_dev, void *stream);
 
+/* The layer's forward in one call: x [T, K] (tl_type, ld ldx, any alignment of
+ * its elements) to the row form (e4m3) in the workspace, and y = x . w as
+ * tiled_linear_fp8_gemm_forward, with the same results as the two calls.  With
+ * few tokens the product's reading of w begins under the quantisation.
+ * workspace: 256-byte aligned, tiled_linear_fp8_linear_workspace_bytes (0 if the
+ * arguments are invalid).  Errors: TL_ERR_INVALID, TL_ERR_WORKSPACE, TL_ERR_CUDA. */
+size_t tiled_linear_fp8_linear_workspace_bytes(int64_t T, int64_t K, int64_t n);
+tl_status tiled_linear_fp8_linear(int64_t T, int64_t K, int64_t n, int32_t type, const void *x_dev, int64_t ldx,
+                                  int32_t w_format, const void *w_q, int64_t ldw, const void *w_scale, void *y_dev,
+                                  int64_t ldy, void *workspace_dev, size_t workspace_bytes, int32_t *err_dev,
+                                  void *stream);
+
+/* The layer's backward in one call: dy [T, n] to the row and col forms and x to the
+ * col form in the workspace, then dx [T, K] and dw [K, n] (bf16) as
+ * tiled_linear_fp8_gemm_dx and _dw; dx or dw may be NULL where not wanted.
+ * The derivative passes through the rounding to 8 bits.  Errors as the forward. */
+size_t tiled_linear_fp8_linear_backward_workspace_bytes(int64_t T, int64_t K, int64_t n);
+tl_status tiled_linear_fp8_linear_backward(int64_t T, int64_t K, int64_t n, int32_t type, const void *x_dev,
+                                           int64_t ldx, const void *dy_dev, int64_t lddy, int32_t w_format,
+                                           const void *w_q, int64_t ldw, const void *w_scale, void *dx_dev,
+                                           int64_t lddx, void *dw_dev, int64_t lddw, void *workspace_dev,
+                                           size_t workspace_bytes, int32_t *err_dev, void *stream);
+
 /* --- pinned host memory helpers ------------------------------------------ */
 /* Page-locked host allocation (cudaHostAlloc, portable); *out = NULL on
  * failure.  Free with tiled_linear_host_free. */

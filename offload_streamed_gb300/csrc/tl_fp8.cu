@@ -24,6 +24,12 @@
 // tensor memory, so the accumulators share 48: the epilogue reads those first,
 // and the next tile's MMAs wait for no more than that.
 //
+// few (up to 128 tokens): the weight's bytes are the work, so the weight is the
+// MMA's A side, 128 of its rows (columns) a CTA, and the tokens are N = 16 to
+// 128 columns.  The CTAs of a cluster share a reduction: each sums its part in
+// its tensor memory, and they add the parts up through distributed shared
+// memory in a fixed order.
+//
 // Every wait is bounded; see tl_gemm.cu, whose error protocol this shares.
 #include "tl_fp8.h"
 #include "tl_gemm.h"
@@ -35,6 +41,7 @@
 
 #include <algorithm>
 #include <climits>
+#include <type_traits>
 
 namespace tl {
 namespace {
@@ -92,6 +99,18 @@ __host__ __device__ constexpr uint32_t idesc_fp8(int m, int n, bool a_mn, bool b
            (uint32_t(n >> 3) << 17) | (1u << 23) | (uint32_t(m >> 4) << 24);
 }
 __device__ __forceinline__ uint32_t with_scale_id(uint32_t idesc, uint32_t id) { return idesc | (id << 4) | (id << 29); }
+
+__device__ __forceinline__ void tmem_ld_16cols(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32"
+        " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+// Wait until the kernel before this one has completed and its writes are
+// visible (at once, unless the launch allowed this one to begin early).
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // wait_bounded_cluster, without its reading of the clock where the phase is
 // over already: that takes longer than four K-blocks' MMAs.
@@ -423,6 +442,220 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
+// ---- few tokens --------------------------------------------------------------
+
+constexpr int kFewTokens = 128;
+constexpr size_t kFewSmem = 112 * 1024;  // of a CTA: two share an SM
+constexpr uint32_t kFewSfSlots = 4, kFewSfSlot = 1024;
+
+template <int N>
+struct Few {
+    static constexpr uint32_t kStageBytes = kStageHalf + uint32_t(N) * 128;
+    static constexpr uint32_t kFixed = kFewSfSlots * kFewSfSlot + kBarBytes + 1024;
+    static constexpr int kStages = int((kFewSmem - kFixed) / kStageBytes);
+    static constexpr size_t kSmem = size_t(kStages) * kStageBytes + kFixed;
+    static constexpr uint32_t kCols = N <= 16 ? 32 : N <= 32 ? 64 : N <= 64 ? 128 : 256;  // accumulator, then two sets of 4 + 4 scales
+    static_assert(N + 16 <= int(kCols) && kStages >= 3, "tensor memory, shared memory");
+    static_assert(size_t(N) * 128 * 4 <= size_t(kStages) * kStageBytes, "the partial sums fit the stages");
+};
+
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t local, uint32_t rank) {
+    float4 v;
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\t"
+        "mapa.shared::cluster.u32 a, %4, %5;\n\t"
+        "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
+        : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+        : "r"(local), "r"(rank)
+        : "memory");
+    return v;
+}
+
+// map_w: the weight, 128 of its own indices a box; map_t: the tokens, N a box.
+// w: m_dim = own indices of the weight, n_dim = tokens.  out[token][index].
+template <bool W_MN, int N>
+__global__ void __launch_bounds__(kThreads, 2)
+    fp8_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_t, const Fp8Params p,
+                   __nv_bfloat16* out, int64_t ldo, int splits, int per) {
+    using F = Few<N>;
+    const WaitCtx wc{p.err, p.timeout_ns};
+    constexpr int S = F::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t smem0 = smem_addr(smem), sf0 = smem0 + S * F::kStageBytes;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S * F::kStageBytes + kFewSfSlots * kFewSfSlot);
+    const uint32_t bar0 = smem_addr(bars);
+    auto full_bar = [&](uint32_t s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](uint32_t s) { return bar0 + 8u * (S + s); };
+    auto sf_full_bar = [&](uint32_t q) { return bar0 + 8u * (2 * S + q); };
+    auto sf_empty_bar = [&](uint32_t q) { return bar0 + 8u * (2 * S + kFewSfSlots + q); };
+    const uint32_t done_bar = bar0 + 8u * (2 * S + 2 * kFewSfSlots);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 2 * kFewSfSlots + 1);
+    static_assert((2 * S + 2 * int(kFewSfSlots) + 1) * 8 + 4 <= int(kBarBytes), "barrier area");
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = splits > 1 ? cluster_ctarank() : 0;
+    const int m0 = int(blockIdx.x / uint32_t(splits)) * 128;
+    const int t0 = int(blockIdx.y) * N, tokens = min(N, p.n_dim - t0);  // this CTA's block of tokens
+    const int kb0 = int(rank) * per, kb1 = min(p.num_k, kb0 + per);  // this CTA's K-blocks, perhaps none
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(full_bar(s), 1);
+            mbar_init(empty_bar(s), 1);
+        }
+        for (uint32_t q = 0; q < kFewSfSlots; ++q) {
+            mbar_init(sf_full_bar(q), 1);
+            mbar_init(sf_empty_bar(q), 1);
+        }
+        mbar_init(done_bar, 1);
+        mbar_init_fence();
+    }
+    if (warp == 2) {
+        tmem_alloc<false>(smem_addr(tmem_slot), F::kCols);
+        tmem_relinquish<false>();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // The weight is there before the kernel ahead of this one began
+            // (Fp8GemmDesc::early); the tokens may be what that one makes.
+            auto load_w = [&](int kb, uint32_t s) {
+                const int k0 = kb * kFp8BlockK;
+                if (W_MN) tma_load_2d(smem0 + s * F::kStageBytes, &map_w, full_bar(s), m0, k0);
+                else tma_load_2d(smem0 + s * F::kStageBytes, &map_w, full_bar(s), k0, m0);
+            };
+            const int ahead = min(S, kb1 - kb0);
+            for (int i = 0; i < ahead; ++i) {
+                mbar_arrive_expect_tx(full_bar(i), F::kStageBytes);
+                load_w(kb0 + i, i);
+            }
+            grid_dependency_wait();
+            uint32_t fills = 0;
+            for (int kb = kb0; kb < kb1; ++kb, ++fills) {
+                const uint32_t s = fills % S;
+                if (int(fills) >= ahead) {
+                    if (!wait_bounded(empty_bar(s), ((fills / S) & 1u) ^ 1u, wc, kErrProducerWait)) break;
+                    mbar_arrive_expect_tx(full_bar(s), F::kStageBytes);
+                    load_w(kb, s);
+                }
+                tma_load_2d(smem0 + s * F::kStageBytes + kStageHalf, &map_t, full_bar(s), kb * kFp8BlockK, t0);
+            }
+            const uint32_t outstanding = fills < uint32_t(S) ? fills : uint32_t(S);
+            for (uint32_t j = 0; j < outstanding; ++j) {
+                const uint32_t f = fills - 1 - j;
+                wait_bounded(full_bar(f % S), (f / S) & 1u, wc, kErrDrainWait, false);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            uint32_t fills = 0, chunk = 0;
+            for (int kb = kb0; kb < kb1; ++kb, ++fills) {
+                const uint32_t id = uint32_t(kb) % kChunkBlocks, q = chunk % kFewSfSlots;
+                const uint32_t set = tmem_base + N + (chunk & 1u) * 8u;
+                if (id == 0 || kb == kb0) {
+                    // the MMAs that last read this set are done
+                    if (chunk >= 2 && !wait_bounded(sf_empty_bar((chunk - 2) % kFewSfSlots), ((chunk - 2) / kFewSfSlots) & 1u, wc, kErrMmaWaitTmem))
+                        break;
+                    if (!wait_bounded(sf_full_bar(q), (chunk / kFewSfSlots) & 1u, wc, kErrMmaWaitFull)) break;
+                    tc_fence_after();
+                    tmem_copy_scales<false>(set, sf0 + q * kFewSfSlot);
+                    tmem_copy_scales<false>(set + 4, sf0 + q * kFewSfSlot + 512);
+                }
+                const uint32_t s = fills % S;
+                if (!wait_bounded(full_bar(s), (fills / S) & 1u, wc, kErrMmaWaitFull)) break;
+                tc_fence_after();
+                const uint32_t sa = smem0 + s * F::kStageBytes, sb = sa + kStageHalf;
+                const uint32_t idesc = with_scale_id(p.idesc, id);
+#pragma unroll
+                for (int j = 0; j < kFp8BlockK / 32; ++j)
+                    umma_fp8<false>(tmem_base, fp8_desc(W_MN, sa, j), fp8_desc(false, sb, j), idesc, set, set + 4,
+                                    (kb != kb0 || j) ? 1u : 0u);
+                umma_commit(empty_bar(s));
+                if (id == kChunkBlocks - 1 || kb == kb1 - 1) {
+                    umma_commit(sf_empty_bar(q));
+                    ++chunk;
+                }
+            }
+            umma_commit(done_bar);
+            wait_bounded(done_bar, 0, wc, kErrDrainWait, false);
+        }
+    } else if (warp == 3) {
+        grid_dependency_wait();
+        uint32_t chunk = 0;
+        if (kb1 > kb0)
+            for (int c = kb0 / kChunkBlocks; c <= (kb1 - 1) / kChunkBlocks; ++c, ++chunk) {
+                uint32_t w[8];
+                scale_words<4>(p.a, m0, c, p.num_k, lane, w);
+                scale_words<4>(p.b, t0, c, p.num_k, lane, w + 4);
+                const uint32_t q = chunk % kFewSfSlots, dst = sf0 + q * kFewSfSlot + uint32_t(lane) * 16;
+                if (!warp_wait(sf_empty_bar(q), ((chunk / kFewSfSlots) & 1u) ^ 1u, wc, kErrProducerWait, lane)) break;
+                st_shared_v4(dst, w[0], w[1], w[2], w[3]);
+                st_shared_v4(dst + 512, w[4], w[5], w[6], w[7]);
+                fence_proxy_async_shared();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sf_full_bar(q));
+            }
+    } else if (warp >= kFirstEpilogueWarp) {
+        grid_dependency_wait();  // (the result may be what the kernel before this one reads)
+        const int q = warp & 3, i = q * 32 + lane;
+        const bool ok = warp_wait(done_bar, 0, wc, kErrEpilogueWait, lane);
+        tc_fence_after();
+        const uint32_t t_row = tmem_base + (uint32_t(q * 32) << 16);
+        float* part = reinterpret_cast<float*>(smem);  // [token][128], once the stages are done with
+        constexpr int kStep = N < 32 ? N : 32;
+        if (ok)
+#pragma unroll 1
+            for (int c = 0; c < tokens; c += kStep) {
+                uint32_t v[kStep];
+                if constexpr (kStep == 32) tmem_ld_32cols(t_row + uint32_t(c), v);
+                else tmem_ld_16cols(t_row + uint32_t(c), v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < kStep; ++j)
+                    if (c + j < tokens) {
+                        const float f = kb1 > kb0 ? __uint_as_float(v[j]) : 0.0f;
+                        if (splits > 1) part[(c + j) * 128 + i] = f;
+                        else if (m0 + i < p.m_dim) out[int64_t(t0 + c + j) * ldo + m0 + i] = __float2bfloat16_rn(f);
+                    }
+            }
+        tc_fence_before();
+    }
+    if (splits > 1) {
+        cluster_sync();  // every part stands
+        for (int e = int(rank) * kThreads + int(threadIdx.x); e < tokens * 32; e += splits * kThreads) {
+            const int t = e / 32, i = e % 32 * 4;
+            float4 v[8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+                if (r < splits) v[r] = ld_cluster_f32x4(smem0 + uint32_t(t * 128 + i) * 4u, uint32_t(r));
+            float4 sum = v[0];
+#pragma unroll
+            for (int r = 1; r < 8; ++r)
+                if (r < splits) sum = make_float4(sum.x + v[r].x, sum.y + v[r].y, sum.z + v[r].z, sum.w + v[r].w);
+            __nv_bfloat16* dst = out + int64_t(t0 + t) * ldo + m0 + i;
+            if (m0 + i + 4 <= p.m_dim) {  // (rows of the result start on 16 bytes, so i does on 8)
+                *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
+            } else {
+                const float f[4] = {sum.x, sum.y, sum.z, sum.w};
+                for (int j = 0; j < 4; ++j)
+                    if (m0 + i + j < p.m_dim) dst[j] = __float2bfloat16_rn(f[j]);
+            }
+        }
+        cluster_sync();  // nobody leaves while its part is read
+    } else {
+        __syncthreads();
+    }
+    if (warp == 2) {
+        tc_fence_after();
+        tmem_dealloc<false>(tmem_base, F::kCols);
+    }
+}
+
 bool map_operand(CUtensorMap* map, const Fp8Operand& o, int64_t dim, int64_t k, uint32_t box_rows, std::string* why) {
     return o.mn_major ? swizzled_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, o.q, uint64_t(dim), uint64_t(k), uint64_t(o.ld), 128, why)
                       : swizzled_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, o.q, uint64_t(k), uint64_t(dim), uint64_t(o.ld), box_rows, why);
@@ -432,25 +665,75 @@ Scales scales_of(const Fp8Operand& o, int64_t dim) {
     return Scales{o.scale, o.mn_major ? 1 : o.tile_cols, o.mn_major ? o.tile_cols : 1, int32_t(dim), o.tiles ? 1 : 0};
 }
 
-template <typename K>
-cudaError_t launch_clusters(K kern, int grid, int cluster, int threads, size_t smem, cudaStream_t stream, const CUtensorMap& ma,
-                            const CUtensorMap& mb, const CUtensorMap& md, const Fp8Params& p) {
+template <typename T>
+struct Same {
+    using type = T;
+};
+// early: the kernel may begin before the one ahead of it in the stream has
+// completed (it waits for that where it has to).
+template <typename... A>
+cudaError_t launch_clusters(void (*kern)(A...), dim3 grid, int cluster, size_t smem, bool early, cudaStream_t stream,
+                            typename Same<A>::type... args) {
     int per_sm = 0;
-    const cudaError_t e = ctas_per_sm(reinterpret_cast<const void*>(kern), threads, smem, &per_sm);
+    const cudaError_t e = ctas_per_sm(reinterpret_cast<const void*>(kern), kThreads, smem, &per_sm);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(unsigned(grid), 1, 1);
-    cfg.blockDim = dim3(unsigned(threads), 1, 1);
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = unsigned(cluster);
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, ma, mb, md, p);
+    cfg.numAttrs = early ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+template <bool W_MN, int N>
+cudaError_t launch_few(const CUtensorMap& mw, const CUtensorMap& mt, Fp8Params p, const Fp8GemmDesc& g, int num_sms, cudaStream_t stream) {
+    p.idesc = idesc_fp8(128, N, W_MN, false, g.b.format, g.a.format);
+    const int tiles = (p.m_dim + 127) / 128;
+    const int blocks = (p.n_dim + N - 1) / N;
+    // CTAs of a cluster: as many as two an SM allow, with two K-blocks each.
+    // (8192 x 8192, one token: 4 of 64 tiles' 15.0 us.  25600 x 6400: 4 of 50
+    // tiles' 29.6 us, 8 34.5 us, 6 41.2 us, which pack badly.)
+    int splits = 1;
+    while (splits < 8 && int64_t(tiles) * blocks * splits * 2 <= 2 * num_sms && p.num_k >= 4 * splits) splits *= 2;
+    const int per = (p.num_k + splits - 1) / splits;
+    return launch_clusters(fp8_few_kernel<W_MN, N>, dim3(unsigned(tiles * splits), unsigned(blocks)), splits, Few<N>::kSmem, g.early, stream, mw, mt, p,
+                           static_cast<__nv_bfloat16*>(g.d), g.ldd, splits, per);
+}
+
+// The few-token kernel with the operands' sides exchanged: g.b is the weight.
+cudaError_t few_launch(const Fp8GemmDesc& g, int num_sms, cudaStream_t stream, std::string* why) {
+    const int n = g.m_dim <= 16 ? 16 : g.m_dim <= 32 ? 32 : g.m_dim <= 64 ? 64 : 128;
+    CUtensorMap mw, mt;
+    if (!map_operand(&mw, g.b, g.n_dim, g.k_dim, 128, why) || !map_operand(&mt, g.a, g.m_dim, g.k_dim, uint32_t(n), why))
+        return cudaErrorInvalidValue;
+    Fp8Params p{};
+    p.m_dim = int32_t(g.n_dim);
+    p.n_dim = int32_t(g.m_dim);
+    p.k_dim = int32_t(g.k_dim);
+    p.num_k = int32_t((g.k_dim + kFp8BlockK - 1) / kFp8BlockK);
+    p.a = scales_of(g.b, g.n_dim);
+    p.b = scales_of(g.a, g.m_dim);
+    p.err = g.err;
+    p.timeout_ns = 2000000000ull;
+    auto run = [&](auto mn) {
+        constexpr bool MN = decltype(mn)::value;
+        switch (n) {
+            case 16: return launch_few<MN, 16>(mw, mt, p, g, num_sms, stream);
+            case 32: return launch_few<MN, 32>(mw, mt, p, g, num_sms, stream);
+            case 64: return launch_few<MN, 64>(mw, mt, p, g, num_sms, stream);
+            default: return launch_few<MN, 128>(mw, mt, p, g, num_sms, stream);
+        }
+    };
+    return g.b.mn_major ? run(std::true_type{}) : run(std::false_type{});
 }
 
 }  // namespace
@@ -475,6 +758,20 @@ std::string fp8_gemm_check(const Fp8GemmDesc& g) {
 }
 
 cudaError_t fp8_gemm_launch(const Fp8GemmDesc& g, int num_sms, cudaStream_t stream, std::string* why) {
+    const int64_t pair_tiles = ((g.m_dim + 255) / 256) * ((g.n_dim + 255) / 256);
+    // Few tokens, or fewer tiles than half the CTA pairs and a reduction long
+    // enough to share: the kernel whose clusters split the reduction.  Other
+    // kernel against this one, us, at K x n of the weight and T tokens: 8192 x
+    // 8192, T = 256 (32 tiles) 30.3 / 26.8, T = 512 (64 tiles) 31.7 / 38.2;
+    // 25600 x 6400, T = 256 (25 tiles) 72.7 / 57.5; 8192 x 1024, T = 1024 (16
+    // tiles) 27.1 / 17.6; 1024 x 4096, T = 256 (16 tiles, short) 10.3 / 11.7.
+    constexpr int kLongBlocks = 32;
+    if (!g.a.mn_major && (g.m_dim <= kFewTokens ||
+                          (pair_tiles <= num_sms / 4 && g.k_dim >= int64_t(kLongBlocks) * kFp8BlockK))) {
+        const cudaError_t e = few_launch(g, num_sms, stream, why);
+        if (e != cudaSuccess && why && why->empty()) *why = std::string("kernel launch: ") + cudaGetErrorString(e);
+        return e;
+    }
     CUtensorMap ma, mb, md;
     if (!map_operand(&ma, g.a, g.m_dim, g.k_dim, 128, why) || !map_operand(&mb, g.b, g.n_dim, g.k_dim, 128, why) ||
         !swizzled_map(&md, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, g.d, uint64_t(g.n_dim), uint64_t(g.m_dim), uint64_t(g.ldd), 32, why))
@@ -496,7 +793,7 @@ cudaError_t fp8_gemm_launch(const Fp8GemmDesc& g, int num_sms, cudaStream_t stre
     p.timeout_ns = 2000000000ull;
     p.idesc = idesc_fp8(256, 256, g.a.mn_major, g.b.mn_major, g.a.format, g.b.format);
     const int grid = 2 * std::min(p.num_tiles, slots);
-    auto run = [&](auto kern) { return launch_clusters(kern, grid, 2, kThreads, kSmemPair, stream, ma, mb, md, p); };
+    auto run = [&](auto kern) { return launch_clusters(kern, dim3(unsigned(grid)), 2, kSmemPair, false, stream, ma, mb, md, p); };
     cudaError_t e;
     if (g.a.mn_major) e = g.b.mn_major ? run(fp8_gemm_kernel<true, true>) : cudaErrorInvalidValue;
     else e = g.b.mn_major ? run(fp8_gemm_kernel<false, true>) : run(fp8_gemm_kernel<false, false>);

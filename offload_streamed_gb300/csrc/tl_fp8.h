@@ -50,6 +50,9 @@ struct Fp8GemmDesc {
     void* d = nullptr;
     int64_t ldd = 0;
     int32_t* err = nullptr;
+    // The kernel before this one in the stream writes A alone: B may be read
+    // before that kernel has completed.
+    bool early = false;
 };
 std::string fp8_gemm_check(const Fp8GemmDesc& g);
 cudaError_t fp8_gemm_launch(const Fp8GemmDesc& g, int num_sms, cudaStream_t stream, std::string* why);

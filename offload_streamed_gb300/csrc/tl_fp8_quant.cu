@@ -21,9 +21,6 @@
 namespace tl {
 namespace {
 
-#ifndef QB
-#define QB 3
-#endif
 constexpr int kThreads = 256;
 constexpr int kRowsPer = 8;  // rows of a thread, 16 apart
 
@@ -206,9 +203,12 @@ __device__ __forceinline__ void quantize_tile(const QuantArgs& p, float (*part)[
 }
 
 template <typename T, bool E5M2, int FORMS>
-__global__ void __launch_bounds__(kThreads, QB) fp8_quantize_kernel(const QuantArgs p) {
+__global__ void __launch_bounds__(kThreads, 3) fp8_quantize_kernel(const QuantArgs p) {
     __shared__ __align__(16) float part[kThreads / 32][kFp8Block];  // column maxima, by warp
     __shared__ float warp_max[kThreads / 32];
+    // a product that was launched to begin early may: it waits for this kernel
+    // before it reads what is written here
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const bool whole = p.vec && int64_t(blockIdx.x + 1) * kFp8Block <= p.cols && int64_t(blockIdx.y + 1) * kFp8Block <= p.rows;
     if (whole) quantize_tile<T, E5M2, FORMS, true>(p, part, warp_max);
     else quantize_tile<T, E5M2, FORMS, false>(p, part, warp_max);

@@ -7,7 +7,10 @@
 #include "tl_norm.h"
 #include "tl_unbound_error.h"
 
+#include <algorithm>
+#include <climits>
 #include <exception>
+#include <string>
 
 using namespace tl;
 
@@ -148,8 +151,8 @@ Fp8Operand operand(bool own_is_row, bool tiles, int64_t cols, const void* q, int
     return o;
 }
 
-tl_status fp8_product(int64_t m, int64_t n, int64_t k, const Fp8Operand& a, const Fp8Operand& b, void* d, int64_t ldd,
-                      int32_t* err, void* stream) {
+Fp8GemmDesc product(int64_t m, int64_t n, int64_t k, const Fp8Operand& a, const Fp8Operand& b, void* d, int64_t ldd,
+                    int32_t* err) {
     Fp8GemmDesc g;
     g.m_dim = m;
     g.n_dim = n;
@@ -159,13 +162,22 @@ tl_status fp8_product(int64_t m, int64_t n, int64_t k, const Fp8Operand& a, cons
     g.d = d;
     g.ldd = ldd;
     g.err = err;
-    const std::string bad = fp8_gemm_check(g);
-    if (!bad.empty()) return refuse(TL_ERR_INVALID, bad);
+    return g;
+}
+
+tl_status launch_product(const Fp8GemmDesc& g, void* stream) {
     const int sms = device_sms();
     if (sms < 2) return refuse(TL_ERR_CUDA, "no current device");
     std::string why;
     const cudaError_t e = fp8_gemm_launch(g, sms, static_cast<cudaStream_t>(stream), &why);
     return e == cudaSuccess ? TL_OK : refuse(TL_ERR_CUDA, why);
+}
+
+tl_status fp8_product(int64_t m, int64_t n, int64_t k, const Fp8Operand& a, const Fp8Operand& b, void* d, int64_t ldd,
+                      int32_t* err, void* stream) {
+    const Fp8GemmDesc g = product(m, n, k, a, b, d, ldd, err);
+    const std::string bad = fp8_gemm_check(g);
+    return bad.empty() ? launch_product(g, stream) : refuse(TL_ERR_INVALID, bad);
 }
 
 }  // namespace
@@ -207,6 +219,124 @@ tl_status tiled_linear_fp8_gemm_dw(int64_t T, int64_t K, int64_t n, int32_t x_fo
         return fp8_product(K, n, T, operand(false, false, K, x_q, ldx, x_scale, x_format),
                            operand(false, false, n, dy_q, lddy, dy_scale, dy_format), dw_dev, lddw, err_dev,
                            stream);
+    });
+}
+
+}  // extern "C"
+
+namespace {
+
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+// One 8-bit form of a [rows, cols] matrix in a workspace.
+struct Held {
+    Fp8QuantDesc::Form form;
+    size_t q_bytes = 0, scale_bytes = 0;
+    Held(int64_t rows, int64_t cols, bool by_row) {
+        form.ldq = (cols + 15) / 16 * 16;
+        q_bytes = up256(size_t(rows) * size_t(form.ldq));
+        const int64_t along = by_row ? cols : rows, vectors = by_row ? rows : cols;
+        scale_bytes = up256(size_t((along + 4 * kFp8Block - 1) / (4 * kFp8Block)) * size_t(vectors) * 4);
+    }
+    size_t bytes() const { return q_bytes + scale_bytes; }
+    uint8_t* place(uint8_t* at) {
+        form.q = at;
+        form.scale = at + q_bytes;
+        return at + bytes();
+    }
+};
+
+bool layer_ok(int64_t T, int64_t K, int64_t n) {
+    return T >= 0 && K >= 1 && n >= 1 && T <= INT32_MAX / 2 && K <= INT32_MAX / 2 && n <= INT32_MAX / 2;
+}
+
+bool workspace_ok(const void* p, size_t have, size_t need) {
+    return p && (reinterpret_cast<uintptr_t>(p) & 255u) == 0 && have >= need;
+}
+
+tl_status quantize(int64_t rows, int64_t cols, int32_t type, const void* x, int64_t ldx, const Fp8QuantDesc::Form* row,
+                   const Fp8QuantDesc::Form* col, void* stream) {
+    Fp8QuantDesc d;
+    d.rows = rows;
+    d.cols = cols;
+    d.type = type;
+    d.x = x;
+    d.ldx = ldx;
+    d.format = TL_FP8_E4M3;
+    if (row) d.row = *row;
+    if (col) d.col = *col;
+    const std::string bad = fp8_quantize_check(d);
+    if (!bad.empty()) return refuse(TL_ERR_INVALID, bad);
+    return done(fp8_quantize_launch(d, static_cast<cudaStream_t>(stream)), "fp8 quantise");
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t tiled_linear_fp8_linear_workspace_bytes(int64_t T, int64_t K, int64_t n) {
+    return layer_ok(T, K, n) ? Held(std::max<int64_t>(T, 1), K, true).bytes() : 0;
+}
+
+tl_status tiled_linear_fp8_linear(int64_t T, int64_t K, int64_t n, int32_t type, const void* x_dev, int64_t ldx,
+                                  int32_t w_format, const void* w_q, int64_t ldw, const void* w_scale, void* y_dev,
+                                  int64_t ldy, void* workspace_dev, size_t workspace_bytes, int32_t* err_dev,
+                                  void* stream) {
+    return guarded([&]() -> tl_status {
+        if (!layer_ok(T, K, n)) return refuse(TL_ERR_INVALID, "T must be >= 0, K and n >= 1, all below 2^30");
+        if (T == 0) return TL_OK;
+        if (!workspace_ok(workspace_dev, workspace_bytes, tiled_linear_fp8_linear_workspace_bytes(T, K, n)))
+            return refuse(TL_ERR_WORKSPACE, "workspace is null, not 256-byte aligned or too small");
+        Held x(T, K, true);
+        x.place(static_cast<uint8_t*>(workspace_dev));
+        Fp8GemmDesc g = product(T, n, K, operand(true, false, K, x.form.q, x.form.ldq, x.form.scale, TL_FP8_E4M3),
+                                operand(false, true, n, w_q, ldw, w_scale, w_format), y_dev, ldy, err_dev);
+        g.early = true;  // the quantiser, directly ahead, writes x's form alone
+        const std::string bad = fp8_gemm_check(g);
+        if (!bad.empty()) return refuse(TL_ERR_INVALID, bad);
+        const tl_status st = quantize(T, K, type, x_dev, ldx, &x.form, nullptr, stream);
+        return st == TL_OK ? launch_product(g, stream) : st;
+    });
+}
+
+size_t tiled_linear_fp8_linear_backward_workspace_bytes(int64_t T, int64_t K, int64_t n) {
+    if (!layer_ok(T, K, n)) return 0;
+    const int64_t t = std::max<int64_t>(T, 1);
+    return Held(t, n, true).bytes() + Held(t, n, false).bytes() + Held(t, K, false).bytes();
+}
+
+tl_status tiled_linear_fp8_linear_backward(int64_t T, int64_t K, int64_t n, int32_t type, const void* x_dev,
+                                           int64_t ldx, const void* dy_dev, int64_t lddy, int32_t w_format,
+                                           const void* w_q, int64_t ldw, const void* w_scale, void* dx_dev,
+                                           int64_t lddx, void* dw_dev, int64_t lddw, void* workspace_dev,
+                                           size_t workspace_bytes, int32_t* err_dev, void* stream) {
+    return guarded([&]() -> tl_status {
+        if (!layer_ok(T, K, n)) return refuse(TL_ERR_INVALID, "T must be >= 0, K and n >= 1, all below 2^30");
+        if (!dx_dev && !dw_dev) return refuse(TL_ERR_INVALID, "neither dx nor dw is wanted");
+        if (T == 0)
+            return dw_dev ? tiled_linear_fp8_gemm_dw(T, K, n, 0, nullptr, 0, nullptr, 0, nullptr, 0, nullptr, dw_dev, lddw,
+                                                     err_dev, stream)
+                          : TL_OK;
+        if (!workspace_ok(workspace_dev, workspace_bytes, tiled_linear_fp8_linear_backward_workspace_bytes(T, K, n)))
+            return refuse(TL_ERR_WORKSPACE, "workspace is null, not 256-byte aligned or too small");
+        Held dy_row(T, n, true), dy_col(T, n, false), x_col(T, K, false);
+        x_col.place(dy_col.place(dy_row.place(static_cast<uint8_t*>(workspace_dev))));
+        const auto form = [](const Held& h, bool own_is_row, int64_t cols) {
+            return operand(own_is_row, false, cols, h.form.q, h.form.ldq, h.form.scale, TL_FP8_E4M3);
+        };
+        // everything is checked before anything is enqueued
+        const Fp8GemmDesc gx = product(T, K, n, form(dy_row, true, n), operand(true, true, n, w_q, ldw, w_scale, w_format),
+                                       dx_dev, lddx, err_dev);
+        const Fp8GemmDesc gw = product(K, n, T, form(x_col, false, K), form(dy_col, false, n), dw_dev, lddw, err_dev);
+        std::string bad = dx_dev ? fp8_gemm_check(gx) : std::string();
+        if (bad.empty() && dw_dev) bad = fp8_gemm_check(gw);
+        if (bad.empty() && dw_dev && (!x_dev || ldx < K)) bad = "x is null or its leading dimension is smaller than K";
+        if (!bad.empty()) return refuse(TL_ERR_INVALID, bad);
+        tl_status st = quantize(T, n, type, dy_dev, lddy, dx_dev ? &dy_row.form : nullptr, dw_dev ? &dy_col.form : nullptr, stream);
+        if (st == TL_OK && dx_dev) st = launch_product(gx, stream);
+        if (st == TL_OK && dw_dev) st = quantize(T, K, type, x_dev, ldx, nullptr, &x_col.form, stream);
+        if (st == TL_OK && dw_dev) st = launch_product(gw, stream);
+        return st;
     });
 }
 

@@ -177,6 +177,14 @@ def load():
         for name in ("tiled_linear_fp8_gemm_forward", "tiled_linear_fp8_gemm_dx", "tiled_linear_fp8_gemm_dw"):
             getattr(L, name).argtypes = [i64, i64, i64] + [i32, vp, i64, vp] * 2 + [vp, i64, vp, vp]
             getattr(L, name).restype = st
+        for name in ("tiled_linear_fp8_linear_workspace_bytes", "tiled_linear_fp8_linear_backward_workspace_bytes"):
+            getattr(L, name).argtypes = [i64, i64, i64]
+            getattr(L, name).restype = sz
+        L.tiled_linear_fp8_linear.argtypes = [i64, i64, i64, i32, vp, i64, i32, vp, i64, vp, vp, i64, vp, sz, vp, vp]
+        L.tiled_linear_fp8_linear.restype = st
+        L.tiled_linear_fp8_linear_backward.argtypes = [i64, i64, i64, i32, vp, i64, vp, i64, i32, vp, i64, vp, vp, i64,
+                                                       vp, i64, vp, sz, vp, vp]
+        L.tiled_linear_fp8_linear_backward.restype = st
         L.tiled_linear_host_alloc.argtypes = [sz, ctypes.POINTER(vp)]
         L.tiled_linear_host_alloc.restype = st
         L.tiled_linear_host_free.argtypes = [vp]
@@ -442,6 +450,27 @@ def tiled_linear_fp8_gemm_dw(T, K, n, x_format, x_q, ldx, x_scale, dy_format, dy
                              stream) -> None:
     _check(load().tiled_linear_fp8_gemm_dw(T, K, n, x_format, x_q, ldx, x_scale, dy_format, dy_q, lddy, dy_scale, dw,
                                            lddw, err, stream), "tiled_linear_fp8_gemm_dw")
+
+
+def tiled_linear_fp8_linear_workspace_bytes(T: int, K: int, n: int) -> int:
+    return int(load().tiled_linear_fp8_linear_workspace_bytes(T, K, n))
+
+
+def tiled_linear_fp8_linear(T, K, n, type, x, ldx, w_format, w_q, ldw, w_scale, y, ldy, workspace, workspace_bytes, err,
+                            stream) -> None:
+    _check(load().tiled_linear_fp8_linear(T, K, n, type, x, ldx, w_format, w_q, ldw, w_scale, y, ldy, workspace,
+                                          workspace_bytes, err, stream), "tiled_linear_fp8_linear")
+
+
+def tiled_linear_fp8_linear_backward_workspace_bytes(T: int, K: int, n: int) -> int:
+    return int(load().tiled_linear_fp8_linear_backward_workspace_bytes(T, K, n))
+
+
+def tiled_linear_fp8_linear_backward(T, K, n, type, x, ldx, dy, lddy, w_format, w_q, ldw, w_scale, dx, lddx, dw, lddw,
+                                     workspace, workspace_bytes, err, stream) -> None:
+    _check(load().tiled_linear_fp8_linear_backward(T, K, n, type, x, ldx, dy, lddy, w_format, w_q, ldw, w_scale, dx,
+                                                   lddx, dw, lddw, workspace, workspace_bytes, err, stream),
+           "tiled_linear_fp8_linear_backward")
 
 
 def tiled_linear_host_alloc(nbytes: int) -> int:
@@ -1030,12 +1059,31 @@ def fp8_linear(x, wq, ws):
     """y [T, n] bf16 = x [T, K] . w with w in 8 bits (``fp8_quantize(w, "tile")``);
     x (bf16, fp16 or fp32) is quantised on the way, with a scale for each 128
     columns of a row."""
-    return fp8_matmul(fp8_quantize(x, "row"), (wq, ws))
+    torch, where = _t(), "fp8_linear"
+    ldx, T, device, (K, n) = _ld(x, where, "x"), x.shape[0], x.device, _weight_shape(wq, where)
+    if x.shape[1] != K or device != wq.device:
+        _refuse(where, "x and the weight do not fit each other")
+    kind, stream, w = _type_of(x, where), _stream_of(device, where), _fp8_operand(wq, ws, "tile", where, "the weight")
+    y, ldy = _fp8_result(x, T, n)
+    need = tiled_linear_fp8_linear_workspace_bytes(T, K, n)
+    work = x.new_empty(need, dtype=torch.uint8)
+    tiled_linear_fp8_linear(T, K, n, kind, x.data_ptr(), ldx, *w, y.data_ptr(), ldy, work.data_ptr(), need,
+                            _err_word(device), stream)
+    return y
 
 
 def fp8_linear_backward(x, dy, wq, ws):
     """(dx [T, K], dw [K, n]) bf16 of ``fp8_linear`` for dy [T, n], as products in 8
     bits: dy . w^T with dy's rows in blocks of 128, x^T . dy with blocks of 128
     tokens.  (The derivative passes through the rounding to 8 bits.)"""
-    dy_row, dy_col = fp8_quantize(dy, "row", "col")
-    return fp8_matmul_dx(dy_row, (wq, ws)), fp8_matmul_dw(fp8_quantize(x, "col"), dy_col)
+    torch, where = _t(), "fp8_linear_backward"
+    ldx, lddy, T, device, (K, n) = _ld(x, where, "x"), _ld(dy, where, "dy"), x.shape[0], x.device, _weight_shape(wq, where)
+    if x.shape[1] != K or dy.shape != (T, n) or dy.dtype != x.dtype or device != wq.device or dy.device != device:
+        _refuse(where, "x, dy and the weight do not fit each other")
+    kind, stream, w = _type_of(x, where), _stream_of(device, where), _fp8_operand(wq, ws, "tile", where, "the weight")
+    (dx, lddx), (dw, lddw) = _fp8_result(x, T, K), _fp8_result(x, K, n)
+    need = tiled_linear_fp8_linear_backward_workspace_bytes(T, K, n)
+    work = x.new_empty(need, dtype=torch.uint8)
+    tiled_linear_fp8_linear_backward(T, K, n, kind, x.data_ptr(), ldx, dy.data_ptr(), lddy, *w, dx.data_ptr(), lddx,
+                                     dw.data_ptr(), lddw, work.data_ptr(), need, _err_word(device), stream)
+    return dx, dw
