@@ -624,6 +624,27 @@ tl_status tiled_linear_fp8_linear_backward(int64_t T, int64_t K, int64_t n, int3
                                            int64_t lddx, void *dw_dev, int64_t lddw, void *workspace_dev,
                                            size_t workspace_bytes, int32_t *err_dev, void *stream);
 
+/* --- orthogonalising an update ----------------------------------------------
+ * For each of `batch` matrices G [rows, cols] (tl_type, ld ldg, g_apart elements
+ * from one to the next), by Newton-Schulz products, as an optimizer does with a
+ * weight's momentum:
+ *   X = G / (|G|_F + eps);  steps times:  P = X X^T,  X = a X + (b P + c P^2) X
+ *   out = bf16(scale X)    (ld ldo, o_apart apart)
+ * where rows > cols the products are formed on the other side, with the same
+ * result.  The iterate is fp32; the products take it in fp16 (scaled by 2^8, so
+ * its elements must stay below 255: a, b, c that keep the singular values near
+ * one do) and sum in fp32.  1 <= steps <= 100; the matrices are independent of
+ * each other.  out may be G.  The order of all sums depends on the sizes alone.
+ * out is 16-byte aligned, ldo and o_apart multiples of 8.  workspace: 256-byte
+ * aligned, tiled_linear_orthogonalize_workspace_bytes (0 if the sizes are
+ * invalid).  batch = 0 is a no-op.
+ * Errors: TL_ERR_INVALID, TL_ERR_WORKSPACE, TL_ERR_CUDA. */
+size_t tiled_linear_orthogonalize_workspace_bytes(int64_t batch, int64_t rows, int64_t cols);
+tl_status tiled_linear_orthogonalize(int64_t batch, int64_t rows, int64_t cols, int32_t type, const void *g_dev,
+                                     int64_t ldg, int64_t g_apart, int32_t steps, float a, float b, float c, float eps,
+                                     float scale, void *out_dev, int64_t ldo, int64_t o_apart, void *workspace_dev,
+                                     size_t workspace_bytes, int32_t *err_dev, void *stream);
+
 /* --- pinned host memory helpers ------------------------------------------ */
 /* Page-locked host allocation (cudaHostAlloc, portable); *out = NULL on
  * failure.  Free with tiled_linear_host_free. */

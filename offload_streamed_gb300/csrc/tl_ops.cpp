@@ -5,6 +5,7 @@
 #include "tl_fp8.h"
 #include "tl_launch.h"
 #include "tl_norm.h"
+#include "tl_ortho.h"
 #include "tl_unbound_error.h"
 
 #include <algorithm>
@@ -337,6 +338,48 @@ tl_status tiled_linear_fp8_linear_backward(int64_t T, int64_t K, int64_t n, int3
         if (st == TL_OK && dw_dev) st = quantize(T, K, type, x_dev, ldx, nullptr, &x_col.form, stream);
         if (st == TL_OK && dw_dev) st = launch_product(gw, stream);
         return st;
+    });
+}
+
+size_t tiled_linear_orthogonalize_workspace_bytes(int64_t batch, int64_t rows, int64_t cols) {
+    return ortho_workspace(batch, rows, cols);
+}
+
+tl_status tiled_linear_orthogonalize(int64_t batch, int64_t rows, int64_t cols, int32_t type, const void* g_dev,
+                                     int64_t ldg, int64_t g_apart, int32_t steps, float a, float b, float c, float eps,
+                                     float scale, void* out_dev, int64_t ldo, int64_t o_apart, void* workspace_dev,
+                                     size_t workspace_bytes, int32_t* err_dev, void* stream) {
+    return guarded([&]() -> tl_status {
+        OrthoDesc d;
+        d.batch = batch;
+        d.rows = rows;
+        d.cols = cols;
+        d.type = type;
+        d.g = g_dev;
+        d.ldg = ldg;
+        d.g_apart = g_apart;
+        d.steps = steps;
+        d.a = a;
+        d.b = b;
+        d.c = c;
+        d.eps = eps;
+        d.scale = scale;
+        d.out = out_dev;
+        d.ldo = ldo;
+        d.o_apart = o_apart;
+        d.workspace = workspace_dev;
+        d.err = err_dev;
+        const std::string bad = ortho_check(d);
+        if (!bad.empty()) return refuse(TL_ERR_INVALID, bad);
+        if (batch == 0) return TL_OK;
+        if (!workspace_ok(workspace_dev, workspace_bytes, ortho_workspace(batch, rows, cols)))
+            return refuse(TL_ERR_WORKSPACE, "workspace is null, not 256-byte aligned or too small");
+        const int sms = device_sms();
+        if (sms < 2) return refuse(TL_ERR_CUDA, "no current device");
+        std::string why;
+        const cudaError_t e = ortho_launch(d, sms, static_cast<cudaStream_t>(stream), &why);
+        if (e == cudaSuccess) return TL_OK;
+        return refuse(TL_ERR_CUDA, why.empty() ? std::string("orthogonalize: ") + cudaGetErrorString(e) : why);
     });
 }
 

@@ -185,6 +185,11 @@ def load():
         L.tiled_linear_fp8_linear_backward.argtypes = [i64, i64, i64, i32, vp, i64, vp, i64, i32, vp, i64, vp, vp, i64,
                                                        vp, i64, vp, sz, vp, vp]
         L.tiled_linear_fp8_linear_backward.restype = st
+        L.tiled_linear_orthogonalize_workspace_bytes.argtypes = [i64, i64, i64]
+        L.tiled_linear_orthogonalize_workspace_bytes.restype = sz
+        L.tiled_linear_orthogonalize.argtypes = [i64, i64, i64, i32, vp, i64, i64, i32] + [ctypes.c_float] * 5 + \
+            [vp, i64, i64, vp, sz, vp, vp]
+        L.tiled_linear_orthogonalize.restype = st
         L.tiled_linear_host_alloc.argtypes = [sz, ctypes.POINTER(vp)]
         L.tiled_linear_host_alloc.restype = st
         L.tiled_linear_host_free.argtypes = [vp]
@@ -471,6 +476,17 @@ def tiled_linear_fp8_linear_backward(T, K, n, type, x, ldx, dy, lddy, w_format, 
     _check(load().tiled_linear_fp8_linear_backward(T, K, n, type, x, ldx, dy, lddy, w_format, w_q, ldw, w_scale, dx,
                                                    lddx, dw, lddw, workspace, workspace_bytes, err, stream),
            "tiled_linear_fp8_linear_backward")
+
+
+def tiled_linear_orthogonalize_workspace_bytes(batch: int, rows: int, cols: int) -> int:
+    return int(load().tiled_linear_orthogonalize_workspace_bytes(batch, rows, cols))
+
+
+def tiled_linear_orthogonalize(batch, rows, cols, type, g, ldg, g_apart, steps, a, b, c, eps, scale, out, ldo, o_apart,
+                               workspace, workspace_bytes, err, stream) -> None:
+    _check(load().tiled_linear_orthogonalize(batch, rows, cols, type, g, ldg, g_apart, steps, a, b, c, eps, scale, out,
+                                             ldo, o_apart, workspace, workspace_bytes, err, stream),
+           "tiled_linear_orthogonalize")
 
 
 def tiled_linear_host_alloc(nbytes: int) -> int:
@@ -1087,3 +1103,32 @@ def fp8_linear_backward(x, dy, wq, ws):
     tiled_linear_fp8_linear_backward(T, K, n, kind, x.data_ptr(), ldx, dy.data_ptr(), lddy, *w, dx.data_ptr(), lddx,
                                      dw.data_ptr(), lddw, work.data_ptr(), need, _err_word(device), stream)
     return dx, dw
+
+
+def orthogonalize(g, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315), eps: float = 1e-7, scale: float = 1.0):
+    """bf16 scale * X, X the matrix g (or each matrix of g [batch, rows, cols]; bf16,
+    fp16 or fp32) after `steps` Newton-Schulz steps X = a X + (b P + c P^2) X,
+    P = X X^T, from g / (|g|_F + eps): its singular values drawn to about one."""
+    torch, where = _t(), "orthogonalize"
+    if not g.is_cuda or g.dim() not in (2, 3):
+        _refuse(where, "g must be a matrix or a stack of matrices on a CUDA device")
+    device = g.device
+    kind, stream = _type_of(g, where), _stream_of(device, where)
+    stack = g if g.dim() == 3 else g.unsqueeze(0)
+    batch, rows, cols = stack.shape
+    if rows < 1 or cols < 1:
+        _refuse(where, "the matrices have no elements")
+    apart, ldg, step = stack.stride()
+    if (cols > 1 and step != 1) or (rows > 1 and ldg < cols):
+        _refuse(where, "the rows of g are not contiguous")
+    ldg = ldg if rows > 1 else cols
+    ldo = _up(cols, 8)
+    out = g.new_empty((batch, rows, ldo), dtype=torch.bfloat16)
+    need = tiled_linear_orthogonalize_workspace_bytes(batch, rows, cols)
+    work = g.new_empty(need, dtype=torch.uint8)
+    a, b, c = coefficients
+    tiled_linear_orthogonalize(batch, rows, cols, kind, stack.data_ptr(), ldg, apart if batch > 1 else 0, steps, a, b, c,
+                               eps, scale, out.data_ptr(), ldo, rows * ldo, work.data_ptr(), need, _err_word(device),
+                               stream)
+    out = out if ldo == cols else out[:, :, :cols]
+    return out if g.dim() == 3 else out[0]
