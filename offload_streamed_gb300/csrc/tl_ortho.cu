@@ -12,6 +12,12 @@
 // are symmetric, so only the tiles on and above the diagonal are computed and
 // each is written twice, once mirrored.
 //
+// Two kernels share the work: large products go through CTA pairs with 256 x 256
+// tiles, products of few such tiles through single CTAs with 128 x 128 tiles, a
+// cluster of them sharing a reduction.  The launches follow each other closely:
+// each may begin while the one before it ends, and waits for that one's results
+// before it reads any.
+//
 // Numbers.  The iterate X is held in fp32; the products take it in fp16, whose
 // 11 bits keep the result's error well under that of its own rounding to bf16
 // (in bf16 operands it would be several times larger).  P is near the identity
@@ -59,6 +65,29 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t sr
                  "r"(src), "r"(x), "r"(y), "r"(z)
                  : "memory");
 }
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x, int32_t y, int32_t z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t local, uint32_t rank) {
+    float4 v;
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\t"
+        "mapa.shared::cluster.u32 a, %4, %5;\n\t"
+        "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
+        : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+        : "r"(local), "r"(rank)
+        : "memory");
+    return v;
+}
+// The launch before this one is complete and its results visible; and the next
+// one may begin.
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_dependents_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // kind::f16 with fp16 operands (formats 0) and fp32 sums.
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int m, int n, bool a_mn, bool b_mn) {
     return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | (uint32_t(n >> 3) << 17) | (uint32_t(m >> 4) << 24);
@@ -72,6 +101,9 @@ struct OrthoParams {
     const __half* e;  // SQUARE: E, ld and distance of a matrix
     float* x;         // UPDATE, LAST: the iterate
     int64_t ld, apart;
+    void* out;        // small products: E, Q, X in fp16 or the bf16 result
+    int64_t ldo, o_apart;
+    int32_t splits, per;
     int32_t* err;
     uint64_t timeout_ns;
 };
@@ -242,6 +274,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
+    grid_dependents_go();
+    grid_dependency_wait();
 
     if (warp == 0) {
         if (lane == 0) {
@@ -353,9 +387,239 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
+// ---- small products ----------------------------------------------------------------
+// One 128 x 128 tile a cluster; its CTAs have a part of the reduction each, leave
+// their sums in shared memory, and each finishes some of the tile's rows from all
+// of them, in a fixed order.
+constexpr int kSmallStages = 3;
+constexpr int kPartLd = 132;  // floats of a row of sums: 16-byte accesses of a column of lanes meet no bank twice
+constexpr int kTurnLd = 40;   // halves of a row of the turned tile
+constexpr uint32_t kTurn = 128 * kPartLd * 4;  // where the turned tile is, after the sums
+constexpr size_t kSmallSmem = size_t(kSmallStages) * 2 * kHalfStage + kBarBytes + 1024;
+static_assert(size_t(kTurn) + 128 * kTurnLd * 2 <= size_t(kSmallStages) * 2 * kHalfStage, "sums and turned tile fit the stages");
+
+template <bool A_MN, bool B_MN, int MODE>
+__global__ void __launch_bounds__(kThreads, 2)
+    ortho_small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const OrthoParams p) {
+    const WaitCtx wc{p.err, p.timeout_ns};
+    constexpr int S = kSmallStages;
+    constexpr uint32_t kStage = 2 * kHalfStage;
+    constexpr bool SYM = MODE == GRAM || MODE == SQUARE;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t smem0 = smem_addr(smem);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S * kStage);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 1);
+    const uint32_t bar0 = smem_addr(bars);
+    auto full_bar = [&](uint32_t s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](uint32_t s) { return bar0 + 8u * (S + s); };
+    const uint32_t done_bar = bar0 + 8u * (2 * S);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = p.splits > 1 ? cluster_ctarank() : 0;
+    const int tile = int(blockIdx.x / uint32_t(p.splits));
+    const int b = tile / p.per_matrix;
+    int mb, nb;
+    if constexpr (SYM) {
+        triangle_coords(tile - b * p.per_matrix, p.num_n, mb, nb);
+    } else {
+        mb = (tile - b * p.per_matrix) / p.num_n;
+        nb = tile - b * p.per_matrix - mb * p.num_n;
+    }
+    const int m0 = mb * 128, n0 = nb * 128;
+    const int kb0 = int(rank) * p.per, kb1 = min(p.num_k, kb0 + p.per);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(full_bar(s), 1);
+            mbar_init(empty_bar(s), 1);
+        }
+        mbar_init(done_bar, 1);
+        mbar_init_fence();
+    }
+    if (warp == 2) {
+        tmem_alloc<false>(smem_addr(tmem_slot), 128);
+        tmem_relinquish<false>();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    grid_dependents_go();
+    grid_dependency_wait();
+
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t fills = 0;
+            for (int kb = kb0; kb < kb1; ++kb, ++fills) {
+                const uint32_t s = fills % S;
+                if (!wait_bounded(empty_bar(s), ((fills / S) & 1u) ^ 1u, wc, kErrProducerWait)) break;
+                const uint32_t sa = smem0 + s * kStage, sb = sa + kHalfStage, fb = full_bar(s);
+                const int k0 = kb * kBlockK;
+                mbar_arrive_expect_tx(fb, kStage);
+                if (A_MN) {
+                    tma_load_3d(sa, &map_a, fb, m0, k0, b);
+                    tma_load_3d(sa + kMnChunk, &map_a, fb, m0 + 64, k0, b);
+                } else {
+                    tma_load_3d(sa, &map_a, fb, k0, m0, b);
+                }
+                if (B_MN) {
+                    tma_load_3d(sb, &map_b, fb, n0, k0, b);
+                    tma_load_3d(sb + kMnChunk, &map_b, fb, n0 + 64, k0, b);
+                } else {
+                    tma_load_3d(sb, &map_b, fb, k0, n0, b);
+                }
+            }
+            const uint32_t outstanding = fills < uint32_t(S) ? fills : uint32_t(S);
+            for (uint32_t j = 0; j < outstanding; ++j) {
+                const uint32_t f = fills - 1 - j;
+                wait_bounded(full_bar(f % S), (f / S) & 1u, wc, kErrDrainWait, false);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t idesc = idesc_f16_f32(128, 128, A_MN, B_MN);
+            uint32_t fills = 0;
+            for (int kb = kb0; kb < kb1; ++kb, ++fills) {
+                const uint32_t s = fills % S;
+                if (!wait_bounded(full_bar(s), (fills / S) & 1u, wc, kErrMmaWaitFull)) break;
+                tc_fence_after();
+                const uint32_t sa = smem0 + s * kStage, sb = sa + kHalfStage;
+#pragma unroll
+                for (int j = 0; j < kBlockK / kUmmaK; ++j)
+                    umma_bf16(tmem_base, operand_desc(A_MN, sa, j), operand_desc(B_MN, sb, j), idesc, (kb != kb0 || j) ? 1u : 0u);
+                umma_commit(empty_bar(s));
+            }
+            umma_commit(done_bar);
+            wait_bounded(done_bar, 0, wc, kErrDrainWait, false);
+        }
+    } else if (warp >= kFirstEpilogueWarp) {
+        const int q = warp & 3, i = q * 32 + lane;
+        const bool ok = warp_wait(done_bar, 0, wc, kErrEpilogueWait, lane);
+        tc_fence_after();
+        if (ok)
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 32) {
+                uint32_t v[32];
+                tmem_ld_32cols(tmem_base + (uint32_t(q * 32) << 16) + uint32_t(c), v);
+                tmem_ld_wait();
+                const bool any = kb1 > kb0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    st_shared_v4(smem0 + uint32_t(i * kPartLd + c + 4 * j) * 4u, any ? v[4 * j] : 0u, any ? v[4 * j + 1] : 0u,
+                                 any ? v[4 * j + 2] : 0u, any ? v[4 * j + 3] : 0u);
+            }
+        tc_fence_before();
+    }
+    // This CTA finishes rows [r0, r0 + rows) of the tile, 32 at a time (what the
+    // turned tile holds); a thread has four columns of every eighth row.  What
+    // those elements need from global memory is asked for before the CTAs meet.
+    constexpr int kPer = 4;
+    const int rows = 128 / p.splits, r0 = int(rank) * rows;
+    const int c = lane * 4, col = n0 + c;
+    uint4 mem[kPer];
+    auto in = [&](int r) { return r < r0 + rows && m0 + r < p.m_dim && col < p.n_dim; };
+    auto fetch = [&](int base) {
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) {
+            const int r = base + warp + 8 * u;
+            const int64_t at = int64_t(b) * p.apart + int64_t(m0 + r) * p.ld + col;
+            mem[u] = make_uint4(0, 0, 0, 0);
+            if constexpr (MODE == SQUARE) {
+                if (in(r)) {
+                    const uint2 e = *reinterpret_cast<const uint2*>(p.e + at);
+                    mem[u].x = e.x;
+                    mem[u].y = e.y;
+                }
+            } else if constexpr (MODE == UPDATE || MODE == LAST) {
+                if (in(r)) mem[u] = *reinterpret_cast<const uint4*>(p.x + at);
+            }
+        }
+    };
+    fetch(r0);
+    if (p.splits > 1) cluster_sync(); else __syncthreads();
+
+    __half* turn = reinterpret_cast<__half*>(smem + kTurn);
+    const bool mirrored = SYM && mb != nb;
+    for (int base = r0; base < r0 + rows; base += 32) {
+        if (base > r0) fetch(base);
+        const int have = min(32, r0 + rows - base);
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) {
+            const int r = base + warp + 8 * u;
+            if (r >= r0 + rows) break;
+            const uint32_t at = smem0 + uint32_t(r * kPartLd + c) * 4u;
+            float4 v[8];
+#pragma unroll
+            for (int t = 0; t < 8; ++t)
+                if (t < p.splits) v[t] = ld_cluster_f32x4(at, uint32_t(t));
+            float4 acc = v[0];
+#pragma unroll
+            for (int t = 1; t < 8; ++t)
+                if (t < p.splits) acc = make_float4(acc.x + v[t].x, acc.y + v[t].y, acc.z + v[t].z, acc.w + v[t].w);
+            const int row = m0 + r;
+            float f[4] = {acc.x, acc.y, acc.z, acc.w};
+            if constexpr (MODE == GRAM) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) f[j] = (f[j] * (kDown * kDown) - (row == col + j ? 1.0f : 0.0f)) * kUp;
+            } else if constexpr (MODE == SQUARE) {
+                const float2 e0 = __half22float2(*reinterpret_cast<const __half2*>(&mem[u].x));
+                const float2 e1 = __half22float2(*reinterpret_cast<const __half2*>(&mem[u].y));
+                const float e[4] = {e0.x, e0.y, e1.x, e1.y};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) f[j] = p.k1 * e[j] + p.k2 * (f[j] * kDown);
+            } else {
+                const float x[4] = {__uint_as_float(mem[u].x), __uint_as_float(mem[u].y), __uint_as_float(mem[u].z), __uint_as_float(mem[u].w)};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) f[j] = p.k0 * x[j] + f[j] * (kDown * kDown);
+            }
+            uint2 w;
+            if constexpr (MODE == LAST)
+                w = make_uint2(pack_bf16x2(f[0] * p.scale, f[1] * p.scale), pack_bf16x2(f[2] * p.scale, f[3] * p.scale));
+            else if constexpr (MODE == UPDATE)
+                w = make_uint2(pack_f16x2(f[0] * kUp, f[1] * kUp), pack_f16x2(f[2] * kUp, f[3] * kUp));
+            else
+                w = make_uint2(pack_f16x2(f[0], f[1]), pack_f16x2(f[2], f[3]));
+            const uint16_t h[4] = {uint16_t(w.x & 0xffffu), uint16_t(w.x >> 16), uint16_t(w.y & 0xffffu), uint16_t(w.y >> 16)};
+            // (rows of E, Q and X are padded to 8 elements: four at a time stay
+            // inside them; the padding of the result's rows is the caller's)
+            if (in(r)) {
+                if constexpr (MODE == UPDATE)
+                    *reinterpret_cast<float4*>(p.x + int64_t(b) * p.apart + int64_t(row) * p.ld + col) = make_float4(f[0], f[1], f[2], f[3]);
+                uint16_t* dst = static_cast<uint16_t*>(p.out) + int64_t(b) * p.o_apart + int64_t(row) * p.ldo + col;
+                if (MODE != LAST || col + 4 <= p.n_dim) *reinterpret_cast<uint2*>(dst) = w;
+                else
+                    for (int j = 0; col + j < p.n_dim; ++j) dst[j] = h[j];
+            }
+            if (mirrored) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) reinterpret_cast<uint16_t*>(turn)[(c + j) * kTurnLd + (r - base)] = h[j];
+            }
+        }
+        if (mirrored) {
+            __syncthreads();
+            // column i of these rows is row n0 + i of the result, from column m0 + base on
+            for (int idx = int(threadIdx.x); idx < 128 * (have / 8); idx += kThreads) {
+                const int i = idx / (have / 8), g = idx % (have / 8) * 8;
+                const int row = n0 + i, at = m0 + base + g;
+                if (row < p.n_dim && at < p.m_dim)
+                    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + int64_t(b) * p.o_apart + int64_t(row) * p.ldo + at) =
+                        *reinterpret_cast<const uint4*>(turn + i * kTurnLd + g);
+            }
+            __syncthreads();
+        }
+    }
+    if (p.splits > 1) cluster_sync();  // nobody leaves while its sums are read
+    else __syncthreads();
+    if (warp == 2) {
+        tc_fence_after();
+        tmem_dealloc<false>(tmem_base, 128);
+    }
+}
+
 // ---- the norm and the first iterate ----------------------------------------------
 constexpr int kNormThreads = 256;
-constexpr int kNormParts = 128;  // partial sums of squares a matrix
+constexpr int kNormParts = 256;  // partial sums of squares a matrix
 
 struct StartArgs {
     const void* g;
@@ -382,14 +646,28 @@ __device__ __forceinline__ float block_sum(float v) {
     return sum;
 }
 
-// Walk over the vectors of a matrix that this CTA (of `parts`) has: f(row, col, vector).
+// Walk over the vectors of a matrix that this CTA (of `parts`) has, four loads
+// at a time: f(row, col, vector).
 template <typename T, int VEC, typename F>
 __device__ __forceinline__ void each_vector(const StartArgs& p, int part, int parts, F&& f) {
     const T* g = static_cast<const T*>(p.g) + int64_t(blockIdx.y) * p.g_apart;
-    const int64_t per_row = p.cols / VEC, n = p.rows * per_row;
-    for (int64_t i = int64_t(part) * kNormThreads + threadIdx.x; i < n; i += int64_t(parts) * kNormThreads) {
-        const int64_t r = i / per_row, c = (i - r * per_row) * VEC;
-        f(r, c, *reinterpret_cast<const Vec<T, VEC>*>(g + r * p.ldg + c));
+    const uint32_t per_row = uint32_t(p.cols / VEC);
+    const uint64_t n = uint64_t(p.rows) * per_row, step = uint64_t(parts) * kNormThreads;
+    for (uint64_t i0 = uint64_t(part) * kNormThreads + threadIdx.x; i0 < n; i0 += 4 * step) {
+        Vec<T, VEC> v[4];
+        uint32_t r[4], c[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint64_t i = i0 + k * step;
+            if (i >= n) continue;
+            // (a 32-bit division where the index allows it)
+            r[k] = n <= 0xffffffffull ? uint32_t(i) / per_row : uint32_t(i / per_row);
+            c[k] = uint32_t(i - uint64_t(r[k]) * per_row) * VEC;
+            v[k] = *reinterpret_cast<const Vec<T, VEC>*>(g + int64_t(r[k]) * p.ldg + c[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (i0 + k * step < n) f(int64_t(r[k]), int64_t(c[k]), v[k]);
     }
 }
 
@@ -501,6 +779,33 @@ struct Half {
     int64_t inner, outer, ld, apart;
 };
 
+cudaError_t launch(const void* kern, int grid, int cluster, size_t smem, cudaStream_t stream, void** args) {
+    int per_sm = 0;
+    const cudaError_t e = ctas_per_sm(kern, kThreads, smem, &per_sm);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(unsigned(grid));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = unsigned(cluster);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelExC(&cfg, kern, args);
+}
+
+// Products of up to a quarter as many 256 x 256 tiles as there are CTA pairs go
+// through the small kernel.  The whole update, us, by pairs alone / with this
+// rule / with one twice as wide: 512 x 512 166 / 134 / 135, 128 x 512 116 /
+// 107 / 107, 1024 x 4096 279 / 257 / 261, 2048 x 2048 290 / 291 / 310.
+bool small_product(int64_t pair_tiles, int num_sms) { return pair_tiles <= num_sms / 8; }
+
 template <bool A_MN, bool B_MN, int MODE>
 cudaError_t product(const Half& a, const Half& b, int64_t m, int64_t n, int64_t k, const OutMaps& maps, OrthoParams p, int64_t batch,
                     int num_sms, cudaStream_t stream, std::string* why) {
@@ -508,38 +813,37 @@ cudaError_t product(const Half& a, const Half& b, int64_t m, int64_t n, int64_t 
     if (!swizzled_map(&ma, kF16, 2, a.p, uint64_t(a.inner), uint64_t(a.outer), uint64_t(a.ld), A_MN ? 64 : 128, why, uint64_t(batch), uint64_t(a.apart)) ||
         !swizzled_map(&mb, kF16, 2, b.p, uint64_t(b.inner), uint64_t(b.outer), uint64_t(b.ld), B_MN ? 64 : 128, why, uint64_t(batch), uint64_t(b.apart)))
         return cudaErrorInvalidValue;
+    const bool sym = MODE == GRAM || MODE == SQUARE;
+    auto tiles = [&](int64_t side) {
+        p.num_m = int32_t((m + side - 1) / side);
+        p.num_n = int32_t((n + side - 1) / side);
+        return sym ? int64_t(p.num_n) * (p.num_n + 1) / 2 : int64_t(p.num_m) * p.num_n;
+    };
     p.m_dim = int32_t(m);
     p.n_dim = int32_t(n);
-    p.num_m = int32_t((m + 255) / 256);
-    p.num_n = int32_t((n + 255) / 256);
     p.num_k = int32_t((k + kBlockK - 1) / kBlockK);
-    const bool sym = MODE == GRAM || MODE == SQUARE;
-    const int64_t per = sym ? int64_t(p.num_n) * (p.num_n + 1) / 2 : int64_t(p.num_m) * p.num_n;
-    if (per * batch > INT32_MAX) {
+    const bool small = small_product(tiles(256) * batch, num_sms);
+    const int64_t per = tiles(small ? 128 : 256);
+    if (per * batch > INT32_MAX / 8) {
         if (why) *why = "too many output tiles";
         return cudaErrorInvalidValue;
     }
     p.per_matrix = int32_t(per);
     p.num_tiles = int32_t(per * batch);
+    OutMaps to = maps;
+    void* args[] = {&ma, &mb, &to, &p};
+    if (small) {
+        p.splits = 1;
+        while (p.splits < 8 && int64_t(p.num_tiles) * p.splits * 2 <= 2 * num_sms) p.splits *= 2;
+        p.per = (p.num_k + p.splits - 1) / p.splits;
+        void* few[] = {&ma, &mb, &p};
+        return launch(reinterpret_cast<const void*>(ortho_small_kernel<A_MN, B_MN, MODE>), p.num_tiles * p.splits, p.splits, kSmallSmem,
+                      stream, few);
+    }
     const int slots = std::max(1, num_sms / 2);
     choose_tile_order(k, 256, p.num_m, p.num_n, slots, &p.raster, &p.group, &p.stream_shared);
-    auto kern = ortho_kernel<A_MN, B_MN, MODE>;
-    int per_sm = 0;
-    cudaError_t e = ctas_per_sm(reinterpret_cast<const void*>(kern), kThreads, kOrthoSmem, &per_sm);
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(unsigned(2 * std::min(p.num_tiles, slots)));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kOrthoSmem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, ma, mb, maps, p);
+    return launch(reinterpret_cast<const void*>(ortho_kernel<A_MN, B_MN, MODE>), 2 * std::min(p.num_tiles, slots), 2, kOrthoSmem, stream,
+                  args);
 }
 
 }  // namespace
@@ -615,6 +919,9 @@ cudaError_t ortho_launch(const OrthoDesc& d, int num_sms, cudaStream_t stream, s
 
     for (int step = 0; step < d.steps && e == cudaSuccess; ++step) {
         const Half x{base + (step & 1 ? w.h1 : w.h0), d.cols, d.rows, w.ldx, w.x_apart};
+        p.out = base + w.e;
+        p.ldo = w.ldp;
+        p.o_apart = w.p_apart;
         const Half pe{base + w.e, w.r, w.r, w.ldp, w.p_apart}, pq{base + w.q, w.r, w.r, w.ldp, w.p_apart};
         e = tall ? product<true, true, GRAM>(x, x, w.r, w.r, w.c, gram, p, d.batch, num_sms, stream, why)
                  : product<false, false, GRAM>(x, x, w.r, w.r, w.c, gram, p, d.batch, num_sms, stream, why);
@@ -622,6 +929,7 @@ cudaError_t ortho_launch(const OrthoDesc& d, int num_sms, cudaStream_t stream, s
         p.e = static_cast<const __half*>(pe.p);
         p.ld = w.ldp;
         p.apart = w.p_apart;
+        p.out = base + w.q;
         e = product<false, false, SQUARE>(pe, pe, w.r, w.r, w.r, square, p, d.batch, num_sms, stream, why);
         if (e != cudaSuccess) break;
         p.x = reinterpret_cast<float*>(base + w.x);
@@ -629,6 +937,9 @@ cudaError_t ortho_launch(const OrthoDesc& d, int num_sms, cudaStream_t stream, s
         p.apart = w.x_apart;
         const bool end = step == d.steps - 1;
         const OutMaps& to = end ? last : update[step & 1];
+        p.out = end ? d.out : base + (step & 1 ? w.h0 : w.h1);
+        p.ldo = end ? d.ldo : w.ldx;
+        p.o_apart = end ? d.o_apart : w.x_apart;
         if (tall)
             e = end ? product<false, false, LAST>(x, pq, d.rows, d.cols, w.r, to, p, d.batch, num_sms, stream, why)
                     : product<false, false, UPDATE>(x, pq, d.rows, d.cols, w.r, to, p, d.batch, num_sms, stream, why);
