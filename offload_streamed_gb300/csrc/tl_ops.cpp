@@ -65,6 +65,7 @@ tl_status tiled_linear_norm_forward(int64_t rows, int64_t cols, int32_t type, co
         d.rstd = rstd_dev;
         const std::string bad = norm_check(d, false);
         if (!bad.empty()) return refuse(TL_ERR_INVALID, bad);
+        if (rows == 0) return TL_OK;
         const int sms = device_sms();
         if (sms < 1) return refuse(TL_ERR_CUDA, "no current device");
         return done(norm_forward_launch(d, sms, static_cast<cudaStream_t>(stream)), "layer norm");
