@@ -19,14 +19,22 @@
 // before it reads any.
 //
 // Numbers.  The iterate X is held in fp32; the products take it in fp16, whose
-// 11 bits keep the result's error well under that of its own rounding to bf16
-// (in bf16 operands it would be several times larger).  P is near the identity
-// in the steps that matter, so what is held and multiplied is E = P - 1, and
-//   a X + (b P + c P^2) X = (a + b + c) X + Q X,   Q = (b + 2c) E + c E^2:
-// with the usual coefficients b + 2c and a + b + c are small, and so is the
-// effect of rounding E and Q to fp16.  X, E and Q are scaled by 2^8 there, far
-// from fp16's subnormals; |X| <= 255 is needed, which singular values below
-// 255 ensure.  Sums are fp32 in tensor memory.
+// 11 bits keep the result's error under that of its own rounding to bf16 (in
+// bf16 operands it would be several times larger).  Once the singular values are
+// near one, P is near the identity, and what is held and multiplied is
+// E = P - s 1 with s = 1:
+//   a X + (b P + c P^2) X = (a + b s + c s^2) X + Q X,  Q = (b + 2 c s) E + c E^2.
+// With the usual coefficients both factors are small there, and so is the effect
+// of rounding E and Q to fp16.  While the singular values are small a X is most of
+// the result, and s = 0 leaves that part to the fp32 iterate.  So s follows the
+// square of one representative singular value, 1 / sqrt(R) at first, until that
+// is about one, and is 1 from there on (shift_of_step).  What the roundings but
+// the last to bf16 make of the result's norm, emulated, with this s / with s = 1 /
+// with s = 0 throughout: 256 x 256 0.7 / 1.1 / 1.5e-3, 512 x 512 with strong
+// directions 0.6 / 2.8 / 0.5e-3, 512 x 2048 0.4 / 0.9 / 1.4e-3.  X, E and Q are
+// scaled by 2^8 in fp16, far from its subnormals; |X| <= 255 is needed, which
+// singular values below 255 ensure.
+// Sums are fp32 in tensor memory.
 #include "tl_ortho.h"
 #include "tl_gemm.h"
 #include "tl_kernel_common.cuh"
@@ -38,6 +46,7 @@
 
 #include <algorithm>
 #include <climits>
+#include <cmath>
 
 namespace tl {
 namespace {
@@ -97,7 +106,7 @@ struct OrthoParams {
     int32_t m_dim, n_dim, num_k;
     int32_t num_m, num_n, per_matrix, num_tiles;  // tiles of a matrix and of all
     int32_t raster, group, stream_shared;
-    float k0, k1, k2, scale;
+    float shift, k0, k1, k2, scale;
     const __half* e;  // SQUARE: E, ld and distance of a matrix
     float* x;         // UPDATE, LAST: the iterate
     int64_t ld, apart;
@@ -173,7 +182,7 @@ __device__ __forceinline__ void ortho_columns(const OrthoParams& p, const OutMap
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
             const float acc = __uint_as_float(v[j]) * (kDown * kDown);  // the product itself
-            if constexpr (MODE == GRAM) f[j] = (row == c0 + j ? acc - 1.0f : acc) * kUp;
+            if constexpr (MODE == GRAM) f[j] = (row == c0 + j ? acc - p.shift : acc) * kUp;
             else if constexpr (MODE == SQUARE) f[j] = p.k1 * f[j] + p.k2 * (acc * kUp);
             else f[j] = p.k0 * f[j] + acc;
         }
@@ -561,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             float f[4] = {acc.x, acc.y, acc.z, acc.w};
             if constexpr (MODE == GRAM) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) f[j] = (f[j] * (kDown * kDown) - (row == col + j ? 1.0f : 0.0f)) * kUp;
+                for (int j = 0; j < 4; ++j) f[j] = (f[j] * (kDown * kDown) - (row == col + j ? p.shift : 0.0f)) * kUp;
             } else if constexpr (MODE == SQUARE) {
                 const float2 e0 = __half22float2(*reinterpret_cast<const __half2*>(&mem[u].x));
                 const float2 e1 = __half22float2(*reinterpret_cast<const __half2*>(&mem[u].y));
@@ -773,6 +782,19 @@ bool mirror_map(CUtensorMap* map, const void* base, uint64_t n, uint64_t ld, uin
     return r == CUDA_SUCCESS;
 }
 
+// s of each step: see the top of this file.
+struct Shift {
+    double sigma;
+    bool near = false;
+    explicit Shift(int64_t r) : sigma(1.0 / std::sqrt(double(r))) {}
+    float next(const OrthoDesc& d) {
+        const double v = std::min(1.0, sigma * sigma);
+        near = near || !(v < 0.8);
+        sigma = std::fabs(sigma * (d.a + sigma * sigma * (d.b + sigma * sigma * d.c)));
+        return near ? 1.0f : float(v);
+    }
+};
+
 // An operand of a product: `outer` rows of `inner` halves.
 struct Half {
     const void* p;
@@ -894,9 +916,6 @@ cudaError_t ortho_launch(const OrthoDesc& d, int num_sms, cudaStream_t stream, s
 
     const bool tall = d.rows > d.cols;
     OrthoParams p{};
-    p.k0 = d.a + d.b + d.c;
-    p.k1 = d.b + 2.0f * d.c;
-    p.k2 = d.c;
     p.scale = d.scale;
     p.err = d.err;
     p.timeout_ns = 2000000000ull;
@@ -917,7 +936,12 @@ cudaError_t ortho_launch(const OrthoDesc& d, int num_sms, cudaStream_t stream, s
     gram.wide = square.wide = last.wide = update[0].wide;  // not used there
     update[0].mirror = update[1].mirror = last.mirror = gram.mirror;
 
+    Shift shift(w.r);
     for (int step = 0; step < d.steps && e == cudaSuccess; ++step) {
+        p.shift = shift.next(d);
+        p.k0 = d.a + p.shift * (d.b + p.shift * d.c);
+        p.k1 = d.b + 2.0f * d.c * p.shift;
+        p.k2 = d.c;
         const Half x{base + (step & 1 ? w.h1 : w.h0), d.cols, d.rows, w.ldx, w.x_apart};
         p.out = base + w.e;
         p.ldo = w.ldp;

@@ -4,9 +4,9 @@ against the iteration in 64 bits.
 Tolerance, as a share of the result's norm, derived from the kernel's roundings:
  * the result to bf16: 2^-9 of each element at most, 2^-9 / sqrt(3) of the norm
    in the mean: 1.13e-3, taken whole, 2^-9 = 1.95e-3;
- * a step rounds X, E and Q to fp16 (2^-12 of the largest element of each, at
-   most); these enter the next iterate through at most |b + 2c| + 2 |c| |E| and
-   |Q|, together under 4 for singular values in 0..1.3: 4 * 3 * 2^-12 * 1/sqrt(3)
+ * a step rounds X, E = X X^T - s and Q to fp16 (2^-12 of the largest element of
+   each, at most); these enter the next iterate through at most |b + 2cs| + 2 |c| |E|
+   and |Q|, together under 4 for singular values in 0..1.3: 4 * 3 * 2^-12 * 1/sqrt(3)
    a step in the mean, and the map's slope there is at most about one in
    magnitude, so that the last steps' errors stay: sqrt(steps) of it at most:
    5 steps, 3.8e-3;
