@@ -500,6 +500,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int kb0 = int(rank) * per, kb1 = min(p.num_k, kb0 + per);  // this CTA's K-blocks, perhaps none
 
     if (threadIdx.x == 0) {
+        tma_prefetch_map(&map_w);
+        tma_prefetch_map(&map_t);
         for (int s = 0; s < S; ++s) {
             mbar_init(full_bar(s), 1);
             mbar_init(empty_bar(s), 1);

@@ -264,6 +264,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 
     if (threadIdx.x == 0) {
+        tma_prefetch_map(&map_a);
+        tma_prefetch_map(&map_b);
         for (int s = 0; s < S; ++s) {
             mbar_init(full_bar(s), 1);
             mbar_init(empty_bar(s), 1);
@@ -288,8 +290,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == 0) {
         if (lane == 0) {
-            tma_prefetch_map(&map_a);
-            tma_prefetch_map(&map_b);
             const uint64_t pol_n = l2_policy_evict_normal(), pol_s = p.stream_shared ? pol_n : l2_policy_evict_first();
             const uint64_t pol_a = SYM ? pol_n : p.raster == 0 ? l2_policy_evict_last() : pol_s;
             const uint64_t pol_b = SYM ? pol_n : p.raster == 0 ? pol_s : l2_policy_evict_last();
@@ -400,15 +400,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 // One 128 x 128 tile a cluster; its CTAs have a part of the reduction each, leave
 // their sums in shared memory, and each finishes some of the tile's rows from all
 // of them, in a fixed order.
-constexpr int kSmallStages = 3;
+constexpr int kSmallStages = 6;
 constexpr int kPartLd = 132;  // floats of a row of sums: 16-byte accesses of a column of lanes meet no bank twice
-constexpr int kTurnLd = 40;   // halves of a row of the turned tile
+constexpr int kTurnLd = 136;  // halves of a row of the turned tile
 constexpr uint32_t kTurn = 128 * kPartLd * 4;  // where the turned tile is, after the sums
 constexpr size_t kSmallSmem = size_t(kSmallStages) * 2 * kHalfStage + kBarBytes + 1024;
 static_assert(size_t(kTurn) + 128 * kTurnLd * 2 <= size_t(kSmallStages) * 2 * kHalfStage, "sums and turned tile fit the stages");
 
+__device__ __forceinline__ float4 ld_shared_f32x4(uint32_t a) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+    return v;
+}
+
 template <bool A_MN, bool B_MN, int MODE>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, 1)
     ortho_small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const OrthoParams p) {
     const WaitCtx wc{p.err, p.timeout_ns};
     constexpr int S = kSmallStages;
@@ -439,6 +445,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int kb0 = int(rank) * p.per, kb1 = min(p.num_k, kb0 + p.per);
 
     if (threadIdx.x == 0) {
+        tma_prefetch_map(&map_a);  // while the launch before this one ends
+        tma_prefetch_map(&map_b);
         for (int s = 0; s < S; ++s) {
             mbar_init(full_bar(s), 1);
             mbar_init(empty_bar(s), 1);
@@ -520,52 +528,58 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
         tc_fence_before();
     }
-    // This CTA finishes rows [r0, r0 + rows) of the tile, 32 at a time (what the
-    // turned tile holds); a thread has four columns of every eighth row.  What
-    // those elements need from global memory is asked for before the CTAs meet.
-    constexpr int kPer = 4;
+    // This CTA finishes rows [r0, r0 + rows) of the tile, a warp every eighth of
+    // them, a lane four columns.  What a batch of rows needs from global memory is
+    // asked for together, the first batch's before the sums are there.
+    constexpr int kBatch = 8;
     const int rows = 128 / p.splits, r0 = int(rank) * rows;
     const int c = lane * 4, col = n0 + c;
-    uint4 mem[kPer];
+    uint4 mem[kBatch];
     auto in = [&](int r) { return r < r0 + rows && m0 + r < p.m_dim && col < p.n_dim; };
-    auto fetch = [&](int base) {
+    auto fetch = [&](int first) {
+        if constexpr (MODE != GRAM) {
 #pragma unroll
-        for (int u = 0; u < kPer; ++u) {
-            const int r = base + warp + 8 * u;
-            const int64_t at = int64_t(b) * p.apart + int64_t(m0 + r) * p.ld + col;
-            mem[u] = make_uint4(0, 0, 0, 0);
-            if constexpr (MODE == SQUARE) {
-                if (in(r)) {
+            for (int u = 0; u < kBatch; ++u) {
+                const int r = first + 8 * u;
+                const int64_t at = int64_t(b) * p.apart + int64_t(m0 + r) * p.ld + col;
+                mem[u] = make_uint4(0, 0, 0, 0);
+                if (!in(r)) continue;
+                if constexpr (MODE == SQUARE) {
                     const uint2 e = *reinterpret_cast<const uint2*>(p.e + at);
                     mem[u].x = e.x;
                     mem[u].y = e.y;
+                } else {
+                    mem[u] = *reinterpret_cast<const uint4*>(p.x + at);
                 }
-            } else if constexpr (MODE == UPDATE || MODE == LAST) {
-                if (in(r)) mem[u] = *reinterpret_cast<const uint4*>(p.x + at);
             }
         }
     };
-    fetch(r0);
+    fetch(r0 + warp);
     if (p.splits > 1) cluster_sync(); else __syncthreads();
 
-    __half* turn = reinterpret_cast<__half*>(smem + kTurn);
+    uint16_t* turn = reinterpret_cast<uint16_t*>(smem + kTurn);
     const bool mirrored = SYM && mb != nb;
-    for (int base = r0; base < r0 + rows; base += 32) {
-        if (base > r0) fetch(base);
-        const int have = min(32, r0 + rows - base);
+#pragma unroll 1
+    for (int first = r0 + warp; first < r0 + rows; first += 8 * kBatch) {
+        if (first > r0 + warp) fetch(first);
 #pragma unroll
-        for (int u = 0; u < kPer; ++u) {
-            const int r = base + warp + 8 * u;
+        for (int u = 0; u < kBatch; ++u) {
+            const int r = first + 8 * u;
             if (r >= r0 + rows) break;
             const uint32_t at = smem0 + uint32_t(r * kPartLd + c) * 4u;
-            float4 v[8];
+            float4 acc;
+            if (p.splits == 1) {
+                acc = ld_shared_f32x4(at);
+            } else {
+                float4 v[8];
 #pragma unroll
-            for (int t = 0; t < 8; ++t)
-                if (t < p.splits) v[t] = ld_cluster_f32x4(at, uint32_t(t));
-            float4 acc = v[0];
+                for (int t = 0; t < 8; ++t)
+                    if (t < p.splits) v[t] = ld_cluster_f32x4(at, uint32_t(t));
+                acc = v[0];
 #pragma unroll
-            for (int t = 1; t < 8; ++t)
-                if (t < p.splits) acc = make_float4(acc.x + v[t].x, acc.y + v[t].y, acc.z + v[t].z, acc.w + v[t].w);
+                for (int t = 1; t < 8; ++t)
+                    if (t < p.splits) acc = make_float4(acc.x + v[t].x, acc.y + v[t].y, acc.z + v[t].z, acc.w + v[t].w);
+            }
             const int row = m0 + r;
             float f[4] = {acc.x, acc.y, acc.z, acc.w};
             if constexpr (MODE == GRAM) {
@@ -602,24 +616,23 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
             if (mirrored) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) reinterpret_cast<uint16_t*>(turn)[(c + j) * kTurnLd + (r - base)] = h[j];
+                for (int j = 0; j < 4; ++j) turn[(c + j) * kTurnLd + (r - r0)] = h[j];
             }
         }
-        if (mirrored) {
-            __syncthreads();
-            // column i of these rows is row n0 + i of the result, from column m0 + base on
-            for (int idx = int(threadIdx.x); idx < 128 * (have / 8); idx += kThreads) {
-                const int i = idx / (have / 8), g = idx % (have / 8) * 8;
-                const int row = n0 + i, at = m0 + base + g;
-                if (row < p.n_dim && at < p.m_dim)
-                    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + int64_t(b) * p.o_apart + int64_t(row) * p.ldo + at) =
-                        *reinterpret_cast<const uint4*>(turn + i * kTurnLd + g);
-            }
-            __syncthreads();
+    }
+    if (mirrored) {
+        __syncthreads();
+        // column i of these rows is row n0 + i of the result, from column m0 + r0 on
+        const int groups = rows / 8;
+        for (int idx = int(threadIdx.x); idx < 128 * groups; idx += kThreads) {
+            const int i = idx / groups, g = idx % groups * 8;
+            const int row = n0 + i, at = m0 + r0 + g;
+            if (row < p.n_dim && at < p.m_dim)
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + int64_t(b) * p.o_apart + int64_t(row) * p.ldo + at) =
+                    *reinterpret_cast<const uint4*>(turn + i * kTurnLd + g);
         }
     }
     if (p.splits > 1) cluster_sync();  // nobody leaves while its sums are read
-    else __syncthreads();
     if (warp == 2) {
         tc_fence_after();
         tmem_dealloc<false>(tmem_base, 128);
@@ -824,8 +837,8 @@ cudaError_t launch(const void* kern, int grid, int cluster, size_t smem, cudaStr
 
 // Products of up to a quarter as many 256 x 256 tiles as there are CTA pairs go
 // through the small kernel.  The whole update, us, by pairs alone / with this
-// rule / with one twice as wide: 512 x 512 166 / 134 / 135, 128 x 512 116 /
-// 107 / 107, 1024 x 4096 279 / 257 / 261, 2048 x 2048 290 / 291 / 310.
+// rule / with one three times as wide: 512 x 512 166 / 123 / 123, 128 x 512 116 /
+// 105 / 105, 1024 x 4096 279 / 203 / 227, 2048 x 2048 290 / 291 / 317.
 bool small_product(int64_t pair_tiles, int num_sms) { return pair_tiles <= num_sms / 8; }
 
 template <bool A_MN, bool B_MN, int MODE>
@@ -855,8 +868,11 @@ cudaError_t product(const Half& a, const Half& b, int64_t m, int64_t n, int64_t 
     OutMaps to = maps;
     void* args[] = {&ma, &mb, &to, &p};
     if (small) {
+        // CTAs of a cluster: as many as there are SMs for, with four K-blocks
+        // each.  512 x 512, us: two of 8 K-blocks 123, eight 154, one 157;
+        // 1024 x 4096: eight of 64 203, one 277.
         p.splits = 1;
-        while (p.splits < 8 && int64_t(p.num_tiles) * p.splits * 2 <= 2 * num_sms) p.splits *= 2;
+        while (p.splits < 8 && int64_t(p.num_tiles) * p.splits * 2 <= num_sms && p.num_k >= 4 * p.splits) p.splits *= 2;
         p.per = (p.num_k + p.splits - 1) / p.splits;
         void* few[] = {&ma, &mb, &p};
         return launch(reinterpret_cast<const void*>(ortho_small_kernel<A_MN, B_MN, MODE>), p.num_tiles * p.splits, p.splits, kSmallSmem,

@@ -911,8 +911,9 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5):
             _refuse(where, "weight and bias differ in dtype")
         ptype, bp = _type_of(bias, where), bias.data_ptr()
     kind, stream = _type_of(x, where), _stream_of(device, where)
-    y = x.new_empty((rows, cols))
-    mean, rstd = x.new_empty(rows, dtype=torch.float32), x.new_empty(rows, dtype=torch.float32)
+    y = torch.empty((rows, cols), dtype=x.dtype, device=device)
+    mean = torch.empty(rows, dtype=torch.float32, device=device)
+    rstd = torch.empty(rows, dtype=torch.float32, device=device)
     tiled_linear_norm_forward(rows, cols, kind, x.data_ptr(), ldx, ptype, wp, bp, eps, y.data_ptr(), cols,
                               mean.data_ptr(), rstd.data_ptr(), _err_word(device), stream)
     return y, mean, rstd
@@ -935,10 +936,11 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None):
         if v.dtype != torch.float32:
             _refuse(where, f"{name} must be float32")
     kind, stream = _type_of(x, where), _stream_of(device, where)
-    dx = x.new_empty((rows, cols))
-    dweight, dbias = x.new_empty(cols, dtype=torch.float32), x.new_empty(cols, dtype=torch.float32)
+    dx = torch.empty((rows, cols), dtype=x.dtype, device=device)
+    dweight = torch.empty(cols, dtype=torch.float32, device=device)
+    dbias = torch.empty(cols, dtype=torch.float32, device=device)
     need = tiled_linear_norm_backward_workspace_bytes(rows, cols)
-    ws = x.new_empty(need, dtype=torch.uint8)
+    ws = torch.empty(need, dtype=torch.uint8, device=device)
     tiled_linear_norm_backward(rows, cols, kind, dy.data_ptr(), lddy, x.data_ptr(), ldx, mean.data_ptr(),
                                rstd.data_ptr(), ptype, wp, dx.data_ptr(), cols, dweight.data_ptr(), dbias.data_ptr(),
                                ws.data_ptr(), need, _err_word(device), stream)
@@ -993,8 +995,8 @@ def fp8_quantize(x, *forms: str, format: str = "e4m3"):
     dtype = torch.float8_e4m3fn if format == "e4m3" else torch.float8_e5m2
     ldq, out, args = _up(cols, 16), [], {}
     for form in forms:
-        scale = x.new_empty(_fp8_scales(rows, cols, form), dtype=torch.uint8)
-        q = x.new_empty((rows, ldq), dtype=dtype)
+        scale = torch.empty(_fp8_scales(rows, cols, form), dtype=torch.uint8, device=device)
+        q = torch.empty((rows, ldq), dtype=dtype, device=device)
         args[form] = (q.data_ptr(), ldq, scale.data_ptr())
         out.append((q if ldq == cols else q[:, :cols], scale))
     none = (None, 0, None)
@@ -1017,7 +1019,7 @@ def _fp8_operand(q, scale, form: str, where: str, name: str):
 
 def _fp8_result(x, rows: int, cols: int):
     ld = _up(cols, 8)
-    out = x.new_empty((rows, ld), dtype=_torch.bfloat16)
+    out = _torch.empty((rows, ld), dtype=_torch.bfloat16, device=x.device)
     return (out if ld == cols else out[:, :cols]), ld
 
 
@@ -1082,7 +1084,7 @@ def fp8_linear(x, wq, ws):
     kind, stream, w = _type_of(x, where), _stream_of(device, where), _fp8_operand(wq, ws, "tile", where, "the weight")
     y, ldy = _fp8_result(x, T, n)
     need = tiled_linear_fp8_linear_workspace_bytes(T, K, n)
-    work = x.new_empty(need, dtype=torch.uint8)
+    work = torch.empty(need, dtype=torch.uint8, device=device)
     tiled_linear_fp8_linear(T, K, n, kind, x.data_ptr(), ldx, *w, y.data_ptr(), ldy, work.data_ptr(), need,
                             _err_word(device), stream)
     return y
@@ -1099,7 +1101,7 @@ def fp8_linear_backward(x, dy, wq, ws):
     kind, stream, w = _type_of(x, where), _stream_of(device, where), _fp8_operand(wq, ws, "tile", where, "the weight")
     (dx, lddx), (dw, lddw) = _fp8_result(x, T, K), _fp8_result(x, K, n)
     need = tiled_linear_fp8_linear_backward_workspace_bytes(T, K, n)
-    work = x.new_empty(need, dtype=torch.uint8)
+    work = torch.empty(need, dtype=torch.uint8, device=device)
     tiled_linear_fp8_linear_backward(T, K, n, kind, x.data_ptr(), ldx, dy.data_ptr(), lddy, *w, dx.data_ptr(), lddx,
                                      dw.data_ptr(), lddw, work.data_ptr(), need, _err_word(device), stream)
     return dx, dw
@@ -1123,9 +1125,9 @@ def orthogonalize(g, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315), eps
         _refuse(where, "the rows of g are not contiguous")
     ldg = ldg if rows > 1 else cols
     ldo = _up(cols, 8)
-    out = g.new_empty((batch, rows, ldo), dtype=torch.bfloat16)
+    out = torch.empty((batch, rows, ldo), dtype=torch.bfloat16, device=device)
     need = tiled_linear_orthogonalize_workspace_bytes(batch, rows, cols)
-    work = g.new_empty(need, dtype=torch.uint8)
+    work = torch.empty(need, dtype=torch.uint8, device=device)
     a, b, c = coefficients
     tiled_linear_orthogonalize(batch, rows, cols, kind, stack.data_ptr(), ldg, apart if batch > 1 else 0, steps, a, b, c,
                                eps, scale, out.data_ptr(), ldo, rows * ldo, work.data_ptr(), need, _err_word(device),
