@@ -21,6 +21,10 @@
 //    belong to one warp (shuffles alone); longer ones to a CTA, or to a
 //    cluster of up to eight when a CTA cannot hold them.  There every
 //    warp leaves its sums for all others, and one barrier a row is all there is.
+// Measured: 8192 x 8192 bf16 forward 59 us (4.5 TB/s), backward 83 us (4.8 TB/s,
+// its reduction included), 8 x 8192 3.7 and 6.9 us.  What bounds them is the
+// latency of a row's chain (copy, sums, barrier, write) with the two rows that an
+// SM's registers and shared memory leave in flight.
 // All statistics and sums are fp32.  A row's variance is joined from the
 // warps' sums of squares about their own means, which loses nothing to
 // cancellation, whatever the row's mean.  Every order of summation is fixed by
@@ -36,7 +40,7 @@ namespace {
 
 constexpr int kMaxRing = 4;         // rows in flight per thread
 constexpr int kWarpRowWarps = 8;    // rows of a CTA at a time where a warp has a row
-constexpr int kMaxWarps = 32;       // of a CTA that shares a row
+constexpr int kMaxWarps = 16;       // of a CTA that shares a row
 constexpr int kMaxCluster = 8;
 constexpr size_t kSmemBudget = 220 * 1024;  // of an SM, for its CTAs
 constexpr uint32_t kMaxPolls = 200000;  // of an mbarrier, up to 10 us each
@@ -65,6 +69,9 @@ struct NormArgs {
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // At most `pending` of the thread's newest groups may be unfinished.
@@ -222,6 +229,10 @@ __device__ __forceinline__ void fetch(const Cols<T, VEC, ITEMS, FULL>& c, const 
 #pragma unroll
         for (int k = 0; k < ITEMS; ++k)
             if (c.has(k)) cp_async16(slot + k * c.kSlot, row + k * c.kStep);
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int k = 0; k < ITEMS; ++k)
+            if (c.has(k)) cp_async4(slot + k * c.kSlot, row + k * c.kStep);
     } else {
         Vec<T, 1> v[ITEMS];
 #pragma unroll
@@ -243,6 +254,16 @@ struct Param {
     template <typename T, int ITEMS, bool FULL>
     __device__ __forceinline__ Param(uint32_t base, const Cols<T, VEC, ITEMS, FULL>& c, const void* p, int32_t type, float none) {
         at = base + (threadIdx.x / 32) * (ITEMS * VEC / kChunk) * kStep + (threadIdx.x % 32) * (kChunk * 4);
+        if (VEC > 1 && p && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {  // (a thread's columns start on VEC)
+            Vec<float, 4> u[ITEMS * VEC / kChunk];
+#pragma unroll
+            for (int k = 0; k < ITEMS * VEC / kChunk; ++k)
+                if (c.has(k * kChunk / VEC)) u[k] = load4_as_f32(p, type, c.col(k * kChunk / VEC) + k * kChunk % VEC);
+#pragma unroll
+            for (int k = 0; k < ITEMS * VEC / kChunk; ++k)
+                if (c.has(k * kChunk / VEC)) sts(at + k * kStep, u[k]);
+            return;
+        }
 #pragma unroll
         for (int k = 0; k < ITEMS; ++k)
             if (c.has(k))
@@ -307,10 +328,10 @@ __device__ __forceinline__ bool full_warp(const NormArgs& p) {
 // barrier counts warps, whatever instruction they arrive by).
 __device__ __forceinline__ void row_barrier() { asm volatile("barrier.sync 0;" ::: "memory"); }
 
-// Threads of a CTA that shares a row: 512 with 32 columns each, or, where rows
-// are read element by element, 1024 with 16 each.
-constexpr int max_threads(int vec) { return vec > 1 ? 512 : 1024; }
-constexpr int row_items(int vec) { return vec > 1 ? 32 : 16; }
+// Threads of a CTA that shares a row, at most, and the columns that each has:
+// 32, or 16 where rows are read element by element (32 in rows over 65536).
+constexpr int kRowThreads = 512;
+constexpr int row_items(int vec, int64_t cols) { return vec > 1 || cols > 65536 ? 32 : 16; }
 
 // ---- forward -----------------------------------------------------------------
 template <typename T, int VEC, int ITEMS, bool WARP_ROW, bool FULL>
@@ -449,7 +470,7 @@ __device__ __forceinline__ void norm_forward_rows(const NormArgs& p, uint8_t* sm
 }
 
 template <typename T, int VEC, int ITEMS, bool WARP_ROW>
-__global__ void __launch_bounds__(WARP_ROW ? kWarpRowWarps * 32 : max_threads(VEC), 1)
+__global__ void __launch_bounds__(WARP_ROW ? kWarpRowWarps * 32 : kRowThreads, 1)
     norm_forward_kernel(const NormArgs p) {
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ __align__(16) Moments red[2][kMaxCluster * kMaxWarps];  // by CTA of the cluster, then by warp
@@ -605,51 +626,68 @@ __device__ __forceinline__ void norm_backward_rows(const NormArgs& p, uint8_t* s
     if (!p.dweight && !p.dbias) return;
 
     if constexpr (WARP_ROW) {
-        // join the warps' sums, one warp after another
-        float* acc = reinterpret_cast<float*>(smem);  // the ring is done with
-        row_barrier();
-        for (int w = 0; w < warps; ++w) {
-            if (warp == w) {
+        // every warp leaves its sums where the ring was; a thread then has
+        // columns of all warps, in their order
+        float* acc = reinterpret_cast<float*>(smem);
+        __syncthreads();
+        float* mine = acc + warp * 2 * p.cols;
 #pragma unroll
-                for (int k = 0; k < ITEMS; ++k)
-                    if (at.c.has(k))
+        for (int k = 0; k < ITEMS; ++k)
+            if (at.c.has(k))
 #pragma unroll
-                        for (int e = 0; e < VEC; ++e) {
-                            const int c = at.c.col(k) + e;
-                            acc[c] = (w ? acc[c] : 0.0f) + lane_of(aw[k], e);
-                            acc[p.cols + c] = (w ? acc[p.cols + c] : 0.0f) + lane_of(ab[k], e);
-                        }
-            }
-            row_barrier();
-        }
+                for (int e = 0; e < VEC; ++e) {
+                    mine[at.c.col(k) + e] = lane_of(aw[k], e);
+                    mine[p.cols + at.c.col(k) + e] = lane_of(ab[k], e);
+                }
+        __syncthreads();
         for (int c = threadIdx.x; c < p.cols; c += blockDim.x) {
+            float sw = 0, sb = 0;
+            for (int w = 0; w < warps; ++w) {
+                sw += acc[w * 2 * p.cols + c];
+                sb += acc[(w * 2 + 1) * p.cols + c];
+            }
             if (gridDim.x == 1) {
-                if (p.dweight) p.dweight[c] = acc[c];
-                if (p.dbias) p.dbias[c] = acc[p.cols + c];
+                if (p.dweight) p.dweight[c] = sw;
+                if (p.dbias) p.dbias[c] = sb;
             } else {
-                p.partials[int64_t(blockIdx.x) * 2 * p.cols + c] = acc[c];
-                p.partials[(int64_t(blockIdx.x) * 2 + 1) * p.cols + c] = acc[p.cols + c];
+                p.partials[int64_t(blockIdx.x) * 2 * p.cols + c] = sw;
+                p.partials[(int64_t(blockIdx.x) * 2 + 1) * p.cols + c] = sb;
             }
         }
     } else {
         const bool whole = gridDim.x == uint32_t(p.cluster);
         float* to_w = whole ? p.dweight : p.partials + at.row * 2 * p.cols;
         float* to_b = whole ? p.dbias : p.partials + (at.row * 2 + 1) * p.cols;
+        // (rows of vectors have a multiple of four columns; the caller's arrays
+        // may start anywhere)
+        const bool wide = VEC > 1 && ((reinterpret_cast<uintptr_t>(to_w) | reinterpret_cast<uintptr_t>(to_b)) & 15) == 0;
 #pragma unroll
         for (int k = 0; k < ITEMS; ++k)
-            if (at.c.has(k))
+            if (at.c.has(k)) {
+                if (wide) {
+                    if constexpr (VEC > 1)
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    const int c = at.c.col(k) + e;
-                    if (to_w) to_w[c] = lane_of(aw[k], e);
-                    if (to_b) to_b[c] = lane_of(ab[k], e);
+                        for (int q = 0; q < VEC / 4; ++q) {
+                            const int c = at.c.col(k) + 4 * q;
+                            if (to_w) *reinterpret_cast<float4*>(to_w + c) = make_float4(aw[k][2 * q].x, aw[k][2 * q].y, aw[k][2 * q + 1].x, aw[k][2 * q + 1].y);
+                            if (to_b) *reinterpret_cast<float4*>(to_b + c) = make_float4(ab[k][2 * q].x, ab[k][2 * q].y, ab[k][2 * q + 1].x, ab[k][2 * q + 1].y);
+                        }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        const int c = at.c.col(k) + e;
+                        if (to_w) to_w[c] = lane_of(aw[k], e);
+                        if (to_b) to_b[c] = lane_of(ab[k], e);
+                    }
                 }
+            }
     }
 }
 
 template <typename T, int VEC, int ITEMS, bool WARP_ROW>
-__global__ void __launch_bounds__(WARP_ROW ? kWarpRowWarps * 32 : max_threads(VEC), 1)
+__global__ void __launch_bounds__(WARP_ROW ? kWarpRowWarps * 32 : kRowThreads, 1)
     norm_backward_kernel(const NormArgs p) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // norm_reduce_kernel, which waits for this one
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ __align__(16) float2 red[2][kMaxCluster * kMaxWarps];  // by CTA of the cluster, then by warp
     __shared__ uint64_t bars[2];
@@ -682,6 +720,7 @@ __global__ void __launch_bounds__(kReduceWarps * 32)
     const int c = blockIdx.x * 32 + lane;
     float* out = blockIdx.y == 0 ? dweight : dbias;
     if (!out) return;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the partial sums are there
     float s = 0;
     if (c < cols)
 #pragma unroll 8
@@ -701,16 +740,14 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 using NormKernel = void (*)(NormArgs);
 
-// Elements a thread has of each row: 8 or 32 where a warp has the row (e says
-// which), row_items() where a CTA or cluster does.
+// Elements a thread has of each row: 8 or 32 where a warp has the row, 16 or 32
+// where a CTA or cluster does.
 template <typename T, int VEC>
 NormKernel pick(bool backward, bool warp_row, int e) {
-    constexpr int kRow = row_items(VEC) / VEC;
-    if (backward) {
-        if (!warp_row) return norm_backward_kernel<T, VEC, kRow, false>;
-        return e == 8 ? norm_backward_kernel<T, VEC, 8 / VEC, true> : norm_backward_kernel<T, VEC, 32 / VEC, true>;
-    }
-    if (!warp_row) return norm_forward_kernel<T, VEC, kRow, false>;
+    if (!warp_row && e == 32) return backward ? norm_backward_kernel<T, VEC, 32 / VEC, false> : norm_forward_kernel<T, VEC, 32 / VEC, false>;
+    if constexpr (VEC == 1)
+        if (!warp_row) return backward ? norm_backward_kernel<T, 1, 16, false> : norm_forward_kernel<T, 1, 16, false>;
+    if (backward) return e == 8 ? norm_backward_kernel<T, VEC, 8 / VEC, true> : norm_backward_kernel<T, VEC, 32 / VEC, true>;
     return e == 8 ? norm_forward_kernel<T, VEC, 8 / VEC, true> : norm_forward_kernel<T, VEC, 32 / VEC, true>;
 }
 
@@ -718,16 +755,14 @@ NormKernel pick(bool backward, bool warp_row, int e) {
 // columns each in the longest rows.  Two CTAs of 256 threads, an SM's, work
 // on different rows, and one moves data while the other waits for its row's
 // sums.  Measured, forward / backward: 2048 x 65536 bf16 with 8 CTAs of 8192
-// columns 214 / 284 us, with 4 of 16384 266 / 360 us; 8192 x 16384 with two
-// CTAs 118 / 172 us, with one 124 / 176 us.
+// columns 209 / 259 us, with 4 of 16384 266 / 360 us; 8192 x 16384 with two
+// CTAs 116 / 154 us, with one 124 / 176 us.
 int cluster_size(int64_t cols) {
     int c = 1;
     while (c < kMaxCluster && cols > int64_t(c) * 8192) c *= 2;
     return c;
 }
-static_assert(max_threads(1) * row_items(1) == max_threads(8) * row_items(8) &&
-                  kNormMaxCols == int64_t(kMaxCluster) * max_threads(1) * row_items(1),
-              "both kinds of row fit the same clusters");
+static_assert(kNormMaxCols == int64_t(kMaxCluster) * kRowThreads * 32 && 8192 == kRowThreads * 16, "the rows fit their clusters");
 
 struct Plan {
     NormKernel kernel;
@@ -752,19 +787,19 @@ cudaError_t make_plan(const NormDesc& d, bool backward, int num_sms, Plan* out) 
         p.seg = int(d.cols);
     } else {
         p.cluster = cluster_size(d.cols);
-        e = row_items(vec);
+        e = row_items(vec, d.cols);
         const int64_t per = (d.cols + p.cluster - 1) / p.cluster;
         p.seg = int((per + vec - 1) / vec * vec);
         p.threads = int(((p.seg + e - 1) / e + 31) / 32 * 32);
     }
     const size_t row_bytes = size_t(p.threads) * e * esize * (backward ? 2 : 1);
     const size_t fixed = size_t(p.threads) * e * 4 * (backward ? 1 : 2);
-    // only the vector copies are asynchronous: without them a longer ring
-    // hides nothing
+    // single 2-byte elements cannot be copied asynchronously: a longer ring
+    // would hide nothing
     auto fits = [&](size_t budget) { return budget < fixed ? 0 : int(std::min<size_t>(kMaxRing, (budget - fixed) / row_bytes)); };
-    p.ring = vec == 1 ? 1 : fits(kSmemBudget / 2) >= 2 ? fits(kSmemBudget / 2) : std::max(1, fits(kSmemBudget));
+    p.ring = vec == 1 && esize == 2 ? 1 : fits(kSmemBudget / 2) >= 2 ? fits(kSmemBudget / 2) : std::max(1, fits(kSmemBudget));
     p.smem = p.ring * row_bytes + fixed;
-    if (backward && p.warp_row) p.smem = std::max(p.smem, size_t(d.cols) * 8);
+    if (backward && p.warp_row) p.smem = std::max(p.smem, size_t(kWarpRowWarps) * size_t(d.cols) * 8);
     if (d.type == TL_TYPE_BF16)
         p.kernel = vec > 1 ? pick<__nv_bfloat16, 8>(backward, p.warp_row, e) : pick<__nv_bfloat16, 1>(backward, p.warp_row, e);
     else if (d.type == TL_TYPE_F16)
@@ -777,7 +812,15 @@ cudaError_t make_plan(const NormDesc& d, bool backward, int num_sms, Plan* out) 
     if (per_sm < 1) return cudaErrorInvalidConfiguration;
     per_sm = std::min(per_sm, kCtasPerSm);
     const int64_t units = p.warp_row ? (d.rows + kWarpRowWarps - 1) / kWarpRowWarps : d.rows;
-    const int64_t room = std::max<int64_t>(1, int64_t(std::min(num_sms, kMaxSms)) * per_sm / p.cluster);
+    const int64_t sms = std::min(num_sms, kMaxSms);
+    int64_t room = std::max<int64_t>(1, sms * per_sm / p.cluster);
+    // Each CTA of the backward also writes a sum for every column, which the
+    // reduction reads: with few rows, fewer CTAs that walk over several of them
+    // do less in all, as long as their rows come ahead of them.  Backward, us,
+    // with this / with a row a CTA: 512 x 8192 bf16 22 / 33, 256 x 4096 12 / 18,
+    // 300 x 30000 44 / 54.  (Two an SM where elements come one by one: 517 x
+    // 5003 fp32 24 / 33, with one 30.)
+    if (backward && p.ring > 1 && units < 8 * room) room = std::max({int64_t(1), sms / p.cluster * (vec > 1 ? 1 : 2), units / 8});
     p.grid = int(std::min(units, std::min(room, norm_partials(d.rows, d.cols)))) * p.cluster;
     *out = p;
     return cudaSuccess;
@@ -864,9 +907,17 @@ cudaError_t norm_backward_launch(const NormDesc& d, int num_sms, cudaStream_t st
     if (e == cudaSuccess) e = launch(p, d, stream);
     const int n = p.grid / p.cluster;
     if (e != cudaSuccess || n == 1 || (!d.dweight && !d.dbias)) return e;
-    norm_reduce_kernel<<<dim3(unsigned((d.cols + 31) / 32), 2), kReduceWarps * 32, 0, stream>>>(
-        d.partials, n, int32_t(d.cols), d.dweight, d.dbias);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(unsigned((d.cols + 31) / 32), 2);
+    cfg.blockDim = dim3(kReduceWarps * 32);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];  // its launch may overlap the end of the kernel before it
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, norm_reduce_kernel, static_cast<const float*>(d.partials), int32_t(n), int32_t(d.cols), d.dweight,
+                              d.dbias);
 }
 
 }  // namespace tl

@@ -136,6 +136,27 @@ __device__ __forceinline__ void pack(const float2 (&v)[4], Vec<__nv_bfloat16, 8>
     for (int i = 0; i < 4; ++i) reinterpret_cast<__nv_bfloat162*>(u.v)[i] = __float22bfloat162_rn(v[i]);
 }
 
+// Four of them from element i on, which is a multiple of four, the array's start
+// being 16-byte aligned.
+__device__ __forceinline__ Vec<float, 4> load4_as_f32(const void* p, int32_t type, int64_t i) {
+    if (type == TL_TYPE_F32) return *reinterpret_cast<const Vec<float, 4>*>(static_cast<const float*>(p) + i);
+    const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
+    Vec<float, 4> v;
+    if (type == TL_TYPE_BF16) {
+        v.v[0] = __uint_as_float(u.x << 16);
+        v.v[1] = __uint_as_float(u.x & 0xffff0000u);
+        v.v[2] = __uint_as_float(u.y << 16);
+        v.v[3] = __uint_as_float(u.y & 0xffff0000u);
+    } else {
+        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&u.x)), b = __half22float2(*reinterpret_cast<const __half2*>(&u.y));
+        v.v[0] = a.x;
+        v.v[1] = a.y;
+        v.v[2] = b.x;
+        v.v[3] = b.y;
+    }
+    return v;
+}
+
 inline size_t type_bytes(int32_t type) { return type == TL_TYPE_F32 ? 4 : 2; }
 inline bool type_known(int32_t type) { return type >= TL_TYPE_BF16 && type <= TL_TYPE_F32; }
 
