@@ -140,24 +140,41 @@ constexpr uint32_t kHalfStage = 16384;  // one operand's K-block of a CTA
 constexpr size_t kOrthoSmem = size_t(kOrthoStages) * 2 * kHalfStage + 8 * kEpiBuf + kBarBytes + 1024;
 static_assert(kOrthoSmem <= 232448, "shared memory budget");
 
-// The epilogue of 64 columns of a warp's 32 rows: lane l has row row0 + l.
+// What 32 columns of lane l's row (row0 + l) need from global memory.
+template <int MODE>
+__device__ __forceinline__ void ortho_fetch(const OrthoParams& p, int col, int row, int b, uint4 (&mem)[8]) {
+    if constexpr (MODE != GRAM) {
+        constexpr int kVecs = MODE == SQUARE ? 4 : 8, kPer = MODE == SQUARE ? 8 : 4;
+        const int64_t at = int64_t(b) * p.apart + int64_t(row) * p.ld + col;
+        const uint4* src = MODE == SQUARE ? reinterpret_cast<const uint4*>(p.e + at) : reinterpret_cast<const uint4*>(p.x + at);
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) {  // (rows are padded to 8 elements: whole vectors stay inside them)
+            mem[j] = make_uint4(0, 0, 0, 0);
+            if (row < p.m_dim && col + kPer * j < p.n_dim) mem[j] = src[j];
+        }
+    }
+}
+
+// The epilogue of 64 columns of a warp's 32 rows: lane l has row row0 + l, what
+// its first 32 columns need is in mem[0], and what the next 64 columns' first 32
+// need is there afterwards (`more`).
 template <int MODE>
 __device__ __forceinline__ void ortho_columns(const OrthoParams& p, const OutMaps& maps, uint32_t taddr, uint32_t box_half,
-                                              uint32_t box_wide, int col, int row0, int b, bool mirrored, int lane) {
+                                              uint32_t box_wide, int col, int row0, int b, bool mirrored, bool more, int lane,
+                                              uint4 (&mem)[2][8]) {
     const int row = row0 + lane;
     uint32_t w[32];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         uint32_t v[32];
         const int c0 = col + 32 * h;
+        if (h == 0 || more) ortho_fetch<MODE>(p, c0 + 32, row, b, mem[h ^ 1]);
+        tmem_ld_32cols(taddr + 32u * uint32_t(h), v);
         float f[32];
         if constexpr (MODE == SQUARE) {
-            const __half* src = p.e + int64_t(b) * p.apart + int64_t(row) * p.ld + c0;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {  // rows of E are padded to whole 16-byte vectors
-                uint4 u = make_uint4(0, 0, 0, 0);
-                if (row < p.m_dim && c0 + 8 * j < p.n_dim) u = __ldg(reinterpret_cast<const uint4*>(src) + j);
-                const __half2* e2 = reinterpret_cast<const __half2*>(&u);
+            for (int j = 0; j < 4; ++j) {
+                const __half2* e2 = reinterpret_cast<const __half2*>(&mem[h][j]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float2 e = __half22float2(e2[i]);
@@ -166,18 +183,14 @@ __device__ __forceinline__ void ortho_columns(const OrthoParams& p, const OutMap
                 }
             }
         } else if constexpr (MODE == UPDATE || MODE == LAST) {
-            const float* src = p.x + int64_t(b) * p.apart + int64_t(row) * p.ld + c0;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                float4 u = make_float4(0, 0, 0, 0);
-                if (row < p.m_dim && c0 + 4 * j < p.n_dim) u = *(reinterpret_cast<const float4*>(src) + j);
-                f[4 * j] = u.x;
-                f[4 * j + 1] = u.y;
-                f[4 * j + 2] = u.z;
-                f[4 * j + 3] = u.w;
+                f[4 * j] = __uint_as_float(mem[h][j].x);
+                f[4 * j + 1] = __uint_as_float(mem[h][j].y);
+                f[4 * j + 2] = __uint_as_float(mem[h][j].z);
+                f[4 * j + 3] = __uint_as_float(mem[h][j].w);
             }
         }
-        tmem_ld_32cols(taddr + 32u * uint32_t(h), v);
         tmem_ld_wait();
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
@@ -370,12 +383,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             place(tile, b, mb, nb);
             const int row0 = mb * 256 + int(rank) * 128 + q * 32, n0 = nb * 256;
             const int chunks = row0 < p.m_dim ? min(4, (p.n_dim - n0 + 63) / 64) : 0;
+            uint4 mem[2][8];
+            if (chunks > 0) ortho_fetch<MODE>(p, n0, row0 + lane, b, mem[0]);
             if (!warp_wait(tfull_bar(acc), uint32_t(it >> 1) & 1u, wc, kErrEpilogueWait, lane)) break;
             tc_fence_after();
             const uint32_t t_row = tmem_base + (uint32_t(q * 32) << 16) + acc * 256;
 #pragma unroll 1
             for (int c = 0; c < chunks; ++c)
-                ortho_columns<MODE>(p, maps, t_row + uint32_t(c) * 64u, box_half, box_wide, n0 + c * 64, row0, b, mb != nb, lane);
+                ortho_columns<MODE>(p, maps, t_row + uint32_t(c) * 64u, box_half, box_wide, n0 + c * 64, row0, b, mb != nb,
+                                    c + 1 < chunks, lane, mem);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
@@ -529,95 +545,88 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
     }
     // This CTA finishes rows [r0, r0 + rows) of the tile, a warp every eighth of
-    // them, a lane four columns.  What a batch of rows needs from global memory is
-    // asked for together, the first batch's before the sums are there.
-    constexpr int kBatch = 8;
-    const int rows = 128 / p.splits, r0 = int(rank) * rows;
+    // them, a lane four columns: 16 / splits rows a warp, with `splits` sums each.
+    // What the rows need from global memory is asked for before the sums are
+    // there, and all sixteen reads of sums are under way before one is used.
+    const int rows = 128 / p.splits, r0 = int(rank) * rows, log = 31 - __clz(p.splits);
     const int c = lane * 4, col = n0 + c;
-    uint4 mem[kBatch];
-    auto in = [&](int r) { return r < r0 + rows && m0 + r < p.m_dim && col < p.n_dim; };
-    auto fetch = [&](int first) {
-        if constexpr (MODE != GRAM) {
+    uint4 mem[16];
+    auto row_of = [&](int u) { return r0 + warp + 8 * u; };
+    auto in = [&](int u) { return u < 16 >> log && m0 + row_of(u) < p.m_dim && col < p.n_dim; };
+    if constexpr (MODE != GRAM) {
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                const int r = first + 8 * u;
-                const int64_t at = int64_t(b) * p.apart + int64_t(m0 + r) * p.ld + col;
-                mem[u] = make_uint4(0, 0, 0, 0);
-                if (!in(r)) continue;
-                if constexpr (MODE == SQUARE) {
-                    const uint2 e = *reinterpret_cast<const uint2*>(p.e + at);
-                    mem[u].x = e.x;
-                    mem[u].y = e.y;
-                } else {
-                    mem[u] = *reinterpret_cast<const uint4*>(p.x + at);
-                }
+        for (int u = 0; u < 16; ++u) {
+            mem[u] = make_uint4(0, 0, 0, 0);
+            if (!in(u)) continue;
+            const int64_t at = int64_t(b) * p.apart + int64_t(m0 + row_of(u)) * p.ld + col;
+            if constexpr (MODE == SQUARE) {
+                const uint2 e = *reinterpret_cast<const uint2*>(p.e + at);
+                mem[u].x = e.x;
+                mem[u].y = e.y;
+            } else {
+                mem[u] = *reinterpret_cast<const uint4*>(p.x + at);
             }
         }
-    };
-    fetch(r0 + warp);
+    }
     if (p.splits > 1) cluster_sync(); else __syncthreads();
+
+    float4 acc[16];
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+        const uint32_t at = smem0 + uint32_t(row_of(q >> log) * kPartLd + c) * 4u;
+        acc[q] = log == 0 ? ld_shared_f32x4(at) : ld_cluster_f32x4(at, uint32_t(q & (p.splits - 1)));
+    }
+    // the sums of a row, neighbours first: row u's end up in acc[u]
+#pragma unroll
+    for (int level = 0; level < 3; ++level)
+        if (level < log)
+#pragma unroll
+            for (int i = 0; i < 8 >> level; ++i)
+                acc[i] = make_float4(acc[2 * i].x + acc[2 * i + 1].x, acc[2 * i].y + acc[2 * i + 1].y, acc[2 * i].z + acc[2 * i + 1].z,
+                                     acc[2 * i].w + acc[2 * i + 1].w);
 
     uint16_t* turn = reinterpret_cast<uint16_t*>(smem + kTurn);
     const bool mirrored = SYM && mb != nb;
-#pragma unroll 1
-    for (int first = r0 + warp; first < r0 + rows; first += 8 * kBatch) {
-        if (first > r0 + warp) fetch(first);
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            const int r = first + 8 * u;
-            if (r >= r0 + rows) break;
-            const uint32_t at = smem0 + uint32_t(r * kPartLd + c) * 4u;
-            float4 acc;
-            if (p.splits == 1) {
-                acc = ld_shared_f32x4(at);
-            } else {
-                float4 v[8];
+    for (int u = 0; u < 16; ++u) {
+        if (u >= 16 >> log) break;
+        const int r = row_of(u), row = m0 + r;
+        float f[4] = {acc[u].x, acc[u].y, acc[u].z, acc[u].w};
+        if constexpr (MODE == GRAM) {
 #pragma unroll
-                for (int t = 0; t < 8; ++t)
-                    if (t < p.splits) v[t] = ld_cluster_f32x4(at, uint32_t(t));
-                acc = v[0];
+            for (int j = 0; j < 4; ++j) f[j] = (f[j] * (kDown * kDown) - (row == col + j ? p.shift : 0.0f)) * kUp;
+        } else if constexpr (MODE == SQUARE) {
+            const float2 e0 = __half22float2(*reinterpret_cast<const __half2*>(&mem[u].x));
+            const float2 e1 = __half22float2(*reinterpret_cast<const __half2*>(&mem[u].y));
+            const float e[4] = {e0.x, e0.y, e1.x, e1.y};
 #pragma unroll
-                for (int t = 1; t < 8; ++t)
-                    if (t < p.splits) acc = make_float4(acc.x + v[t].x, acc.y + v[t].y, acc.z + v[t].z, acc.w + v[t].w);
-            }
-            const int row = m0 + r;
-            float f[4] = {acc.x, acc.y, acc.z, acc.w};
-            if constexpr (MODE == GRAM) {
+            for (int j = 0; j < 4; ++j) f[j] = p.k1 * e[j] + p.k2 * (f[j] * kDown);
+        } else {
+            const float x[4] = {__uint_as_float(mem[u].x), __uint_as_float(mem[u].y), __uint_as_float(mem[u].z), __uint_as_float(mem[u].w)};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) f[j] = (f[j] * (kDown * kDown) - (row == col + j ? p.shift : 0.0f)) * kUp;
-            } else if constexpr (MODE == SQUARE) {
-                const float2 e0 = __half22float2(*reinterpret_cast<const __half2*>(&mem[u].x));
-                const float2 e1 = __half22float2(*reinterpret_cast<const __half2*>(&mem[u].y));
-                const float e[4] = {e0.x, e0.y, e1.x, e1.y};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) f[j] = p.k1 * e[j] + p.k2 * (f[j] * kDown);
-            } else {
-                const float x[4] = {__uint_as_float(mem[u].x), __uint_as_float(mem[u].y), __uint_as_float(mem[u].z), __uint_as_float(mem[u].w)};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) f[j] = p.k0 * x[j] + f[j] * (kDown * kDown);
-            }
-            uint2 w;
-            if constexpr (MODE == LAST)
-                w = make_uint2(pack_bf16x2(f[0] * p.scale, f[1] * p.scale), pack_bf16x2(f[2] * p.scale, f[3] * p.scale));
-            else if constexpr (MODE == UPDATE)
-                w = make_uint2(pack_f16x2(f[0] * kUp, f[1] * kUp), pack_f16x2(f[2] * kUp, f[3] * kUp));
+            for (int j = 0; j < 4; ++j) f[j] = p.k0 * x[j] + f[j] * (kDown * kDown);
+        }
+        uint2 w;
+        if constexpr (MODE == LAST)
+            w = make_uint2(pack_bf16x2(f[0] * p.scale, f[1] * p.scale), pack_bf16x2(f[2] * p.scale, f[3] * p.scale));
+        else if constexpr (MODE == UPDATE)
+            w = make_uint2(pack_f16x2(f[0] * kUp, f[1] * kUp), pack_f16x2(f[2] * kUp, f[3] * kUp));
+        else
+            w = make_uint2(pack_f16x2(f[0], f[1]), pack_f16x2(f[2], f[3]));
+        const uint16_t h[4] = {uint16_t(w.x & 0xffffu), uint16_t(w.x >> 16), uint16_t(w.y & 0xffffu), uint16_t(w.y >> 16)};
+        // (rows of E, Q and X are padded to 8 elements: four at a time stay
+        // inside them; the padding of the result's rows is the caller's)
+        if (in(u)) {
+            if constexpr (MODE == UPDATE)
+                *reinterpret_cast<float4*>(p.x + int64_t(b) * p.apart + int64_t(row) * p.ld + col) = make_float4(f[0], f[1], f[2], f[3]);
+            uint16_t* dst = static_cast<uint16_t*>(p.out) + int64_t(b) * p.o_apart + int64_t(row) * p.ldo + col;
+            if (MODE != LAST || col + 4 <= p.n_dim) *reinterpret_cast<uint2*>(dst) = w;
             else
-                w = make_uint2(pack_f16x2(f[0], f[1]), pack_f16x2(f[2], f[3]));
-            const uint16_t h[4] = {uint16_t(w.x & 0xffffu), uint16_t(w.x >> 16), uint16_t(w.y & 0xffffu), uint16_t(w.y >> 16)};
-            // (rows of E, Q and X are padded to 8 elements: four at a time stay
-            // inside them; the padding of the result's rows is the caller's)
-            if (in(r)) {
-                if constexpr (MODE == UPDATE)
-                    *reinterpret_cast<float4*>(p.x + int64_t(b) * p.apart + int64_t(row) * p.ld + col) = make_float4(f[0], f[1], f[2], f[3]);
-                uint16_t* dst = static_cast<uint16_t*>(p.out) + int64_t(b) * p.o_apart + int64_t(row) * p.ldo + col;
-                if (MODE != LAST || col + 4 <= p.n_dim) *reinterpret_cast<uint2*>(dst) = w;
-                else
-                    for (int j = 0; col + j < p.n_dim; ++j) dst[j] = h[j];
-            }
-            if (mirrored) {
+                for (int j = 0; col + j < p.n_dim; ++j) dst[j] = h[j];
+        }
+        if (mirrored) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) turn[(c + j) * kTurnLd + (r - r0)] = h[j];
-            }
+            for (int j = 0; j < 4; ++j) turn[(c + j) * kTurnLd + (r - r0)] = h[j];
         }
     }
     if (mirrored) {
@@ -641,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---- the norm and the first iterate ----------------------------------------------
 constexpr int kNormThreads = 256;
-constexpr int kNormParts = 256;  // partial sums of squares a matrix
+constexpr int kNormParts = 1024;  // partial sums of squares a matrix, at most
 
 struct StartArgs {
     const void* g;
@@ -707,7 +716,9 @@ __global__ void __launch_bounds__(kNormThreads) ortho_squares_kernel(const Start
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kNormThreads) ortho_start_kernel(const StartArgs p, int parts) {
     const float* all = p.parts + int64_t(blockIdx.y) * kNormParts;
-    const float sum = block_sum(int(threadIdx.x) < parts ? all[threadIdx.x] : 0.0f);
+    float mine = 0;
+    for (int i = int(threadIdx.x); i < parts; i += kNormThreads) mine += all[i];
+    const float sum = block_sum(mine);
     const float inv = 1.0f / (sqrtf(sum) + p.eps);
     float* x = p.x + int64_t(blockIdx.y) * p.apart;
     __half* h = p.h + int64_t(blockIdx.y) * p.apart;
@@ -735,8 +746,8 @@ cudaError_t start_launch(const StartArgs& a, int64_t batch, int num_sms, cudaStr
     constexpr int V = 16 / int(sizeof(T));
     const int64_t vectors = a.rows * a.cols / (a.vec ? V : 1);
     const int64_t want = (vectors + 4 * kNormThreads - 1) / (4 * kNormThreads);
-    const int parts = int(std::max<int64_t>(1, std::min<int64_t>(want, kNormParts)));
     const int64_t room = std::max<int64_t>(1, 8 * num_sms / batch);
+    const int parts = int(std::max<int64_t>(1, std::min({want, room, int64_t(kNormParts)})));
     const dim3 g1{unsigned(parts), unsigned(batch)}, g2{unsigned(std::max<int64_t>(1, std::min(want, room))), unsigned(batch)};
     if (a.vec) {
         ortho_squares_kernel<T, V><<<g1, kNormThreads, 0, stream>>>(a);
