@@ -648,7 +648,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                     if (m0 + i + j < p.m_dim) dst[j] = __float2bfloat16_rn(f[j]);
             }
         }
-        cluster_sync();  // nobody leaves while its part is read
+        cluster_arrive_relaxed();  // nobody leaves while its part is read
+        cluster_wait_only();
     } else {
         __syncthreads();
     }

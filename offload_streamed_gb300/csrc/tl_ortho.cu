@@ -481,6 +481,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     grid_dependents_go();
     grid_dependency_wait();
 
+    // This CTA finishes rows [r0, r0 + rows) of the tile, a warp every eighth of
+    // them, a lane four columns: 16 / splits rows a warp, with `splits` sums each.
+    // What the rows need from global memory is asked for first of all, and
+    // all sixteen reads of sums are under way before one is used.
+    const int rows = 128 / p.splits, r0 = int(rank) * rows, log = 31 - __clz(p.splits);
+    const int c = lane * 4, col = n0 + c;
+    uint4 mem[16];
+    auto row_of = [&](int u) { return r0 + warp + 8 * u; };
+    auto in = [&](int u) { return u < 16 >> log && m0 + row_of(u) < p.m_dim && col < p.n_dim; };
+    if constexpr (MODE != GRAM) {
+#pragma unroll
+        for (int u = 0; u < 16; ++u) {
+            mem[u] = make_uint4(0, 0, 0, 0);
+            if (!in(u)) continue;
+            const int64_t at = int64_t(b) * p.apart + int64_t(m0 + row_of(u)) * p.ld + col;
+            if constexpr (MODE == SQUARE) {
+                const uint2 e = *reinterpret_cast<const uint2*>(p.e + at);
+                mem[u].x = e.x;
+                mem[u].y = e.y;
+            } else {
+                mem[u] = *reinterpret_cast<const uint4*>(p.x + at);
+            }
+        }
+    }
     if (warp == 0) {
         if (lane == 0) {
             uint32_t fills = 0;
@@ -544,37 +568,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         tc_fence_before();
     }
-    // This CTA finishes rows [r0, r0 + rows) of the tile, a warp every eighth of
-    // them, a lane four columns: 16 / splits rows a warp, with `splits` sums each.
-    // What the rows need from global memory is asked for before the sums are
-    // there, and all sixteen reads of sums are under way before one is used.
-    const int rows = 128 / p.splits, r0 = int(rank) * rows, log = 31 - __clz(p.splits);
-    const int c = lane * 4, col = n0 + c;
-    uint4 mem[16];
-    auto row_of = [&](int u) { return r0 + warp + 8 * u; };
-    auto in = [&](int u) { return u < 16 >> log && m0 + row_of(u) < p.m_dim && col < p.n_dim; };
-    if constexpr (MODE != GRAM) {
-#pragma unroll
-        for (int u = 0; u < 16; ++u) {
-            mem[u] = make_uint4(0, 0, 0, 0);
-            if (!in(u)) continue;
-            const int64_t at = int64_t(b) * p.apart + int64_t(m0 + row_of(u)) * p.ld + col;
-            if constexpr (MODE == SQUARE) {
-                const uint2 e = *reinterpret_cast<const uint2*>(p.e + at);
-                mem[u].x = e.x;
-                mem[u].y = e.y;
-            } else {
-                mem[u] = *reinterpret_cast<const uint4*>(p.x + at);
-            }
-        }
-    }
     if (p.splits > 1) cluster_sync(); else __syncthreads();
 
     float4 acc[16];
 #pragma unroll
     for (int q = 0; q < 16; ++q) {
         const uint32_t at = smem0 + uint32_t(row_of(q >> log) * kPartLd + c) * 4u;
-        acc[q] = log == 0 ? ld_shared_f32x4(at) : ld_cluster_f32x4(at, uint32_t(q & (p.splits - 1)));
+        const uint32_t from = uint32_t(q & (p.splits - 1));
+        acc[q] = from == rank ? ld_shared_f32x4(at) : ld_cluster_f32x4(at, from);
     }
     // the sums of a row, neighbours first: row u's end up in acc[u]
 #pragma unroll
@@ -584,6 +585,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 8 >> level; ++i)
                 acc[i] = make_float4(acc[2 * i].x + acc[2 * i + 1].x, acc[2 * i].y + acc[2 * i + 1].y, acc[2 * i].z + acc[2 * i + 1].z,
                                      acc[2 * i].w + acc[2 * i + 1].w);
+
+    if (p.splits > 1) cluster_arrive_relaxed();  // this thread has read what it reads of the others'
 
     uint16_t* turn = reinterpret_cast<uint16_t*>(smem + kTurn);
     const bool mirrored = SYM && mb != nb;
@@ -641,7 +644,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     *reinterpret_cast<const uint4*>(turn + i * kTurnLd + g);
         }
     }
-    if (p.splits > 1) cluster_sync();  // nobody leaves while its sums are read
+    if (p.splits > 1) cluster_wait_only();  // nobody leaves while its sums are read
     if (warp == 2) {
         tc_fence_after();
         tmem_dealloc<false>(tmem_base, 128);

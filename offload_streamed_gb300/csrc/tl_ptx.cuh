@@ -87,6 +87,13 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t saddr, uint32_t rank) {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
+// The same without ordering memory: for CTAs that only wait until the others
+// have read their shared memory (cluster_sync's release would also wait for the
+// threads' global stores).
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+    asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait_only() { asm volatile("barrier.cluster.wait;" ::: "memory"); }
 // Phase test with acquire at cluster scope: data another CTA of the cluster
 // stored before its (release.cluster) arrival is visible after success.
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
