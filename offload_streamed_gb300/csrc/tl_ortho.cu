@@ -851,8 +851,8 @@ cudaError_t launch(const void* kern, int grid, int cluster, size_t smem, cudaStr
 
 // Products of up to a quarter as many 256 x 256 tiles as there are CTA pairs go
 // through the small kernel.  The whole update, us, by pairs alone / with this
-// rule / with one three times as wide: 512 x 512 166 / 123 / 123, 128 x 512 116 /
-// 105 / 105, 1024 x 4096 279 / 203 / 227, 2048 x 2048 290 / 291 / 317.
+// rule / with one three times as wide: 512 x 512 166 / 105 / 105, 128 x 512 116 /
+// 97 / 97, 1024 x 4096 279 / 191 / 203, 2048 x 2048 290 / 290 / 315.
 bool small_product(int64_t pair_tiles, int num_sms) { return pair_tiles <= num_sms / 8; }
 
 template <bool A_MN, bool B_MN, int MODE>
@@ -883,8 +883,7 @@ cudaError_t product(const Half& a, const Half& b, int64_t m, int64_t n, int64_t 
     void* args[] = {&ma, &mb, &to, &p};
     if (small) {
         // CTAs of a cluster: as many as there are SMs for, with four K-blocks
-        // each.  512 x 512, us: two of 8 K-blocks 123, eight 154, one 157;
-        // 1024 x 4096: eight of 64 203, one 277.
+        // each.  512 x 512 (8 K-blocks), us: two CTAs 105, eight 134, one 124.
         p.splits = 1;
         while (p.splits < 8 && int64_t(p.num_tiles) * p.splits * 2 <= num_sms && p.num_k >= 4 * p.splits) p.splits *= 2;
         p.per = (p.num_k + p.splits - 1) / p.splits;
