@@ -260,3 +260,49 @@ def test_same_bits_and_another_stream(tl, T):
         b = tl.fp8_linear(x * 1, wq, ws)
     s.synchronize()
     assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32])
+@pytest.mark.parametrize("T", [3, 200])
+def test_other_types_of_x_and_strides(tl, T, dtype):
+    """The layer's one call gives what quantising and the products give, for every type and stride of x."""
+    x, w, dy = make(T, 300, 1, dtype, spread=0.5), make(300, 200, 2, spread=0.2), make(T, 200, 3, dtype, spread=0.5)
+    wq, ws = tl.fp8_quantize(w.cuda(), "tile")
+    xd, dyd = torch.zeros(T, 333, dtype=dtype, device="cuda")[:, 5:305], torch.zeros(T, 211, dtype=dtype, device="cuda")[:, :200]
+    xd.copy_(x)
+    dyd.copy_(dy)
+    assert torch.equal(tl.fp8_linear(xd, wq, ws), tl.fp8_matmul(tl.fp8_quantize(x.cuda(), "row"), (wq, ws)))
+    dx, dw = tl.fp8_linear_backward(xd, dyd, wq, ws)
+    row, col = tl.fp8_quantize(dy.cuda(), "row", "col")
+    assert torch.equal(dx, tl.fp8_matmul_dx(row, (wq, ws)))
+    assert torch.equal(dw, tl.fp8_matmul_dw(tl.fp8_quantize(x.cuda(), "col"), col))
+
+
+def test_offsets_past_32_bits(tl):
+    """More than 2^31 elements in x: the last rows' forms and products are theirs."""
+    T, K, n = 34000, 65536, 128
+    x = torch.empty(T, K, dtype=torch.bfloat16, device="cuda").normal_()
+    wq, ws = tl.fp8_quantize(make(K, n, 2, spread=0.1).cuda(), "tile")
+    y = tl.fp8_linear(x, wq, ws)
+    few = tl.fp8_linear(x[-300:].clone(), wq, ws)
+    assert torch.equal(y[-300:], few) or (y[-300:].float() - few.float()).norm() <= 2.0 ** -8 * few.float().norm()
+    q, s = tl.fp8_quantize(x, "row")
+    q1, s1 = tl.fp8_quantize(x[-2:].clone(), "row")
+    assert torch.equal(q[-2:].view(torch.uint8), q1.view(torch.uint8)) and torch.equal(s[:, -2:], s1)
+
+
+def test_refusals_of_the_functions(tl):
+    """What does not fit is refused with a message before anything runs."""
+    w = make(256, 128, 1).cuda()
+    wq, ws = tl.fp8_quantize(w, "tile")
+    x = make(4, 256, 2).cuda()
+    for fn, words in ((lambda: tl.fp8_linear(x[:, :255], wq, ws), "fit"), (lambda: tl.fp8_linear(x, wq, ws[:, :0]), "scales"),
+                      (lambda: tl.fp8_linear(x, wq.float(), ws), "float8"), (lambda: tl.fp8_linear(x.double(), wq, ws), "dtype"),
+                      (lambda: tl.fp8_linear(x, wq[:, 1:], ws), "16-byte"), (lambda: tl.fp8_quantize(x, "rows"), "form"),
+                      (lambda: tl.fp8_quantize(x), "form"), (lambda: tl.fp8_quantize(x, "row", format="e3m4"), "format"),
+                      (lambda: tl.fp8_quantize(x.T, "row"), "contiguous"), (lambda: tl.fp8_linear(x.cpu(), wq, ws), "CUDA"),
+                      (lambda: tl.fp8_matmul(tl.fp8_quantize(x, "col"), (wq, ws)), "scales"),
+                      (lambda: tl.fp8_linear_backward(x, x, wq, ws), "fit")):
+        with pytest.raises(tl.TiledLinearError) as e:
+            fn()
+        assert e.value.status == tl.TL_ERR_INVALID and words in str(e.value), e.value

@@ -239,3 +239,20 @@ def test_norm_on_another_stream(tl):
         got = tl.layer_norm(x2, wd, bd)[0]
     s.synchronize()
     assert torch.equal(got, want)
+
+
+def test_norm_offsets_past_32_bits(tl):
+    """More than 2^31 elements: the last rows are where they belong."""
+    rows, cols = 36000, 65536
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda").normal_()
+    w, b = torch.ones(cols, device="cuda"), torch.zeros(cols, device="cuda")
+    y, mean, rstd = tl.layer_norm(x, w, b)
+    last = x[-3:].cpu()
+    y64, m64, r64, _ = forward64(last, w.cpu(), b.cpu(), 1e-5)
+    assert torch.allclose(mean[-3:].double().cpu(), m64, atol=1e-6) and torch.allclose(rstd[-3:].double().cpu(), r64, rtol=1e-5)
+    assert torch.allclose(y[-3:].double().cpu(), y64, rtol=2.0 ** -8, atol=1e-5)
+    dx, dw, db = tl.layer_norm_backward(x, x, mean, rstd, w)  # dy = x
+    want = backward64(last, last, mean[-3:].cpu(), rstd[-3:].cpu(), w.cpu())[0]
+    assert torch.allclose(dx[-3:].double().cpu(), want, rtol=2.0 ** -8, atol=1e-4)
+    # dbias = column sums of x: 36000 terms of size one, fp32 (36000 u times their magnitudes, about 30000)
+    assert torch.allclose(db[:64].double().cpu(), x[:, :64].double().sum(0).cpu(), atol=36000 * U * 30000)
