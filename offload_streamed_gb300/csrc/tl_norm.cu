@@ -21,10 +21,10 @@
 //    belong to one warp (shuffles alone); longer ones to a CTA, or to a
 //    cluster of up to eight when a CTA cannot hold them.  There every
 //    warp leaves its sums for all others, and one barrier a row is all there is.
-// Measured: 8192 x 8192 bf16 forward 59 us (4.5 TB/s), backward 83 us (4.8 TB/s,
-// its reduction included), 8 x 8192 3.7 and 6.9 us.  What bounds them is the
-// latency of a row's chain (copy, sums, barrier, write) with the two rows that an
-// SM's registers and shared memory leave in flight.
+// Measured: 8192 x 8192 bf16 forward 57 us (4.7 TB/s), backward 81 us (5.0 TB/s,
+// its reduction included); 2048 x 65536, clusters of eight, 133 and 183 us (4.0
+// and 4.4 TB/s).  DRAM is about half busy at 8192 x 8192, with 15 warps an SM;
+// what their counted stalls wait for most is shared memory.
 // All statistics and sums are fp32.  A row's variance is joined from the
 // warps' sums of squares about their own means, which loses nothing to
 // cancellation, whatever the row's mean.  Every order of summation is fixed by
@@ -99,7 +99,7 @@ __device__ __forceinline__ void cluster_barrier() {
 // its entry to every CTA; the stores carry their own completion to the
 // receiving CTA's mbarrier, so that no fence waits for the row's other writes
 // (a cluster barrier's release does: 2048 x 65536 bf16 forward 258 us with it,
-// 214 us with this).
+// 214 us with this, both measured with a grid of more clusters than run at a time).
 // Two mbarriers and two buffers in turn: a CTA sends for the row after next
 // only once it has had the next row's entries from all, and each of those was
 // sent by a warp that was done with this row.
@@ -814,13 +814,25 @@ cudaError_t make_plan(const NormDesc& d, bool backward, int num_sms, Plan* out) 
     const int64_t units = p.warp_row ? (d.rows + kWarpRowWarps - 1) / kWarpRowWarps : d.rows;
     const int64_t sms = std::min(num_sms, kMaxSms);
     int64_t room = std::max<int64_t>(1, sms * per_sm / p.cluster);
+    // More clusters than run at a time would begin their rows when the others had
+    // done theirs.  Forward / backward, us, with as many as run / with as many as
+    // the SMs' CTAs would make: 2048 x 65536 bf16 133 / 183 and 205 / 253, 4096 x
+    // 32768 124 / 171 and 201 / 244.
+    if (p.cluster > 1) {
+        int clusters = 0;
+        const cudaError_t c = clusters_at_a_time(reinterpret_cast<const void*>(p.kernel), p.threads, p.smem, p.cluster, &clusters);
+        if (c != cudaSuccess) return c;
+        if (clusters < 1) return cudaErrorInvalidConfiguration;
+        room = std::min<int64_t>(room, clusters);
+    }
     // Each CTA of the backward also writes a sum for every column, which the
     // reduction reads: with few rows, fewer CTAs that walk over several of them
     // do less in all, as long as their rows come ahead of them.  Backward, us,
     // with this / with a row a CTA: 512 x 8192 bf16 22 / 33, 256 x 4096 12 / 18,
     // 300 x 30000 44 / 54.  (Two an SM where elements come one by one: 517 x
     // 5003 fp32 24 / 33, with one 30.)
-    if (backward && p.ring > 1 && units < 8 * room) room = std::max({int64_t(1), sms / p.cluster * (vec > 1 ? 1 : 2), units / 8});
+    if (backward && p.ring > 1 && units < 8 * room)
+        room = std::min(room, std::max({int64_t(1), sms / p.cluster * (vec > 1 ? 1 : 2), units / 8}));
     p.grid = int(std::min(units, std::min(room, norm_partials(d.rows, d.cols)))) * p.cluster;
     *out = p;
     return cudaSuccess;
