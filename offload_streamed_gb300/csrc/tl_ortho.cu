@@ -883,13 +883,22 @@ cudaError_t product(const Half& a, const Half& b, int64_t m, int64_t n, int64_t 
     void* args[] = {&ma, &mb, &to, &p};
     if (small) {
         // CTAs of a cluster: as many as there are SMs for, with four K-blocks
-        // each.  512 x 512 (8 K-blocks), us: two CTAs 105, eight 134, one 124.
+        // each, and as many clusters as run at a time.  512 x 512 (8 K-blocks),
+        // us: two CTAs 105, eight 134, one 124.  With / without that last bound:
+        // 6 x 200 x 4096 196 / 221, 6 x 256 x 2048 148 / 175.
         p.splits = 1;
-        while (p.splits < 8 && int64_t(p.num_tiles) * p.splits * 2 <= num_sms && p.num_k >= 4 * p.splits) p.splits *= 2;
+        const void* kern = reinterpret_cast<const void*>(ortho_small_kernel<A_MN, B_MN, MODE>);
+        int per_sm = 0, clusters = 0;
+        cudaError_t e = ctas_per_sm(kern, kThreads, kSmallSmem, &per_sm);
+        while (e == cudaSuccess && p.splits < 8 && int64_t(p.num_tiles) * p.splits * 2 <= num_sms && p.num_k >= 4 * p.splits) {
+            e = clusters_at_a_time(kern, kThreads, kSmallSmem, 2 * p.splits, &clusters);
+            if (e != cudaSuccess || p.num_tiles > clusters) break;
+            p.splits *= 2;
+        }
+        if (e != cudaSuccess) return e;
         p.per = (p.num_k + p.splits - 1) / p.splits;
         void* few[] = {&ma, &mb, &p};
-        return launch(reinterpret_cast<const void*>(ortho_small_kernel<A_MN, B_MN, MODE>), p.num_tiles * p.splits, p.splits, kSmallSmem,
-                      stream, few);
+        return launch(kern, p.num_tiles * p.splits, p.splits, kSmallSmem, stream, few);
     }
     const int slots = std::max(1, num_sms / 2);
     choose_tile_order(k, 256, p.num_m, p.num_n, slots, &p.raster, &p.group, &p.stream_shared);
