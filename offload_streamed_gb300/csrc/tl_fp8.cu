@@ -697,16 +697,31 @@ cudaError_t launch_clusters(void (*kern)(A...), dim3 grid, int cluster, size_t s
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
+// Asked about, never launched: how many clusters of fp8_few_kernel's threads and
+// shared memory run at a time.  For a kernel that uses tensor memory the runtime
+// answers for one CTA an SM, whatever it allocates; two of fp8_few_kernel fit
+// (twice its kCols are at most 512 columns) and are seen to run.
+__global__ void __launch_bounds__(kThreads, 2) few_shape_kernel() {}
+
 template <bool W_MN, int N>
 cudaError_t launch_few(const CUtensorMap& mw, const CUtensorMap& mt, Fp8Params p, const Fp8GemmDesc& g, int num_sms, cudaStream_t stream) {
     p.idesc = idesc_fp8(128, N, W_MN, false, g.b.format, g.a.format);
     const int tiles = (p.m_dim + 127) / 128;
     const int blocks = (p.n_dim + N - 1) / N;
-    // CTAs of a cluster: as many as two an SM allow, with two K-blocks each.
-    // (8192 x 8192, one token: 4 of 64 tiles' 15.0 us.  25600 x 6400: 4 of 50
-    // tiles' 29.6 us, 8 34.5 us, 6 41.2 us, which pack badly.)
-    int splits = 1;
-    while (splits < 8 && int64_t(tiles) * blocks * splits * 2 <= 2 * num_sms && p.num_k >= 4 * splits) splits *= 2;
+    // CTAs of a cluster: as many as two an SM allow, with two K-blocks each and
+    // all clusters at a time.  One token, us, with 2 / 4 / 8: 8192 x 1024 (8
+    // tiles) 15.7 / 10.1 / 7.6, 16384 x 4736 (37) 26.9 / 16.8 / 22.3, 25600 x 6400
+    // (50) 40.4 / 28.8 / 33.9, 8192 x 8192 (64) 16.7 / 14.9 / 18.0, 8192 x 9728
+    // (76) 17.1 / 22.9 / 23.4.
+    int splits = 1, per_sm = 0, clusters = 0;
+    const void* shape = reinterpret_cast<const void*>(few_shape_kernel);
+    cudaError_t e = ctas_per_sm(shape, kThreads, Few<N>::kSmem, &per_sm);
+    while (e == cudaSuccess && splits < 8 && int64_t(tiles) * blocks * splits * 2 <= 2 * num_sms && p.num_k >= 4 * splits) {
+        e = clusters_at_a_time(shape, kThreads, Few<N>::kSmem, 2 * splits, &clusters);
+        if (e != cudaSuccess || int64_t(tiles) * blocks > clusters) break;
+        splits *= 2;
+    }
+    if (e != cudaSuccess) return e;
     const int per = (p.num_k + splits - 1) / splits;
     return launch_clusters(fp8_few_kernel<W_MN, N>, dim3(unsigned(tiles * splits), unsigned(blocks)), splits, Few<N>::kSmem, g.early, stream, mw, mt, p,
                            static_cast<__nv_bfloat16*>(g.d), g.ldd, splits, per);
