@@ -418,7 +418,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 // of them, in a fixed order.
 constexpr int kSmallStages = 6;
 constexpr int kPartLd = 132;  // floats of a row of sums: 16-byte accesses of a column of lanes meet no bank twice
-constexpr int kTurnLd = 136;  // halves of a row of the turned tile
+// Halves of a row of the turned tile: a warp's 4-byte writes, four rows apart, meet
+// each bank four times.  (136, which allows 16-byte reads, with 2-byte writes: 16
+// times.  The whole update, us, with this / with that: 4 x 200 x 520 102 / 111,
+// 512 x 512 98 / 104, 3 x 777 x 130 110 / 126, 1024 x 4096 187 / 192.)
+constexpr int kTurnLd = 130;
 constexpr uint32_t kTurn = 128 * kPartLd * 4;  // where the turned tile is, after the sums
 constexpr size_t kSmallSmem = size_t(kSmallStages) * 2 * kHalfStage + kBarBytes + 1024;
 static_assert(size_t(kTurn) + 128 * kTurnLd * 2 <= size_t(kSmallStages) * 2 * kHalfStage, "sums and turned tile fit the stages");
@@ -481,14 +485,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     grid_dependents_go();
     grid_dependency_wait();
 
-    // This CTA finishes rows [r0, r0 + rows) of the tile, a warp every eighth of
+    // This CTA finishes rows [r0, r0 + rows) of the tile, a warp an eighth of
     // them, a lane four columns: 16 / splits rows a warp, with `splits` sums each.
     // What the rows need from global memory is asked for first of all, and
     // all sixteen reads of sums are under way before one is used.
     const int rows = 128 / p.splits, r0 = int(rank) * rows, log = 31 - __clz(p.splits);
     const int c = lane * 4, col = n0 + c;
     uint4 mem[16];
-    auto row_of = [&](int u) { return r0 + warp + 8 * u; };
+    auto row_of = [&](int u) { return r0 + (warp << (4 - log)) + u; };
     auto in = [&](int u) { return u < 16 >> log && m0 + row_of(u) < p.m_dim && col < p.n_dim; };
     if constexpr (MODE != GRAM) {
 #pragma unroll
@@ -590,6 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     uint16_t* turn = reinterpret_cast<uint16_t*>(smem + kTurn);
     const bool mirrored = SYM && mb != nb;
+    uint2 above = make_uint2(0, 0);  // the halves of the row before
 #pragma unroll
     for (int u = 0; u < 16; ++u) {
         if (u >= 16 >> log) break;
@@ -627,9 +632,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             else
                 for (int j = 0; col + j < p.n_dim; ++j) dst[j] = h[j];
         }
-        if (mirrored) {
+        if (mirrored) {  // a column's halves of two rows at a time (a warp has at least two)
+            if (u & 1) {
+                const uint32_t two[4] = {__byte_perm(above.x, w.x, 0x5410), __byte_perm(above.x, w.x, 0x7632),
+                                         __byte_perm(above.y, w.y, 0x5410), __byte_perm(above.y, w.y, 0x7632)};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) turn[(c + j) * kTurnLd + (r - r0)] = h[j];
+                for (int j = 0; j < 4; ++j) *reinterpret_cast<uint32_t*>(turn + (c + j) * kTurnLd + (r - r0 - 1)) = two[j];
+            }
+            above = w;
         }
     }
     if (mirrored) {
@@ -639,9 +649,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int idx = int(threadIdx.x); idx < 128 * groups; idx += kThreads) {
             const int i = idx / groups, g = idx % groups * 8;
             const int row = n0 + i, at = m0 + r0 + g;
+            const uint32_t* from = reinterpret_cast<const uint32_t*>(turn + i * kTurnLd + g);
             if (row < p.n_dim && at < p.m_dim)
                 *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + int64_t(b) * p.o_apart + int64_t(row) * p.ldo + at) =
-                    *reinterpret_cast<const uint4*>(turn + i * kTurnLd + g);
+                    make_uint4(from[0], from[1], from[2], from[3]);
         }
     }
     if (p.splits > 1) cluster_wait_only();  // nobody leaves while its sums are read
