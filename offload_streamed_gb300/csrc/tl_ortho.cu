@@ -863,7 +863,8 @@ cudaError_t launch(const void* kern, int grid, int cluster, size_t smem, cudaStr
 // Products of up to a quarter as many 256 x 256 tiles as there are CTA pairs go
 // through the small kernel.  The whole update, us, by pairs alone / with this
 // rule / with one three times as wide: 512 x 512 166 / 105 / 105, 128 x 512 116 /
-// 97 / 97, 1024 x 4096 279 / 191 / 203, 2048 x 2048 290 / 290 / 315.
+// 97 / 97, 1024 x 4096 279 / 191 / 203, 2048 x 2048 290 / 290 / 315 (all with the
+// turned tiles' writes as they were before kTurnLd's).
 bool small_product(int64_t pair_tiles, int num_sms) { return pair_tiles <= num_sms / 8; }
 
 template <bool A_MN, bool B_MN, int MODE>
