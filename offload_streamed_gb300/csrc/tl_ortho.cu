@@ -590,7 +590,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 acc[i] = make_float4(acc[2 * i].x + acc[2 * i + 1].x, acc[2 * i].y + acc[2 * i + 1].y, acc[2 * i].z + acc[2 * i + 1].z,
                                      acc[2 * i].w + acc[2 * i + 1].w);
 
-    if (p.splits > 1) cluster_arrive_relaxed();  // this thread has read what it reads of the others'
+    // This thread has read what it reads of the others' sums.  The arrival has to
+    // release: a relaxed one may pass the loads, and the other CTAs, gone, would
+    // leave their shared memory to the next launch's.  Nothing has been stored
+    // yet that it could wait for.
+    if (p.splits > 1) cluster_arrive();
 
     uint16_t* turn = reinterpret_cast<uint16_t*>(smem + kTurn);
     const bool mirrored = SYM && mb != nb;
@@ -655,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     make_uint4(from[0], from[1], from[2], from[3]);
         }
     }
-    if (p.splits > 1) cluster_wait_only();  // nobody leaves while its sums are read
+    if (p.splits > 1) cluster_wait();  // nobody leaves while its sums are read
     if (warp == 2) {
         tc_fence_after();
         tmem_dealloc<false>(tmem_base, 128);
