@@ -420,8 +420,9 @@ constexpr int kSmallStages = 6;
 constexpr int kPartLd = 132;  // floats of a row of sums: 16-byte accesses of a column of lanes meet no bank twice
 // Halves of a row of the turned tile: a warp's 4-byte writes, four rows apart, meet
 // each bank four times.  (136, which allows 16-byte reads, with 2-byte writes: 16
-// times.  The whole update, us, with this / with that: 4 x 200 x 520 102 / 111,
-// 512 x 512 98 / 104, 3 x 777 x 130 110 / 126, 1024 x 4096 187 / 192.)
+// times.  The whole update, us, with this / with that, both before the ninth warp
+// (kSmallThreads): 4 x 200 x 520 102 / 111, 512 x 512 98 / 104, 3 x 777 x 130 110 /
+// 126, 1024 x 4096 187 / 192.)
 constexpr int kTurnLd = 130;
 constexpr uint32_t kTurn = 128 * kPartLd * 4;  // where the turned tile is, after the sums
 constexpr size_t kSmallSmem = size_t(kSmallStages) * 2 * kHalfStage + kBarBytes + 1024;
@@ -433,8 +434,16 @@ __device__ __forceinline__ float4 ld_shared_f32x4(uint32_t a) {
     return v;
 }
 
+// The warps that finish rows go on as soon as they have read the others' sums.  A
+// ninth waits for their reads and arrives with release semantics at the barrier
+// past which the others may leave: a relaxed arrival is not ordered after the
+// reads, and a releasing one holds its warp up.  The whole update, us, with this /
+// with a releasing arrival of every warp: 4 x 200 x 520 107 / 125, 512 x 512 103 /
+// 118, 1024 x 4096 189 / 198, 3 x 777 x 130 114 / 116.
+constexpr int kSmallThreads = kThreads + 32;
+
 template <bool A_MN, bool B_MN, int MODE>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kSmallThreads, 1)
     ortho_small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const OrthoParams p) {
     const WaitCtx wc{p.err, p.timeout_ns};
     constexpr int S = kSmallStages;
@@ -494,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint4 mem[16];
     auto row_of = [&](int u) { return r0 + (warp << (4 - log)) + u; };
     auto in = [&](int u) { return u < 16 >> log && m0 + row_of(u) < p.m_dim && col < p.n_dim; };
-    if constexpr (MODE != GRAM) {
+    if (MODE != GRAM && warp < kThreads / 32) {
 #pragma unroll
         for (int u = 0; u < 16; ++u) {
             mem[u] = make_uint4(0, 0, 0, 0);
@@ -554,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             umma_commit(done_bar);
             wait_bounded(done_bar, 0, wc, kErrDrainWait, false);
         }
-    } else if (warp >= kFirstEpilogueWarp) {
+    } else if (warp >= kFirstEpilogueWarp && warp < kThreads / 32) {
         const int q = warp & 3, i = q * 32 + lane;
         const bool ok = warp_wait(done_bar, 0, wc, kErrEpilogueWait, lane);
         tc_fence_after();
@@ -574,6 +583,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (p.splits > 1) cluster_sync(); else __syncthreads();
 
+    if (warp == kThreads / 32) {
+        if (p.splits > 1) {
+            cta_barrier_sync(1, kSmallThreads);  // the others' reads are done
+            cluster_arrive();
+            cluster_wait();
+        }
+        return;
+    }
     float4 acc[16];
 #pragma unroll
     for (int q = 0; q < 16; ++q) {
@@ -590,11 +607,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 acc[i] = make_float4(acc[2 * i].x + acc[2 * i + 1].x, acc[2 * i].y + acc[2 * i + 1].y, acc[2 * i].z + acc[2 * i + 1].z,
                                      acc[2 * i].w + acc[2 * i + 1].w);
 
-    // This thread has read what it reads of the others' sums.  The arrival has to
-    // release: a relaxed one may pass the loads, and the other CTAs, gone, would
-    // leave their shared memory to the next launch's.  Nothing has been stored
-    // yet that it could wait for.
-    if (p.splits > 1) cluster_arrive();
+    if (p.splits > 1) {
+        cta_barrier_arrive(1, kSmallThreads);
+        cluster_arrive_relaxed();  // (the ninth warp's arrival orders the reads)
+    }
 
     uint16_t* turn = reinterpret_cast<uint16_t*>(smem + kTurn);
     const bool mirrored = SYM && mb != nb;
@@ -647,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     if (mirrored) {
-        __syncthreads();
+        cta_barrier_sync(2, kThreads);
         // column i of these rows is row n0 + i of the result, from column m0 + r0 on
         const int groups = rows / 8;
         for (int idx = int(threadIdx.x); idx < 128 * groups; idx += kThreads) {
@@ -843,13 +859,13 @@ struct Half {
     int64_t inner, outer, ld, apart;
 };
 
-cudaError_t launch(const void* kern, int grid, int cluster, size_t smem, cudaStream_t stream, void** args) {
+cudaError_t launch(const void* kern, int threads, int grid, int cluster, size_t smem, cudaStream_t stream, void** args) {
     int per_sm = 0;
-    const cudaError_t e = ctas_per_sm(kern, kThreads, smem, &per_sm);
+    const cudaError_t e = ctas_per_sm(kern, threads, smem, &per_sm);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(unsigned(grid));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(unsigned(threads));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -901,25 +917,26 @@ cudaError_t product(const Half& a, const Half& b, int64_t m, int64_t n, int64_t 
         // CTAs of a cluster: as many as there are SMs for, with four K-blocks
         // each, and as many clusters as run at a time.  512 x 512 (8 K-blocks),
         // us: two CTAs 105, eight 134, one 124.  With / without that last bound:
-        // 6 x 200 x 4096 196 / 221, 6 x 256 x 2048 148 / 175.
+        // 6 x 200 x 4096 196 / 221, 6 x 256 x 2048 148 / 175.  (Both before
+        // kTurnLd and kSmallThreads.)
         p.splits = 1;
         const void* kern = reinterpret_cast<const void*>(ortho_small_kernel<A_MN, B_MN, MODE>);
         int per_sm = 0, clusters = 0;
-        cudaError_t e = ctas_per_sm(kern, kThreads, kSmallSmem, &per_sm);
+        cudaError_t e = ctas_per_sm(kern, kSmallThreads, kSmallSmem, &per_sm);
         while (e == cudaSuccess && p.splits < 8 && int64_t(p.num_tiles) * p.splits * 2 <= num_sms && p.num_k >= 4 * p.splits) {
-            e = clusters_at_a_time(kern, kThreads, kSmallSmem, 2 * p.splits, &clusters);
+            e = clusters_at_a_time(kern, kSmallThreads, kSmallSmem, 2 * p.splits, &clusters);
             if (e != cudaSuccess || p.num_tiles > clusters) break;
             p.splits *= 2;
         }
         if (e != cudaSuccess) return e;
         p.per = (p.num_k + p.splits - 1) / p.splits;
         void* few[] = {&ma, &mb, &p};
-        return launch(kern, p.num_tiles * p.splits, p.splits, kSmallSmem, stream, few);
+        return launch(kern, kSmallThreads, p.num_tiles * p.splits, p.splits, kSmallSmem, stream, few);
     }
     const int slots = std::max(1, num_sms / 2);
     choose_tile_order(k, 256, p.num_m, p.num_n, slots, &p.raster, &p.group, &p.stream_shared);
-    return launch(reinterpret_cast<const void*>(ortho_kernel<A_MN, B_MN, MODE>), 2 * std::min(p.num_tiles, slots), 2, kOrthoSmem, stream,
-                  args);
+    return launch(reinterpret_cast<const void*>(ortho_kernel<A_MN, B_MN, MODE>), kThreads, 2 * std::min(p.num_tiles, slots), 2,
+                  kOrthoSmem, stream, args);
 }
 
 }  // namespace

@@ -87,13 +87,21 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t saddr, uint32_t rank) {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
+// A CTA's barrier `id` (0 is __syncthreads') for `threads` of its threads: arrive,
+// or arrive and wait.  What a thread has accessed before it arrives is done once
+// a thread has waited.
+__device__ __forceinline__ void cta_barrier_arrive(int id, int threads) {
+    asm volatile("barrier.cta.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ void cta_barrier_sync(int id, int threads) {
+    asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
 // The same in two halves: what a thread has read or written before it arrives is
 // done once any thread of the cluster has waited.
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
-// The same without ordering memory: for CTAs that only wait until the others
-// have read their shared memory (cluster_sync's release would also wait for the
-// threads' global stores).
+// An arrival that orders nothing: for threads whose accesses the arrival of another
+// thread of their CTA orders.
 __device__ __forceinline__ void cluster_arrive_relaxed() {
     asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
 }

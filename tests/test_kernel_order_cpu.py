@@ -17,14 +17,22 @@ def code(name):
 
 @pytest.mark.parametrize("name,kernel", [("tl_ortho.cu", "ortho_small_kernel(")])
 def test_ctas_part_after_their_remote_reads(name, kernel):
-    """A CTA that reads another's shared memory arrives with release semantics before the other may leave: a relaxed
-    arrival is not ordered after the loads."""
+    """A CTA that reads another's shared memory has done so before the other may leave: every relaxed arrival at the
+    cluster's barrier, which is not ordered after the reads, comes after one at a barrier of the CTA, and the warp that
+    waits there arrives at the cluster's with release semantics."""
     src = code(name)
     body = src[src.index(kernel):]
     body = body[:body.index("\n}\n")]
-    after = body[body.rindex("ld_cluster_f32x4("):]
-    assert re.search(r"\bcluster_arrive\(\)|\bcluster_sync\(\)", after), "no releasing arrival after the remote reads"
-    assert "relaxed" not in after
+    last = body.rindex("ld_cluster_f32x4(")
+    relaxed = [m.start() for m in re.finditer(r"cluster_arrive_relaxed\(\)", body)]
+    if relaxed:
+        (handed,) = re.finditer(r"cta_barrier_arrive\((\d), (\w+)\);", body)
+        assert last < handed.start() < min(relaxed)
+        taken = body.index("cta_barrier_sync(%s, %s);" % handed.groups())
+        assert re.match(r"\s*cluster_arrive\(\);\s*cluster_wait\(\);", body[taken:].split(";", 1)[1])
+    else:
+        assert re.search(r"\bcluster_arrive\(\)|\bcluster_sync\(\)", body[last:])
+    assert re.search(r"\bcluster_wait\(\)", body[last:])
     ptx = code("tl_ptx.cuh")
     for fn, words in (("cluster_arrive", "barrier.cluster.arrive.release;"), ("cluster_wait", "barrier.cluster.wait.acquire;")):
         assert re.search(r"void %s\(\) \{ asm volatile\(\"%s\"" % (fn, re.escape(words)), ptx), fn
