@@ -445,6 +445,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ---- few tokens --------------------------------------------------------------
 
 constexpr int kFewTokens = 128;
+// A ninth warp: when the others have read the parts of the sums, it arrives with
+// release semantics at the barrier past which the cluster's CTAs may leave.
+constexpr int kFewThreads = kThreads + 32;
 constexpr size_t kFewSmem = 112 * 1024;  // of a CTA: two share an SM
 constexpr uint32_t kFewSfSlots = 4, kFewSfSlot = 1024;
 
@@ -474,7 +477,7 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t local, uint32_t rank
 // map_w: the weight, 128 of its own indices a box; map_t: the tokens, N a box.
 // w: m_dim = own indices of the weight, n_dim = tokens.  out[token][index].
 template <bool W_MN, int N>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kFewThreads, 2)
     fp8_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_t, const Fp8Params p,
                    __nv_bfloat16* out, int64_t ldo, int splits, int per) {
     using F = Few<N>;
@@ -602,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(sf_full_bar(q));
             }
-    } else if (warp >= kFirstEpilogueWarp) {
+    } else if (warp >= kFirstEpilogueWarp && warp < kThreads / 32) {
         grid_dependency_wait();  // (the result may be what the kernel before this one reads)
         const int q = warp & 3, i = q * 32 + lane;
         const bool ok = warp_wait(done_bar, 0, wc, kErrEpilogueWait, lane);
@@ -629,27 +632,47 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     if (splits > 1) {
         cluster_sync();  // every part stands
-        for (int e = int(rank) * kThreads + int(threadIdx.x); e < tokens * 32; e += splits * kThreads) {
-            const int t = e / 32, i = e % 32 * 4;
-            float4 v[8];
+        if (warp == kThreads / 32) {
+            cta_barrier_sync(1, kFewThreads);  // the others' reads are done
+            cluster_arrive();
+        } else {
+            // Four outputs of a token at a time; at most this many of a thread,
+            // with two CTAs.  All are read and summed before one is written:
+            // nobody waits for the writes.
+            constexpr int kMine = N * 32 / (2 * kThreads);
+            uint2 w[kMine];
+            const int e0 = int(rank) * kThreads + int(threadIdx.x), step = splits * kThreads;
 #pragma unroll
-            for (int r = 0; r < 8; ++r)
-                if (r < splits) v[r] = ld_cluster_f32x4(smem0 + uint32_t(t * 128 + i) * 4u, uint32_t(r));
-            float4 sum = v[0];
+            for (int u = 0; u < kMine; ++u) {
+                const int e = e0 + u * step;
+                if (e >= tokens * 32) break;
+                float4 v[8];
 #pragma unroll
-            for (int r = 1; r < 8; ++r)
-                if (r < splits) sum = make_float4(sum.x + v[r].x, sum.y + v[r].y, sum.z + v[r].z, sum.w + v[r].w);
-            __nv_bfloat16* dst = out + int64_t(t0 + t) * ldo + m0 + i;
-            if (m0 + i + 4 <= p.m_dim) {  // (rows of the result start on 16 bytes, so i does on 8)
-                *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
-            } else {
-                const float f[4] = {sum.x, sum.y, sum.z, sum.w};
-                for (int j = 0; j < 4; ++j)
-                    if (m0 + i + j < p.m_dim) dst[j] = __float2bfloat16_rn(f[j]);
+                for (int r = 0; r < 8; ++r)
+                    if (r < splits) v[r] = ld_cluster_f32x4(smem0 + uint32_t(e / 32 * 128 + e % 32 * 4) * 4u, uint32_t(r));
+                float4 sum = v[0];
+#pragma unroll
+                for (int r = 1; r < 8; ++r)
+                    if (r < splits) sum = make_float4(sum.x + v[r].x, sum.y + v[r].y, sum.z + v[r].z, sum.w + v[r].w);
+                w[u] = make_uint2(pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
+            }
+            cta_barrier_arrive(1, kFewThreads);
+            cluster_arrive_relaxed();  // (the ninth warp's arrival orders the reads)
+#pragma unroll
+            for (int u = 0; u < kMine; ++u) {
+                const int e = e0 + u * step, i = e % 32 * 4;
+                if (e >= tokens * 32) break;
+                __nv_bfloat16* dst = out + int64_t(t0 + e / 32) * ldo + m0 + i;
+                if (m0 + i + 4 <= p.m_dim) {  // (rows of the result start on 16 bytes, so i does on 8)
+                    *reinterpret_cast<uint2*>(dst) = w[u];
+                } else {
+                    const uint32_t h[4] = {w[u].x, w[u].x >> 16, w[u].y, w[u].y >> 16};
+                    for (int j = 0; j < 4; ++j)
+                        if (m0 + i + j < p.m_dim) dst[j] = __ushort_as_bfloat16(uint16_t(h[j]));
+                }
             }
         }
-        cluster_arrive_relaxed();  // nobody leaves while its part is read
-        cluster_wait_only();
+        cluster_wait();  // nobody leaves while its part is read
     } else {
         __syncthreads();
     }
@@ -675,14 +698,14 @@ struct Same {
 // early: the kernel may begin before the one ahead of it in the stream has
 // completed (it waits for that where it has to).
 template <typename... A>
-cudaError_t launch_clusters(void (*kern)(A...), dim3 grid, int cluster, size_t smem, bool early, cudaStream_t stream,
+cudaError_t launch_clusters(void (*kern)(A...), dim3 grid, int threads, int cluster, size_t smem, bool early, cudaStream_t stream,
                             typename Same<A>::type... args) {
     int per_sm = 0;
-    const cudaError_t e = ctas_per_sm(reinterpret_cast<const void*>(kern), kThreads, smem, &per_sm);
+    const cudaError_t e = ctas_per_sm(reinterpret_cast<const void*>(kern), threads, smem, &per_sm);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.blockDim = dim3(unsigned(threads), 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -701,7 +724,7 @@ cudaError_t launch_clusters(void (*kern)(A...), dim3 grid, int cluster, size_t s
 // shared memory run at a time.  For a kernel that uses tensor memory the runtime
 // answers for one CTA an SM, whatever it allocates; two of fp8_few_kernel fit
 // (twice its kCols are at most 512 columns) and are seen to run.
-__global__ void __launch_bounds__(kThreads, 2) few_shape_kernel() {}
+__global__ void __launch_bounds__(kFewThreads, 2) few_shape_kernel() {}
 
 template <bool W_MN, int N>
 cudaError_t launch_few(const CUtensorMap& mw, const CUtensorMap& mt, Fp8Params p, const Fp8GemmDesc& g, int num_sms, cudaStream_t stream) {
@@ -715,16 +738,16 @@ cudaError_t launch_few(const CUtensorMap& mw, const CUtensorMap& mt, Fp8Params p
     // (76) 17.1 / 22.9 / 23.4.
     int splits = 1, per_sm = 0, clusters = 0;
     const void* shape = reinterpret_cast<const void*>(few_shape_kernel);
-    cudaError_t e = ctas_per_sm(shape, kThreads, Few<N>::kSmem, &per_sm);
+    cudaError_t e = ctas_per_sm(shape, kFewThreads, Few<N>::kSmem, &per_sm);
     while (e == cudaSuccess && splits < 8 && int64_t(tiles) * blocks * splits * 2 <= 2 * num_sms && p.num_k >= 4 * splits) {
-        e = clusters_at_a_time(shape, kThreads, Few<N>::kSmem, 2 * splits, &clusters);
+        e = clusters_at_a_time(shape, kFewThreads, Few<N>::kSmem, 2 * splits, &clusters);
         if (e != cudaSuccess || int64_t(tiles) * blocks > clusters) break;
         splits *= 2;
     }
     if (e != cudaSuccess) return e;
     const int per = (p.num_k + splits - 1) / splits;
-    return launch_clusters(fp8_few_kernel<W_MN, N>, dim3(unsigned(tiles * splits), unsigned(blocks)), splits, Few<N>::kSmem, g.early, stream, mw, mt, p,
-                           static_cast<__nv_bfloat16*>(g.d), g.ldd, splits, per);
+    return launch_clusters(fp8_few_kernel<W_MN, N>, dim3(unsigned(tiles * splits), unsigned(blocks)), kFewThreads, splits, Few<N>::kSmem, g.early,
+                           stream, mw, mt, p, static_cast<__nv_bfloat16*>(g.d), g.ldd, splits, per);
 }
 
 // The few-token kernel with the operands' sides exchanged: g.b is the weight.
@@ -811,7 +834,7 @@ cudaError_t fp8_gemm_launch(const Fp8GemmDesc& g, int num_sms, cudaStream_t stre
     p.timeout_ns = 2000000000ull;
     p.idesc = idesc_fp8(256, 256, g.a.mn_major, g.b.mn_major, g.a.format, g.b.format);
     const int grid = 2 * std::min(p.num_tiles, slots);
-    auto run = [&](auto kern) { return launch_clusters(kern, dim3(unsigned(grid)), 2, kSmemPair, false, stream, ma, mb, md, p); };
+    auto run = [&](auto kern) { return launch_clusters(kern, dim3(unsigned(grid)), kThreads, 2, kSmemPair, false, stream, ma, mb, md, p); };
     cudaError_t e;
     if (g.a.mn_major) e = g.b.mn_major ? run(fp8_gemm_kernel<true, true>) : cudaErrorInvalidValue;
     else e = g.b.mn_major ? run(fp8_gemm_kernel<false, true>) : run(fp8_gemm_kernel<false, false>);

@@ -105,7 +105,6 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 __device__ __forceinline__ void cluster_arrive_relaxed() {
     asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
 }
-__device__ __forceinline__ void cluster_wait_only() { asm volatile("barrier.cluster.wait;" ::: "memory"); }
 // Phase test with acquire at cluster scope: data another CTA of the cluster
 // stored before its (release.cluster) arrival is visible after success.
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {

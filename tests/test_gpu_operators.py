@@ -35,3 +35,21 @@ def test_small_updates_in_a_row(tl, batch, rows, cols):
     torch.cuda.synchronize()
     for i, o in enumerate(got):
         assert torch.equal(o, want[i % 3]), i
+
+
+@pytest.mark.parametrize("T,K,n", [(1, 1024, 4096), (5, 8192, 1000), (64, 4096, 520), (128, 2048, 392)])
+def test_few_tokens_in_a_row(tl, T, K, n):
+    """The few-token product, whose clusters share a reduction, on two streams at once: every call gives the bits of a
+    call alone, and so does the gradient by the tokens."""
+    x, dy = [normal(s, T, K) for s in range(3)], [normal(s + 9, T, n) for s in range(3)]
+    w = [tl.fp8_quantize(normal(s + 3, K, n), "tile") for s in range(3)]
+    want = [(tl.fp8_linear(a, *b), tl.fp8_matmul_dx(tl.fp8_quantize(d, "row"), b)) for a, b, d in zip(x, w, dy)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for i in range(60):
+        with torch.cuda.stream(streams[i % 2]):
+            got.append((tl.fp8_linear(x[i % 3], *w[i % 3]), tl.fp8_matmul_dx(tl.fp8_quantize(dy[i % 3], "row"), w[i % 3])))
+    torch.cuda.synchronize()
+    for i, (y, dx) in enumerate(got):
+        assert torch.equal(y, want[i % 3][0]) and torch.equal(dx, want[i % 3][1]), i

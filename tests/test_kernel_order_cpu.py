@@ -15,7 +15,7 @@ def code(name):
     return re.sub(r"//[^\n]*|/\*.*?\*/", "", src, flags=re.S)
 
 
-@pytest.mark.parametrize("name,kernel", [("tl_ortho.cu", "ortho_small_kernel(")])
+@pytest.mark.parametrize("name,kernel", [("tl_ortho.cu", "ortho_small_kernel("), ("tl_fp8.cu", "fp8_few_kernel(")])
 def test_ctas_part_after_their_remote_reads(name, kernel):
     """A CTA that reads another's shared memory has done so before the other may leave: every relaxed arrival at the
     cluster's barrier, which is not ordered after the reads, comes after one at a barrier of the CTA, and the warp that
@@ -29,7 +29,7 @@ def test_ctas_part_after_their_remote_reads(name, kernel):
         (handed,) = re.finditer(r"cta_barrier_arrive\((\d), (\w+)\);", body)
         assert last < handed.start() < min(relaxed)
         taken = body.index("cta_barrier_sync(%s, %s);" % handed.groups())
-        assert re.match(r"\s*cluster_arrive\(\);\s*cluster_wait\(\);", body[taken:].split(";", 1)[1])
+        assert re.match(r"\s*cluster_arrive\(\);", body[taken:].split(";", 1)[1])
     else:
         assert re.search(r"\bcluster_arrive\(\)|\bcluster_sync\(\)", body[last:])
     assert re.search(r"\bcluster_wait\(\)", body[last:])
