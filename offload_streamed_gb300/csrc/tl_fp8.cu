@@ -141,9 +141,18 @@ struct Fp8Params {
     uint64_t timeout_ns;
 };
 
+// A word that a kernel which may still run when this one begins has written, read
+// after the wait for it: __ldg is for what no one writes while this kernel runs.
+__device__ __forceinline__ uint32_t ld_written_u32(const uint32_t* p) {
+    uint32_t v;
+    asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+
 // The words of ROWS indices from i0 on, 32 apart (lane l has i0 + l, i0 + 32 + l,
-// ...), for chunk c: 1.0 (127) outside the matrix.
-template <int ROWS>
+// ...), for chunk c: 1.0 (127) outside the matrix.  EARLY: the vectors' words may
+// be what the kernel ahead writes (the tiles' bytes never are: Fp8GemmDesc::early).
+template <int ROWS, bool EARLY>
 __device__ __forceinline__ void scale_words(const Scales& s, int i0, int c, int num_k, int lane, uint32_t* w) {
     if (s.tiles) {  // one word for 128 indices, the same in all lanes
 #pragma unroll
@@ -162,7 +171,10 @@ __device__ __forceinline__ void scale_words(const Scales& s, int i0, int c, int 
     } else {
         const uint32_t* at = static_cast<const uint32_t*>(s.p) + int64_t(c) * s.dim + i0 + lane;
 #pragma unroll
-        for (int j = 0; j < ROWS; ++j) w[j] = i0 + 32 * j + lane < s.dim ? __ldg(at + 32 * j) : 0x7f7f7f7fu;
+        for (int j = 0; j < ROWS; ++j) {
+            w[j] = 0x7f7f7f7fu;
+            if (i0 + 32 * j + lane < s.dim) w[j] = EARLY ? ld_written_u32(at + 32 * j) : __ldg(at + 32 * j);
+        }
     }
 }
 
@@ -376,8 +388,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) {
                     if (c0 + i >= chunks) break;
-                    scale_words<4>(p.a, m0, c0 + i, p.num_k, lane, w[i]);
-                    scale_words<8>(p.b, n0, c0 + i, p.num_k, lane, w[i] + 4);
+                    scale_words<4, false>(p.a, m0, c0 + i, p.num_k, lane, w[i]);
+                    scale_words<8, false>(p.b, n0, c0 + i, p.num_k, lane, w[i] + 4);
                 }
                 const uint32_t q = batch % kSfSlots;
                 if (!warp_wait(sf_empty_bar(q), ((batch / kSfSlots) & 1u) ^ 1u, wc, kErrProducerWait, lane)) {
@@ -595,8 +607,8 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         if (kb1 > kb0)
             for (int c = kb0 / kChunkBlocks; c <= (kb1 - 1) / kChunkBlocks; ++c, ++chunk) {
                 uint32_t w[8];
-                scale_words<4>(p.a, m0, c, p.num_k, lane, w);
-                scale_words<4>(p.b, t0, c, p.num_k, lane, w + 4);
+                scale_words<4, true>(p.a, m0, c, p.num_k, lane, w);
+                scale_words<4, true>(p.b, t0, c, p.num_k, lane, w + 4);
                 const uint32_t q = chunk % kFewSfSlots, dst = sf0 + q * kFewSfSlot + uint32_t(lane) * 16;
                 if (!warp_wait(sf_empty_bar(q), ((chunk / kFewSfSlots) & 1u) ^ 1u, wc, kErrProducerWait, lane)) break;
                 st_shared_v4(dst, w[0], w[1], w[2], w[3]);

@@ -36,3 +36,27 @@ def test_ctas_part_after_their_remote_reads(name, kernel):
     ptx = code("tl_ptx.cuh")
     for fn, words in (("cluster_arrive", "barrier.cluster.arrive.release;"), ("cluster_wait", "barrier.cluster.wait.acquire;")):
         assert re.search(r"void %s\(\) \{ asm volatile\(\"%s\"" % (fn, re.escape(words)), ptx), fn
+
+
+def body_of(src, start):
+    body = src[src.index(start):]
+    return body[:body.index("\n}\n")]
+
+
+@pytest.mark.parametrize("name,start", [("tl_fp8.cu", "fp8_few_kernel("), ("tl_ortho.cu", "ortho_small_kernel("),
+                                        ("tl_ortho.cu", " ortho_kernel("), ("tl_norm.cu", "norm_reduce_kernel(")])
+def test_early_kernels_read_what_was_written(name, start):
+    """A kernel that may begin before the one ahead has completed reads none of that one's results as read-only data:
+    such a load need not come after the wait, nor see what was written before it."""
+    src = code(name)
+    body = body_of(src, start)
+    assert "griddepcontrol.wait" in body or "grid_dependency_wait()" in body
+    assert "__ldg" not in body
+    calls = re.findall(r"scale_words<\d+(?:, (\w+))?>\(p\.\w", body)
+    assert all(c == "true" for c in calls), calls
+    if calls:
+        words = body_of(src, "void scale_words(")
+        assert re.search(r"EARLY \? ld_written_u32\([^:]*\) : __ldg\(", words)
+        assert re.search(r"uint32_t ld_written_u32\([^{]*\{[^}]*asm volatile\(\"ld\.relaxed\.gpu\.global", src)
+        rest = words.replace(re.search(r"EARLY \? [^;]*;", words).group(0), "")
+        assert rest.count("__ldg") == 1 and "__ldg(at + j * s.k_step)" in rest  # the tiles' bytes
