@@ -513,8 +513,9 @@ tl_status tiled_linear_forward_static(int64_t T, int64_t K, int64_t M, int32_t N
  * caller and are in use until the call's work has completed: calls that may
  * overlap (other streams) need their own.  err_dev is a device int32, zeroed
  * by the caller before first use, that is only ever OR-ed into: non-zero once
- * a bounded wait has given up, and the results of that call are then not
- * valid.  Calls may share one, on any stream. */
+ * a bounded wait has given up, and the results of the call that gave up are
+ * then not valid.  Calls may share one, on any stream: none reads it, so those
+ * that did not give up are not affected (which did, it does not say). */
 enum { TL_TYPE_BF16 = 0, TL_TYPE_F16 = 1, TL_TYPE_F32 = 2 };  /* tl_type */
 
 /* Layer norm over the columns of each row.

@@ -30,7 +30,8 @@
 // its tensor memory, and they add the parts up through distributed shared
 // memory in a fixed order.
 //
-// Every wait is bounded; see tl_gemm.cu, whose error protocol this shares.
+// Every wait is bounded; see tl_gemm.cu, whose error protocol this shares but for
+// one thing: the error word is many launches', so its bits end no wait here.
 #include "tl_fp8.h"
 #include "tl_gemm.h"
 #include "tl_kernel_common.cuh"
@@ -210,7 +211,7 @@ template <bool A_MN, bool B_MN>
 __global__ void __launch_bounds__(kThreads, 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                     const __grid_constant__ CUtensorMap map_d, const Fp8Params p) {
-    const WaitCtx wc{p.err, p.timeout_ns};
+    const WaitCtx wc{p.err, p.timeout_ns, true};
     constexpr int S = kStagesPair;
     constexpr uint32_t kStage = 2 * kStageBlocks * kStageHalf;
     extern __shared__ uint8_t smem_raw[];
@@ -493,7 +494,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     fp8_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_t, const Fp8Params p,
                    __nv_bfloat16* out, int64_t ldo, int splits, int per) {
     using F = Few<N>;
-    const WaitCtx wc{p.err, p.timeout_ns};
+    const WaitCtx wc{p.err, p.timeout_ns, true};
     constexpr int S = F::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));

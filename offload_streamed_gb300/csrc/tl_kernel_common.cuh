@@ -43,6 +43,9 @@ struct Geo {
 struct WaitCtx {
     int32_t* err;
     uint64_t timeout_ns;
+    // Other launches report in the same word: what it holds ends no wait of this
+    // one, whose own time does.
+    bool shared = false;
 };
 
 __device__ __noinline__ inline bool wait_slow(uint32_t bar, uint32_t parity, int32_t* err, int32_t code,
@@ -68,7 +71,7 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, cons
                                              bool stop_on_error = true) {
     if (mbar_try_wait(bar, parity)) return true;
     const bool downstream = code == kErrProducerWait || code == kErrEpilogueWait;
-    return wait_slow(bar, parity, w.err, code, stop_on_error, downstream ? 2 * w.timeout_ns : w.timeout_ns);
+    return wait_slow(bar, parity, w.err, code, stop_on_error && !w.shared, downstream ? 2 * w.timeout_ns : w.timeout_ns);
 }
 
 // Bounded wait with cluster-scope acquire (the dynamic tile queue).
@@ -78,7 +81,7 @@ __device__ __noinline__ inline bool wait_bounded_cluster(uint32_t bar, uint32_t 
     for (uint32_t n = 1;; ++n) {
         if (mbar_try_wait_cluster(bar, parity)) return true;
         if ((n & 255u) == 0) {
-            if (*reinterpret_cast<volatile int32_t*>(w.err) != 0) return false;
+            if (!w.shared && *reinterpret_cast<volatile int32_t*>(w.err) != 0) return false;
             if (global_timer_ns() - t0 > 2 * w.timeout_ns) {
                 atomicOr(w.err, code);
                 return false;

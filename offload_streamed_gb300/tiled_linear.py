@@ -884,7 +884,8 @@ def _err_word(device) -> int:
 
 def check_operators(device=None) -> None:
     """Wait for the device and raise TL_ERR_TIMEOUT if a kernel of the functions
-    below has given up one of its bounded waits since the last check."""
+    below has given up one of its bounded waits since the last check.  The results of
+    one call at least since then are not valid, and which is not known."""
     torch = _t()
     index = torch.cuda.current_device() if device is None else torch.device(device).index or 0
     if index in _err_words:

@@ -53,3 +53,29 @@ def test_few_tokens_in_a_row(tl, T, K, n):
     torch.cuda.synchronize()
     for i, (y, dx) in enumerate(got):
         assert torch.equal(y, want[i % 3][0]) and torch.equal(dx, want[i % 3][1]), i
+
+
+def test_a_word_that_is_set_already(tl):
+    """The error word is shared by all calls: what an earlier one has left in it ends no later call's waits, however
+    long (one output tile here sums over 8 million tokens), and check_operators reports and clears it."""
+    T, K, n = 65535 * 128, 16, 16
+    x, dy = (normal(s, T, 16) for s in (1, 2))
+    xc, dyc = tl.fp8_quantize(x, "col"), tl.fp8_quantize(dy, "col")
+    row = tl.fp8_quantize(dy[:64, :16].contiguous(), "row")
+    w = tl.fp8_quantize(normal(3, K, n), "tile")
+    g = normal(4, 2, 256, 1024)
+    calls = [lambda: tl.fp8_matmul_dw(xc, dyc), lambda: tl.fp8_matmul_dx(row, w), lambda: tl.orthogonalize(g),
+             lambda: tl.layer_norm(x)[0]]
+    want = [c() for c in calls]
+    tl.check_operators()
+    word = tl._err_words[x.device.index][0]
+    word[0] = 1 << 20
+    out = torch.full((1 << 20,), float("nan"), device="cuda")  # what a freed result may hold
+    del out
+    got = [c() for c in calls]
+    with pytest.raises(tl.TiledLinearError) as e:
+        tl.check_operators()
+    assert e.value.status == tl.TL_ERR_TIMEOUT and hex(1 << 20) in str(e.value)
+    tl.check_operators()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert all(torch.equal(c(), b) for c, b in zip(calls, want))
