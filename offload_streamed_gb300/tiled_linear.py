@@ -887,12 +887,15 @@ def check_operators(device=None) -> None:
     below has given up one of its bounded waits since the last check.  The results of
     one call at least since then are not valid, and which is not known."""
     torch = _t()
-    index = torch.cuda.current_device() if device is None else torch.device(device).index or 0
+    index = None if device is None else torch.device(device).index
+    if index is None:  # "cuda" is the current device, too
+        index = torch.cuda.current_device()
     if index in _err_words:
         torch.cuda.synchronize(index)
         bits = int(_err_words[index][0][0])
         if bits:
             _err_words[index][0].zero_()
+            torch.cuda.synchronize(index)  # before any stream's next call
             raise TiledLinearError(TL_ERR_TIMEOUT, "check_operators", f"error word {bits:#x}")
 
 

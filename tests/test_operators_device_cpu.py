@@ -1,0 +1,45 @@
+"""Which device's error word ``check_operators`` reads, without a GPU: the words are host tensors here."""
+import pytest
+import torch
+
+
+@pytest.fixture
+def tl(monkeypatch):
+    from offload_streamed_gb300 import tiled_linear as tl
+    words = {i: (torch.zeros(4, dtype=torch.int32), 0) for i in (0, 1)}
+    waits = []
+    monkeypatch.setattr(tl, "_err_words", words)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(torch.cuda, "synchronize", lambda d=None: waits.append((d, int(words[d][0][0]))))
+    tl.waits = waits
+    return tl
+
+
+@pytest.mark.parametrize("device", [None, "cuda", "cuda:1", torch.device("cuda"), torch.device("cuda", 1)])
+def test_current_device(tl, device):
+    tl._err_words[0][0][0] = 3
+    tl.check_operators(device)
+    tl._err_words[1][0][0] = 5
+    with pytest.raises(tl.TiledLinearError) as e:
+        tl.check_operators(device)
+    assert e.value.status == tl.TL_ERR_TIMEOUT and "0x5" in str(e.value)
+    tl.check_operators(device)
+    assert tl._err_words[0][0][0] == 3
+
+
+@pytest.mark.parametrize("device", ["cuda:0", torch.device("cuda", 0)])
+def test_named_device(tl, device):
+    tl._err_words[1][0][0] = 5
+    tl.check_operators(device)
+    tl._err_words[0][0][0] = 3
+    with pytest.raises(tl.TiledLinearError) as e:
+        tl.check_operators(device)
+    assert "0x3" in str(e.value) and tl._err_words[1][0][0] == 5
+
+
+def test_cleared_before_another_stream_goes_on(tl):
+    """The word is zero on the device when the error is raised: a bit that a later call sets is not lost."""
+    tl._err_words[1][0][0] = 5
+    with pytest.raises(tl.TiledLinearError):
+        tl.check_operators()
+    assert tl.waits == [(1, 5), (1, 0)]
