@@ -518,6 +518,13 @@ tl_status tiled_linear_forward_static(int64_t T, int64_t K, int64_t M, int32_t N
  * that did not give up are not affected (which did, it does not say). */
 enum { TL_TYPE_BF16 = 0, TL_TYPE_F16 = 1, TL_TYPE_F32 = 2 };  /* tl_type */
 
+/* An err_dev for callers that have none: *word_dev is the address of a device
+ * int32 of the library's, one for each device, here the current one's; zero until
+ * a call that was given it gives up.  Whoever reads it clears it.  Nothing is
+ * allocated or enqueued: the call may stand in a stream capture.
+ * Errors: TL_ERR_INVALID, TL_ERR_CUDA. */
+tl_status tiled_linear_operator_error_word(int32_t **word_dev);
+
 /* Layer norm over the columns of each row.
  *   mean[r] = sum(x[r]) / cols, rstd[r] = 1 / sqrt(sum((x[r] - mean)^2) / cols + eps)
  *   y[r, c] = (x[r, c] - mean[r]) rstd[r] weight[c] + bias[c]

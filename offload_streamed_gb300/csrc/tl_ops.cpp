@@ -2,6 +2,7 @@
 // norm, 8-bit product, orthogonalised update): argument checks, workspaces
 // and launches.  The kernels are in tl_norm.cu, tl_fp8.cu and tl_ortho.cu.
 #include "tiled_linear.h"
+#include "tl_err_word.h"
 #include "tl_fp8.h"
 #include "tl_launch.h"
 #include "tl_norm.h"
@@ -42,6 +43,14 @@ tl_status guarded(F&& f) {
 }  // namespace
 
 extern "C" {
+
+tl_status tiled_linear_operator_error_word(int32_t** word_dev) {
+    return guarded([&]() -> tl_status {
+        if (!word_dev) return refuse(TL_ERR_INVALID, "word_dev is null");
+        *word_dev = nullptr;
+        return done(operator_err_word(word_dev), "the operators' error word");
+    });
+}
 
 tl_status tiled_linear_norm_forward(int64_t rows, int64_t cols, int32_t type, const void* x_dev, int64_t ldx,
                                     int32_t param_type, const void* weight_dev, const void* bias_dev, float eps,

@@ -164,6 +164,8 @@ def load():
         L.tiled_linear_selftest_timeout.restype = st
         L.tiled_linear_forward_static.argtypes = [i64, i64, i64, i32, vp, vp, vp, vp, vp]
         L.tiled_linear_forward_static.restype = st
+        L.tiled_linear_operator_error_word.argtypes = [ctypes.POINTER(vp)]
+        L.tiled_linear_operator_error_word.restype = st
         L.tiled_linear_norm_forward.argtypes = [i64, i64, i32, vp, i64, i32, vp, vp, ctypes.c_float, vp, i64, vp,
                                                 vp, vp, vp]
         L.tiled_linear_norm_forward.restype = st
@@ -413,6 +415,12 @@ def tiled_linear_forward_static(T, K, M, N, w_host, x_dev, y_dev, status_host, s
     st = load().tiled_linear_forward_static(T, K, M, N, w_host, x_dev, y_dev, status_host, stream)
     if st != TL_OK:
         raise TiledLinearError(st, "tiled_linear_forward_static")
+
+
+def tiled_linear_operator_error_word() -> int:
+    p = ctypes.c_void_p()
+    _check(load().tiled_linear_operator_error_word(ctypes.byref(p)), "tiled_linear_operator_error_word")
+    return p.value
 
 
 def tiled_linear_norm_forward(rows, cols, type, x, ldx, param_type, weight, bias, eps, y, ldy, mean, rstd, err,
@@ -872,13 +880,22 @@ def _stream_of(device, where: str) -> int:
 _err_words = {}
 
 
+class _Word:
+    """One int32 at an address, as torch takes memory that is not its own."""
+
+    def __init__(self, address: int):
+        self.__cuda_array_interface__ = {"shape": (1,), "typestr": "<i4", "data": (address, False), "version": 2}
+
+
 def _err_word(device) -> int:
-    """Device address of the error word that this process's calls on `device` share."""
+    """Device address of the error word that this process's calls on `device` share:
+    the library's own, so that a first call may be captured in a graph."""
     got = _err_words.get(device.index)
     if got is None:
-        word = _torch.zeros(4, dtype=_torch.int32, device=device)
-        _torch.cuda.synchronize(device)  # zero before any stream's first call
-        got = _err_words.setdefault(device.index, (word, word.data_ptr()))
+        with _torch.cuda.device(device):
+            at = tiled_linear_operator_error_word()
+            word = _torch.as_tensor(_Word(at), device=device)
+        got = _err_words.setdefault(device.index, (word, at))
     return got[1]
 
 

@@ -1,5 +1,9 @@
 """The operators around the product in company: calls in flight together, on several streams, in graphs, and after one
 another without a pause."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -79,3 +83,39 @@ def test_a_word_that_is_set_already(tl):
     tl.check_operators()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert all(torch.equal(c(), b) for c, b in zip(calls, want))
+
+
+FIRST_CALL = """
+import sys, torch
+sys.path.insert(0, {root!r})
+from offload_streamed_gb300 import tiled_linear as tl
+normal = lambda s, *shape: torch.randn(*shape, generator=torch.Generator(device="cuda").manual_seed(s), device="cuda").bfloat16()
+x, other = normal(1, 40, 1024), normal(2, 40, 1024)
+wq = normal(3, 1024, 512).to(torch.float8_e4m3fn)
+ws = torch.full((8, 4), 127, dtype=torch.uint8, device="cuda")
+mean, rstd = torch.zeros(40, device="cuda"), torch.ones(40, device="cuda")
+call = {call}
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    got = call(x)
+g.replay()
+first = [t.clone() for t in got]
+want = call(x)
+assert all(torch.equal(a, b) for a, b in zip(first, want))
+x.copy_(other)
+g.replay()
+want = call(other)
+assert all(torch.equal(a, b) for a, b in zip(got, want)) and not torch.equal(got[0], first[0])
+tl.check_operators()
+print("captured")
+"""
+
+
+@pytest.mark.parametrize("call", ["lambda x: tl.layer_norm(x)", "lambda x: tl.layer_norm_backward(x, x, mean, rstd)",
+                                  "lambda x: (tl.fp8_linear(x, wq, ws),)", "lambda x: tl.fp8_linear_backward(x, x[:, :512], wq, ws)",
+                                  "lambda x: tl.fp8_quantize(x, 'row')", "lambda x: (tl.orthogonalize(x),)"])
+def test_first_call_in_a_graph(tl, call):
+    """A process's first call of an operator may be captured, and replays with other inputs."""
+    src = FIRST_CALL.format(root=os.path.dirname(os.path.dirname(os.path.abspath(__file__))), call=call)
+    r = subprocess.run([sys.executable, "-c", src], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]

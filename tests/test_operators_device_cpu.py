@@ -43,3 +43,10 @@ def test_cleared_before_another_stream_goes_on(tl):
     with pytest.raises(tl.TiledLinearError):
         tl.check_operators()
     assert tl.waits == [(1, 5), (1, 0)]
+
+
+def test_the_librarys_word_is_refused_without_a_place_for_it():
+    from offload_streamed_gb300 import _build
+    _build.build()
+    from offload_streamed_gb300 import tiled_linear as tl
+    assert tl.load().tiled_linear_operator_error_word(None) == tl.TL_ERR_INVALID
