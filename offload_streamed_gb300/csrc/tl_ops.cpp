@@ -265,8 +265,8 @@ bool workspace_ok(const void* p, size_t have, size_t need) {
     return p && (reinterpret_cast<uintptr_t>(p) & 255u) == 0 && have >= need;
 }
 
-tl_status quantize(int64_t rows, int64_t cols, int32_t type, const void* x, int64_t ldx, const Fp8QuantDesc::Form* row,
-                   const Fp8QuantDesc::Form* col, void* stream) {
+Fp8QuantDesc quantizing(int64_t rows, int64_t cols, int32_t type, const void* x, int64_t ldx, const Fp8QuantDesc::Form* row,
+                        const Fp8QuantDesc::Form* col) {
     Fp8QuantDesc d;
     d.rows = rows;
     d.cols = cols;
@@ -276,8 +276,9 @@ tl_status quantize(int64_t rows, int64_t cols, int32_t type, const void* x, int6
     d.format = TL_FP8_E4M3;
     if (row) d.row = *row;
     if (col) d.col = *col;
-    const std::string bad = fp8_quantize_check(d);
-    if (!bad.empty()) return refuse(TL_ERR_INVALID, bad);
+    return d;
+}
+tl_status quantize(const Fp8QuantDesc& d, void* stream) {  // checked
     return done(fp8_quantize_launch(d, static_cast<cudaStream_t>(stream)), "fp8 quantise");
 }
 
@@ -303,9 +304,11 @@ tl_status tiled_linear_fp8_linear(int64_t T, int64_t K, int64_t n, int32_t type,
         Fp8GemmDesc g = product(T, n, K, operand(true, false, K, x.form.q, x.form.ldq, x.form.scale, TL_FP8_E4M3),
                                 operand(false, true, n, w_q, ldw, w_scale, w_format), y_dev, ldy, err_dev);
         g.early = true;  // the quantiser, directly ahead, writes x's form alone
-        const std::string bad = fp8_gemm_check(g);
+        const Fp8QuantDesc qx = quantizing(T, K, type, x_dev, ldx, &x.form, nullptr);
+        std::string bad = fp8_gemm_check(g);
+        if (bad.empty()) bad = fp8_quantize_check(qx);
         if (!bad.empty()) return refuse(TL_ERR_INVALID, bad);
-        const tl_status st = quantize(T, K, type, x_dev, ldx, &x.form, nullptr, stream);
+        const tl_status st = quantize(qx, stream);
         return st == TL_OK ? launch_product(g, stream) : st;
     });
 }
@@ -342,10 +345,14 @@ tl_status tiled_linear_fp8_linear_backward(int64_t T, int64_t K, int64_t n, int3
         std::string bad = dx_dev ? fp8_gemm_check(gx) : std::string();
         if (bad.empty() && dw_dev) bad = fp8_gemm_check(gw);
         if (bad.empty() && dw_dev && (!x_dev || ldx < K)) bad = "x is null or its leading dimension is smaller than K";
+        const Fp8QuantDesc qdy = quantizing(T, n, type, dy_dev, lddy, dx_dev ? &dy_row.form : nullptr, dw_dev ? &dy_col.form : nullptr);
+        const Fp8QuantDesc qx = quantizing(T, K, type, x_dev, ldx, nullptr, &x_col.form);
+        if (bad.empty()) bad = fp8_quantize_check(qdy);
+        if (bad.empty() && dw_dev) bad = fp8_quantize_check(qx);
         if (!bad.empty()) return refuse(TL_ERR_INVALID, bad);
-        tl_status st = quantize(T, n, type, dy_dev, lddy, dx_dev ? &dy_row.form : nullptr, dw_dev ? &dy_col.form : nullptr, stream);
+        tl_status st = quantize(qdy, stream);
         if (st == TL_OK && dx_dev) st = launch_product(gx, stream);
-        if (st == TL_OK && dw_dev) st = quantize(T, K, type, x_dev, ldx, nullptr, &x_col.form, stream);
+        if (st == TL_OK && dw_dev) st = quantize(qx, stream);
         if (st == TL_OK && dw_dev) st = launch_product(gw, stream);
         return st;
     });

@@ -1,4 +1,5 @@
-"""Which device's error word ``check_operators`` reads, without a GPU: the words are host tensors here."""
+"""Which device's error word ``check_operators`` reads, without a GPU (the words are host tensors here), and what the
+operators' entries refuse before they turn to the device."""
 import pytest
 import torch
 
@@ -50,3 +51,15 @@ def test_the_librarys_word_is_refused_without_a_place_for_it():
     _build.build()
     from offload_streamed_gb300 import tiled_linear as tl
     assert tl.load().tiled_linear_operator_error_word(None) == tl.TL_ERR_INVALID
+
+
+@pytest.mark.parametrize("x,dx", [(257, 256), (257, None)])
+def test_a_backward_that_is_refused_enqueues_nothing(x, dx):
+    """An x that does not fit its type is refused before dx's part is begun (which fails here for want of a device)."""
+    from offload_streamed_gb300 import _build
+    _build.build()
+    from offload_streamed_gb300 import tiled_linear as tl
+    with pytest.raises(tl.TiledLinearError) as e:
+        tl.tiled_linear_fp8_linear_backward(4, 64, 64, tl.TL_TYPE_BF16, x, 64, 256, 64, 0, 256, 64, 256, dx, 64, 256, 64,
+                                            256, 1 << 20, 256, None)
+    assert e.value.status == tl.TL_ERR_INVALID and "aligned" in str(e.value), e.value
