@@ -1055,9 +1055,10 @@ def fp8_matmul(x, w):
     w = (q, scale) in the tile form."""
     _t()
     where, (xq, xs), (wq, ws) = "fp8_matmul", x, w
-    (K, n), T = _weight_shape(wq, where), xq.shape[0]
+    K, n = _weight_shape(wq, where)
     if xq.dim() != 2 or xq.shape[1] != K or xq.device != wq.device:
         _refuse(where, "x and the weight do not fit each other")
+    T = xq.shape[0]
     y, ldy = _fp8_result(xq, T, n)
     tiled_linear_fp8_gemm_forward(T, K, n, *_fp8_operand(xq, xs, "row", where, "x"),
                                   *_fp8_operand(wq, ws, "tile", where, "the weight"), y.data_ptr(), ldy,
@@ -1069,9 +1070,10 @@ def fp8_matmul_dx(dy, w):
     """dx [T, K] bf16 = dy [T, n] . w [K, n]^T, dy in the row form, w in the tile form."""
     _t()
     where, (dyq, dys), (wq, ws) = "fp8_matmul_dx", dy, w
-    (K, n), T = _weight_shape(wq, where), dyq.shape[0]
+    K, n = _weight_shape(wq, where)
     if dyq.dim() != 2 or dyq.shape[1] != n or dyq.device != wq.device:
         _refuse(where, "dy and the weight do not fit each other")
+    T = dyq.shape[0]
     dx, lddx = _fp8_result(dyq, T, K)
     tiled_linear_fp8_gemm_dx(T, K, n, *_fp8_operand(dyq, dys, "row", where, "dy"),
                              *_fp8_operand(wq, ws, "tile", where, "the weight"), dx.data_ptr(), lddx,

@@ -63,3 +63,13 @@ def test_a_backward_that_is_refused_enqueues_nothing(x, dx):
         tl.tiled_linear_fp8_linear_backward(4, 64, 64, tl.TL_TYPE_BF16, x, 64, 256, 64, 0, 256, 64, 256, dx, 64, 256, 64,
                                             256, 1 << 20, 256, None)
     assert e.value.status == tl.TL_ERR_INVALID and "aligned" in str(e.value), e.value
+
+
+@pytest.mark.parametrize("name", ["fp8_matmul", "fp8_matmul_dx"])
+def test_products_refuse_what_is_no_matrix(name):
+    from offload_streamed_gb300 import tiled_linear as tl
+    w, none = torch.zeros(4, 4).to(torch.float8_e4m3fn), torch.zeros(1, 1, dtype=torch.uint8)
+    for shape in ((), (4,), (1, 4, 4)):
+        with pytest.raises(tl.TiledLinearError) as e:
+            getattr(tl, name)((torch.zeros(shape).to(torch.float8_e4m3fn), none), (w, none))
+        assert e.value.status == tl.TL_ERR_INVALID and "fit" in str(e.value)
