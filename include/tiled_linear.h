@@ -515,7 +515,12 @@ tl_status tiled_linear_forward_static(int64_t T, int64_t K, int64_t M, int32_t N
  * by the caller before first use, that is only ever OR-ed into: non-zero once
  * a bounded wait has given up, and the results of the call that gave up are
  * then not valid.  Calls may share one, on any stream: none reads it, so those
- * that did not give up are not affected (which did, it does not say). */
+ * that did not give up are not affected (which did, it does not say).
+ * Every sum has an order that the call's sizes, types, strides and alignments and
+ * the model of the device fix (no atomics add to results): calls that are alike in
+ * these give the same bits.  (A shifted or strided view of the same values may be read by
+ * other vectors and summed in another order; another device may split a
+ * reduction among another number of CTAs.) */
 enum { TL_TYPE_BF16 = 0, TL_TYPE_F16 = 1, TL_TYPE_F32 = 2 };  /* tl_type */
 
 /* An err_dev for callers that have none: *word_dev is the address of a device
@@ -548,9 +553,8 @@ size_t tiled_linear_norm_backward_workspace_bytes(int64_t rows, int64_t cols);
  *   dx[r, c]   = rstd[r] (g[r, c] - mean_c(g[r]) - xh[r, c] mean_c(g[r] xh[r]))
  *   dweight[c] = sum_r dy[r, c] xh[r, c],   dbias[c] = sum_r dy[r, c]
  *  dy, dx: [rows, cols] of `type`; dx may be dy or x.  dweight, dbias: fp32
- *  [cols], overwritten, NULL where not wanted.  The sums over rows have a fixed
- *  order for given sizes: no atomics, the same bits every time.  rows = 0
- *  writes zeros to dweight and dbias.  workspace: 16-byte aligned.
+ *  [cols], overwritten, NULL where not wanted.  rows = 0 writes zeros to dweight
+ *  and dbias.  workspace: 16-byte aligned.
  * Errors: TL_ERR_INVALID, TL_ERR_WORKSPACE, TL_ERR_CUDA. */
 tl_status tiled_linear_norm_backward(int64_t rows, int64_t cols, int32_t type, const void *dy_dev, int64_t lddy,
                                      const void *x_dev, int64_t ldx, const float *mean_dev, const float *rstd_dev,
@@ -590,7 +594,7 @@ tl_status tiled_linear_fp8_quantize(int64_t rows, int64_t cols, int32_t type, co
 
 /* y[T, n] (bf16, ld ldy) = x[T, K] . w[K, n]: x in the row form, w in the tile
  * form.  Products are summed in fp32 over the whole reduction and rounded to
- * bf16 once; each element's sum has an order of its own that the sizes fix.
+ * bf16 once.
  * ldy is a multiple of 8, y 16-byte aligned.  T = 0 is a no-op.
  * Errors: TL_ERR_INVALID, TL_ERR_CUDA. */
 tl_status tiled_linear_fp8_gemm_forward(int64_t T, int64_t K, int64_t n, int32_t x_format, const void *x_q, int64_t ldx,
@@ -642,7 +646,7 @@ tl_status tiled_linear_fp8_linear_backward(int64_t T, int64_t K, int64_t n, int3
  * result.  The iterate is fp32; the products take it in fp16 (scaled by 2^8, so
  * its elements must stay below 255: a, b, c that keep the singular values near
  * one do) and sum in fp32.  1 <= steps <= 100; the matrices are independent of
- * each other.  out may be G.  The order of all sums depends on the sizes alone.
+ * each other.  out may be G.
  * out is 16-byte aligned, ldo and o_apart multiples of 8.  workspace: 256-byte
  * aligned, tiled_linear_orthogonalize_workspace_bytes (0 if the sizes are
  * invalid).  batch = 0 is a no-op.

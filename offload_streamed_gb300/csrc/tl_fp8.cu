@@ -736,7 +736,8 @@ cudaError_t launch_clusters(void (*kern)(A...), dim3 grid, int threads, int clus
 // Asked about, never launched: how many clusters of fp8_few_kernel's threads and
 // shared memory run at a time.  For a kernel that uses tensor memory the runtime
 // answers for one CTA an SM, whatever it allocates; two of fp8_few_kernel fit
-// (twice its kCols are at most 512 columns) and are seen to run.
+// (twice its kCols are at most 512 columns, and its launch bounds keep its
+// registers to what two allow) and are seen to run.
 __global__ void __launch_bounds__(kFewThreads, 2) few_shape_kernel() {}
 
 template <bool W_MN, int N>
@@ -746,9 +747,9 @@ cudaError_t launch_few(const CUtensorMap& mw, const CUtensorMap& mt, Fp8Params p
     const int blocks = (p.n_dim + N - 1) / N;
     // CTAs of a cluster: as many as two an SM allow, with two K-blocks each and
     // all clusters at a time.  One token, us, with 2 / 4 / 8: 8192 x 1024 (8
-    // tiles) 15.7 / 10.1 / 7.6, 16384 x 4736 (37) 26.9 / 16.8 / 22.3, 25600 x 6400
-    // (50) 40.4 / 28.8 / 33.9, 8192 x 8192 (64) 16.7 / 14.9 / 18.0, 8192 x 9728
-    // (76) 17.1 / 22.9 / 23.4.
+    // tiles) 15.5 / 10.0 / 7.7, 16384 x 4736 (37) 27.6 / 17.5 / 23.1, 25600 x 6400
+    // (50) 40.9 / 29.1 / 34.5, 8192 x 8192 (64) 16.8 / 14.9 / 18.6, 8192 x 9728
+    // (76) 17.5 / 23.1 / 23.9.
     int splits = 1, per_sm = 0, clusters = 0;
     const void* shape = reinterpret_cast<const void*>(few_shape_kernel);
     cudaError_t e = ctas_per_sm(shape, kFewThreads, Few<N>::kSmem, &per_sm);
@@ -816,9 +817,9 @@ cudaError_t fp8_gemm_launch(const Fp8GemmDesc& g, int num_sms, cudaStream_t stre
     // Few tokens, or fewer tiles than half the CTA pairs and a reduction long
     // enough to share: the kernel whose clusters split the reduction.  Other
     // kernel against this one, us, at K x n of the weight and T tokens: 8192 x
-    // 8192, T = 256 (32 tiles) 30.3 / 26.8, T = 512 (64 tiles) 31.7 / 38.2;
-    // 25600 x 6400, T = 256 (25 tiles) 72.7 / 57.5; 8192 x 1024, T = 1024 (16
-    // tiles) 27.1 / 17.6; 1024 x 4096, T = 256 (16 tiles, short) 10.3 / 11.7.
+    // 8192, T = 256 (32 tiles) 30.3 / 25.1, T = 512 (64 tiles) 31.8 / 38.5;
+    // 25600 x 6400, T = 256 (25 tiles) 72.9 / 55.4; 8192 x 1024, T = 1024 (16
+    // tiles) 27.7 / 17.3; 1024 x 4096, T = 256 (16 tiles, short) 10.5 / 10.3.
     constexpr int kLongBlocks = 32;
     if (!g.a.mn_major && (g.m_dim <= kFewTokens ||
                           (pair_tiles <= num_sms / 4 && g.k_dim >= int64_t(kLongBlocks) * kFp8BlockK))) {

@@ -28,7 +28,8 @@
 // All statistics and sums are fp32.  A row's variance is joined from the
 // warps' sums of squares about their own means, which loses nothing to
 // cancellation, whatever the row's mean.  Every order of summation is fixed by
-// the sizes alone.
+// the sizes, the type, the alignment (which picks the vectors) and the device's
+// SMs and clusters (which pick the grid).
 #include "tl_norm.h"
 #include "tl_launch.h"
 #include "tl_types.cuh"
@@ -754,9 +755,9 @@ NormKernel pick(bool backward, bool warp_row, int e) {
 // CTAs that share a row: one for each 8192 columns, up to eight, and more
 // columns each in the longest rows.  Two CTAs of 256 threads, an SM's, work
 // on different rows, and one moves data while the other waits for its row's
-// sums.  Measured, forward / backward: 2048 x 65536 bf16 with 8 CTAs of 8192
-// columns 209 / 259 us, with 4 of 16384 266 / 360 us; 8192 x 16384 with two
-// CTAs 116 / 154 us, with one 124 / 176 us.
+// sums.  Measured, forward / backward, us, with 8192 / with 16384 columns a CTA:
+// 2048 x 65536 bf16 133 / 183 and 139 / 182, 4096 x 32768 123 / 171 and 136 / 170,
+// 8192 x 16384 112 / 150 and 120 / 152.
 int cluster_size(int64_t cols) {
     int c = 1;
     while (c < kMaxCluster && cols > int64_t(c) * 8192) c *= 2;

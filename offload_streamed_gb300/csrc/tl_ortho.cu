@@ -882,9 +882,10 @@ cudaError_t launch(const void* kern, int threads, int grid, int cluster, size_t 
 
 // Products of up to a quarter as many 256 x 256 tiles as there are CTA pairs go
 // through the small kernel.  The whole update, us, by pairs alone / with this
-// rule / with one three times as wide: 512 x 512 166 / 105 / 105, 128 x 512 116 /
-// 97 / 97, 1024 x 4096 279 / 191 / 203, 2048 x 2048 290 / 290 / 315 (all with the
-// turned tiles' writes as they were before kTurnLd's).
+// rule / with one three times as wide: 512 x 512 164 / 103 / 103, 128 x 512 112 /
+// 98 / 99, 1024 x 4096 277 / 190 / 190, 2048 x 2048 290 / 289 / 261.  (When the rule
+// was chosen, before kTurnLd and kSmallThreads, the last two of the wider one
+// were 203 and 315: what it costs elsewhere now is not measured.)
 bool small_product(int64_t pair_tiles, int num_sms) { return pair_tiles <= num_sms / 8; }
 
 template <bool A_MN, bool B_MN, int MODE>
@@ -914,11 +915,10 @@ cudaError_t product(const Half& a, const Half& b, int64_t m, int64_t n, int64_t 
     OutMaps to = maps;
     void* args[] = {&ma, &mb, &to, &p};
     if (small) {
-        // CTAs of a cluster: as many as there are SMs for, with four K-blocks
-        // each, and as many clusters as run at a time.  512 x 512 (8 K-blocks),
-        // us: two CTAs 105, eight 134, one 124.  With / without that last bound:
-        // 6 x 200 x 4096 196 / 221, 6 x 256 x 2048 148 / 175.  (Both before
-        // kTurnLd and kSmallThreads.)
+        // CTAs of a cluster: as many as there are SMs for, with two K-blocks each,
+        // and as many clusters as run at a time.  512 x 512 (8 K-blocks), us: one
+        // CTA 131, two 114, four 103 (chosen), eight 139.  With / without that last
+        // bound: 6 x 200 x 4096 192 / 222, 6 x 256 x 2048 143 / 174.
         p.splits = 1;
         const void* kern = reinterpret_cast<const void*>(ortho_small_kernel<A_MN, B_MN, MODE>);
         int per_sm = 0, clusters = 0;

@@ -820,7 +820,11 @@ class HostAdam:
 # --- operators around the product ---------------------------------------------
 # Functions of torch tensors: device-resident, enqueued on the current stream,
 # with outputs and workspaces from torch's allocator on that stream.  They take
-# no gradient through autograd: each backward is a function of its own.
+# no gradient through autograd: each backward is a function of its own.  Inputs are
+# matrices of contiguous rows, any distance apart that keeps them from overlapping.
+# Results of the 8-bit products and of orthogonalize have rows on 16-byte
+# boundaries: where the width is no multiple of 8 they are views with gaps between
+# the rows (.contiguous() packs them).
 
 TL_TYPE_BF16, TL_TYPE_F16, TL_TYPE_F32 = range(3)
 _torch = None
@@ -918,7 +922,7 @@ def check_operators(device=None) -> None:
 
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-5):
     """(y, mean, rstd): layer norm over the columns of x [rows, cols] (bf16, fp16 or
-    fp32; any row stride).  weight, bias: [cols], both of one of those types, or
+    fp32; any stride of rows that do not overlap).  weight, bias: [cols], both of one of those types, or
     None for ones / zeros.  mean and rstd are fp32 [rows], for the backward."""
     torch, where = _t(), "layer_norm"
     ldx, (rows, cols), device = _ld(x, where, "x"), x.shape, x.device
@@ -1099,7 +1103,7 @@ def fp8_matmul_dw(x, dy):
 def fp8_linear(x, wq, ws):
     """y [T, n] bf16 = x [T, K] . w with w in 8 bits (``fp8_quantize(w, "tile")``);
     x (bf16, fp16 or fp32) is quantised on the way, with a scale for each 128
-    columns of a row."""
+    columns of a row.  (y's rows have gaps where n is no multiple of 8, as dx's and dw's.)"""
     torch, where = _t(), "fp8_linear"
     ldx, T, device, (K, n) = _ld(x, where, "x"), x.shape[0], x.device, _weight_shape(wq, where)
     if x.shape[1] != K or device != wq.device:
@@ -1133,7 +1137,8 @@ def fp8_linear_backward(x, dy, wq, ws):
 def orthogonalize(g, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315), eps: float = 1e-7, scale: float = 1.0):
     """bf16 scale * X, X the matrix g (or each matrix of g [batch, rows, cols]; bf16,
     fp16 or fp32) after `steps` Newton-Schulz steps X = a X + (b P + c P^2) X,
-    P = X X^T, from g / (|g|_F + eps): its singular values drawn to about one."""
+    P = X X^T, from g / (|g|_F + eps): its singular values drawn to about one.  (The
+    rows of the result have gaps where cols is no multiple of 8.)"""
     torch, where = _t(), "orthogonalize"
     if not g.is_cuda or g.dim() not in (2, 3):
         _refuse(where, "g must be a matrix or a stack of matrices on a CUDA device")

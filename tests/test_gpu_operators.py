@@ -3,6 +3,7 @@ another without a pause."""
 import os
 import subprocess
 import sys
+import threading
 
 import pytest
 import torch
@@ -119,3 +120,36 @@ def test_first_call_in_a_graph(tl, call):
     src = FIRST_CALL.format(root=os.path.dirname(os.path.dirname(os.path.abspath(__file__))), call=call)
     r = subprocess.run([sys.executable, "-c", src], capture_output=True, text=True, timeout=120)
     assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
+
+
+def test_two_threads(tl):
+    """Calls from two threads, each on a stream of its own, at the same time: the bits of calls alone."""
+    x, dy, w = normal(1, 70, 1024), normal(2, 70, 512), normal(3, 1024, 512)
+    stack = normal(4, 3, 120, 260)
+
+    def calls():
+        y, mean, rstd = tl.layer_norm(x)
+        wq, ws = tl.fp8_quantize(w, "tile")
+        return (y, *tl.layer_norm_backward(x, x, mean, rstd), tl.fp8_linear(y, wq, ws), *tl.fp8_linear_backward(y, dy, wq, ws),
+                tl.orthogonalize(stack))
+
+    want = calls()
+    torch.cuda.synchronize()
+    bad, device = [], torch.cuda.current_device()
+
+    def run():
+        torch.cuda.set_device(device)
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(20):
+                got = calls()
+                s.synchronize()
+                bad.extend(i for i, (a, b) in enumerate(zip(got, want)) if not torch.equal(a, b))
+
+    threads = [threading.Thread(target=run) for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(60)
+        assert not t.is_alive()
+    assert not bad, bad
