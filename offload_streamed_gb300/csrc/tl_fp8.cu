@@ -115,7 +115,7 @@ __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepco
 
 // wait_bounded_cluster, without its reading of the clock where the phase is
 // over already: that takes longer than four K-blocks' MMAs.
-__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, const WaitCtx& w, int32_t code) {
+__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, const SharedWaitCtx& w, int32_t code) {
     return mbar_try_wait_cluster(bar, parity) || wait_bounded_cluster(bar, parity, w, code);
 }
 
@@ -211,7 +211,7 @@ template <bool A_MN, bool B_MN>
 __global__ void __launch_bounds__(kThreads, 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                     const __grid_constant__ CUtensorMap map_d, const Fp8Params p) {
-    const WaitCtx wc{p.err, p.timeout_ns, true};
+    const SharedWaitCtx wc{p.err, p.timeout_ns};
     constexpr int S = kStagesPair;
     constexpr uint32_t kStage = 2 * kStageBlocks * kStageHalf;
     extern __shared__ uint8_t smem_raw[];
@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     fp8_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_t, const Fp8Params p,
                    __nv_bfloat16* out, int64_t ldo, int splits, int per) {
     using F = Few<N>;
-    const WaitCtx wc{p.err, p.timeout_ns, true};
+    const SharedWaitCtx wc{p.err, p.timeout_ns};
     constexpr int S = F::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));

@@ -43,9 +43,15 @@ struct Geo {
 struct WaitCtx {
     int32_t* err;
     uint64_t timeout_ns;
-    // Other launches report in the same word: what it holds ends no wait of this
-    // one, whose own time does.
-    bool shared = false;
+    static constexpr bool kShared = false;
+};
+// Other launches report in the same word: what it holds ends no wait of this one,
+// whose own time does.  (A type, not a member: a third member would put the
+// context on the stack of every kernel that waits.)
+struct SharedWaitCtx {
+    int32_t* err;
+    uint64_t timeout_ns;
+    static constexpr bool kShared = true;
 };
 
 __device__ __noinline__ inline bool wait_slow(uint32_t bar, uint32_t parity, int32_t* err, int32_t code,
@@ -67,21 +73,23 @@ __device__ __noinline__ inline bool wait_slow(uint32_t bar, uint32_t parity, int
 // stage and the epilogue's wait for an accumulator (both downstream of the
 // MMA thread) use twice that, so when a pipeline stalls the role nearest the
 // stall reports first.
-__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, const WaitCtx& w, int32_t code,
+template <typename W>
+__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, const W& w, int32_t code,
                                              bool stop_on_error = true) {
     if (mbar_try_wait(bar, parity)) return true;
     const bool downstream = code == kErrProducerWait || code == kErrEpilogueWait;
-    return wait_slow(bar, parity, w.err, code, stop_on_error && !w.shared, downstream ? 2 * w.timeout_ns : w.timeout_ns);
+    return wait_slow(bar, parity, w.err, code, stop_on_error && !W::kShared, downstream ? 2 * w.timeout_ns : w.timeout_ns);
 }
 
 // Bounded wait with cluster-scope acquire (the dynamic tile queue).
-__device__ __noinline__ inline bool wait_bounded_cluster(uint32_t bar, uint32_t parity, const WaitCtx& w,
+template <typename W>
+__device__ __noinline__ bool wait_bounded_cluster(uint32_t bar, uint32_t parity, const W& w,
                                                          int32_t code) {
     const uint64_t t0 = global_timer_ns();
     for (uint32_t n = 1;; ++n) {
         if (mbar_try_wait_cluster(bar, parity)) return true;
         if ((n & 255u) == 0) {
-            if (!w.shared && *reinterpret_cast<volatile int32_t*>(w.err) != 0) return false;
+            if (!W::kShared && *reinterpret_cast<volatile int32_t*>(w.err) != 0) return false;
             if (global_timer_ns() - t0 > 2 * w.timeout_ns) {
                 atomicOr(w.err, code);
                 return false;
@@ -92,7 +100,8 @@ __device__ __noinline__ inline bool wait_bounded_cluster(uint32_t bar, uint32_t 
 
 // Warp-uniform wait: lane 0 waits (bounded); then every lane observes the
 // completed phase itself, which cannot move on before this warp arrives.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const WaitCtx& w, int32_t code,
+template <typename W>
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const W& w, int32_t code,
                                           int lane) {
     int ok = 1;
     if (lane == 0) ok = wait_bounded(bar, parity, w, code) ? 1 : 0;

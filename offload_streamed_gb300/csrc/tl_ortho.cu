@@ -249,7 +249,7 @@ template <bool A_MN, bool B_MN, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     ortho_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                  const __grid_constant__ OutMaps maps, const OrthoParams p) {
-    const WaitCtx wc{p.err, p.timeout_ns, true};
+    const SharedWaitCtx wc{p.err, p.timeout_ns};
     constexpr int S = kOrthoStages;
     constexpr uint32_t kStage = 2 * kHalfStage;
     constexpr bool SYM = MODE == GRAM || MODE == SQUARE;
@@ -445,7 +445,7 @@ constexpr int kSmallThreads = kThreads + 32;
 template <bool A_MN, bool B_MN, int MODE>
 __global__ void __launch_bounds__(kSmallThreads, 1)
     ortho_small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const OrthoParams p) {
-    const WaitCtx wc{p.err, p.timeout_ns, true};
+    const SharedWaitCtx wc{p.err, p.timeout_ns};
     constexpr int S = kSmallStages;
     constexpr uint32_t kStage = 2 * kHalfStage;
     constexpr bool SYM = MODE == GRAM || MODE == SQUARE;
