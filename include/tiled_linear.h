@@ -657,6 +657,119 @@ tl_status tiled_linear_orthogonalize(int64_t batch, int64_t rows, int64_t cols, 
                                      float scale, void *out_dev, int64_t ldo, int64_t o_apart, void *workspace_dev,
                                      size_t workspace_bytes, int32_t *err_dev, void *stream);
 
+/* --- a linear layer whose weight depends on the row ----------------------------
+ * Experts and adapters.  Conventions as for the operators above: device-resident
+ * matrices, `stream` of the current device, workspaces in use until the call's
+ * work has completed and 256-byte aligned, err_dev as there, sums in an order that
+ * sizes, types, alignments and the device's model fix.
+ *
+ * Rows in groups: offsets [groups + 1] (device int32) names an order's places; group
+ * g owns places offsets[g] .. offsets[g + 1] - 1, perhaps none.  Where a call takes
+ * rows_dev, place p stands for row rows[p] of the matrix, else for row p.  Whatever
+ * these arrays hold, nothing outside the matrices is read or written: places past
+ * R, or rows outside the matrix, are left out or count as zeros.
+ * groups (experts, adapters) is 1..1024. */
+
+/* The order of entries by group.  ids [T, k] (k 1..32): an entry's group; one
+ * outside 0..groups-1 belongs to none.  slots [T, k]: an entry's place, -1 of none;
+ * rows [T k]: the token t of the entry at each place; offsets [groups + 1].  Places
+ * of a group are in the entries' order; behind the last group's are the entries of
+ * no group.  T = 0 writes zeros to offsets.
+ * workspace: tiled_linear_route_workspace_bytes (0 if the sizes are invalid).
+ * Errors: TL_ERR_INVALID, TL_ERR_WORKSPACE, TL_ERR_CUDA. */
+size_t tiled_linear_route_workspace_bytes(int64_t T, int64_t k, int64_t groups);
+tl_status tiled_linear_group_rows(int64_t T, int64_t k, int64_t groups, const int32_t *ids_dev, int32_t *slots_dev,
+                                  int32_t *rows_dev, int32_t *offsets_dev, void *workspace_dev, size_t workspace_bytes,
+                                  void *stream);
+
+/* The k experts of each token with the largest of its logits [T, experts] (tl_type,
+ * ld), largest first, the lowest index first among equals, and their weights [T, k]
+ * (fp32): with l the logits,
+ *   normalize != 0:  w_j = exp(l_j) / sum of exp(l_i) over the chosen i
+ *   normalize == 0:  w_j = exp(l_j) / sum of exp(l_e) over all experts e
+ * A logit of -inf or NaN is never chosen and counts as -inf; where too few are left,
+ * ids are -1 and weights 0.  (+inf gives weights of NaN.)  The rest as
+ * tiled_linear_group_rows of the ids.  k <= experts. */
+tl_status tiled_linear_route(int64_t T, int64_t experts, int64_t k, int32_t type, const void *logits_dev, int64_t ld,
+                             int32_t normalize, float *weights_dev, int32_t *ids_dev, int32_t *slots_dev,
+                             int32_t *rows_dev, int32_t *offsets_dev, void *workspace_dev, size_t workspace_bytes,
+                             void *stream);
+
+/* The weights' gradient by the logits: dlogits [T, experts] (the logits' type, ld
+ * lddl) for dweights [T, k], the choice held fixed.  ids as the forward wrote them.
+ * Errors: TL_ERR_INVALID, TL_ERR_CUDA. */
+tl_status tiled_linear_route_backward(int64_t T, int64_t experts, int64_t k, int32_t type, const void *logits_dev,
+                                      int64_t ld, const int32_t *ids_dev, const float *dweights_dev, int32_t normalize,
+                                      void *dlogits_dev, int64_t lddl, void *stream);
+
+/* out[t] = sum_j weights[t, j] y[slots[t, j]] (fp32 sums in j's order, rounded once),
+ * y [rows, cols] and out [T, cols] of `type`; weights NULL for ones; a slot outside
+ * 0..rows-1 adds nothing.  Its gradients: dy[slots[t, j]] = weights[t, j] dout[t]
+ * (a slot that no entry names is left as it was; none may be named twice) and
+ * dweights[t, j] = sum_c dout[t, c] y[slots[t, j], c] (fp32; 0 for a slot outside;
+ * NULL where not wanted, and y may then be NULL).  cols is 1..1048576; any alignment
+ * of the elements is taken, rows on 16-byte boundaries 16 bytes at a time.
+ * Errors: TL_ERR_INVALID, TL_ERR_CUDA. */
+tl_status tiled_linear_combine(int64_t T, int64_t k, int64_t cols, int64_t rows, int32_t type, const void *y_dev,
+                               int64_t ldy, const int32_t *slots_dev, const float *weights_dev, void *out_dev,
+                               int64_t ldout, void *stream);
+tl_status tiled_linear_combine_backward(int64_t T, int64_t k, int64_t cols, int64_t rows, int32_t type,
+                                        const void *dout_dev, int64_t lddout, const int32_t *slots_dev,
+                                        const void *y_dev, int64_t ldy, const float *weights_dev, void *dy_dev,
+                                        int64_t lddy, float *dweights_dev, void *stream);
+
+/* Products grouped by expert: with w [groups][K, n] (ld ldw, w_apart elements from
+ * one to the next), x [x_rows, K], dy [R, n] and group g's places p,
+ *   forward: y[p] = x[row(p)] . w[g]           y [R, n]
+ *   dx     : dx[p] = dy[p] . w[g]^T            dx [R, K]
+ *   dw     : dw[g] = sum_p x[row(p)]^T dy[p]   dw [groups][K, n], zeros for no places
+ * of `type` (bf16 or fp16), with fp32 sums.  Places of no group: y and dx are left
+ * as they were.  Leading dimensions and distances are multiples of 8 elements,
+ * matrices 16-byte aligned.  Errors: TL_ERR_INVALID, TL_ERR_CUDA. */
+tl_status tiled_linear_grouped_forward(int64_t R, int64_t K, int64_t n, int64_t groups, int32_t type,
+                                       const void *x_dev, int64_t ldx, int64_t x_rows, const int32_t *rows_dev,
+                                       const void *w_dev, int64_t ldw, int64_t w_apart, const int32_t *offsets_dev,
+                                       void *y_dev, int64_t ldy, int32_t *err_dev, void *stream);
+tl_status tiled_linear_grouped_dx(int64_t R, int64_t K, int64_t n, int64_t groups, int32_t type, const void *dy_dev,
+                                  int64_t lddy, const void *w_dev, int64_t ldw, int64_t w_apart,
+                                  const int32_t *offsets_dev, void *dx_dev, int64_t lddx, int32_t *err_dev,
+                                  void *stream);
+tl_status tiled_linear_grouped_dw(int64_t R, int64_t K, int64_t n, int64_t groups, int32_t type, const void *x_dev,
+                                  int64_t ldx, int64_t x_rows, const int32_t *rows_dev, const void *dy_dev,
+                                  int64_t lddy, const int32_t *offsets_dev, void *dw_dev, int64_t lddw,
+                                  int64_t dw_apart, int32_t *err_dev, void *stream);
+
+/* Low-rank adapters beside a shared projection: row t of x [T, K] belongs to adapter
+ * id = ids[t] (none where that is outside 0..adapters-1), a [adapters][K, r] and
+ * b [adapters][r, n] (r 1..128), s = scale_dev[id] (or `scale` where that is NULL):
+ *   h[t] = x[t] . a[id]  [T, r] (kept for the backward)    y[t] = base[t] + s h[t] . b[id]
+ * and without an adapter h = 0, y = base.  y is made from the unrounded h.  All of
+ * `type` (bf16 or fp16) but base [T, n], which may be fp32 (base_type) or NULL for
+ * zeros: the shared projection's own result, however it was computed.  y may be base.
+ * Backward, with dh = s dy . b^T:
+ *   dx = base + dh . a^T   base [T, K]: the shared projection's part; dx may be base
+ *   da[id] = sum x[t]^T dh[t],   db[id] = s sum h[t]^T dy[t]     zeros without rows
+ * dx, or da and db both, may be NULL where not wanted.
+ * Leading dimensions and distances (of base: any) are multiples of 8 elements,
+ * matrices (base: its elements) 16-byte aligned.  Workspace for either:
+ * tiled_linear_adapter_workspace_bytes (0 if the sizes are invalid).
+ * Errors: TL_ERR_INVALID, TL_ERR_WORKSPACE, TL_ERR_CUDA. */
+size_t tiled_linear_adapter_workspace_bytes(int64_t T, int64_t r, int64_t adapters);
+tl_status tiled_linear_adapter_forward(int64_t T, int64_t K, int64_t n, int64_t r, int64_t adapters, int32_t type,
+                                       const void *x_dev, int64_t ldx, const void *a_dev, int64_t lda, int64_t a_apart,
+                                       const void *b_dev, int64_t ldb, int64_t b_apart, const int32_t *ids_dev,
+                                       const float *scale_dev, float scale, int32_t base_type, const void *base_dev,
+                                       int64_t ldbase, void *y_dev, int64_t ldy, void *h_dev, int64_t ldh,
+                                       void *workspace_dev, size_t workspace_bytes, int32_t *err_dev, void *stream);
+tl_status tiled_linear_adapter_backward(int64_t T, int64_t K, int64_t n, int64_t r, int64_t adapters, int32_t type,
+                                        const void *x_dev, int64_t ldx, const void *h_dev, int64_t ldh,
+                                        const void *dy_dev, int64_t lddy, const void *a_dev, int64_t lda,
+                                        int64_t a_apart, const void *b_dev, int64_t ldb, int64_t b_apart,
+                                        const int32_t *ids_dev, const float *scale_dev, float scale, int32_t base_type,
+                                        const void *base_dev, int64_t ldbase, void *dx_dev, int64_t lddx, void *da_dev,
+                                        int64_t ldda, int64_t da_apart, void *db_dev, int64_t lddb, int64_t db_apart,
+                                        void *workspace_dev, size_t workspace_bytes, int32_t *err_dev, void *stream);
+
 /* --- pinned host memory helpers ------------------------------------------ */
 /* Page-locked host allocation (cudaHostAlloc, portable); *out = NULL on
  * failure.  Free with tiled_linear_host_free. */

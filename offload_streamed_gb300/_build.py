@@ -29,7 +29,7 @@ NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompil
 # Extra flags of single units: the host optimizer's row loop vectorizes its
 # square roots only without errno semantics.
 UNIT_FLAGS = {"tl_adam.cpp": ["-Xcompiler", "-fno-math-errno"]}
-UNITS = ["tl_gemm.cu", "tl_norm.cu", "tl_fp8_quant.cu", "tl_fp8.cu", "tl_ortho.cu", "tl_err_word.cu", "tl_static.cu", "tl_ops.cpp", "tl_ring.cpp", "tl_stats.cpp", "tl_hooks.cpp", "tl_abi.cpp", "tl_adam.cpp",
+UNITS = ["tl_gemm.cu", "tl_norm.cu", "tl_fp8_quant.cu", "tl_fp8.cu", "tl_ortho.cu", "tl_route.cu", "tl_grouped.cu", "tl_grouped_dw.cu", "tl_adapter.cu", "tl_row_ops.cpp", "tl_err_word.cu", "tl_static.cu", "tl_ops.cpp", "tl_ring.cpp", "tl_stats.cpp", "tl_hooks.cpp", "tl_abi.cpp", "tl_adam.cpp",
          "tl_filetier.cpp", "tl_optimizer.cpp"]
 
 

@@ -1,0 +1,163 @@
+// tl_grouped.cuh -- device building blocks of the products whose weight depends
+// on the row: loads of indexed rows, where a group's rows are, the joining of
+// sums that a cluster's CTAs share.
+#pragma once
+#include "tl_grouped.h"
+#include "tl_kernel_common.cuh"
+#include "tl_launch.h"
+#include "tl_tmap.h"
+#include "tl_types.cuh"
+
+#include <climits>
+
+namespace tl {
+namespace gr {
+
+using namespace kc;
+
+constexpr int kMaxGroupsSeen = 1025;  // the groups and the rows behind them
+
+// ---- PTX ---------------------------------------------------------------------
+
+// Four rows of a matrix, 128 bytes of each from column x on, one after another
+// in shared memory (128B-swizzled by address, so 512 bytes from one to the next
+// make the image of one box).  Rows past the matrix arrive as zeros.
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x, const int (&r)[4]) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+        : "memory");
+}
+// The same where the barrier may be in the other CTA of a pair.
+__device__ __forceinline__ void tma_gather4_pair(uint32_t dst, const CUtensorMap* map, uint32_t cluster_bar, int32_t x, const int (&r)[4]) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(cluster_bar), "r"(x), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_box(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x, int32_t y, int32_t z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_box_pair(uint32_t dst, const CUtensorMap* map, uint32_t cluster_bar, int32_t x, int32_t y, int32_t z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(cluster_bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+__device__ __forceinline__ void tma_store_box(const CUtensorMap* map, uint32_t src, int32_t x, int32_t y, int32_t z) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(src), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_ld_16cols(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32"
+        " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_dependents_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t local, uint32_t rank) {
+    float4 v;
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\t"
+        "mapa.shared::cluster.u32 a, %4, %5;\n\t"
+        "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
+        : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+        : "r"(local), "r"(rank)
+        : "memory");
+    return v;
+}
+
+// Instruction descriptor of kind::f16: as idesc_bf16_f32, with A and B both fp16
+// (format 0) where asked, N left out.
+__host__ __device__ constexpr uint32_t idesc_16(int m, bool a_mn, bool b_mn, bool fp16) {
+    return idesc_bf16_f32(m, 0, a_mn, b_mn) & (fp16 ? ~((1u << 7) | (1u << 10)) : ~0u);
+}
+__device__ __forceinline__ uint32_t with_n(uint32_t idesc, int n) { return idesc | (uint32_t(n >> 3) << 17); }
+
+template <bool PAIR>
+__device__ __forceinline__ void umma_16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    if constexpr (PAIR) umma_bf16_pair(d, a, b, idesc, accumulate);
+    else umma_bf16(d, a, b, idesc, accumulate);
+}
+
+// ---- where the rows are ------------------------------------------------------------
+
+// Offsets come from the caller's memory: whatever they hold, a group's rows are some of 0 .. rows - 1.
+__device__ __forceinline__ void group_span(const int32_t* offsets, int groups, int rows, int g, int& begin, int& end) {
+    // (g == groups: the rows behind the last group)
+    begin = min(max(offsets[g], 0), rows);
+    end = g == groups ? rows : min(max(offsets[g + 1], begin), rows);
+}
+
+// Rows p .. p + 3 of an operand, those at or past `end` (`none` stands for them).
+__device__ __forceinline__ void four_rows(const int32_t* index, int p, int end, int none, int (&r)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r[j] = p + j < end ? (index ? __ldg(index + p + j) : p + j) : none;
+}
+
+__device__ __forceinline__ uint16_t round16(float v, bool fp16) {
+    return fp16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+__device__ __forceinline__ float value16(uint16_t v, bool fp16) {
+    return fp16 ? __half2float(__ushort_as_half(v)) : __bfloat162float(__ushort_as_bfloat16(v));
+}
+__device__ __forceinline__ uint32_t round16x2(float lo, float hi, bool fp16) {
+    if (!fp16) return pack_bf16x2(lo, hi);
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+}  // namespace gr
+
+// ---- host side ---------------------------------------------------------------------
+
+template <typename T>
+struct SameType {
+    using type = T;
+};
+// early: the kernel may begin before the one ahead of it in the stream has completed.
+template <typename... A>
+cudaError_t launch_in_clusters(void (*kern)(A...), dim3 grid, int threads, int cluster, size_t smem, bool early, cudaStream_t stream,
+                               typename SameType<A>::type... args) {
+    int per_sm = 0;
+    const cudaError_t e = ctas_per_sm(reinterpret_cast<const void*>(kern), threads, smem, &per_sm);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(unsigned(threads), 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = unsigned(cluster);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = early ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+inline CUtensorMapDataType map_type16(int32_t type) {
+    return type == TL_TYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+}
+
+// The map of an operand's rows for tma_gather4: boxes of one row.
+inline bool rows_map(CUtensorMap* map, int32_t type, const RowsOperand& o, int64_t cols, std::string* why) {
+    return swizzled_map(map, map_type16(type), 2, o.at, uint64_t(cols), uint64_t(o.count), uint64_t(o.ld), 1, why);
+}
+
+}  // namespace tl

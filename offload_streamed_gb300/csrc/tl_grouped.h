@@ -1,0 +1,65 @@
+// tl_grouped.h -- internal interface of the products whose weight depends on the
+// row (host side): rows p = 0 .. rows - 1 in an order in which group g owns
+// offsets[g] .. offsets[g + 1] - 1, and a weight for each group.
+#pragma once
+#include <cstdint>
+#include <string>
+#include <cuda_runtime.h>
+
+namespace tl {
+
+// A matrix whose row for place p is index[p] (p itself without an index).
+struct RowsOperand {
+    const void* at = nullptr;
+    int64_t ld = 0;
+    int64_t count = 0;  // rows of the matrix
+    const int32_t* index = nullptr;
+};
+
+// out[row(p), own] = scale[g] sum_k x[row(p), k] w[g](k, own) (+ base)
+struct GroupedDesc {
+    int64_t rows = 0, reduce = 0, own = 0, groups = 0;
+    int32_t type = 0;  // TL_TYPE_BF16 or TL_TYPE_F16, of x, w and out
+    const int32_t* offsets = nullptr;
+    RowsOperand x;
+    const void* w = nullptr;
+    int64_t ldw = 0, w_apart = 0;
+    bool own_contiguous = true;  // w[g] is [reduce, own]; else [own, reduce]
+    // Not 0: x's columns are two parts of `half` (16, 32, 64 or 128), and both
+    // are multiplied with the same `reduce` <= half weights.
+    int32_t half = 0;
+    RowsOperand out;                // at is written
+    const float* scale = nullptr;   // [groups]; nullptr: scale_all
+    float scale_all = 1.0f;
+    const void* base = nullptr;     // rows as out's; nullptr: none
+    int64_t ldbase = 0;
+    int32_t base_type = 0;
+    bool all_rows = false;          // rows behind the last group are written, too: base, or zeros
+    // Not nullptr (own <= 128): the unrounded result, too, as two parts of split_half
+    // columns whose sum it is to twice the type's digits; [out.count, 2 split_half].
+    void* split_out = nullptr;
+    int32_t split_half = 0;
+    bool early = false;  // the kernel ahead writes x alone: w may be read before it has completed
+    int32_t* err = nullptr;
+};
+std::string grouped_check(const GroupedDesc& d);
+cudaError_t grouped_launch(const GroupedDesc& d, int num_sms, cudaStream_t stream, std::string* why);
+
+// dw[g](i, j) = scale[g] sum over g's places of x[row(p), i] dy[row(p), j]
+struct GroupedDwDesc {
+    int64_t rows = 0, m_dim = 0, n_dim = 0, groups = 0;
+    int32_t type = 0;
+    const int32_t* offsets = nullptr;
+    RowsOperand x, dy;
+    int32_t half = 0;  // not 0: dy's columns are two parts of `half`, which are added (n_dim <= half)
+    void* dw = nullptr;
+    int64_t lddw = 0, dw_apart = 0;
+    bool transposed = false;  // dw[g] is [n_dim, m_dim] (n_dim <= 128 only)
+    const float* scale = nullptr;
+    float scale_all = 1.0f;
+    int32_t* err = nullptr;
+};
+std::string grouped_dw_check(const GroupedDwDesc& d);
+cudaError_t grouped_dw_launch(const GroupedDwDesc& d, int num_sms, cudaStream_t stream, std::string* why);
+
+}  // namespace tl

@@ -2,45 +2,18 @@
 // norm, 8-bit product, orthogonalised update): argument checks, workspaces
 // and launches.  The kernels are in tl_norm.cu, tl_fp8.cu and tl_ortho.cu.
 #include "tiled_linear.h"
+#include "tl_entry.h"
 #include "tl_err_word.h"
 #include "tl_fp8.h"
 #include "tl_launch.h"
 #include "tl_norm.h"
 #include "tl_ortho.h"
-#include "tl_unbound_error.h"
 
 #include <algorithm>
 #include <climits>
-#include <exception>
 #include <string>
 
 using namespace tl;
-
-namespace {
-
-tl_status refuse(tl_status st, const std::string& why) {
-    tl::set_unbound_error(why);
-    return st;
-}
-
-tl_status done(cudaError_t e, const char* what) {
-    if (e == cudaSuccess) return TL_OK;
-    return refuse(TL_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
-}
-
-// Nothing is thrown across the ABI.
-template <typename F>
-tl_status guarded(F&& f) {
-    try {
-        return f();
-    } catch (const std::exception& e) {
-        return refuse(TL_ERR_STATE, e.what());
-    } catch (...) {
-        return refuse(TL_ERR_STATE, "unknown exception");
-    }
-}
-
-}  // namespace
 
 extern "C" {
 
@@ -259,10 +232,6 @@ struct Held {
 
 bool layer_ok(int64_t T, int64_t K, int64_t n) {
     return T >= 0 && K >= 1 && n >= 1 && T <= INT32_MAX / 2 && K <= INT32_MAX / 2 && n <= INT32_MAX / 2;
-}
-
-bool workspace_ok(const void* p, size_t have, size_t need) {
-    return p && (reinterpret_cast<uintptr_t>(p) & 255u) == 0 && have >= need;
 }
 
 Fp8QuantDesc quantizing(int64_t rows, int64_t cols, int32_t type, const void* x, int64_t ldx, const Fp8QuantDesc::Form* row,

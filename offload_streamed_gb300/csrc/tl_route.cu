@@ -1,0 +1,676 @@
+// tl_route.cu -- the router around products grouped by expert: the k best
+// experts of each token and their weights, the entries' order by expert, the
+// weighted sum of the experts' answers, and the gradients of both.
+//
+// Choosing.  A warp holds a token's logits, logit e in lane e % 32, as keys whose
+// order as unsigned integers is that of the logits (0: never chosen).  A round
+// takes the warp's largest key with one integer reduction and removes it.  Keys
+// of 16-bit logits carry the expert's index in their lower half, the lowest index
+// the largest, so a round needs no second reduction for it.
+//
+// Order by expert.  A stable counting sort, whose places depend on nothing but
+// the ids: each CTA counts its entries by expert; then each sums all CTAs' counts
+// (those before its own apart), and its warps, whose entries lie one after
+// another, rank theirs 32 at a time by the lanes of equal id.  Counting is fused
+// into the choice, so a call is two launches, or one where a single CTA does it.
+#include "tl_launch.h"
+#include "tl_route.h"
+#include "tl_types.cuh"
+
+#include <algorithm>
+#include <climits>
+
+namespace tl {
+namespace {
+
+constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
+
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_dependents_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// ---- the entries' order ----------------------------------------------------
+
+struct Sort {
+    const int32_t* ids;
+    int32_t* slots;
+    int32_t* rows;
+    int32_t* offsets;
+    int32_t* counts;  // [groups + 1][CTAs]
+    int32_t entries, k, groups;
+    int32_t per;  // entries of a CTA
+};
+
+__device__ __forceinline__ int bin_of(int id, int groups) { return unsigned(id) < unsigned(groups) ? id : groups; }
+
+// Exclusive sum over the CTA's threads; *all is the total.
+__device__ int scan_cta(int v, int* scratch, int* all) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    int s = v;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const int u = __shfl_up_sync(0xffffffffu, s, d);
+        if (lane >= d) s += u;
+    }
+    if (lane == 31) scratch[warp] = s;
+    __syncthreads();
+    if (warp == 0) {
+        int w = lane < warps ? scratch[lane] : 0;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int u = __shfl_up_sync(0xffffffffu, w, d);
+            if (lane >= d) w += u;
+        }
+        scratch[lane] = w;
+    }
+    __syncthreads();
+    *all = scratch[31];
+    return s - v + (warp ? scratch[warp - 1] : 0);
+}
+
+// The places of entries first .. first + len - 1, `cta` of `ctas`.  at: [warps][groups + 1],
+// start: [groups + 1].  With one CTA there are no counts to read.
+__device__ void place_entries(const Sort& p, int first, int len, int cta, int ctas, int* at, int* start, int* scratch) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, bins = p.groups + 1;
+    for (int i = threadIdx.x; i < kSortWarps * bins; i += kSortThreads) at[i] = 0;
+    __syncthreads();
+    // how many of each group a warp has
+    const int span = (len + kSortThreads - 1) / kSortThreads * 32;
+    const int from = first + min(len, warp * span), to = first + min(len, (warp + 1) * span);
+    int* mine = at + warp * bins;
+    for (int i = from; i < to; i += 32) {
+        const int b = i + lane < to ? bin_of(p.ids[i + lane], p.groups) : -1;
+        const unsigned same = __match_any_sync(0xffffffffu, b);
+        if (b >= 0 && (same & ((1u << lane) - 1)) == 0) mine[b] += __popc(same);
+        __syncwarp();
+    }
+    __syncthreads();
+    // all entries of a group, and those in CTAs before this one
+    for (int g = warp; g < bins; g += kSortWarps) {
+        int before = 0, total = 0;
+        if (ctas > 1) {
+            for (int c = lane; c < ctas; c += 32) {
+                const int v = __ldcg(p.counts + int64_t(g) * ctas + c);
+                total += v;
+                before += c < cta ? v : 0;
+            }
+        } else {
+            total = at[lane * bins + g];
+        }
+        total = __reduce_add_sync(0xffffffffu, total);
+        before = __reduce_add_sync(0xffffffffu, before);
+        // where a warp's entries of the group begin, from the group's first in this CTA on
+        const int v = at[lane * bins + g];
+        int s = v;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int u = __shfl_up_sync(0xffffffffu, s, d);
+            if (lane >= d) s += u;
+        }
+        at[lane * bins + g] = s - v + before;
+        if (lane == 0) start[g] = total;
+    }
+    __syncthreads();
+    int all;
+    const int g = threadIdx.x, v = g < p.groups ? start[g] : 0;
+    const int begin = scan_cta(v, scratch, &all);
+    if (g < p.groups) start[g] = begin;
+    if (g == 0) start[p.groups] = all;
+    if (cta == 0) {
+        if (g < p.groups) p.offsets[g] = begin;
+        if (g == 0) p.offsets[p.groups] = all;
+    }
+    __syncthreads();
+    for (int i = from; i < to; i += 32) {
+        const int b = i + lane < to ? bin_of(p.ids[i + lane], p.groups) : -1;
+        const unsigned same = __match_any_sync(0xffffffffu, b), earlier = same & ((1u << lane) - 1);
+        int place = 0;
+        if (b >= 0) place = start[b] + mine[b] + __popc(earlier);
+        __syncwarp();
+        if (b >= 0) {
+            if (earlier == 0) mine[b] += __popc(same);
+            p.slots[i + lane] = b < p.groups ? place : -1;
+            p.rows[place] = (i + lane) / p.k;
+        }
+        __syncwarp();
+    }
+}
+
+__device__ __forceinline__ void place_all(const Sort& p, bool alone) {
+    extern __shared__ int sort_smem[];
+    __shared__ int scratch[32];
+    int* start = sort_smem + kSortWarps * (p.groups + 1);
+    const int cta = alone ? 0 : int(blockIdx.x), first = cta * p.per;
+    place_entries(p, first, min(p.per, p.entries - first), cta, alone ? 1 : int(gridDim.x), sort_smem, start, scratch);
+}
+
+__global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const Sort p) {
+    extern __shared__ int sort_smem[];
+    grid_dependents_go();
+    for (int b = threadIdx.x; b <= p.groups; b += kSortThreads) sort_smem[b] = 0;
+    __syncthreads();
+    const int first = int(blockIdx.x) * p.per, last = min(p.entries, first + p.per);
+    for (int i = first + int(threadIdx.x); i < last; i += kSortThreads) atomicAdd(sort_smem + bin_of(p.ids[i], p.groups), 1);
+    __syncthreads();
+    for (int b = threadIdx.x; b <= p.groups; b += kSortThreads) p.counts[int64_t(b) * gridDim.x + blockIdx.x] = sort_smem[b];
+}
+
+__global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const Sort p) {
+    grid_dependency_wait();  // the counts (and, of a route, the ids) are there
+    place_all(p, gridDim.x == 1);
+}
+
+// ---- choosing --------------------------------------------------------------
+
+// A logit as a key: larger logits have larger keys, zeros of both signs the same
+// one, and -inf and NaN zero, which is never chosen.  16-bit logits (`inf`: the
+// bits of infinity): the lower half holds the index.
+__device__ __forceinline__ uint32_t key16(uint16_t raw, int e, uint32_t inf) {
+    const uint32_t size = raw & 0x7fffu;
+    if (size > inf || raw == (0x8000u | inf)) return 0;
+    const uint32_t u = size == 0 ? 0x8000u : raw & 0x8000u ? 0xffffu ^ raw : raw | 0x8000u;
+    return u << 16 | uint32_t(0xffff - e);
+}
+__device__ __forceinline__ uint16_t raw16(uint32_t key) {
+    const uint32_t u = key >> 16;
+    return uint16_t(u & 0x8000u ? u & 0x7fffu : 0xffffu ^ u);
+}
+template <typename T>
+__device__ __forceinline__ uint32_t key_of(T v, int e);
+template <>
+__device__ __forceinline__ uint32_t key_of<__nv_bfloat16>(__nv_bfloat16 v, int e) {
+    return key16(__bfloat16_as_ushort(v), e, 0x7f80u);
+}
+template <>
+__device__ __forceinline__ uint32_t key_of<__half>(__half v, int e) {
+    return key16(__half_as_ushort(v), e, 0x7c00u);
+}
+template <>
+__device__ __forceinline__ uint32_t key_of<float>(float v, int) {
+    const uint32_t raw = __float_as_uint(v), size = raw & 0x7fffffffu;
+    if (size > 0x7f800000u || raw == 0xff800000u) return 0;
+    return size == 0 ? 0x80000000u : raw & 0x80000000u ? ~raw : raw | 0x80000000u;
+}
+template <typename T>
+__device__ __forceinline__ float key_value(uint32_t key);
+template <>
+__device__ __forceinline__ float key_value<__nv_bfloat16>(uint32_t key) {
+    return to_f32(__ushort_as_bfloat16(raw16(key)));
+}
+template <>
+__device__ __forceinline__ float key_value<__half>(uint32_t key) {
+    return to_f32(__ushort_as_half(raw16(key)));
+}
+template <>
+__device__ __forceinline__ float key_value<float>(uint32_t key) {
+    return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) v += __shfl_xor_sync(0xffffffffu, v, d);
+    return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+    return v;
+}
+
+struct Choice {
+    const void* logits;
+    int64_t ld;
+    float* weights;
+    int32_t tokens;
+    int32_t normalize;
+    int32_t per;  // tokens of a CTA
+};
+
+// V logits a lane.  Writes ids and weights of a CTA's tokens and its counts; alone: places the entries too.
+template <typename T, int V>
+__global__ void __launch_bounds__(kSortThreads) route_kernel(const Choice c, const Sort p, int32_t* ids, const bool alone) {
+    extern __shared__ int sort_smem[];
+    grid_dependents_go();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, k = p.k, experts = p.groups;
+    for (int b = threadIdx.x; b <= experts; b += kSortThreads) sort_smem[b] = 0;
+    __syncthreads();
+    const int first = int(blockIdx.x) * c.per, last = min(c.tokens, first + c.per);
+    for (int t = first + warp; t < last; t += kSortWarps) {
+        const T* row = static_cast<const T*>(c.logits) + int64_t(t) * c.ld;
+        uint32_t key[V], top = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int e = i * 32 + lane;
+            key[i] = e < experts ? key_of<T>(row[e], e) : 0;
+        }
+        float sum = 0, best = 0;
+        if (!c.normalize) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) top = max(top, key[i]);
+            top = __reduce_max_sync(0xffffffffu, top);
+            best = key_value<T>(top);
+            if (top) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) sum += key[i] ? expf(key_value<T>(key[i]) - best) : 0.0f;
+            }
+            sum = warp_sum(sum);
+        }
+        // lane j keeps the j-th best
+        uint32_t won = 0;
+        int id = -1;
+        uint32_t local = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) local = max(local, key[i]);
+        for (int j = 0; j < k; ++j) {
+            const uint32_t m = __reduce_max_sync(0xffffffffu, local);
+            if (m == 0) break;
+            int e;
+            if constexpr (sizeof(T) == 2) {
+                e = 0xffff - int(m & 0xffffu);
+            } else {
+                uint32_t at = ~0u;
+                if (local == m) {
+#pragma unroll
+                    for (int i = V - 1; i >= 0; --i)
+                        if (key[i] == m) at = uint32_t(i * 32 + lane);
+                }
+                e = int(__reduce_min_sync(0xffffffffu, at));
+            }
+            if (lane == j) {
+                won = m;
+                id = e;
+            }
+            if ((e & 31) == lane) {  // remove the first of the lane's that holds it
+                bool here = true;
+                local = 0;
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const bool it = here && key[i] == m;
+                    here = here && !it;
+                    key[i] = it ? 0 : key[i];
+                    local = max(local, key[i]);
+                }
+            }
+        }
+        const float v = key_value<T>(won);
+        float w = 0;
+        if (c.normalize) {
+            best = __shfl_sync(0xffffffffu, v, 0);
+            w = id >= 0 ? expf(v - best) : 0.0f;
+            sum = warp_sum(w);
+        } else if (id >= 0) {
+            w = expf(v - best);
+        }
+        if (lane < k) {
+            ids[int64_t(t) * k + lane] = id;
+            c.weights[int64_t(t) * k + lane] = id >= 0 ? w / sum : 0.0f;
+            if (!alone) atomicAdd(sort_smem + bin_of(id, experts), 1);
+        }
+    }
+    __syncthreads();
+    if (alone) {
+        place_all(p, true);
+        return;
+    }
+    for (int b = threadIdx.x; b <= experts; b += kSortThreads) p.counts[int64_t(b) * gridDim.x + blockIdx.x] = sort_smem[b];
+}
+
+// A warp for each token, whose row of gradients grows in shared memory.
+constexpr int kBackThreads = 256;
+template <typename T>
+__global__ void __launch_bounds__(kBackThreads) route_backward_kernel(const T* logits, int64_t ld, const int32_t* ids, const float* dweights,
+                                                                      T* out, int64_t ldo, int tokens, int experts, int k, bool normalize) {
+    extern __shared__ float back_smem[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float* row = back_smem + warp * experts;
+    const int64_t t = int64_t(blockIdx.x) * (kBackThreads / 32) + warp;
+    if (t >= tokens) return;
+    const T* l = logits + t * ld;
+    int id = lane < k ? ids[t * k + lane] : -1;
+    if (unsigned(id) >= unsigned(experts)) id = -1;
+    const float g = id >= 0 ? dweights[t * k + lane] : 0.0f;
+    auto held = [](float v) { return v == v ? v : -INFINITY; };  // NaN counts as -inf
+    for (int e = lane; e < experts; e += 32) row[e] = 0;
+    float d, s = 0, best, sum = 0;
+    if (normalize) {
+        const float v = id >= 0 ? held(to_f32(l[id])) : -INFINITY;
+        best = warp_max(v);
+        const float w = v > -INFINITY ? expf(v - best) : 0.0f;
+        sum = warp_sum(w);
+        const float p = sum > 0 ? w / sum : w;
+        s = warp_sum(p * g);
+        d = p * (g - s);
+    } else {
+        d = g;
+        best = -INFINITY;
+        for (int e = lane; e < experts; e += 32) best = fmaxf(best, held(to_f32(l[e])));
+        best = warp_max(best);
+        if (best > -INFINITY)
+            for (int e = lane; e < experts; e += 32) sum += expf(held(to_f32(l[e])) - best);
+        sum = warp_sum(sum);
+        const float v = id >= 0 ? held(to_f32(l[id])) : -INFINITY;
+        s = warp_sum(v > -INFINITY ? expf(v - best) / sum * g : 0.0f);
+    }
+    __syncwarp();
+    for (int j = 0; j < k; ++j) {  // in turn: an expert named twice gets both
+        if (lane == j && id >= 0) row[id] += d;
+        __syncwarp();
+    }
+    for (int e = lane; e < experts; e += 32) {
+        float v = row[e];
+        if (!normalize) {
+            const float at = held(to_f32(l[e]));
+            v = at > -INFINITY ? expf(at - best) / sum * (v - s) : 0.0f;
+        }
+        out[t * ldo + e] = from_f32<T>(v);
+    }
+}
+
+// ---- the sum of the experts' answers ------------------------------------------
+
+// `lanes` threads (a power of two) share a token's row, a vector of N elements
+// each; the grid's second dimension walks the row's further vectors.
+constexpr int kCombineThreads = 256;
+template <typename T, int N>
+__global__ void __launch_bounds__(kCombineThreads) combine_kernel(const T* y, int64_t ldy, const int32_t* slots, const float* weights, T* out,
+                                                                  int64_t ldo, int tokens, int k, int rows, int vectors, int lanes) {
+    const int64_t t = int64_t(blockIdx.x) * (kCombineThreads / lanes) + threadIdx.x / lanes;
+    const int v = int(blockIdx.y) * lanes + int(threadIdx.x % lanes);
+    if (t >= tokens || v >= vectors) return;
+    using L = Lanes<N>;
+    constexpr int M = N == 1 ? 1 : N / 2, kBatch = 4;
+    L sum[M];
+#pragma unroll
+    for (int i = 0; i < M; ++i) sum[i] = splat<L>(0.0f);
+    for (int j0 = 0; j0 < k; j0 += kBatch) {
+        Vec<T, N> u[kBatch];
+        float w[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            w[j] = 0;
+            if (j0 + j < k) {
+                const int s = slots[t * k + j0 + j];
+                const bool there = unsigned(s) < unsigned(rows);
+                if (there) {
+                    u[j] = *reinterpret_cast<const Vec<T, N>*>(y + int64_t(s) * ldy + int64_t(v) * N);
+                    w[j] = weights ? weights[t * k + j0 + j] : 1.0f;
+                } else {  // a missing answer adds nothing, whatever its weight
+#pragma unroll
+                    for (int i = 0; i < N; ++i) u[j].v[i] = from_f32<T>(0.0f);
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+            if (j0 + j < k) {
+                L a[M];
+                unpack(u[j], a);
+#pragma unroll
+                for (int i = 0; i < M; ++i) sum[i] = fma(a[i], splat<L>(w[j]), sum[i]);
+            }
+    }
+    Vec<T, N> o;
+    pack(sum, o);
+    *reinterpret_cast<Vec<T, N>*>(out + t * ldo + int64_t(v) * N) = o;
+}
+
+// A CTA's `lanes` threads walk a token's row once for each of its entries: dout
+// comes from memory the first time and from the first-level cache after that.
+template <typename T, int N>
+__global__ void __launch_bounds__(kCombineThreads) combine_backward_kernel(const T* dout, int64_t lddout, const T* y, int64_t ldy,
+                                                                           const int32_t* slots, const float* weights, T* dy, int64_t lddy,
+                                                                           float* dweights, int tokens, int k, int rows, int vectors, int lanes) {
+    __shared__ float part[kMaxTop][kCombineThreads / 32];
+    const int64_t t = int64_t(blockIdx.x) * (kCombineThreads / lanes) + threadIdx.x / lanes;
+    const int first = int(threadIdx.x % lanes), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    using L = Lanes<N>;
+    constexpr int M = N == 1 ? 1 : N / 2;
+    const bool mine = t < tokens;  // (whole warps: lanes is 32 at least)
+    for (int j = 0; j < k; ++j) {
+        L dot[M];
+#pragma unroll
+        for (int i = 0; i < M; ++i) dot[i] = splat<L>(0.0f);
+        const int s = mine ? slots[t * k + j] : -1;
+        if (unsigned(s) < unsigned(rows)) {
+            const float w = weights ? weights[t * k + j] : 1.0f;
+#pragma unroll 2
+            for (int v = first; v < vectors; v += lanes) {
+                L g[M];
+                unpack(*reinterpret_cast<const Vec<T, N>*>(dout + t * lddout + int64_t(v) * N), g);
+                if (dweights) {
+                    L a[M];
+                    unpack(*reinterpret_cast<const Vec<T, N>*>(y + int64_t(s) * ldy + int64_t(v) * N), a);
+#pragma unroll
+                    for (int i = 0; i < M; ++i) dot[i] = fma(g[i], a[i], dot[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < M; ++i) g[i] = mul(g[i], splat<L>(w));
+                Vec<T, N> o;
+                pack(g, o);
+                *reinterpret_cast<Vec<T, N>*>(dy + int64_t(s) * lddy + int64_t(v) * N) = o;
+            }
+        }
+        if (dweights) {
+            float f = 0;
+#pragma unroll
+            for (int i = 0; i < M; ++i) f += total(dot[i]);
+            f = warp_sum(f);
+            if (lane == 0) part[j][warp] = f;
+        }
+    }
+    if (!dweights) return;
+    __syncthreads();
+    const int per = lanes / 32, groups = kCombineThreads / lanes;  // warps of a token, tokens of a CTA
+    for (int i = threadIdx.x; i < groups * k; i += kCombineThreads) {
+        const int64_t token = int64_t(blockIdx.x) * groups + i / k;
+        if (token >= tokens) continue;
+        float f = 0;
+        for (int w = 0; w < per; ++w) f += part[i % k][i / k * per + w];
+        dweights[token * k + i % k] = f;
+    }
+}
+
+bool off(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
+
+// Tokens (or entries) of a CTA: as many CTAs as SMs where there is work for them.
+constexpr int kSortCtas = 152;
+
+int route_per(int64_t tokens) { return int(std::max<int64_t>(kSortWarps, (tokens + kSortCtas - 1) / kSortCtas)); }
+int group_per(int64_t entries) { return int(std::max<int64_t>(2 * kSortThreads, (entries + kSortCtas - 1) / kSortCtas)); }
+// One CTA does all: a second launch costs more than the further rounds.
+constexpr int64_t kAloneTokens = 128, kAloneEntries = 8192;
+
+template <typename... P, typename... A>
+cudaError_t launch(void (*kern)(P...), unsigned grid, size_t smem, bool early, cudaStream_t stream, A... args) {
+    int per_sm = 0;  // (asked for the shared memory that it allows)
+    const cudaError_t e = ctas_per_sm(reinterpret_cast<const void*>(kern), kSortThreads, smem, &per_sm);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kSortThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = early ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, P(args)...);
+}
+
+size_t place_smem(int64_t groups) { return size_t(kSortWarps + 1) * size_t(groups + 1) * 4; }
+
+Sort sort_of(const RouteDesc& d, int64_t per) {
+    return Sort{d.ids, d.slots, d.rows, d.offsets, d.counts, int32_t(d.tokens * d.k), int32_t(d.k), int32_t(d.groups), int32_t(per)};
+}
+
+template <typename T>
+cudaError_t route_typed(const RouteDesc& d, cudaStream_t stream) {
+    const bool alone = d.tokens <= kAloneTokens;
+    const int per = alone ? int(d.tokens) : route_per(d.tokens);
+    const unsigned grid = unsigned((d.tokens + per - 1) / per);
+    const Sort s = sort_of(d, int64_t(per) * d.k);
+    const Choice c{d.logits, d.ld, d.weights, int32_t(d.tokens), d.normalize ? 1 : 0, per};
+    const size_t smem = alone ? place_smem(d.groups) : size_t(d.groups + 1) * 4;
+    auto run = [&](auto kern) { return launch(kern, grid, smem, false, stream, c, s, d.ids, alone); };
+    cudaError_t e;
+    if (d.groups <= 32) e = run(route_kernel<T, 1>);
+    else if (d.groups <= 64) e = run(route_kernel<T, 2>);
+    else if (d.groups <= 128) e = run(route_kernel<T, 4>);
+    else if (d.groups <= 256) e = run(route_kernel<T, 8>);
+    else if (d.groups <= 512) e = run(route_kernel<T, 16>);
+    else e = run(route_kernel<T, 32>);
+    if (e != cudaSuccess || alone) return e;
+    return launch(sort_place_kernel, grid, place_smem(d.groups), true, stream, s);
+}
+
+int row_lanes(int64_t vectors, int most) {
+    int lanes = 32;
+    while (lanes < most && lanes < vectors) lanes *= 2;
+    return lanes;
+}
+
+// Vectors of 16 bytes where every row of every matrix starts on 16 bytes and holds whole ones.
+template <typename T>
+bool whole_vectors(const CombineDesc& d, bool backward) {
+    const int64_t n = 16 / sizeof(T);
+    if (d.cols % n || off(d.out, 16) || d.ldout % n) return false;
+    if (d.y && (off(d.y, 16) || d.ldy % n)) return false;
+    return !backward || (!off(d.dout, 16) && d.lddout % n == 0);
+}
+
+template <typename T, int N>
+cudaError_t combine_vectors(const CombineDesc& d, bool backward, cudaStream_t stream) {
+    const int64_t vectors = (d.cols + N - 1) / N;
+    const int lanes = row_lanes(vectors, kCombineThreads), tokens = kCombineThreads / lanes;
+    dim3 grid(unsigned((d.tokens + tokens - 1) / tokens));
+    if (!backward) {
+        grid.y = unsigned((vectors + lanes - 1) / lanes);
+        combine_kernel<T, N><<<grid, kCombineThreads, 0, stream>>>(static_cast<const T*>(d.y), d.ldy, d.slots, d.weights, static_cast<T*>(d.out), d.ldout,
+                                                                   int(d.tokens), int(d.k), int(d.rows), int(vectors), lanes);
+    } else {
+        combine_backward_kernel<T, N><<<grid, kCombineThreads, 0, stream>>>(static_cast<const T*>(d.dout), d.lddout, static_cast<const T*>(d.y), d.ldy, d.slots,
+                                                                            d.weights, static_cast<T*>(d.out), d.ldout, d.dweights, int(d.tokens), int(d.k),
+                                                                            int(d.rows), int(vectors), lanes);
+    }
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t combine_typed(const CombineDesc& d, bool backward, cudaStream_t stream) {
+    return whole_vectors<T>(d, backward) ? combine_vectors<T, 16 / sizeof(T)>(d, backward, stream) : combine_vectors<T, 1>(d, backward, stream);
+}
+
+template <typename F>
+cudaError_t by_type(int32_t type, F&& f) {
+    if (type == TL_TYPE_BF16) return f(__nv_bfloat16());
+    if (type == TL_TYPE_F16) return f(__half());
+    return f(float());
+}
+
+std::string entries_check(int64_t tokens, int64_t k, int64_t groups) {
+    if (tokens < 0 || k < 1 || k > kMaxTop) return "tokens must be >= 0 and the entries of a token 1..32";
+    if (groups < 1 || groups > kMaxGroups) return "groups must be 1..1024";
+    if (tokens > INT32_MAX / 2 || tokens * k > INT32_MAX / 2) return "too many entries";
+    return {};
+}
+
+}  // namespace
+
+std::string route_check(const RouteDesc& d, bool with_logits) {
+    std::string bad = entries_check(d.tokens, d.k, d.groups);
+    if (!bad.empty()) return bad;
+    if (with_logits && d.k > d.groups) return "more entries a token than experts";
+    if (!d.offsets || off(d.offsets, 4)) return "offsets is null or not 4-byte aligned";
+    if (d.tokens == 0) return {};
+    if (!d.ids || !d.slots || !d.rows) return "null pointer";
+    if (off(d.ids, 4) || off(d.slots, 4) || off(d.rows, 4)) return "ids, slots and rows must be 4-byte aligned";
+    if (!with_logits) return {};
+    if (!type_known(d.type)) return "unknown tl_type";
+    if (!d.logits || !d.weights) return "null pointer";
+    if (off(d.logits, type_bytes(d.type)) || off(d.weights, 4)) return "logits or weights are not aligned to their elements";
+    if (d.ld < d.groups) return "the logits' leading dimension is smaller than a row";
+    return {};
+}
+
+size_t route_workspace(int64_t tokens, int64_t k, int64_t groups) {
+    if (!entries_check(tokens, k, groups).empty()) return 0;
+    return size_t(groups + 1) * kSortCtas * 4;
+}
+
+cudaError_t group_rows_launch(const RouteDesc& d, cudaStream_t stream) {
+    if (d.tokens == 0) return cudaMemsetAsync(d.offsets, 0, size_t(d.groups + 1) * 4, stream);
+    const int64_t entries = d.tokens * d.k;
+    const bool alone = entries <= kAloneEntries;
+    const int per = alone ? int(entries) : group_per(entries);
+    const unsigned grid = unsigned((entries + per - 1) / per);
+    const Sort s = sort_of(d, per);
+    if (grid > 1) {
+        const cudaError_t e = launch(sort_count_kernel, grid, size_t(d.groups + 1) * 4, false, stream, s);
+        if (e != cudaSuccess) return e;
+    }
+    return launch(sort_place_kernel, grid, place_smem(d.groups), grid > 1, stream, s);
+}
+
+cudaError_t route_launch(const RouteDesc& d, cudaStream_t stream) {
+    if (d.tokens == 0) return cudaMemsetAsync(d.offsets, 0, size_t(d.groups + 1) * 4, stream);
+    return by_type(d.type, [&](auto t) { return route_typed<decltype(t)>(d, stream); });
+}
+
+std::string route_backward_check(const RouteBackwardDesc& d) {
+    std::string bad = entries_check(d.tokens, d.k, d.experts);
+    if (!bad.empty()) return bad;
+    if (d.k > d.experts) return "more entries a token than experts";
+    if (!type_known(d.type)) return "unknown tl_type";
+    if (d.tokens == 0) return {};
+    if (!d.logits || !d.ids || !d.dweights || !d.dlogits) return "null pointer";
+    if (off(d.logits, type_bytes(d.type)) || off(d.dlogits, type_bytes(d.type)) || off(d.ids, 4) || off(d.dweights, 4))
+        return "an operand is not aligned to its elements";
+    if (d.ld < d.experts || d.ldd < d.experts) return "a leading dimension is smaller than a row";
+    return {};
+}
+
+cudaError_t route_backward_launch(const RouteBackwardDesc& d, cudaStream_t stream) {
+    if (d.tokens == 0) return cudaSuccess;
+    constexpr int tokens = kBackThreads / 32;
+    const unsigned grid = unsigned((d.tokens + tokens - 1) / tokens);
+    return by_type(d.type, [&](auto t) {
+        using T = decltype(t);
+        route_backward_kernel<T><<<grid, kBackThreads, size_t(tokens) * size_t(d.experts) * 4, stream>>>(
+            static_cast<const T*>(d.logits), d.ld, d.ids, d.dweights, static_cast<T*>(d.dlogits), d.ldd, int(d.tokens), int(d.experts), int(d.k),
+            d.normalize);
+        return cudaGetLastError();
+    });
+}
+
+std::string combine_check(const CombineDesc& d, bool backward) {
+    if (d.tokens < 0 || d.k < 1 || d.k > kMaxTop) return "tokens must be >= 0 and the entries of a token 1..32";
+    if (d.tokens > INT32_MAX / 2 || d.tokens * d.k > INT32_MAX / 2) return "too many entries";
+    if (d.cols < 1 || d.cols > (1 << 20)) return "cols must be 1..1048576";
+    if (d.rows < 0 || d.rows > INT32_MAX / 2) return "rows must be >= 0 and below 2^30";
+    if (!type_known(d.type)) return "unknown tl_type";
+    if (d.tokens == 0) return {};
+    if (!d.slots || off(d.slots, 4) || off(d.weights, 4)) return "slots are null, or slots or weights not 4-byte aligned";
+    const size_t e = type_bytes(d.type);
+    if (!backward) {
+        if (!d.out || off(d.out, e) || d.ldout < d.cols) return "out is null, not aligned to its elements, or its leading dimension too small";
+        if (d.rows > 0 && (!d.y || off(d.y, e) || d.ldy < d.cols)) return "y is null, not aligned to its elements, or its leading dimension too small";
+        return {};
+    }
+    if (!d.dout || off(d.dout, e) || d.lddout < d.cols) return "dout is null, not aligned to its elements, or its leading dimension too small";
+    if (d.rows > 0 && (!d.out || off(d.out, e) || d.ldout < d.cols)) return "dy is null, not aligned to its elements, or its leading dimension too small";
+    if (off(d.dweights, 4)) return "dweights is not 4-byte aligned";
+    if (d.dweights && d.rows > 0 && (!d.y || off(d.y, e) || d.ldy < d.cols)) return "y is null, not aligned to its elements, or its leading dimension too small";
+    return {};
+}
+
+cudaError_t combine_launch(const CombineDesc& d, cudaStream_t stream) {
+    if (d.tokens == 0) return cudaSuccess;
+    return by_type(d.type, [&](auto t) { return combine_typed<decltype(t)>(d, false, stream); });
+}
+
+cudaError_t combine_backward_launch(const CombineDesc& d, cudaStream_t stream) {
+    if (d.tokens == 0) return cudaSuccess;
+    return by_type(d.type, [&](auto t) { return combine_typed<decltype(t)>(d, true, stream); });
+}
+
+}  // namespace tl

@@ -192,6 +192,26 @@ def load():
         L.tiled_linear_orthogonalize.argtypes = [i64, i64, i64, i32, vp, i64, i64, i32] + [ctypes.c_float] * 5 + \
             [vp, i64, i64, vp, sz, vp, vp]
         L.tiled_linear_orthogonalize.restype = st
+        L.tiled_linear_route_workspace_bytes.argtypes = [i64, i64, i64]
+        L.tiled_linear_route_workspace_bytes.restype = sz
+        L.tiled_linear_group_rows.argtypes = [i64, i64, i64, vp, vp, vp, vp, vp, sz, vp]
+        L.tiled_linear_route.argtypes = [i64, i64, i64, i32, vp, i64, i32, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.tiled_linear_route_backward.argtypes = [i64, i64, i64, i32, vp, i64, vp, vp, i32, vp, i64, vp]
+        L.tiled_linear_combine.argtypes = [i64, i64, i64, i64, i32, vp, i64, vp, vp, vp, i64, vp]
+        L.tiled_linear_combine_backward.argtypes = [i64, i64, i64, i64, i32, vp, i64, vp, vp, i64, vp, vp, i64, vp, vp]
+        L.tiled_linear_grouped_forward.argtypes = [i64, i64, i64, i64, i32, vp, i64, i64, vp, vp, i64, i64, vp, vp, i64, vp, vp]
+        L.tiled_linear_grouped_dx.argtypes = [i64, i64, i64, i64, i32, vp, i64, vp, i64, i64, vp, vp, i64, vp, vp]
+        L.tiled_linear_grouped_dw.argtypes = [i64, i64, i64, i64, i32, vp, i64, i64, vp, vp, i64, vp, vp, i64, i64, vp, vp]
+        L.tiled_linear_adapter_workspace_bytes.argtypes = [i64, i64, i64]
+        L.tiled_linear_adapter_workspace_bytes.restype = sz
+        L.tiled_linear_adapter_forward.argtypes = [i64] * 5 + [i32, vp, i64, vp, i64, i64, vp, i64, i64, vp, vp, ctypes.c_float,
+                                                               i32, vp, i64, vp, i64, vp, i64, vp, sz, vp, vp]
+        L.tiled_linear_adapter_backward.argtypes = [i64] * 5 + [i32, vp, i64, vp, i64, vp, i64, vp, i64, i64, vp, i64, i64, vp,
+                                                                vp, ctypes.c_float, i32, vp, i64, vp, i64, vp, i64, i64, vp,
+                                                                i64, i64, vp, sz, vp, vp]
+        for name in ("group_rows", "route", "route_backward", "combine", "combine_backward", "grouped_forward", "grouped_dx",
+                     "grouped_dw", "adapter_forward", "adapter_backward"):
+            getattr(L, "tiled_linear_" + name).restype = st
         L.tiled_linear_host_alloc.argtypes = [sz, ctypes.POINTER(vp)]
         L.tiled_linear_host_alloc.restype = st
         L.tiled_linear_host_free.argtypes = [vp]
@@ -495,6 +515,85 @@ def tiled_linear_orthogonalize(batch, rows, cols, type, g, ldg, g_apart, steps, 
     _check(load().tiled_linear_orthogonalize(batch, rows, cols, type, g, ldg, g_apart, steps, a, b, c, eps, scale, out,
                                              ldo, o_apart, workspace, workspace_bytes, err, stream),
            "tiled_linear_orthogonalize")
+
+
+def tiled_linear_route_workspace_bytes(T: int, k: int, groups: int) -> int:
+    return int(load().tiled_linear_route_workspace_bytes(T, k, groups))
+
+
+def tiled_linear_group_rows(T, k, groups, ids, slots, rows, offsets, workspace, workspace_bytes, stream) -> None:
+    _check(load().tiled_linear_group_rows(T, k, groups, ids, slots, rows, offsets, workspace, workspace_bytes, stream),
+           "tiled_linear_group_rows")
+
+
+def tiled_linear_route(T, experts, k, type, logits, ld, normalize, weights, ids, slots, rows, offsets,
+                       workspace, workspace_bytes, stream) -> None:
+    _check(load().tiled_linear_route(T, experts, k, type, logits, ld, normalize, weights, ids, slots, rows, offsets,
+                                     workspace, workspace_bytes, stream),
+           "tiled_linear_route")
+
+
+def tiled_linear_route_backward(T, experts, k, type, logits, ld, ids, dweights, normalize, dlogits, lddl,
+                                stream) -> None:
+    _check(load().tiled_linear_route_backward(T, experts, k, type, logits, ld, ids, dweights, normalize, dlogits,
+                                              lddl, stream),
+           "tiled_linear_route_backward")
+
+
+def tiled_linear_combine(T, k, cols, rows, type, y, ldy, slots, weights, out, ldout, stream) -> None:
+    _check(load().tiled_linear_combine(T, k, cols, rows, type, y, ldy, slots, weights, out, ldout, stream),
+           "tiled_linear_combine")
+
+
+def tiled_linear_combine_backward(T, k, cols, rows, type, dout, lddout, slots, y, ldy, weights, dy, lddy,
+                                  dweights, stream) -> None:
+    _check(load().tiled_linear_combine_backward(T, k, cols, rows, type, dout, lddout, slots, y, ldy, weights, dy,
+                                                lddy, dweights, stream),
+           "tiled_linear_combine_backward")
+
+
+def tiled_linear_grouped_forward(R, K, n, groups, type, x, ldx, x_rows, rows, w, ldw, w_apart, offsets, y,
+                                 ldy, err, stream) -> None:
+    _check(load().tiled_linear_grouped_forward(R, K, n, groups, type, x, ldx, x_rows, rows, w, ldw, w_apart, offsets,
+                                               y, ldy, err, stream),
+           "tiled_linear_grouped_forward")
+
+
+def tiled_linear_grouped_dx(R, K, n, groups, type, dy, lddy, w, ldw, w_apart, offsets, dx, lddx, err, stream) -> None:
+    _check(load().tiled_linear_grouped_dx(R, K, n, groups, type, dy, lddy, w, ldw, w_apart, offsets, dx, lddx, err,
+                                          stream),
+           "tiled_linear_grouped_dx")
+
+
+def tiled_linear_grouped_dw(R, K, n, groups, type, x, ldx, x_rows, rows, dy, lddy, offsets, dw, lddw,
+                            dw_apart, err, stream) -> None:
+    _check(load().tiled_linear_grouped_dw(R, K, n, groups, type, x, ldx, x_rows, rows, dy, lddy, offsets, dw, lddw,
+                                          dw_apart, err, stream),
+           "tiled_linear_grouped_dw")
+
+
+def tiled_linear_adapter_workspace_bytes(T: int, r: int, adapters: int) -> int:
+    return int(load().tiled_linear_adapter_workspace_bytes(T, r, adapters))
+
+
+def tiled_linear_adapter_forward(T, K, n, r, adapters, type, x, ldx, a, lda, a_apart, b, ldb, b_apart, ids,
+                                 scale_dev, scale, base_type, base, ldbase, y, ldy, h, ldh, workspace,
+                                 workspace_bytes, err, stream) -> None:
+    _check(load().tiled_linear_adapter_forward(T, K, n, r, adapters, type, x, ldx, a, lda, a_apart, b, ldb, b_apart,
+                                               ids, scale_dev, scale, base_type, base, ldbase, y, ldy, h, ldh,
+                                               workspace, workspace_bytes, err, stream),
+           "tiled_linear_adapter_forward")
+
+
+def tiled_linear_adapter_backward(T, K, n, r, adapters, type, x, ldx, h, ldh, dy, lddy, a, lda, a_apart, b,
+                                  ldb, b_apart, ids, scale_dev, scale, base_type, base, ldbase, dx, lddx,
+                                  da, ldda, da_apart, db, lddb, db_apart, workspace, workspace_bytes, err,
+                                  stream) -> None:
+    _check(load().tiled_linear_adapter_backward(T, K, n, r, adapters, type, x, ldx, h, ldh, dy, lddy, a, lda, a_apart,
+                                                b, ldb, b_apart, ids, scale_dev, scale, base_type, base, ldbase, dx,
+                                                lddx, da, ldda, da_apart, db, lddb, db_apart, workspace,
+                                                workspace_bytes, err, stream),
+           "tiled_linear_adapter_backward")
 
 
 def tiled_linear_host_alloc(nbytes: int) -> int:
@@ -1162,3 +1261,281 @@ def orthogonalize(g, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315), eps
                                stream)
     out = out if ldo == cols else out[:, :, :cols]
     return out if g.dim() == 3 else out[0]
+
+
+# --- a linear layer whose weight depends on the row ----------------------------
+# The router's experts and the adapters of many requests.  Functions of torch tensors
+# like the ones above.  Matrices of bf16 or fp16 are taken as they lie where their
+# rows start on 16-byte boundaries, and are copied into such rows first where they
+# do not (a weight that is used often is better kept in them).  Results whose width is no
+# multiple of 8 are views with gaps between the rows.
+
+def _half_type(t, where: str, name: str) -> int:
+    kind = _types.get(t.dtype)
+    if kind not in (TL_TYPE_BF16, TL_TYPE_F16):
+        _refuse(where, f"{name} has dtype {t.dtype}: bfloat16 or float16 is wanted")
+    return kind
+
+
+def _int32(t, shape, device, where: str, name: str) -> int:
+    if t.dtype != _torch.int32 or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
+        _refuse(where, f"{name} must be contiguous int32 {list(shape)} on the matrix's device")
+    return t.data_ptr()
+
+
+def _matrix16(t, where: str, name: str):
+    """(tensor to keep, pointer, ld) of a matrix in rows on 16-byte boundaries."""
+    ld = _ld(t, where, name)
+    rows, cols = t.shape
+    if rows <= 1:
+        ld = _up(cols, 8)
+    if t.data_ptr() % 16 or ld % 8:
+        ld = _up(cols, 8)
+        kept = _torch.empty((rows, ld), dtype=t.dtype, device=t.device)
+        kept[:, :cols].copy_(t)
+        t = kept
+    return t, t.data_ptr(), ld
+
+
+def _stack16(t, where: str, name: str):
+    """(tensor to keep, pointer, ld, distance) of a stack of matrices, likewise."""
+    if not t.is_cuda or t.dim() != 3 or 0 in t.shape:
+        _refuse(where, f"{name} must be a stack of matrices with elements on a CUDA device")
+    count, rows, cols = t.shape
+    apart, ld, step = t.stride()
+    if cols > 1 and step != 1:
+        _refuse(where, f"the rows of {name} are not contiguous")
+    if rows == 1:
+        ld = _up(cols, 8)
+    if count == 1:
+        apart = rows * ld
+    if ld < cols or apart < (rows - 1) * ld + cols:
+        _refuse(where, f"the rows or matrices of {name} overlap")
+    if t.data_ptr() % 16 or ld % 8 or apart % 8:
+        ld = _up(cols, 8)
+        kept = _torch.empty((count, rows, ld), dtype=t.dtype, device=t.device)
+        kept[:, :, :cols].copy_(t)
+        t, apart = kept, rows * ld
+    return t, t.data_ptr(), ld, apart
+
+
+def _result16(shape, like):
+    """An empty result in rows on 16-byte boundaries, and its ld."""
+    ld = _up(shape[-1], 8)
+    out = _torch.empty((*shape[:-1], ld), dtype=like.dtype, device=like.device)
+    return (out if ld == shape[-1] else out[..., :shape[-1]]), ld
+
+
+def _grouping(T: int, k: int, groups: int, device):
+    """Empty slots, rows and offsets, and the workspace of the grouping."""
+    torch = _torch
+    need = tiled_linear_route_workspace_bytes(T, k, groups)
+    return (torch.empty((T, k), dtype=torch.int32, device=device), torch.empty(T * k, dtype=torch.int32, device=device),
+            torch.empty(groups + 1, dtype=torch.int32, device=device), torch.empty(need, dtype=torch.uint8, device=device), need)
+
+
+def group_rows(ids, groups: int):
+    """(slots, rows, offsets): the order by group of the entries ids [T, k] (int32; an id
+    outside 0..groups-1 is of no group).  Places offsets[g]..offsets[g + 1] - 1 hold
+    group g's entries in the order they have in ids, rows[place] is an entry's t and
+    slots [T, k] its place (-1 of no group; those entries' rows come last)."""
+    where, _ = "group_rows", _t()
+    if not ids.is_cuda or ids.dim() != 2:
+        _refuse(where, "ids must be a matrix on a CUDA device")
+    (T, k), device = ids.shape, ids.device
+    if groups < 1:
+        _refuse(where, "groups must be 1..1024")
+    ip, stream = _int32(ids, ids.shape, device, where, "ids"), _stream_of(device, where)
+    slots, rows, offsets, work, need = _grouping(T, k, groups, device)
+    tiled_linear_group_rows(T, k, groups, ip, slots.data_ptr(), rows.data_ptr(), offsets.data_ptr(), work.data_ptr(), need, stream)
+    return slots, rows, offsets
+
+
+def route(logits, k: int, normalize: bool = True):
+    """(weights, ids, slots, rows, offsets): the k experts with the largest of each token's
+    logits [T, experts] (bf16, fp16 or fp32), largest first, the lowest index first among
+    equals; their weights (fp32 [T, k]), a softmax over the k (normalize) or over all
+    experts; and the entries' order by expert as ``group_rows`` gives it.  A logit of
+    -inf or NaN is never chosen: where too few are left, ids are -1 and weights 0."""
+    torch, where = _t(), "route"
+    ld, (T, experts), device = _ld(logits, where, "logits"), logits.shape, logits.device
+    kind, stream = _type_of(logits, where), _stream_of(device, where)
+    if not 1 <= k <= experts:
+        _refuse(where, f"k must be 1..{experts}")
+    weights = torch.empty((T, k), dtype=torch.float32, device=device)
+    ids = torch.empty((T, k), dtype=torch.int32, device=device)
+    slots, rows, offsets, work, need = _grouping(T, k, experts, device)
+    tiled_linear_route(T, experts, k, kind, logits.data_ptr(), ld, int(normalize), weights.data_ptr(), ids.data_ptr(),
+                       slots.data_ptr(), rows.data_ptr(), offsets.data_ptr(), work.data_ptr(), need, stream)
+    return weights, ids, slots, rows, offsets
+
+
+def route_backward(dweights, logits, ids, normalize: bool = True):
+    """dlogits (like logits) of ``route``'s weights for dweights [T, k] (fp32), with its
+    ids [T, k]; the choice itself has no derivative."""
+    torch, where = _t(), "route_backward"
+    ld, (T, experts), device = _ld(logits, where, "logits"), logits.shape, logits.device
+    kind, stream = _type_of(logits, where), _stream_of(device, where)
+    if ids.dim() != 2 or ids.shape[0] != T:
+        _refuse(where, "ids and logits do not fit each other")
+    k, ip = ids.shape[1], _int32(ids, ids.shape, device, where, "ids")
+    if dweights.shape != ids.shape or dweights.dtype != torch.float32 or dweights.device != device or not dweights.is_contiguous():
+        _refuse(where, "dweights must be contiguous float32, as ids")
+    out = torch.empty((T, experts), dtype=logits.dtype, device=device)
+    tiled_linear_route_backward(T, experts, k, kind, logits.data_ptr(), ld, ip, dweights.data_ptr(), int(normalize), out.data_ptr(),
+                                experts, stream)
+    return out
+
+
+def _combine_args(slots, weights, device, where: str):
+    if slots.dim() != 2:
+        _refuse(where, "slots must be a matrix")
+    sp, wp = _int32(slots, slots.shape, device, where, "slots"), None
+    if weights is not None:
+        if weights.shape != slots.shape or weights.dtype != _torch.float32 or weights.device != device or not weights.is_contiguous():
+            _refuse(where, "weights must be contiguous float32, as slots")
+        wp = weights.data_ptr()
+    return sp, wp
+
+
+def combine(y, slots, weights=None):
+    """out [T, cols] = sum over j of weights[t, j] y[slots[t, j]] for y [rows, cols] (bf16,
+    fp16 or fp32), slots [T, k] as ``route`` gives them (-1 adds nothing) and weights
+    fp32 [T, k], None for ones (which gives the gradient of rows picked up by ``rows``)."""
+    torch, where = _t(), "combine"
+    ldy, (rows, cols), device = _ld(y, where, "y"), y.shape, y.device
+    kind, stream = _type_of(y, where), _stream_of(device, where)
+    sp, wp = _combine_args(slots, weights, device, where)
+    T, k = slots.shape
+    out = torch.empty((T, cols), dtype=y.dtype, device=device)
+    tiled_linear_combine(T, k, cols, rows, kind, y.data_ptr(), ldy, sp, wp, out.data_ptr(), cols, stream)
+    return out
+
+
+def combine_backward(dout, slots, y=None, weights=None):
+    """(dy, dweights) of ``combine`` for dout [T, cols]: dy [rows, cols], rows as y's (T k without
+    y), of which those that no slot names are left unset; dweights fp32 [T, k], None without y."""
+    torch, where = _t(), "combine_backward"
+    ldd, (T, cols), device = _ld(dout, where, "dout"), dout.shape, dout.device
+    kind, stream = _type_of(dout, where), _stream_of(device, where)
+    sp, wp = _combine_args(slots, weights, device, where)
+    if slots.shape[0] != T:
+        _refuse(where, "slots and dout do not fit each other")
+    k, yp, ldy, dweights = slots.shape[1], None, 0, None
+    rows = T * k
+    if y is not None:
+        ldy, rows = _ld(y, where, "y"), y.shape[0]
+        if y.shape[1] != cols or y.dtype != dout.dtype or y.device != device:
+            _refuse(where, "y and dout differ in columns, dtype or device")
+        yp, dweights = y.data_ptr(), torch.empty((T, k), dtype=torch.float32, device=device)
+    dy = torch.empty((rows, cols), dtype=dout.dtype, device=device)
+    tiled_linear_combine_backward(T, k, cols, rows, kind, dout.data_ptr(), ldd, sp, yp, ldy, wp, dy.data_ptr(), cols,
+                                  None if dweights is None else dweights.data_ptr(), stream)
+    return dy, dweights
+
+
+def _grouped_args(x, w, offsets, rows, where: str):
+    kind, (xk, xp, ldx) = _half_type(x, where, "x"), _matrix16(x, where, "x")
+    wk, wp, ldw, apart = _stack16(w, where, "the weight")
+    groups, K, n = w.shape
+    if x.shape[1] != K or w.dtype != x.dtype or w.device != x.device:
+        _refuse(where, "x and the weight do not fit each other")
+    op, rp, R = _int32(offsets, (groups + 1,), x.device, where, "offsets"), None, x.shape[0]
+    if rows is not None:
+        R = rows.shape[0] if rows.dim() == 1 else -1
+        rp = _int32(rows, (R,), x.device, where, "rows")
+    return kind, (xk, wk), (xp, ldx, x.shape[0], rp), (wp, ldw, apart), op, (R, K, n, groups)
+
+
+def grouped_linear(x, w, offsets, rows=None):
+    """y [R, n]: y[p] = x[p] . w[g] for the places p = offsets[g]..offsets[g + 1] - 1 of each
+    group g, with w [groups, K, n] and x [R, K] (both bf16 or fp16), or x[rows[p]] for
+    x [tokens, K] and rows [R] (``route``'s).  offsets: int32 [groups + 1] on the
+    device, groups of any size; rows of y in no group are left unset."""
+    where, _ = "grouped_linear", _t()
+    kind, kept, xa, wa, op, (R, K, n, groups) = _grouped_args(x, w, offsets, rows, where)
+    stream = _stream_of(x.device, where)
+    y, ldy = _result16((R, n), x)
+    tiled_linear_grouped_forward(R, K, n, groups, kind, *xa, *wa, op, y.data_ptr(), ldy, _err_word(x.device), stream)
+    return y
+
+
+def grouped_linear_backward(x, dy, w, offsets, rows=None):
+    """(dx [R, K], dw [groups, K, n]) of ``grouped_linear`` for dy [R, n]: dx[p] = dy[p] . w[g]^T
+    (with rows, the gradient by x is ``combine(dx, slots)``), dw[g] = the sum over g's
+    places of x^T dy, zeros where there are none."""
+    where, _ = "grouped_linear_backward", _t()
+    kind, kept, xa, wa, op, (R, K, n, groups) = _grouped_args(x, w, offsets, rows, where)
+    dk, dp, lddy = _matrix16(dy, where, "dy")
+    if dy.shape != (R, n) or dy.dtype != x.dtype or dy.device != x.device:
+        _refuse(where, "x, dy and the weight do not fit each other")
+    stream, err = _stream_of(x.device, where), _err_word(x.device)
+    (dx, lddx), (dw, lddw) = _result16((R, K), x), _result16((groups, K, n), x)
+    tiled_linear_grouped_dx(R, K, n, groups, kind, dp, lddy, *wa, op, dx.data_ptr(), lddx, err, stream)
+    tiled_linear_grouped_dw(R, K, n, groups, kind, *xa, dp, lddy, op, dw.data_ptr(), lddw, K * lddw, err, stream)
+    return dx, dw
+
+
+def _adapter_args(x, a, b, ids, scale, where: str):
+    kind, (xk, xp, ldx) = _half_type(x, where, "x"), _matrix16(x, where, "x")
+    (ak, ap, lda, a_apart), (bk, bp, ldb, b_apart) = _stack16(a, where, "a"), _stack16(b, where, "b")
+    adapters, K, r = a.shape
+    if x.shape[1] != K or b.shape[:2] != (adapters, r) or any(t.dtype != x.dtype or t.device != x.device for t in (a, b)):
+        _refuse(where, "x, a and b do not fit each other")
+    ip, sp, s = _int32(ids, (x.shape[0],), x.device, where, "ids"), None, 1.0
+    if _torch.is_tensor(scale):
+        _vector(scale, adapters, x.device, where, "scale")
+        if scale.dtype != _torch.float32:
+            _refuse(where, "scale must be float32")
+        sp = scale.data_ptr()
+    else:
+        s = float(scale)
+    return kind, (xk, ak, bk), (xp, ldx), (ap, lda, a_apart), (bp, ldb, b_apart), ip, (sp, s), (x.shape[0], K, b.shape[2], r, adapters)
+
+
+def _adapter_base(base, shape, like, where: str):
+    if base is None:
+        return TL_TYPE_F32, None, 0
+    if base.shape != shape or base.device != like.device or base.dtype not in (like.dtype, _torch.float32):
+        _refuse(where, f"base must be {list(shape)} of x's dtype or float32 on its device")
+    return _type_of(base, where), base.data_ptr(), _ld(base, where, "base")
+
+
+def _adapter_work(T: int, r: int, adapters: int, device):
+    need = tiled_linear_adapter_workspace_bytes(T, r, adapters)
+    return _torch.empty(need, dtype=_torch.uint8, device=device), need
+
+
+def adapter_linear(x, a, b, ids, base=None, scale=1.0):
+    """(y, h): y[t] = base[t] + s h[t] . b[ids[t]], h[t] = x[t] . a[ids[t]], for x [T, K], a
+    [adapters, K, r] and b [adapters, r, n] (bf16 or fp16, r up to 128), ids int32 [T] on
+    the device (one outside 0..adapters-1: no adapter, h = 0 and y = base).  base
+    [T, n] (x's dtype or fp32; None for zeros) is the shared projection's result,
+    streamed, in 8 bits or any other; scale: one number, or fp32 [adapters].  h, kept
+    for the backward, is rounded to x's dtype, y is made from the unrounded one."""
+    where, _ = "adapter_linear", _t()
+    kind, kept, xa, aa, ba, ip, sa, (T, K, n, r, adapters) = _adapter_args(x, a, b, ids, scale, where)
+    bt, bp, ldbase = _adapter_base(base, (T, n), x, where)
+    stream, (work, need) = _stream_of(x.device, where), _adapter_work(T, r, adapters, x.device)
+    (y, ldy), (h, ldh) = _result16((T, n), x), _result16((T, r), x)
+    tiled_linear_adapter_forward(T, K, n, r, adapters, kind, *xa, *aa, *ba, ip, *sa, bt, bp, ldbase, y.data_ptr(), ldy,
+                                 h.data_ptr(), ldh, work.data_ptr(), need, _err_word(x.device), stream)
+    return y, h
+
+
+def adapter_linear_backward(x, h, dy, a, b, ids, base=None, scale=1.0):
+    """(dx [T, K], da, db) of ``adapter_linear`` for dy [T, n]: with dh = s dy . b^T, dx = base +
+    dh . a^T (base [T, K], x's dtype or fp32: the gradient through the shared projection),
+    da and db like a and b, zeros for adapters without rows."""
+    where, _ = "adapter_linear_backward", _t()
+    kind, kept, xa, aa, ba, ip, sa, (T, K, n, r, adapters) = _adapter_args(x, a, b, ids, scale, where)
+    (hk, hp, ldh), (dk, dp, lddy) = _matrix16(h, where, "h"), _matrix16(dy, where, "dy")
+    if h.shape != (T, r) or dy.shape != (T, n) or any(t.dtype != x.dtype or t.device != x.device for t in (h, dy)):
+        _refuse(where, "x, h and dy do not fit each other")
+    bt, bp, ldbase = _adapter_base(base, (T, K), x, where)
+    stream, (work, need) = _stream_of(x.device, where), _adapter_work(T, r, adapters, x.device)
+    (dx, lddx), (da, ldda), (db, lddb) = _result16((T, K), x), _result16((adapters, K, r), x), _result16((adapters, r, n), x)
+    tiled_linear_adapter_backward(T, K, n, r, adapters, kind, *xa, hp, ldh, dp, lddy, *aa, *ba, ip, *sa, bt, bp, ldbase,
+                                  dx.data_ptr(), lddx, da.data_ptr(), ldda, K * ldda, db.data_ptr(), lddb, r * lddb,
+                                  work.data_ptr(), need, _err_word(x.device), stream)
+    return dx, da, db
