@@ -725,11 +725,15 @@ tl_status tiled_linear_combine_backward(int64_t T, int64_t k, int64_t cols, int6
  *   dw     : dw[g] = sum_p x[row(p)]^T dy[p]   dw [groups][K, n], zeros for no places
  * of `type` (bf16 or fp16), with fp32 sums.  Places of no group: y and dx are left
  * as they were.  Leading dimensions and distances are multiples of 8 elements,
- * matrices 16-byte aligned.  Errors: TL_ERR_INVALID, TL_ERR_CUDA. */
+ * matrices 16-byte aligned.  With rows_dev, forward and dw need a workspace of
+ * tiled_linear_grouped_workspace_bytes (0 if the sizes are invalid), else none.
+ * Errors: TL_ERR_INVALID, TL_ERR_WORKSPACE, TL_ERR_CUDA. */
+size_t tiled_linear_grouped_workspace_bytes(int64_t R, int64_t K);
 tl_status tiled_linear_grouped_forward(int64_t R, int64_t K, int64_t n, int64_t groups, int32_t type,
                                        const void *x_dev, int64_t ldx, int64_t x_rows, const int32_t *rows_dev,
                                        const void *w_dev, int64_t ldw, int64_t w_apart, const int32_t *offsets_dev,
-                                       void *y_dev, int64_t ldy, int32_t *err_dev, void *stream);
+                                       void *y_dev, int64_t ldy, void *workspace_dev,
+                                       size_t workspace_bytes, int32_t *err_dev, void *stream);
 tl_status tiled_linear_grouped_dx(int64_t R, int64_t K, int64_t n, int64_t groups, int32_t type, const void *dy_dev,
                                   int64_t lddy, const void *w_dev, int64_t ldw, int64_t w_apart,
                                   const int32_t *offsets_dev, void *dx_dev, int64_t lddx, int32_t *err_dev,
@@ -737,7 +741,8 @@ tl_status tiled_linear_grouped_dx(int64_t R, int64_t K, int64_t n, int64_t group
 tl_status tiled_linear_grouped_dw(int64_t R, int64_t K, int64_t n, int64_t groups, int32_t type, const void *x_dev,
                                   int64_t ldx, int64_t x_rows, const int32_t *rows_dev, const void *dy_dev,
                                   int64_t lddy, const int32_t *offsets_dev, void *dw_dev, int64_t lddw,
-                                  int64_t dw_apart, int32_t *err_dev, void *stream);
+                                  int64_t dw_apart, void *workspace_dev, size_t workspace_bytes, int32_t *err_dev,
+                                  void *stream);
 
 /* Low-rank adapters beside a shared projection: row t of x [T, K] belongs to adapter
  * id = ids[t] (none where that is outside 0..adapters-1), a [adapters][K, r] and

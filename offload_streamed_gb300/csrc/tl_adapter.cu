@@ -184,7 +184,7 @@ constexpr int kFewSplits = 16;
 
 struct Workspace {
     int32_t *slots, *rows, *offsets, *counts;
-    uint16_t* split;  // [tokens, 2 half]
+    uint16_t* split;  // [tokens, 2 half], by place
     size_t bytes;
     Workspace(void* base, int64_t tokens, int64_t rank, int64_t adapters) {
         uintptr_t at = reinterpret_cast<uintptr_t>(base);
@@ -255,8 +255,7 @@ GroupedDesc shrink(const AdapterDesc& d, const Workspace& w, bool backward) {
 GroupedDesc expand(const AdapterDesc& d, const Workspace& w, bool backward) {
     GroupedDesc g = product(d, w);
     g.half = half_of(d.rank);
-    g.x.at = w.split;
-    g.x.ld = 2 * g.half;
+    g.x = {w.split, 2 * g.half, d.tokens, nullptr};  // by place
     g.w = backward ? d.a : d.b;
     g.ldw = backward ? d.lda : d.ldb;
     g.w_apart = backward ? d.a_apart : d.b_apart;
@@ -290,8 +289,7 @@ GroupedDwDesc gradient(const AdapterDesc& d, const Workspace& w, bool of_b) {
         g.x.at = d.x;
         g.x.ld = d.ldx;
         g.half = half_of(d.rank);
-        g.dy.at = w.split;
-        g.dy.ld = 2 * g.half;
+        g.dy = {w.split, 2 * g.half, d.tokens, nullptr};  // by place
         g.dw = d.da;
         g.lddw = d.ldda;
         g.dw_apart = d.da_apart;

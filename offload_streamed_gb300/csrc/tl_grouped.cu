@@ -5,15 +5,16 @@
 // in memory) and the rows are its N side.  N is then chosen for each tile in steps
 // of 16 or 32, so that a group's ragged end costs its rows and not a tile of 128 or
 // 256, and a weight for few rows is read once and multiplied at the rate of its
-// bytes.  Rows are picked up where they lie by TMA gathers of four rows (a lane of
-// the loading warp for each four), so that no sorted copy of x is made.
+// bytes.
 // A result's columns are the tensor memory's lanes; it is turned on its way out
 // through shared memory.
 //
 //  grouped_kernel    : a CTA pair (M = 256) and up to 256 rows a tile, persistent,
-//                      two accumulators; for groups of many rows.
+//                      two accumulators; for groups of many rows.  Indexed rows
+//                      are sorted first, into a copy (see Picker in tl_grouped.cuh).
 //  grouped_few_kernel: a CTA and up to 16 .. 128 rows a tile; the CTAs of a cluster
 //                      share the reduction and add their parts in a fixed order.
+//                      Indexed rows are picked up where they lie.
 //
 // Every wait on an mbarrier is bounded, as in tl_gemm.cu.
 #include "tl_grouped.cuh"
@@ -34,6 +35,9 @@ struct Params {
     uint32_t w_bytes;  // of the weight a stage and CTA
     int32_t num_m;
     const int32_t* offsets;
+    const uint16_t* x;
+    int64_t ldx;
+    int32_t x_rows, x_cols;
     const int32_t* x_index;
     const int32_t* out_index;
     int32_t out_rows;
@@ -98,9 +102,9 @@ __device__ __forceinline__ void store_four(const Params& p, int64_t row, int col
     }
 }
 
-// The unrounded result as two parts: what rounding keeps and what it takes off,
+// The unrounded result of place p as two parts: what rounding keeps and what it takes off,
 // rounded in its turn (an infinity leaves nothing).
-__device__ __forceinline__ void store_split(const Params& p, int64_t row, int col, const float (&f)[4]) {
+__device__ __forceinline__ void store_split(const Params& p, int64_t place, int col, const float (&f)[4]) {
     uint16_t hi[4], lo[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -109,7 +113,7 @@ __device__ __forceinline__ void store_split(const Params& p, int64_t row, int co
         const float rest = v - value16(hi[j], p.fp16);
         lo[j] = round16(isfinite(rest) ? rest : 0.0f, p.fp16);
     }
-    uint16_t* dst = p.split_out + row * 2 * p.split_half + col;
+    uint16_t* dst = p.split_out + place * 2 * p.split_half + col;
     *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0] | uint32_t(hi[1]) << 16, hi[2] | uint32_t(hi[3]) << 16);
     *reinterpret_cast<uint2*>(dst + p.split_half) = make_uint2(lo[0] | uint32_t(lo[1]) << 16, lo[2] | uint32_t(lo[3]) << 16);
 }
@@ -153,6 +157,8 @@ __device__ __forceinline__ Tile find_tile(const Params& p, const int* first, int
     t.n = (t.count + 31) & ~31;
     return t;
 }
+
+constexpr int kBoxRows = 32;  // of x
 
 template <bool W_MN>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -236,34 +242,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---------------- loads: each CTA its own indices and half of the rows ----------------
         uint32_t fills = 0;
         bool ok = true;
-        for (int tile = int(cluster_id_x()); ok && tile < tiles; tile += step) {
-            const Tile t = tile_at(tile);
-            if (t.g == p.groups) continue;  // rows of no group: nothing to multiply
-            const int m0 = t.m * 256 + int(rank) * kBlockM, half_n = t.n / 2;
-            const bool mine = 4 * lane < half_n;
-            int r[4] = {0, 0, 0, 0};
-            if (mine) {
-                // (past the tile's last row: that row again, whose results are not stored)
-                const int last = t.p0 + t.count - 1, at = t.p0 + int(rank) * half_n + 4 * lane;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int place = min(at + j, last);
-                    r[j] = p.x_index ? __ldg(p.x_index + place) : place;
-                }
-            }
-            const uint32_t bytes = 2u * (p.w_bytes + uint32_t(half_n) * 128u);
-            for (int kb = 0; kb < p.num_k; ++kb, ++fills) {
-                const uint32_t s = fills % S;
-                int go = 1;
-                if (lane == 0) go = wait_bounded(empty_bar(s), ((fills / S) & 1u) ^ 1u, wc, kErrProducerWait) ? 1 : 0;
-                go = __shfl_sync(0xffffffffu, go, 0);
-                if (!go) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t sa = smem0 + s * kPairStage, sb = sa + kStageA;
-                const uint32_t fb = map_to_rank(full_bar(s), 0);
-                if (lane == 0) {
+        if (lane == 0) {
+            for (int tile = int(cluster_id_x()); ok && tile < tiles; tile += step) {
+                const Tile t = tile_at(tile);
+                if (t.g == p.groups) continue;  // rows of no group: nothing to multiply
+                const int m0 = t.m * 256 + int(rank) * kBlockM, half_n = t.n / 2, row0 = t.p0 + int(rank) * half_n;
+                const int boxes = (half_n + kBoxRows - 1) / kBoxRows;
+                const uint32_t bytes = 2u * (p.w_bytes + uint32_t(boxes * kBoxRows) * 128u);
+                for (int kb = 0; kb < p.num_k; ++kb, ++fills) {
+                    const uint32_t s = fills % S;
+                    if (!wait_bounded(empty_bar(s), ((fills / S) & 1u) ^ 1u, wc, kErrProducerWait)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t sa = smem0 + s * kPairStage, sb = sa + kStageA;
+                    const uint32_t fb = map_to_rank(full_bar(s), 0);
                     if (leader) mbar_arrive_expect_tx(full_bar(s), bytes);
                     const int k0 = (p.half ? kb % p.w_blocks : kb) * kBlockK;
                     if (W_MN) {
@@ -271,9 +264,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     } else {
                         tma_load_box_pair(sa, &map_w, fb, k0, m0, t.g);
                     }
+                    // (rows past the tile's last are others or zeros: their results are not stored)
+                    for (int c = 0; c < boxes; ++c) tma_load_2d_pair(sb + c * kBoxRows * 128, &map_x, fb, kb * kBlockK, row0 + c * kBoxRows);
                 }
-                __syncwarp();
-                if (mine) tma_gather4_pair(sb + uint32_t(lane) * 512u, &map_x, fb, kb * kBlockK, r);
             }
         }
         if (leader && lane == 0) {  // loads land before the CTA may exit
@@ -392,8 +385,7 @@ struct Few {
 
 template <bool W_MN, int N>
 __global__ void __launch_bounds__(kFewThreads, 2)
-    grouped_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, const Params p, int splits,
-                       int per) {
+    grouped_few_kernel(const __grid_constant__ CUtensorMap map_w, const Params p, int splits, int per) {
     using F = Few<N>;
     const SharedWaitCtx wc{p.err, p.timeout_ns};
     constexpr int S = F::kStages;
@@ -453,9 +445,8 @@ __global__ void __launch_bounds__(kFewThreads, 2)
 
     if (threadIdx.x == 0) {
         tma_prefetch_map(&map_w);
-        tma_prefetch_map(&map_x);
         for (int s = 0; s < S; ++s) {
-            mbar_init(full_bar(s), 1);
+            mbar_init(full_bar(s), 1 + kPickWarps);
             mbar_init(empty_bar(s), 1);
         }
         mbar_init(done_bar, 1);
@@ -481,43 +472,15 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             }
         };
         // The weight is there before the kernel ahead of this one began
-        // (GroupedDesc::early); the rows may be what that one makes.
-        const int ahead = min(S, kb1 - kb0);
-        if (lane == 0)
-            for (int i = 0; i < ahead; ++i) {
-                mbar_arrive_expect_tx(full_bar(i), p.w_bytes + uint32_t(N) * 128u);
-                load_w(kb0 + i, i);
-            }
-        grid_dependency_wait();
-        const bool mine = 4 * lane < N;
-        int r[4] = {0, 0, 0, 0};
-        if (mine && kb1 > kb0) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int place = p0 + min(4 * lane + j, count - 1);
-                r[j] = p.x_index ? __ldg(p.x_index + place) : place;
-            }
-        }
+        // (GroupedDesc::early).
         uint32_t fills = 0;
-        for (int kb = kb0; kb < kb1; ++kb, ++fills) {
-            const uint32_t s = fills % S;
-            if (int(fills) >= ahead) {
-                int go = 1;
-                if (lane == 0) {
-                    go = wait_bounded(empty_bar(s), ((fills / S) & 1u) ^ 1u, wc, kErrProducerWait) ? 1 : 0;
-                    if (go) {
-                        mbar_arrive_expect_tx(full_bar(s), p.w_bytes + uint32_t(N) * 128u);
-                        load_w(kb, s);
-                    }
-                }
-                go = __shfl_sync(0xffffffffu, go, 0);
-                if (!go) break;
-            }
-            __syncwarp();
-            if (mine) tma_gather4(smem0 + s * F::kStageBytes + kStageA + uint32_t(lane) * 512u, &map_x, full_bar(s), kb * kBlockK, r);
-        }
-        __syncwarp();
         if (lane == 0) {
+            for (int kb = kb0; kb < kb1; ++kb, ++fills) {
+                const uint32_t s = fills % S;
+                if (!wait_bounded(empty_bar(s), ((fills / S) & 1u) ^ 1u, wc, kErrProducerWait)) break;
+                mbar_arrive_expect_tx(full_bar(s), p.w_bytes);
+                load_w(kb, s);
+            }
             const uint32_t outstanding = fills < uint32_t(S) ? fills : uint32_t(S);
             for (uint32_t j = 0; j < outstanding; ++j) {
                 const uint32_t f = fills - 1 - j;
@@ -540,6 +503,51 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             wait_bounded(done_bar, 0, wc, kErrDrainWait, false);
         }
     } else if (warp >= kFirstEpilogueWarp && warp < kThreads / 32) {
+        // These warps pick up the rows first, which the kernel ahead of this one may make.
+        grid_dependency_wait();
+        {
+            const Picker pick(int(threadIdx.x) - 32 * kFirstEpilogueWarp);
+            constexpr int kRows = (N + kPickRows - 1) / kPickRows, kUnderWay = S - 1 < 4 ? S - 1 : 4;
+            const uint16_t* src[kRows];
+            bool there[kRows];
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+                // (past the last row: that row again, whose results are not stored)
+                const int place = p0 + min(pick.row + kPickRows * r, count - 1), row = p.x_index ? __ldg(p.x_index + place) : place;
+                there[r] = unsigned(row) < unsigned(p.x_rows);
+                src[r] = p.x + (there[r] ? row * p.ldx : 0);
+            }
+            uint32_t fills = 0, handed = 0;
+            auto hand_over = [&] {
+                fence_proxy_async_shared();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(full_bar(handed % S));
+                ++handed;
+            };
+            bool go = true;
+            for (int kb = kb0; kb < kb1; ++kb, ++fills) {
+                const uint32_t s = fills % S;
+                if (!warp_test(empty_bar(s), ((fills / S) & 1u) ^ 1u)) {
+                    cp_async_wait<0>();
+                    while (handed < fills) hand_over();
+                }
+                if (!warp_wait(empty_bar(s), ((fills / S) & 1u) ^ 1u, wc, kErrProducerWait, lane)) {
+                    go = false;
+                    break;
+                }
+#pragma unroll
+                for (int r = 0; r < kRows; ++r)
+                    pick.copy(smem0 + s * F::kStageBytes + kStageA, r, src[r] + kb * kBlockK, there[r] ? p.x_cols - kb * kBlockK : 0);
+                cp_async_commit();
+                if (fills - handed == kUnderWay) {
+                    cp_async_wait<kUnderWay>();
+                    hand_over();
+                }
+            }
+            cp_async_wait<0>();
+            if (go)
+                while (handed < fills) hand_over();
+        }
         const int q = warp & 3, i = q * 32 + lane;
         const bool ok = warp_wait(done_bar, 0, wc, kErrEpilogueWait, lane);
         tc_fence_after();
@@ -612,7 +620,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             if (have > 0 && p.out) store_four(p, row, col, have, f);
             if (p.split_out && col < p.split_half) {
                 const float w[4] = {f.x, f.y, f.z, f.w};
-                store_split(p, row, col, w);
+                store_split(p, p0 + e / 32, col, w);
             }
         }
     }
@@ -631,7 +639,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) grouped_few_shape_kernel() {}
 bool off(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
 
 template <bool W_MN, int N>
-cudaError_t launch_few(const CUtensorMap& mw, const CUtensorMap& mx, Params p, const GroupedDesc& d, int num_sms, cudaStream_t stream) {
+cudaError_t launch_few(const CUtensorMap& mw, Params p, const GroupedDesc& d, int num_sms, cudaStream_t stream) {
     // the most blocks of rows there can be: whole ones, and one of each group that has a row
     const int64_t seen = d.groups + (d.all_rows ? 1 : 0);
     const int64_t blocks = d.rows / N + std::min(seen, d.rows), units = blocks * p.num_m;
@@ -649,10 +657,37 @@ cudaError_t launch_few(const CUtensorMap& mw, const CUtensorMap& mx, Params p, c
     if (units * splits > INT32_MAX) return cudaErrorInvalidConfiguration;
     const int per = (p.num_k + splits - 1) / splits;
     return launch_in_clusters(grouped_few_kernel<W_MN, N>, dim3(unsigned(units * splits)), kFewThreads, splits, Few<N>::kSmem, d.early, stream, mw,
-                              mx, p, splits, per);
+                              p, splits, per);
+}
+
+// A sorted copy of indexed rows: rows outside the matrix as zeros.
+constexpr int kPickCopyThreads = 256;
+__global__ void __launch_bounds__(kPickCopyThreads) pick_rows_kernel(const uint16_t* x, int64_t ldx, int x_rows, const int32_t* index, int rows,
+                                                                     int vectors, int lanes, uint16_t* out, int64_t ldo) {
+    // `lanes` threads (a power of two) walk a row; four vectors of each under way
+    const int64_t p = int64_t(blockIdx.x) * (kPickCopyThreads / lanes) + threadIdx.x / lanes;
+    if (p >= rows) return;
+    const int row = __ldg(index + p);
+    const bool there = unsigned(row) < unsigned(x_rows);
+    const uint4* src = reinterpret_cast<const uint4*>(x + (there ? row * ldx : 0));
+    uint4* dst = reinterpret_cast<uint4*>(out + p * ldo);
+#pragma unroll 4
+    for (int v = int(threadIdx.x % lanes); v < vectors; v += lanes) dst[v] = there ? __ldg(src + v) : make_uint4(0, 0, 0, 0);
 }
 
 }  // namespace
+
+int64_t picked_ld(int64_t cols) { return (cols + 7) / 8 * 8; }
+
+cudaError_t pick_rows_launch(const RowsOperand& x, int64_t rows, int64_t cols, void* out, cudaStream_t stream) {
+    const int64_t vectors = picked_ld(cols) / 8;  // (x's rows hold as many: their distance is a multiple of 8)
+    int lanes = 32;
+    while (lanes < kPickCopyThreads && lanes * 4 < vectors) lanes *= 2;
+    const int per = kPickCopyThreads / lanes;
+    pick_rows_kernel<<<unsigned((rows + per - 1) / per), kPickCopyThreads, 0, stream>>>(static_cast<const uint16_t*>(x.at), x.ld, int(x.count), x.index,
+                                                                                     int(rows), int(vectors), lanes, static_cast<uint16_t*>(out), picked_ld(cols));
+    return cudaGetLastError();
+}
 
 std::string grouped_check(const GroupedDesc& d) {
     constexpr int64_t kMost = INT32_MAX / 2;
@@ -672,6 +707,7 @@ std::string grouped_check(const GroupedDesc& d) {
     if (d.x.ld >= (int64_t(1) << 38) || d.ldw >= (int64_t(1) << 38) || d.w_apart >= (int64_t(1) << 38)) return "a leading dimension is too large";
     if (d.x.count < 1 || (!d.x.index && d.x.count < d.rows)) return "x has too few rows";
     if (!d.out.index && d.out.count < d.rows) return "the result has too few rows";
+    if (off(d.gathered, 16)) return "the workspace is not 16-byte aligned";
     if (off(d.x.index, 4) || off(d.out.index, 4) || off(d.scale, 4)) return "indexes and scales must be 4-byte aligned";
     if (d.base && (d.base_type != d.type && d.base_type != TL_TYPE_F32)) return "base must be of x's type or fp32";
     if (d.base && (off(d.base, type_bytes(d.base_type)) || d.ldbase < d.own)) return "base is not aligned to its elements, or its leading dimension too small";
@@ -690,6 +726,10 @@ cudaError_t grouped_launch(const GroupedDesc& d, int num_sms, cudaStream_t strea
     p.num_k = int32_t((x_cols + kBlockK - 1) / kBlockK);
     p.w_blocks = int32_t(((d.half ? d.half : d.reduce) + kBlockK - 1) / kBlockK);
     p.offsets = d.offsets;
+    p.x = static_cast<const uint16_t*>(d.x.at);
+    p.ldx = d.x.ld;
+    p.x_rows = int32_t(d.x.count);
+    p.x_cols = int32_t(x_cols);
     p.x_index = d.x.index;
     p.out_index = d.out.index;
     p.out_rows = int32_t(d.out.count);
@@ -708,7 +748,6 @@ cudaError_t grouped_launch(const GroupedDesc& d, int num_sms, cudaStream_t strea
     p.err = d.err;
     p.timeout_ns = 2000000000ull;
     CUtensorMap mx, mw;
-    if (!rows_map(&mx, d.type, d.x, x_cols, why)) return cudaErrorInvalidValue;
     const int64_t inner = d.own_contiguous ? d.own : d.reduce, outer = d.own_contiguous ? d.reduce : d.own;
     const int64_t apart = d.groups > 1 ? d.w_apart : (outer * d.ldw);
     const uint32_t box_rows = d.own_contiguous ? uint32_t(kBlockK) : uint32_t(std::min<int64_t>(kBlockM, (d.own + 7) / 8 * 8));
@@ -729,6 +768,14 @@ cudaError_t grouped_launch(const GroupedDesc& d, int num_sms, cudaStream_t strea
             return cudaErrorInvalidValue;
         }
         const unsigned grid = 2 * unsigned(std::min<int64_t>(tiles, std::max(1, num_sms / 2)));
+        RowsOperand x = d.x;
+        if (x.index) {
+            if (!d.gathered) return cudaErrorInvalidValue;
+            const cudaError_t g = pick_rows_launch(d.x, d.rows, x_cols, d.gathered, stream);
+            if (g != cudaSuccess) return g;
+            x = {d.gathered, picked_ld(x_cols), d.rows, nullptr};
+        }
+        if (!rows_map(&mx, d.type, x, x_cols, kBoxRows, why)) return cudaErrorInvalidValue;
         auto run = [&](auto kern) { return launch_in_clusters(kern, dim3(grid), kThreads, 2, kPairSmem, false, stream, mw, mx, p); };
         e = d.own_contiguous ? run(grouped_kernel<true>) : run(grouped_kernel<false>);
     } else {
@@ -737,10 +784,10 @@ cudaError_t grouped_launch(const GroupedDesc& d, int num_sms, cudaStream_t strea
         const int64_t want = 2 * mean;
         auto run = [&](auto mn) {
             constexpr bool MN = decltype(mn)::value;
-            if (want <= 16) return launch_few<MN, 16>(mw, mx, p, d, num_sms, stream);
-            if (want <= 32) return launch_few<MN, 32>(mw, mx, p, d, num_sms, stream);
-            if (want <= 64) return launch_few<MN, 64>(mw, mx, p, d, num_sms, stream);
-            return launch_few<MN, 128>(mw, mx, p, d, num_sms, stream);
+            if (want <= 16) return launch_few<MN, 16>(mw, p, d, num_sms, stream);
+            if (want <= 32) return launch_few<MN, 32>(mw, p, d, num_sms, stream);
+            if (want <= 64) return launch_few<MN, 64>(mw, p, d, num_sms, stream);
+            return launch_few<MN, 128>(mw, p, d, num_sms, stream);
         };
         e = d.own_contiguous ? run(std::true_type{}) : run(std::false_type{});
     }

@@ -19,23 +19,26 @@ constexpr int kMaxGroupsSeen = 1025;  // the groups and the rows behind them
 
 // ---- PTX ---------------------------------------------------------------------
 
-// Four rows of a matrix, 128 bytes of each from column x on, one after another
-// in shared memory (128B-swizzled by address, so 512 bytes from one to the next
-// make the image of one box).  Rows past the matrix arrive as zeros.
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x, const int (&r)[4]) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
-        : "memory");
-}
-// The same where the barrier may be in the other CTA of a pair.
+// Four rows of a matrix, 128 bytes of each from column x on, one after another in
+// shared memory (128B-swizzled by address, so 512 bytes from one to the next make
+// the image of one box), for a CTA pair, whose barrier may be in the other CTA.
+// Rows past the matrix arrive as zeros.
 __device__ __forceinline__ void tma_gather4_pair(uint32_t dst, const CUtensorMap* map, uint32_t cluster_bar, int32_t x, const int (&r)[4]) {
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2"
         " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(cluster_bar), "r"(x), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
         : "memory");
+}
+// 16 bytes of global memory to shared memory, the last 16 - bytes of them as zeros.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(__cvta_generic_to_global(src)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Wait until at most N of this thread's groups are under way.
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 __device__ __forceinline__ void tma_load_box(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x, int32_t y, int32_t z) {
     asm volatile(
@@ -92,6 +95,19 @@ __device__ __forceinline__ void umma_16(uint32_t d, uint64_t a, uint64_t b, uint
     else umma_bf16(d, a, b, idesc, accumulate);
 }
 
+// Whether a phase has completed, by lane 0's look; if so, as every lane sees it.
+__device__ __forceinline__ bool warp_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return __all_sync(0xffffffffu, ok) != 0;
+}
+
 // ---- where the rows are ------------------------------------------------------------
 
 // Offsets come from the caller's memory: whatever they hold, a group's rows are some of 0 .. rows - 1.
@@ -101,11 +117,33 @@ __device__ __forceinline__ void group_span(const int32_t* offsets, int groups, i
     end = g == groups ? rows : min(max(offsets[g + 1], begin), rows);
 }
 
-// Rows p .. p + 3 of an operand, those at or past `end` (`none` stands for them).
-__device__ __forceinline__ void four_rows(const int32_t* index, int p, int end, int none, int (&r)[4]) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) r[j] = p + j < end ? (index ? __ldg(index + p + j) : p + j) : none;
-}
+// ---- rows picked up ------------------------------------------------------------------
+
+// 128 threads pick up rows 16 bytes at a time by cp.async (TMA's gathers of four rows
+// take some 36 clocks each, whoever issues them: 14 bytes a clock and SM): eight threads for 128 bytes of a row, sixteen rows at
+// a time, into the image that a TMA load of a box with 128-byte swizzle leaves.
+// What they wrote is handed to the tensor cores by a proxy fence of each thread
+// after its copies have landed and an arrival of each warp: a stage when four
+// further ones are under way, or all of them before a wait for a free stage, which
+// would otherwise keep from the tensor cores what that wait depends on.
+// For single CTAs alone: the arrival at the other CTA of a pair would need release
+// semantics in the cluster for each stage, which took longer than the stage's MMAs
+// (8192 x 8192 x 4096 in eight groups, 2 rows a token: 3.0 ms, against 1.2 with
+// gathers and 0.8 with a sorted copy made first).
+constexpr int kPickThreads = 128, kPickWarps = kPickThreads / 32, kPickRows = kPickThreads / 8;
+struct Picker {
+    int row, chunk;     // of the first sixteen rows; 16 bytes of the row's 128
+    uint32_t dst;       // in a box, from its start on
+    __device__ __forceinline__ explicit Picker(int thread) : row(thread >> 3), chunk(thread & 7) {
+        dst = uint32_t(row) * 128u + (uint32_t(chunk ^ (row & 7)) << 4);
+    }
+    // Row row + 16 i of a box at `box`: from `src` on (the row's first element of the
+    // box's columns), `cols` of which are there (none: zeros).
+    __device__ __forceinline__ void copy(uint32_t box, int i, const uint16_t* src, int cols) const {
+        const int have = min(max(cols - 8 * chunk, 0), 8);
+        cp_async16(box + dst + uint32_t(i) * (kPickRows * 128u), src + (have ? 8 * chunk : 0), uint32_t(have) * 2u);
+    }
+};
 
 __device__ __forceinline__ uint16_t round16(float v, bool fp16) {
     return fp16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
@@ -155,9 +193,9 @@ inline CUtensorMapDataType map_type16(int32_t type) {
     return type == TL_TYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
 }
 
-// The map of an operand's rows for tma_gather4: boxes of one row.
-inline bool rows_map(CUtensorMap* map, int32_t type, const RowsOperand& o, int64_t cols, std::string* why) {
-    return swizzled_map(map, map_type16(type), 2, o.at, uint64_t(cols), uint64_t(o.count), uint64_t(o.ld), 1, why);
+// The map of an operand's rows where they follow each other.
+inline bool rows_map(CUtensorMap* map, int32_t type, const RowsOperand& o, int64_t cols, uint32_t box_rows, std::string* why) {
+    return swizzled_map(map, map_type16(type), 2, o.at, uint64_t(cols), uint64_t(o.count), uint64_t(o.ld), box_rows, why);
 }
 
 }  // namespace tl

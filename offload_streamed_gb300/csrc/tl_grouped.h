@@ -16,6 +16,10 @@ struct RowsOperand {
     const int32_t* index = nullptr;
 };
 
+// Indexed rows sorted into a matrix [rows, cols] of 16-bit elements, ld picked_ld.
+int64_t picked_ld(int64_t cols);
+cudaError_t pick_rows_launch(const RowsOperand& x, int64_t rows, int64_t cols, void* out, cudaStream_t stream);
+
 // out[row(p), own] = scale[g] sum_k x[row(p), k] w[g](k, own) (+ base)
 struct GroupedDesc {
     int64_t rows = 0, reduce = 0, own = 0, groups = 0;
@@ -36,9 +40,10 @@ struct GroupedDesc {
     int32_t base_type = 0;
     bool all_rows = false;          // rows behind the last group are written, too: base, or zeros
     // Not nullptr (own <= 128): the unrounded result, too, as two parts of split_half
-    // columns whose sum it is to twice the type's digits; [out.count, 2 split_half].
+    // columns whose sum it is to twice the type's digits; [rows, 2 split_half], by place.
     void* split_out = nullptr;
     int32_t split_half = 0;
+    void* gathered = nullptr;  // workspace for an indexed x's rows, [rows, picked_ld] (all but `half` and small `own` need it)
     bool early = false;  // the kernel ahead writes x alone: w may be read before it has completed
     int32_t* err = nullptr;
 };
@@ -54,6 +59,7 @@ struct GroupedDwDesc {
     int32_t half = 0;  // not 0: dy's columns are two parts of `half`, which are added (n_dim <= half)
     void* dw = nullptr;
     int64_t lddw = 0, dw_apart = 0;
+    void* gathered = nullptr;  // workspace for an indexed x's rows, [rows, picked_ld] (n_dim > 128 needs it)
     bool transposed = false;  // dw[g] is [n_dim, m_dim] (n_dim <= 128 only)
     const float* scale = nullptr;
     float scale_all = 1.0f;

@@ -1,13 +1,16 @@
 // tl_grouped_dw.cu -- the weights' gradients of products whose weight depends on
 // the row: dw[g] = sum over g's rows of x[row]^T dy[row].
 //
-// The reduction runs over a group's rows, 64 a block.  Both operands come by TMA
-// gathers of four rows, whether indexed or not: rows past the group's end are
-// asked for past the matrix's and arrive as zeros, so that the next group's rows
-// (which may hold infinities) add nothing, and no row is masked in the kernel.
+// The reduction runs over a group's rows, 64 a block.  Rows past the group's end
+// are zeros in its last block, so that the next group's rows (which may hold
+// infinities) add nothing.
 //
 //  grouped_dw_kernel       : a CTA pair and 256 x 256 of a dw, persistent, as the
 //                            dW product in tl_gemm.cu; a group without rows gets zeros.
+//                            Blocks come by TMA; in a group's last one, gathers of
+//                            four rows ask for rows past the matrix where the group
+//                            has none, which arrive as zeros.  Indexed rows are sorted
+//                            first, into a copy.
 //  grouped_dw_narrow_kernel: 128 of x's columns and all (at most 128) of dy's, for
 //                            adapters; the CTAs of a cluster share a group's rows and
 //                            add their parts in a fixed order.  It takes a dy in two
@@ -28,13 +31,16 @@ struct DwParams {
     const int32_t* offsets;
     const int32_t* x_index;
     const int32_t* dy_index;
-    int32_t x_none, dy_none;  // a row past each matrix
+    const uint16_t* x;
+    const uint16_t* dy;
+    int64_t ldx, lddy;
+    int32_t x_rows, dy_rows, dy_cols;
     const float* scale;
     float scale_all;
     int32_t fp16;
     uint32_t idesc;
     // narrow only
-    int32_t half, n;  // dy's columns in the product (twice `half` with two parts)
+    int32_t half, n;  // dy_cols rounded up: dy's columns in the product (twice `half` with two parts)
     uint16_t* dw;
     int64_t lddw, dw_apart;
     int32_t transposed;
@@ -48,9 +54,11 @@ constexpr uint32_t kEpiBytes = 4 * 2 * kEpiBuf;
 constexpr size_t kSmem = size_t(kStages) * kStage + kEpiBytes + kBarBytes + 1024;
 static_assert(kSmem <= 232448, "shared memory budget");
 
-__global__ void __launch_bounds__(kThreads, 1)
-    grouped_dw_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_dy,
-                      const __grid_constant__ CUtensorMap map_dw, const DwParams p) {
+struct DwMaps {
+    CUtensorMap x, dy, x_rows, dy_rows, dw;  // boxes of 64 rows, and rows one by one
+};
+
+__global__ void __launch_bounds__(kThreads, 1) grouped_dw_kernel(const __grid_constant__ DwMaps maps, const DwParams p) {
     const SharedWaitCtx wc{p.err, p.timeout_ns};
     constexpr int S = kStages;
     extern __shared__ uint8_t smem_raw[];
@@ -69,8 +77,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t drain_bar = bar0 + 8u * (2 * S + 4);
 
     if (threadIdx.x == 0) {
-        tma_prefetch_map(&map_x);
-        tma_prefetch_map(&map_dy);
+        tma_prefetch_map(&maps.x);
+        tma_prefetch_map(&maps.dy);
         for (int s = 0; s < S; ++s) {
             mbar_init(full_bar(s), 1);
             mbar_init(empty_bar(s), 1);
@@ -94,41 +102,40 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int64_t tiles = int64_t(of_group) * p.groups;
 
     if (warp == 0) {
-        // A lane's four rows of a block, in one of the two 64-wide boxes of 128 columns.
-        const int quad = 4 * (lane & 15), chunk = lane >> 4;
         uint32_t fills = 0;
         bool ok = true;
         for (int64_t tile = cluster_id_x(); ok && tile < tiles; tile += step) {
             const int g = int(tile / of_group), local = int(tile % of_group);
             int begin, end;
             group_span(p.offsets, p.groups, p.rows, g, begin, end);
-            const int cx = local % p.num_m * 256 + int(rank) * 128 + chunk * 64, cy = local / p.num_m * 256 + int(rank) * 128 + chunk * 64;
-            int rx[4], ry[4];
-            four_rows(p.x_index, begin + quad, end, p.x_none, rx);
-            four_rows(p.dy_index, begin + quad, end, p.dy_none, ry);
+            const int cx = local % p.num_m * 256 + int(rank) * 128, cy = local / p.num_m * 256 + int(rank) * 128;
             for (int p0 = begin; p0 < end; p0 += kBlockK, ++fills) {
                 const uint32_t s = fills % S;
-                int nx[4], ny[4];  // the next block's rows, on their way while this one is loaded
-                four_rows(p.x_index, p0 + kBlockK + quad, end, p.x_none, nx);
-                four_rows(p.dy_index, p0 + kBlockK + quad, end, p.dy_none, ny);
+                const uint32_t sa = smem0 + s * kStage, sb = sa + kStageA, fb = map_to_rank(full_bar(s), 0);
                 int go = 1;
                 if (lane == 0) {
                     go = wait_bounded(empty_bar(s), ((fills / S) & 1u) ^ 1u, wc, kErrProducerWait) ? 1 : 0;
                     if (go && leader) mbar_arrive_expect_tx(full_bar(s), 2u * kStage);
+                    if (go && p0 + kBlockK <= end)
+                        for (int c = 0; c < 2; ++c) {
+                            tma_load_2d_pair(sa + c * kMnChunk, &maps.x, fb, cx + 64 * c, p0);
+                            tma_load_2d_pair(sb + c * kMnChunk, &maps.dy, fb, cy + 64 * c, p0);
+                        }
                 }
                 go = __shfl_sync(0xffffffffu, go, 0);
                 if (!go) {
                     ok = false;
                     break;
                 }
-                const uint32_t dst = smem0 + s * kStage + uint32_t(chunk) * kMnChunk + uint32_t(lane & 15) * 512u;
-                const uint32_t fb = map_to_rank(full_bar(s), 0);
-                tma_gather4_pair(dst, &map_x, fb, cx, rx);
-                tma_gather4_pair(dst + kStageA, &map_dy, fb, cy, ry);
+                if (p0 + kBlockK > end) {  // a lane's four rows, in one of the two 64-wide boxes
+                    const int quad = 4 * (lane & 15), chunk = lane >> 4;
+                    const uint32_t at = uint32_t(chunk) * kMnChunk + uint32_t(lane & 15) * 512u;
+                    int r[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    rx[j] = nx[j];
-                    ry[j] = ny[j];
+                    for (int j = 0; j < 4; ++j) r[j] = p0 + quad + j < end ? p0 + quad + j : p.rows;  // (a row past both matrices)
+                    tma_gather4_pair(sa + at, &maps.x_rows, fb, cx + 64 * chunk, r);
+                    tma_gather4_pair(sb + at, &maps.dy_rows, fb, cy + 64 * chunk, r);
+                    __syncwarp();
                 }
             }
         }
@@ -206,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 fence_proxy_async_shared();
                 __syncwarp();
                 if (lane == 0) {
-                    tma_store_box(&map_dw, box, n0 + c * 64, row0, g);
+                    tma_store_box(&maps.dw, box, n0 + c * 64, row0, g);
                     bulk_commit_group();
                 }
                 buf ^= 1u;
@@ -233,9 +240,32 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---- narrow gradients --------------------------------------------------------
 
+// The rows of a block that a picking thread copies, of one operand.
+struct BlockRows {
+    const uint16_t* src[kBlockK / kPickRows];
+    bool there[kBlockK / kPickRows];
+    __device__ __forceinline__ void find(const uint16_t* at, int64_t ld, int rows, const int32_t* index, int p, int end) {
+#pragma unroll
+        for (int i = 0; i < kBlockK / kPickRows; ++i) {
+            const int place = p + kPickRows * i, row = place < end ? (index ? __ldg(index + place) : place) : -1;
+            there[i] = unsigned(row) < unsigned(rows);
+            src[i] = at + (there[i] ? row * ld : 0);
+        }
+    }
+    // columns col .. col + 63 of `cols`, to the box at `box`
+    __device__ __forceinline__ void copy(const Picker& pick, uint32_t box, int col, int cols) const {
+#pragma unroll
+        for (int i = 0; i < kBlockK / kPickRows; ++i) {
+            const int have = there[i] ? cols - col : 0;
+            pick.copy(box, i, src[i] + (have > 0 ? col : 0), have);
+        }
+    }
+};
+
 constexpr int kNarrowThreads = kThreads + 32;  // the ninth warp as in tl_grouped.cu
 constexpr size_t kNarrowSmem = 112 * 1024;     // of a CTA: two share an SM
 constexpr int kNarrowMostStages = 8;
+constexpr int kNarrowUnderWay = 1;  // blocks that a picking thread has under way: fewer than the stages, which are two at least
 constexpr uint32_t kNarrowFixed = kBarBytes + 1024;
 __host__ __device__ constexpr uint32_t narrow_stage(int n) { return kStageA + uint32_t((n + 63) / 64) * kMnChunk; }
 constexpr int narrow_stages(int n) {
@@ -249,8 +279,7 @@ static_assert(part_floats(128, false) * 4 <= size_t(narrow_stages(128)) * narrow
 static_assert(part_floats(64, false) * 4 <= size_t(narrow_stages(16)) * narrow_stage(16) && narrow_stages(256) >= 2, "the parts fit the stages");
 
 __global__ void __launch_bounds__(kNarrowThreads, 2)
-    grouped_dw_narrow_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_dy, const DwParams p, int splits,
-                             int stages) {
+    grouped_dw_narrow_kernel(const DwParams p, int splits, int stages) {
     const SharedWaitCtx wc{p.err, p.timeout_ns};
     const int S = stages;
     const uint32_t stage = narrow_stage(p.n);
@@ -275,10 +304,8 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
     while (cols < uint32_t(p.n)) cols *= 2;
 
     if (threadIdx.x == 0) {
-        tma_prefetch_map(&map_x);
-        tma_prefetch_map(&map_dy);
         for (int s = 0; s < S; ++s) {
-            mbar_init(full_bar(s), 1);
+            mbar_init(full_bar(s), kPickWarps);
             mbar_init(empty_bar(s), 1);
         }
         mbar_init(done_bar, 1);
@@ -293,42 +320,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
 
-    if (warp == 0) {
-        const int quad = 4 * (lane & 15), chunk = lane >> 4, boxes = (p.n + 63) / 64;
-        int rx[4], ry[4];
-        four_rows(p.x_index, begin + kb0 * kBlockK + quad, end, p.x_none, rx);
-        four_rows(p.dy_index, begin + kb0 * kBlockK + quad, end, p.dy_none, ry);
-        uint32_t fills = 0;
-        for (int kb = kb0; kb < kb1; ++kb, ++fills) {
-            const uint32_t s = fills % uint32_t(S);
-            int nx[4], ny[4];
-            four_rows(p.x_index, begin + (kb + 1) * kBlockK + quad, end, p.x_none, nx);
-            four_rows(p.dy_index, begin + (kb + 1) * kBlockK + quad, end, p.dy_none, ny);
-            int go = 1;
-            if (lane == 0) {
-                go = wait_bounded(empty_bar(s), ((fills / uint32_t(S)) & 1u) ^ 1u, wc, kErrProducerWait) ? 1 : 0;
-                if (go) mbar_arrive_expect_tx(full_bar(s), stage);
-            }
-            go = __shfl_sync(0xffffffffu, go, 0);
-            if (!go) break;
-            const uint32_t dst = smem0 + s * stage + uint32_t(lane & 15) * 512u;
-            tma_gather4(dst + uint32_t(chunk) * kMnChunk, &map_x, full_bar(s), m0 + chunk * 64, rx);
-            for (int c = chunk; c < boxes; c += 2) tma_gather4(dst + kStageA + uint32_t(c) * kMnChunk, &map_dy, full_bar(s), c * 64, ry);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                rx[j] = nx[j];
-                ry[j] = ny[j];
-            }
-        }
-        __syncwarp();
-        if (lane == 0) {
-            const uint32_t outstanding = fills < uint32_t(S) ? fills : uint32_t(S);
-            for (uint32_t j = 0; j < outstanding; ++j) {
-                const uint32_t f = fills - 1 - j;
-                wait_bounded(full_bar(f % uint32_t(S)), (f / uint32_t(S)) & 1u, wc, kErrDrainWait, false);
-            }
-        }
-    } else if (warp == 1) {
+    if (warp == 1) {
         if (lane == 0) {
             uint32_t fills = 0;
             const uint32_t idesc = with_n(p.idesc, p.n);
@@ -350,6 +342,47 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
     float* part = reinterpret_cast<float*>(smem);
     const int width = p.half ? p.half : p.n, pitch = p.transposed ? 128 : width + 4;
     if (warp >= kFirstEpilogueWarp && warp < kThreads / 32) {
+        {  // these warps pick up the rows of both operands first
+            const Picker pick(int(threadIdx.x) - 32 * kFirstEpilogueWarp);
+            const int boxes = (p.n + 63) / 64;
+            BlockRows x, dy, nx, ny;
+            x.find(p.x, p.ldx, p.x_rows, p.x_index, begin + kb0 * kBlockK + pick.row, end);
+            dy.find(p.dy, p.lddy, p.dy_rows, p.dy_index, begin + kb0 * kBlockK + pick.row, end);
+            uint32_t fills = 0, handed = 0;
+            auto hand_over = [&] {
+                fence_proxy_async_shared();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(full_bar(handed % uint32_t(S)));
+                ++handed;
+            };
+            bool go = true;
+            for (int kb = kb0; kb < kb1; ++kb, ++fills) {
+                const uint32_t s = fills % uint32_t(S);
+                nx.find(p.x, p.ldx, p.x_rows, p.x_index, begin + (kb + 1) * kBlockK + pick.row, end);
+                ny.find(p.dy, p.lddy, p.dy_rows, p.dy_index, begin + (kb + 1) * kBlockK + pick.row, end);
+                if (!warp_test(empty_bar(s), ((fills / uint32_t(S)) & 1u) ^ 1u)) {
+                    cp_async_wait<0>();
+                    while (handed < fills) hand_over();
+                }
+                if (!warp_wait(empty_bar(s), ((fills / uint32_t(S)) & 1u) ^ 1u, wc, kErrProducerWait, lane)) {
+                    go = false;
+                    break;
+                }
+                const uint32_t sa = smem0 + s * stage, sb = sa + kStageA;
+                for (int c = 0; c < 2; ++c) x.copy(pick, sa + c * kMnChunk, m0 + 64 * c, p.m_dim);
+                for (int c = 0; c < boxes; ++c) dy.copy(pick, sb + c * kMnChunk, 64 * c, p.dy_cols);
+                cp_async_commit();
+                if (fills - handed == kNarrowUnderWay) {
+                    cp_async_wait<kNarrowUnderWay>();
+                    hand_over();
+                }
+                x = nx;
+                dy = ny;
+            }
+            cp_async_wait<0>();
+            if (go)
+                while (handed < fills) hand_over();
+        }
         const int q = warp & 3, i = q * 32 + lane;
         const bool ok = warp_wait(done_bar, 0, wc, kErrEpilogueWait, lane);
         tc_fence_after();
@@ -458,6 +491,7 @@ std::string grouped_dw_check(const GroupedDwDesc& d) {
     if (d.x.ld < d.m_dim || d.dy.ld < (d.half ? 2 * d.half : d.n_dim)) return "a leading dimension is smaller than a row";
     if (d.x.ld >= (int64_t(1) << 38) || d.dy.ld >= (int64_t(1) << 38)) return "a leading dimension is too large";
     if (d.x.count < 1 || d.dy.count < 1 || (!d.x.index && d.x.count < d.rows) || (!d.dy.index && d.dy.count < d.rows)) return "x or dy has too few rows";
+    if (off(d.gathered, 16)) return "the workspace is not 16-byte aligned";
     if (off(d.x.index, 4) || off(d.dy.index, 4) || off(d.scale, 4)) return "indexes and scales must be 4-byte aligned";
     return {};
 }
@@ -480,8 +514,13 @@ cudaError_t grouped_dw_launch(const GroupedDwDesc& d, int num_sms, cudaStream_t 
     p.offsets = d.offsets;
     p.x_index = d.x.index;
     p.dy_index = d.dy.index;
-    p.x_none = int32_t(d.x.count);
-    p.dy_none = int32_t(d.dy.count);
+    p.x = static_cast<const uint16_t*>(d.x.at);
+    p.dy = static_cast<const uint16_t*>(d.dy.at);
+    p.ldx = d.x.ld;
+    p.lddy = d.dy.ld;
+    p.x_rows = int32_t(d.x.count);
+    p.dy_rows = int32_t(d.dy.count);
+    p.dy_cols = d.half ? 2 * d.half : int32_t(d.n_dim);
     p.scale = d.scale;
     p.scale_all = d.scale_all;
     p.fp16 = d.type == TL_TYPE_F16 ? 1 : 0;
@@ -492,8 +531,6 @@ cudaError_t grouped_dw_launch(const GroupedDwDesc& d, int num_sms, cudaStream_t 
     p.transposed = d.transposed ? 1 : 0;
     p.err = d.err;
     p.timeout_ns = 2000000000ull;
-    CUtensorMap mx, my, mw;
-    if (!rows_map(&mx, d.type, d.x, d.m_dim, why) || !rows_map(&my, d.type, d.dy, d.half ? 2 * d.half : d.n_dim, why)) return cudaErrorInvalidValue;
     cudaError_t e;
     if (d.half || d.n_dim <= 128) {
         p.num_m = int32_t((d.m_dim + 127) / 128);
@@ -512,19 +549,30 @@ cudaError_t grouped_dw_launch(const GroupedDwDesc& d, int num_sms, cudaStream_t 
         }
         if (e != cudaSuccess) return e;
         if (units * splits > INT32_MAX) return cudaErrorInvalidConfiguration;
-        e = launch_in_clusters(grouped_dw_narrow_kernel, dim3(unsigned(units * splits)), kNarrowThreads, splits, smem, false, stream, mx, my, p, splits,
-                               stages);
+        e = launch_in_clusters(grouped_dw_narrow_kernel, dim3(unsigned(units * splits)), kNarrowThreads, splits, smem, false, stream, p, splits, stages);
     } else {
         if (d.transposed) return cudaErrorInvalidValue;
         const int64_t apart = d.groups > 1 ? d.dw_apart : outer * d.lddw;
-        if (!swizzled_map(&mw, map_type16(d.type), 2, d.dw, uint64_t(d.n_dim), uint64_t(d.m_dim), uint64_t(d.lddw), 32, why, uint64_t(d.groups), uint64_t(apart)))
+        if (d.dy.index) return cudaErrorInvalidValue;
+        RowsOperand x = d.x, dy = d.dy;
+        if (x.index) {
+            if (!d.gathered) return cudaErrorInvalidValue;
+            e = pick_rows_launch(d.x, d.rows, d.m_dim, d.gathered, stream);
+            if (e != cudaSuccess) return e;
+            x = {d.gathered, picked_ld(d.m_dim), d.rows, nullptr};
+        }
+        x.count = dy.count = d.rows;  // no row past the last place is there
+        DwMaps maps;
+        if (!rows_map(&maps.x, d.type, x, d.m_dim, kBlockK, why) || !rows_map(&maps.dy, d.type, dy, d.n_dim, kBlockK, why) ||
+            !rows_map(&maps.x_rows, d.type, x, d.m_dim, 1, why) || !rows_map(&maps.dy_rows, d.type, dy, d.n_dim, 1, why) ||
+            !swizzled_map(&maps.dw, map_type16(d.type), 2, d.dw, uint64_t(d.n_dim), uint64_t(d.m_dim), uint64_t(d.lddw), 32, why, uint64_t(d.groups), uint64_t(apart)))
             return cudaErrorInvalidValue;
         p.num_m = int32_t((d.m_dim + 255) / 256);
         p.num_n = int32_t((d.n_dim + 255) / 256);
         p.idesc = idesc_16(256, true, true, p.fp16 != 0);
         const int64_t tiles = int64_t(p.num_m) * p.num_n * d.groups;
         const unsigned grid = 2 * unsigned(std::min<int64_t>(tiles, std::max(1, num_sms / 2)));
-        e = launch_in_clusters(grouped_dw_kernel, dim3(grid), kThreads, 2, kSmem, false, stream, mx, my, mw, p);
+        e = launch_in_clusters(grouped_dw_kernel, dim3(grid), kThreads, 2, kSmem, false, stream, maps, p);
     }
     if (e != cudaSuccess && why && why->empty()) *why = std::string("kernel launch: ") + cudaGetErrorString(e);
     return e;

@@ -9,6 +9,7 @@
 #include "tl_launch.h"
 #include "tl_route.h"
 
+#include <algorithm>
 #include <climits>
 #include <string>
 
@@ -138,9 +139,15 @@ tl_status tiled_linear_combine_backward(int64_t T, int64_t k, int64_t cols, int6
     });
 }
 
+size_t tiled_linear_grouped_workspace_bytes(int64_t R, int64_t K) {
+    if (R < 0 || K < 1 || R > INT32_MAX / 2 || K > INT32_MAX / 2) return 0;
+    return std::max<size_t>(256, size_t(R) * size_t(picked_ld(K)) * 2);
+}
+
 tl_status tiled_linear_grouped_forward(int64_t R, int64_t K, int64_t n, int64_t groups, int32_t type, const void* x_dev, int64_t ldx,
                                        int64_t x_rows, const int32_t* rows_dev, const void* w_dev, int64_t ldw, int64_t w_apart,
-                                       const int32_t* offsets_dev, void* y_dev, int64_t ldy, int32_t* err_dev, void* stream) {
+                                       const int32_t* offsets_dev, void* y_dev, int64_t ldy, void* workspace_dev, size_t workspace_bytes,
+                                       int32_t* err_dev, void* stream) {
     return guarded([&]() -> tl_status {
         GroupedDesc d;
         d.rows = R;
@@ -159,6 +166,8 @@ tl_status tiled_linear_grouped_forward(int64_t R, int64_t K, int64_t n, int64_t 
         const std::string bad = grouped_check(d);
         if (!bad.empty()) return refuse(TL_ERR_INVALID, bad);
         if (R == 0) return TL_OK;
+        if (rows_dev && !workspace_ok(workspace_dev, workspace_bytes, tiled_linear_grouped_workspace_bytes(R, K))) return refuse(TL_ERR_WORKSPACE, kWorkspace);
+        d.gathered = workspace_dev;
         const int sms = device_sms();
         if (sms < 2) return refuse(TL_ERR_CUDA, "no current device");
         std::string why;
@@ -196,7 +205,7 @@ tl_status tiled_linear_grouped_dx(int64_t R, int64_t K, int64_t n, int64_t group
 
 tl_status tiled_linear_grouped_dw(int64_t R, int64_t K, int64_t n, int64_t groups, int32_t type, const void* x_dev, int64_t ldx, int64_t x_rows,
                                   const int32_t* rows_dev, const void* dy_dev, int64_t lddy, const int32_t* offsets_dev, void* dw_dev,
-                                  int64_t lddw, int64_t dw_apart, int32_t* err_dev, void* stream) {
+                                  int64_t lddw, int64_t dw_apart, void* workspace_dev, size_t workspace_bytes, int32_t* err_dev, void* stream) {
     return guarded([&]() -> tl_status {
         GroupedDwDesc d;
         d.rows = R;
@@ -213,6 +222,9 @@ tl_status tiled_linear_grouped_dw(int64_t R, int64_t K, int64_t n, int64_t group
         d.err = err_dev;
         const std::string bad = grouped_dw_check(d);
         if (!bad.empty()) return refuse(TL_ERR_INVALID, bad);
+        if (R > 0 && rows_dev && !workspace_ok(workspace_dev, workspace_bytes, tiled_linear_grouped_workspace_bytes(R, K)))
+            return refuse(TL_ERR_WORKSPACE, kWorkspace);
+        d.gathered = workspace_dev;
         const int sms = device_sms();
         if (sms < 2) return refuse(TL_ERR_CUDA, "no current device");
         std::string why;

@@ -199,9 +199,11 @@ def load():
         L.tiled_linear_route_backward.argtypes = [i64, i64, i64, i32, vp, i64, vp, vp, i32, vp, i64, vp]
         L.tiled_linear_combine.argtypes = [i64, i64, i64, i64, i32, vp, i64, vp, vp, vp, i64, vp]
         L.tiled_linear_combine_backward.argtypes = [i64, i64, i64, i64, i32, vp, i64, vp, vp, i64, vp, vp, i64, vp, vp]
-        L.tiled_linear_grouped_forward.argtypes = [i64, i64, i64, i64, i32, vp, i64, i64, vp, vp, i64, i64, vp, vp, i64, vp, vp]
+        L.tiled_linear_grouped_workspace_bytes.argtypes = [i64, i64]
+        L.tiled_linear_grouped_workspace_bytes.restype = sz
+        L.tiled_linear_grouped_forward.argtypes = [i64, i64, i64, i64, i32, vp, i64, i64, vp, vp, i64, i64, vp, vp, i64, vp, sz, vp, vp]
         L.tiled_linear_grouped_dx.argtypes = [i64, i64, i64, i64, i32, vp, i64, vp, i64, i64, vp, vp, i64, vp, vp]
-        L.tiled_linear_grouped_dw.argtypes = [i64, i64, i64, i64, i32, vp, i64, i64, vp, vp, i64, vp, vp, i64, i64, vp, vp]
+        L.tiled_linear_grouped_dw.argtypes = [i64, i64, i64, i64, i32, vp, i64, i64, vp, vp, i64, vp, vp, i64, i64, vp, sz, vp, vp]
         L.tiled_linear_adapter_workspace_bytes.argtypes = [i64, i64, i64]
         L.tiled_linear_adapter_workspace_bytes.restype = sz
         L.tiled_linear_adapter_forward.argtypes = [i64] * 5 + [i32, vp, i64, vp, i64, i64, vp, i64, i64, vp, vp, ctypes.c_float,
@@ -552,10 +554,14 @@ def tiled_linear_combine_backward(T, k, cols, rows, type, dout, lddout, slots, y
            "tiled_linear_combine_backward")
 
 
+def tiled_linear_grouped_workspace_bytes(R: int, K: int) -> int:
+    return int(load().tiled_linear_grouped_workspace_bytes(R, K))
+
+
 def tiled_linear_grouped_forward(R, K, n, groups, type, x, ldx, x_rows, rows, w, ldw, w_apart, offsets, y,
-                                 ldy, err, stream) -> None:
+                                 ldy, workspace, workspace_bytes, err, stream) -> None:
     _check(load().tiled_linear_grouped_forward(R, K, n, groups, type, x, ldx, x_rows, rows, w, ldw, w_apart, offsets,
-                                               y, ldy, err, stream),
+                                               y, ldy, workspace, workspace_bytes, err, stream),
            "tiled_linear_grouped_forward")
 
 
@@ -566,9 +572,9 @@ def tiled_linear_grouped_dx(R, K, n, groups, type, dy, lddy, w, ldw, w_apart, of
 
 
 def tiled_linear_grouped_dw(R, K, n, groups, type, x, ldx, x_rows, rows, dy, lddy, offsets, dw, lddw,
-                            dw_apart, err, stream) -> None:
+                            dw_apart, workspace, workspace_bytes, err, stream) -> None:
     _check(load().tiled_linear_grouped_dw(R, K, n, groups, type, x, ldx, x_rows, rows, dy, lddy, offsets, dw, lddw,
-                                          dw_apart, err, stream),
+                                          dw_apart, workspace, workspace_bytes, err, stream),
            "tiled_linear_grouped_dw")
 
 
@@ -1447,6 +1453,15 @@ def _grouped_args(x, w, offsets, rows, where: str):
     return kind, (xk, wk), (xp, ldx, x.shape[0], rp), (wp, ldw, apart), op, (R, K, n, groups)
 
 
+def _grouped_work(R: int, K: int, rows, device):
+    """The workspace for sorted rows and its size, where there are rows to sort."""
+    if rows is None:
+        return None, None, 0
+    need = tiled_linear_grouped_workspace_bytes(R, K)
+    work = _torch.empty(need, dtype=_torch.uint8, device=device)
+    return work, work.data_ptr(), need
+
+
 def grouped_linear(x, w, offsets, rows=None):
     """y [R, n]: y[p] = x[p] . w[g] for the places p = offsets[g]..offsets[g + 1] - 1 of each
     group g, with w [groups, K, n] and x [R, K] (both bf16 or fp16), or x[rows[p]] for
@@ -1455,8 +1470,8 @@ def grouped_linear(x, w, offsets, rows=None):
     where, _ = "grouped_linear", _t()
     kind, kept, xa, wa, op, (R, K, n, groups) = _grouped_args(x, w, offsets, rows, where)
     stream = _stream_of(x.device, where)
-    y, ldy = _result16((R, n), x)
-    tiled_linear_grouped_forward(R, K, n, groups, kind, *xa, *wa, op, y.data_ptr(), ldy, _err_word(x.device), stream)
+    (y, ldy), (work, *ws) = _result16((R, n), x), _grouped_work(R, K, rows, x.device)
+    tiled_linear_grouped_forward(R, K, n, groups, kind, *xa, *wa, op, y.data_ptr(), ldy, *ws, _err_word(x.device), stream)
     return y
 
 
@@ -1470,9 +1485,9 @@ def grouped_linear_backward(x, dy, w, offsets, rows=None):
     if dy.shape != (R, n) or dy.dtype != x.dtype or dy.device != x.device:
         _refuse(where, "x, dy and the weight do not fit each other")
     stream, err = _stream_of(x.device, where), _err_word(x.device)
-    (dx, lddx), (dw, lddw) = _result16((R, K), x), _result16((groups, K, n), x)
+    (dx, lddx), (dw, lddw), (work, *ws) = _result16((R, K), x), _result16((groups, K, n), x), _grouped_work(R, K, rows, x.device)
     tiled_linear_grouped_dx(R, K, n, groups, kind, dp, lddy, *wa, op, dx.data_ptr(), lddx, err, stream)
-    tiled_linear_grouped_dw(R, K, n, groups, kind, *xa, dp, lddy, op, dw.data_ptr(), lddw, K * lddw, err, stream)
+    tiled_linear_grouped_dw(R, K, n, groups, kind, *xa, dp, lddy, op, dw.data_ptr(), lddw, K * lddw, *ws, err, stream)
     return dx, dw
 
 

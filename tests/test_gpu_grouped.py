@@ -108,7 +108,7 @@ def test_rows_of_no_group_keep_their_bits(tl):
         off, x, w = offsets_of(counts), normal(1, R + extra, K), normal(2, 2, K, n)
         y, dx = torch.full((R + extra, n), 7.0, dtype=BF16, device="cuda"), torch.full((R + extra, K), 7.0, dtype=BF16, device="cuda")
         dy, s, err = normal(3, R + extra, n), torch.cuda.current_stream().cuda_stream, tl.tiled_linear_operator_error_word()
-        tl.tiled_linear_grouped_forward(R + extra, K, n, 2, 0, x.data_ptr(), K, R + extra, None, w.data_ptr(), n, K * n, off.data_ptr(), y.data_ptr(), n, err, s)
+        tl.tiled_linear_grouped_forward(R + extra, K, n, 2, 0, x.data_ptr(), K, R + extra, None, w.data_ptr(), n, K * n, off.data_ptr(), y.data_ptr(), n, None, 0, err, s)
         tl.tiled_linear_grouped_dx(R + extra, K, n, 2, 0, dy.data_ptr(), n, w.data_ptr(), n, K * n, off.data_ptr(), dx.data_ptr(), K, err, s)
         assert (y[R:] == 7).all() and (dx[R:] == 7).all()
         check("y", y[:R], *grouped(x[:R], w, off))
@@ -122,8 +122,8 @@ def test_results_between_others(tl):
     s, err = torch.cuda.current_stream().cuda_stream, tl.tiled_linear_operator_error_word()
     y = torch.full((R, n + 16), 7.0, dtype=BF16, device="cuda")
     dw = torch.full((E, K + 1, n + 8), 7.0, dtype=BF16, device="cuda")
-    tl.tiled_linear_grouped_forward(R, K, n, E, 0, x.data_ptr(), K, R, None, w.data_ptr(), n, K * n, off.data_ptr(), y[:, 8:].data_ptr(), n + 16, err, s)
-    tl.tiled_linear_grouped_dw(R, K, n, E, 0, x.data_ptr(), K, R, None, dy.data_ptr(), n, off.data_ptr(), dw.data_ptr(), n + 8, (K + 1) * (n + 8), err, s)
+    tl.tiled_linear_grouped_forward(R, K, n, E, 0, x.data_ptr(), K, R, None, w.data_ptr(), n, K * n, off.data_ptr(), y[:, 8:].data_ptr(), n + 16, None, 0, err, s)
+    tl.tiled_linear_grouped_dw(R, K, n, E, 0, x.data_ptr(), K, R, None, dy.data_ptr(), n, off.data_ptr(), dw.data_ptr(), n + 8, (K + 1) * (n + 8), None, 0, err, s)
     check("y", y[:, 8:8 + n], *grouped(x, w, off))
     check("dw", dw[:, :K, :n], *grouped_backward(x, dy, w, off)[1])
     assert (y[:, :8] == 7).all() and (y[:, 8 + n:] == 7).all() and (dw[:, K:] == 7).all() and (dw[:, :, n:] == 7).all()
