@@ -1,9 +1,9 @@
 // tl_adapter.cu -- low-rank adapters of many requests beside a shared projection.
 //
-// Many rows: the rows are sorted by adapter (tl_route.cu) and both products are
-// products whose weight depends on the row (tl_grouped.cu): h = x . a, bound by the
-// bytes of x, and y = base + s h . b, bound by those of base and y.  h goes from one
-// to the other in two parts of the type's digits, whose sum is the unrounded h to
+// Many rows: the rows are sorted by adapter (tl_route.cu); h = x . a, bound by the
+// bytes of x, is a product whose weight depends on the row (tl_grouped.cu), and
+// y = base + s h . b, bound by those of base and y, a kernel of its own
+// (expand_kernel).  h goes from one to the other in two parts of the type's digits, whose sum is the unrounded h to
 // twice those digits: rounding it to one would err as much as rounding y does.  The
 // same holds for dh = s dy . b^T in the backward pass.
 //
@@ -17,6 +17,7 @@
 #include "tl_grouped.cuh"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace tl {
 namespace {
@@ -176,6 +177,187 @@ __global__ void __launch_bounds__(kFewThreads) expand_few_kernel(const FewArgs p
     }
 }
 
+// ---- base + s h . b for many rows ------------------------------------------------
+
+// A CTA takes 128 rows of one adapter and 128 columns; bytes bound it, so what
+// counts is how many of base are asked for at a time: all of a thread's before the
+// product, and by as many CTAs as fit.  The product is short (2 x 16 .. 128) and its
+// operands are in shared memory; mma.sync leaves its sums in registers, in which a
+// row's 16-byte vector is one thread's: column 8 c + 2 j + e of each 32 is
+// column 2 c + e of the j-th MMA's eight.
+constexpr int kExpandThreads = 256, kExpandRows = 128, kExpandCols = 128;
+
+struct ExpandArgs {
+    int32_t rows, own, groups, rank;
+    const int32_t* offsets;
+    const int32_t* index;  // the row of each place
+    const uint16_t* h;     // [rows, 2 half], by place
+    const uint16_t* w;
+    int64_t ldw, w_apart;
+    const float* scale;
+    float scale_all;
+    const void* base;
+    int64_t ldbase;
+    int32_t base_f32, base_vectors;
+    uint16_t* out;
+    int64_t ldout;
+    int32_t tiles;  // of columns
+};
+
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+template <bool FP16>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (FP16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// HALF: the padded rank.  Shared memory: h's rows, then the weight as [HALF][128]
+// (own contiguous; columns in the order above) or [128][HALF].
+template <bool CONTIG, int HALF>
+struct Expand {
+    static constexpr int kPitchH = 4 * HALF + 16;                          // bytes; 16 more, so that eight rows are in different banks
+    static constexpr int kPitchW = CONTIG ? 2 * kExpandCols + 16 : 2 * HALF + 16;
+    static constexpr size_t kSmem = size_t(kExpandRows) * kPitchH + size_t(CONTIG ? HALF : kExpandCols) * kPitchW;
+};
+
+template <bool CONTIG, int HALF, bool FP16>
+__global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const ExpandArgs p) {
+    using E = Expand<CONTIG, HALF>;
+    extern __shared__ __align__(16) uint8_t expand_smem[];
+    __shared__ int found[3], sums[kExpandThreads / 32];
+    const int tile = int(blockIdx.x % unsigned(p.tiles)), wanted = int(blockIdx.x / unsigned(p.tiles));
+    gr::find_block(p.offsets, p.groups, p.rows, true, kExpandRows, wanted, found, sums);
+    const int group = found[0], p0 = found[1], count = found[2];
+    if (group < 0) return;
+    const bool none = group == p.groups;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const int row0 = (warp & 3) * 32, col0 = (warp >> 2) * 64;  // of the warp: 32 x 64
+    const int n0 = tile * kExpandCols;
+
+    // what this thread adds to: rows g and g + 8 of two blocks of 16, a vector of each 32 columns
+    int rows[4];
+    uint4 base[4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = row0 + i * 8 + g;
+        rows[i] = r < count ? __ldg(p.index + p0 + r) : -1;
+        if (unsigned(rows[i]) >= unsigned(p.rows)) rows[i] = -1;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int col = n0 + col0 + j * 32 + c * 8;
+            base[i][j] = make_uint4(0, 0, 0, 0);
+            if (p.base_vectors && rows[i] >= 0 && col + 8 <= p.own)
+                base[i][j] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.base) + int64_t(rows[i]) * p.ldbase + col);
+        }
+
+    float acc[2][8][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) acc[i][j][k] = 0;
+    if (!none) {
+        const uint32_t sh = smem_addr(expand_smem), sw = sh + kExpandRows * E::kPitchH;
+        constexpr int kVecH = HALF / 4;  // 16-byte vectors of h's row
+        for (int v = threadIdx.x; v < kExpandRows * kVecH; v += kExpandThreads) {
+            const int r = v / kVecH, k = v % kVecH;
+            gr::cp_async16(sh + uint32_t(r) * E::kPitchH + uint32_t(k) * 16u, p.h + int64_t(p0 + min(r, count - 1)) * (2 * HALF) + k * 8, 16);
+        }
+        gr::cp_async_commit();
+        const uint16_t* w = p.w + int64_t(group) * p.w_apart;
+        if constexpr (CONTIG) {
+            for (int v = threadIdx.x; v < HALF * 16; v += kExpandThreads) {
+                const int k = v / 16, q = v % 16, col = n0 + q * 8;
+                uint4 u = make_uint4(0, 0, 0, 0);
+                if (k < p.rank && col < p.own) u = load_eight(w + int64_t(k) * p.ldw + col, p.own - col);
+                uint8_t* at = expand_smem + kExpandRows * E::kPitchH + k * E::kPitchW + (q / 4 * 32 + q % 4 * 2) * 2;
+                *reinterpret_cast<uint32_t*>(at) = u.x;
+                *reinterpret_cast<uint32_t*>(at + 16) = u.y;
+                *reinterpret_cast<uint32_t*>(at + 32) = u.z;
+                *reinterpret_cast<uint32_t*>(at + 48) = u.w;
+            }
+        } else {
+            constexpr int kVecW = HALF / 8;
+            for (int v = threadIdx.x; v < kExpandCols * kVecW; v += kExpandThreads) {
+                const int col = v / kVecW, k = v % kVecW * 8;
+                uint4 u = make_uint4(0, 0, 0, 0);
+                if (n0 + col < p.own && k < p.rank) u = load_eight(w + int64_t(n0 + col) * p.ldw + k, p.rank - k);
+                *reinterpret_cast<uint4*>(expand_smem + kExpandRows * E::kPitchH + col * E::kPitchW + k * 2) = u;
+            }
+        }
+        gr::cp_async_wait<0>();
+        __syncthreads();
+        // (a lane's row of the four 8 x 8 parts that an ldmatrix takes)
+        const int part = lane >> 3, in = lane & 7;
+#pragma unroll 1
+        for (int ks = 0; ks < HALF / 16; ++ks) {
+            uint32_t a[2][2][4];  // [part of h][block of 16 rows]
+#pragma unroll
+            for (int hl = 0; hl < 2; ++hl)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    ldmatrix4(sh + uint32_t(row0 + i * 16 + (part & 1) * 8 + in) * E::kPitchH + uint32_t(hl * HALF + ks * 16 + (part >> 1) * 8) * 2u, a[hl][i]);
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {  // MMAs' columns j * 8 .., j of each four in one 32
+                uint32_t b[4];
+                const int q = j / 4 * 32, t = j % 4 + (part >> 1);
+                if constexpr (CONTIG)
+                    ldmatrix4_trans(sw + uint32_t(ks * 16 + (part & 1) * 8 + in) * E::kPitchW + uint32_t(col0 + q + t * 8) * 2u, b);
+                else
+                    ldmatrix4(sw + uint32_t(col0 + q + 8 * (in >> 1) + 2 * t + (in & 1)) * E::kPitchW + uint32_t(ks * 16 + (part & 1) * 8) * 2u, b);
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int hl = 0; hl < 2; ++hl) {
+                        mma16816<FP16>(acc[i][j], a[hl][i], b[0], b[1]);
+                        mma16816<FP16>(acc[i][j + 1], a[hl][i], b[2], b[3]);
+                    }
+            }
+        }
+    }
+    const float scale = none ? 0.0f : p.scale ? __ldg(p.scale + group) : p.scale_all;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int col = n0 + col0 + j * 32 + c * 8, have = p.own - col;
+            if (rows[i] < 0 || have <= 0) continue;
+            float b[8];
+            eight_values(base[i][j], FP16, b);
+            if (p.base && (!p.base_vectors || have < 8)) {
+                const int64_t at = int64_t(rows[i]) * p.ldbase + col;
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (k < have) b[k] = p.base_f32 ? static_cast<const float*>(p.base)[at + k] : value16(static_cast<const uint16_t*>(p.base)[at + k], FP16);
+            }
+            uint32_t o[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float* f = acc[i >> 1][j * 4 + k] + (i & 1) * 2;
+                o[k] = gr::round16x2(fmaf(f[0], scale, b[2 * k]), fmaf(f[1], scale, b[2 * k + 1]), FP16);
+            }
+            uint16_t* dst = p.out + int64_t(rows[i]) * p.ldout + col;
+            if (have >= 8) {
+                *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+            } else {
+                for (int k = 0; k < have; ++k) dst[k] = uint16_t(o[k / 2] >> (16 * (k & 1)));
+            }
+        }
+}
+
 bool off(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 int32_t half_of(int64_t rank) { return rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64 ? 64 : 128; }
@@ -252,26 +434,46 @@ GroupedDesc shrink(const AdapterDesc& d, const Workspace& w, bool backward) {
 }
 
 // y (or dx) of all rows: base + s h . b, or base + dh . a^T.
-GroupedDesc expand(const AdapterDesc& d, const Workspace& w, bool backward) {
-    GroupedDesc g = product(d, w);
-    g.half = half_of(d.rank);
-    g.x = {w.split, 2 * g.half, d.tokens, nullptr};  // by place
-    g.w = backward ? d.a : d.b;
-    g.ldw = backward ? d.lda : d.ldb;
-    g.w_apart = backward ? d.a_apart : d.b_apart;
-    g.own_contiguous = !backward;
-    g.reduce = d.rank;
-    g.own = backward ? d.K : d.n;
-    g.out.at = backward ? d.dx : d.y;
-    g.out.ld = backward ? d.lddx : d.ldy;
-    if (!backward) {
-        g.scale = d.scale;
-        g.scale_all = d.scale_all;
-    }
-    g.base = d.base;
-    g.base_type = d.base_type;
-    g.ldbase = d.ldbase;
-    return g;
+cudaError_t expand(const AdapterDesc& d, const Workspace& w, bool backward, cudaStream_t stream) {
+    ExpandArgs p{};
+    p.rows = int32_t(d.tokens);
+    p.own = int32_t(backward ? d.K : d.n);
+    p.groups = int32_t(d.adapters);
+    p.rank = int32_t(d.rank);
+    p.offsets = w.offsets;
+    p.index = w.rows;
+    p.h = w.split;
+    p.w = static_cast<const uint16_t*>(backward ? d.a : d.b);
+    p.ldw = backward ? d.lda : d.ldb;
+    p.w_apart = backward ? d.a_apart : d.b_apart;
+    p.scale = backward ? nullptr : d.scale;  // (dh has it already)
+    p.scale_all = backward ? 1.0f : d.scale_all;
+    p.base = d.base;
+    p.ldbase = d.ldbase;
+    p.base_f32 = d.base_type == TL_TYPE_F32 ? 1 : 0;
+    p.base_vectors = d.base && !p.base_f32 && !off(d.base, 16) && d.ldbase % 8 == 0 ? 1 : 0;
+    p.out = static_cast<uint16_t*>(backward ? d.dx : d.y);
+    p.ldout = backward ? d.lddx : d.ldy;
+    p.tiles = (p.own + kExpandCols - 1) / kExpandCols;
+    // whole blocks of rows, and one of each group (and of the rows behind them) that has a row
+    const int64_t ctas = (d.tokens / kExpandRows + std::min(d.adapters + 1, d.tokens)) * p.tiles;
+    if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
+    auto run = [&](auto contig, auto half) {
+        constexpr bool CONTIG = decltype(contig)::value;
+        constexpr int HALF = decltype(half)::value;
+        constexpr size_t smem = Expand<CONTIG, HALF>::kSmem;
+        return d.type == TL_TYPE_F16 ? launch_in_clusters(expand_kernel<CONTIG, HALF, true>, dim3(unsigned(ctas)), kExpandThreads, 1, smem, false, stream, p)
+                                     : launch_in_clusters(expand_kernel<CONTIG, HALF, false>, dim3(unsigned(ctas)), kExpandThreads, 1, smem, false, stream, p);
+    };
+    auto by_half = [&](auto contig) {
+        switch (half_of(d.rank)) {
+            case 16: return run(contig, std::integral_constant<int, 16>{});
+            case 32: return run(contig, std::integral_constant<int, 32>{});
+            case 64: return run(contig, std::integral_constant<int, 64>{});
+            default: return run(contig, std::integral_constant<int, 128>{});
+        }
+    };
+    return backward ? by_half(std::false_type{}) : by_half(std::true_type{});
 }
 
 GroupedDwDesc gradient(const AdapterDesc& d, const Workspace& w, bool of_b) {
@@ -374,10 +576,21 @@ std::string adapter_check(const AdapterDesc& d, bool backward) {
     if (d.tokens > 0 && (!d.ids || off(d.ids, 4))) return "ids is null or not 4-byte aligned";
     const Workspace w(reinterpret_cast<void*>(uintptr_t(256)), d.tokens, d.rank, d.adapters);
     std::string bad = grouped_check(shrink(d, w, backward));
-    if (bad.empty() && (!backward || d.dx)) bad = grouped_check(expand(d, w, backward));
-    if (bad.empty() && d.tokens > 0 && (backward ? !d.dx && !d.da : !d.h || !d.y)) bad = "null pointer";
-    if (bad.empty() && backward && !d.da != !d.db) bad = "one of da and db is null, the other not";
-    if (bad.empty() && backward && d.da) {
+    if (!bad.empty()) return bad;
+    if (d.tokens > 0) {
+        if (backward ? !d.dx && !d.da : !d.h || !d.y) return "null pointer";
+        if (!d.x || !d.a || !d.b || off(d.x, 16) || off(d.a, 16) || off(d.b, 16)) return "x, a or b is null or not 16-byte aligned";
+        if (d.lda % 8 || d.ldb % 8 || d.a_apart % 8 || d.b_apart % 8 || d.ldx % 8) return "leading dimensions must be multiples of 8 elements";
+        if (d.ldx < d.K || d.lda < d.rank || d.ldb < d.n) return "a leading dimension is smaller than a row";
+        if (d.adapters > 1 && (d.a_apart < (d.K - 1) * d.lda + d.rank || d.b_apart < (d.rank - 1) * d.ldb + d.n)) return "the adapters' weights overlap";
+        const void* out = backward ? d.dx : d.y;
+        const int64_t ldout = backward ? d.lddx : d.ldy, cols = backward ? d.K : d.n;
+        if (out && (off(out, 16) || ldout % 8 || ldout < cols)) return "the result is not 16-byte aligned, or its leading dimension no multiple of 8 or too small";
+        if (d.base && d.base_type != d.type && d.base_type != TL_TYPE_F32) return "base must be of x's type or fp32";
+        if (d.base && (off(d.base, type_bytes(d.base_type)) || d.ldbase < cols)) return "base is not aligned to its elements, or its leading dimension too small";
+    }
+    if (backward && !d.da != !d.db) return "one of da and db is null, the other not";
+    if (backward && d.da) {
         bad = grouped_dw_check(gradient(d, w, false));
         if (bad.empty()) bad = grouped_dw_check(gradient(d, w, true));
     }
@@ -390,7 +603,7 @@ cudaError_t adapter_forward_launch(const AdapterDesc& d, int num_sms, cudaStream
     const Workspace w(d.workspace, d.tokens, d.rank, d.adapters);
     cudaError_t e = sort_rows(d, w, stream);
     if (e == cudaSuccess) e = grouped_launch(shrink(d, w, false), num_sms, stream, why);
-    if (e == cudaSuccess) e = grouped_launch(expand(d, w, false), num_sms, stream, why);
+    if (e == cudaSuccess) e = expand(d, w, false, stream);
     return e;
 }
 
@@ -400,7 +613,7 @@ cudaError_t adapter_backward_launch(const AdapterDesc& d, int num_sms, cudaStrea
     if (d.tokens > 0) {
         e = sort_rows(d, w, stream);
         if (e == cudaSuccess) e = grouped_launch(shrink(d, w, true), num_sms, stream, why);
-        if (e == cudaSuccess && d.dx) e = grouped_launch(expand(d, w, true), num_sms, stream, why);
+        if (e == cudaSuccess && d.dx) e = expand(d, w, true, stream);
     }
     if (e == cudaSuccess && d.da) e = grouped_dw_launch(gradient(d, w, false), num_sms, stream, why);
     if (e == cudaSuccess && d.da) e = grouped_dw_launch(gradient(d, w, true), num_sms, stream, why);

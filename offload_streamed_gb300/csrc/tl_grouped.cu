@@ -28,16 +28,14 @@ using namespace gr;
 
 struct Params {
     int32_t rows, reduce, own, groups;
-    int32_t num_k;     // K-blocks of x
-    int32_t w_blocks;  // K-blocks of the weight (fewer with two parts)
-    int32_t half;
+    int32_t num_k;     // K-blocks
     int32_t w_boxes;   // 64-wide boxes of the weight a CTA loads where own is contiguous
     uint32_t w_bytes;  // of the weight a stage and CTA
     int32_t num_m;
     const int32_t* offsets;
     const uint16_t* x;
     int64_t ldx;
-    int32_t x_rows, x_cols;
+    int32_t x_rows;
     const int32_t* x_index;
     const int32_t* out_index;
     int32_t out_rows;
@@ -45,10 +43,6 @@ struct Params {
     int64_t ldout;
     const float* scale;
     float scale_all;
-    const void* base;
-    int64_t ldbase;
-    int32_t base_f32;
-    int32_t base_vectors;  // base's rows start on 16 bytes
     uint16_t* split_out;
     int32_t split_half;
     int32_t fp16;
@@ -58,39 +52,17 @@ struct Params {
     uint64_t timeout_ns;
 };
 
-// The MMAs of one K-block.  With two parts in x's columns, a step's weight is that
-// of the same step of its part.
+// The MMAs of one K-block.
 template <bool W_MN, bool PAIR>
 __device__ __forceinline__ void block_mmas(const Params& p, int kb, bool fresh, uint32_t d, uint32_t sa, uint32_t sb, uint32_t idesc) {
-    const int left = ((p.half ? 2 * p.half : p.reduce) - kb * kBlockK + kUmmaK - 1) / kUmmaK;
-    const int steps = min(kBlockK / kUmmaK, left);
-    const int wrap = p.half && p.half < kBlockK ? p.half / kUmmaK - 1 : kBlockK / kUmmaK - 1;
+    const int steps = min(kBlockK / kUmmaK, (p.reduce - kb * kBlockK + kUmmaK - 1) / kUmmaK);
     for (int j = 0; j < steps; ++j)
-        umma_16<PAIR>(d, operand_desc(W_MN, sa, j & wrap), operand_desc(false, sb, j), idesc, (!fresh || j != 0) ? 1u : 0u);
+        umma_16<PAIR>(d, operand_desc(W_MN, sa, j), operand_desc(false, sb, j), idesc, (!fresh || j != 0) ? 1u : 0u);
 }
 
 __device__ __forceinline__ int out_row(const Params& p, int place) { return p.out_index ? __ldg(p.out_index + place) : place; }
 
-// Four values of base at columns col .. col + 3, of which `have` are there.
-__device__ __forceinline__ float4 base_four(const Params& p, int64_t row, int col, int have) {
-    float v[4] = {0, 0, 0, 0};
-    const int64_t at = row * p.ldbase + col;
-    if (have == 4 && p.base_vectors) {  // (col is a multiple of 4)
-        if (p.base_f32) return *reinterpret_cast<const float4*>(static_cast<const float*>(p.base) + at);
-        const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.base) + at);
-        v[0] = value16(uint16_t(u.x), p.fp16);
-        v[1] = value16(uint16_t(u.x >> 16), p.fp16);
-        v[2] = value16(uint16_t(u.y), p.fp16);
-        v[3] = value16(uint16_t(u.y >> 16), p.fp16);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (j < have) v[j] = p.base_f32 ? static_cast<const float*>(p.base)[at + j] : value16(static_cast<const uint16_t*>(p.base)[at + j], p.fp16);
-    }
-    return make_float4(v[0], v[1], v[2], v[3]);
-}
-
-// Four results of a row at columns col .. col + 3, scaled and with base: stored as `have` of them.
+// Four results of a row at columns col .. col + 3: stored as `have` of them.
 __device__ __forceinline__ void store_four(const Params& p, int64_t row, int col, int have, float4 f) {
     uint16_t* dst = static_cast<uint16_t*>(p.out) + row * p.ldout + col;
     const uint2 w = make_uint2(round16x2(f.x, f.y, p.fp16), round16x2(f.z, f.w, p.fp16));
@@ -204,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_relinquish<true>();
     }
     // every group's tiles, counted by each CTA for itself
-    const int seen = p.groups + (p.all_rows ? 1 : 0);
+    const int seen = p.groups;
     {
         const int per = (seen + kThreads - 1) / kThreads, g0 = min(seen, int(threadIdx.x) * per), g1 = min(seen, g0 + per);
         int mine = 0;
@@ -245,7 +217,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
             for (int tile = int(cluster_id_x()); ok && tile < tiles; tile += step) {
                 const Tile t = tile_at(tile);
-                if (t.g == p.groups) continue;  // rows of no group: nothing to multiply
                 const int m0 = t.m * 256 + int(rank) * kBlockM, half_n = t.n / 2, row0 = t.p0 + int(rank) * half_n;
                 const int boxes = (half_n + kBoxRows - 1) / kBoxRows;
                 const uint32_t bytes = 2u * (p.w_bytes + uint32_t(boxes * kBoxRows) * 128u);
@@ -258,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t sa = smem0 + s * kPairStage, sb = sa + kStageA;
                     const uint32_t fb = map_to_rank(full_bar(s), 0);
                     if (leader) mbar_arrive_expect_tx(full_bar(s), bytes);
-                    const int k0 = (p.half ? kb % p.w_blocks : kb) * kBlockK;
+                    const int k0 = kb * kBlockK;
                     if (W_MN) {
                         for (int c = 0; c < p.w_boxes; ++c) tma_load_box_pair(sa + c * kMnChunk, &map_w, fb, m0 + 64 * c, k0, t.g);
                     } else {
@@ -287,8 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!wait_bounded(tempty_bar(acc), ((uint32_t(it) >> 1) & 1u) ^ 1u, wc, kErrMmaWaitTmem)) break;
                 tc_fence_after();
                 const uint32_t d = tmem_base + acc * kBlockN, idesc = with_n(p.idesc, t.n);
-                const int num_k = t.g == p.groups ? 0 : p.num_k;
-                for (int kb = 0; kb < num_k; ++kb, ++fills) {
+                for (int kb = 0; kb < p.num_k; ++kb, ++fills) {
                     const uint32_t s = fills % S;
                     if (!wait_bounded(full_bar(s), (fills / S) & 1u, wc, kErrMmaWaitFull)) {
                         ok = false;
@@ -315,14 +285,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t acc = it & 1;
             const int col = t.m * 256 + int(rank) * kBlockM + q * 32 + c8;  // this lane's first
             const int have = min(8, p.own - col);
-            const bool none = t.g == p.groups;
-            const float scale = none ? 0.0f : p.scale ? __ldg(p.scale + t.g) : p.scale_all;
             if (!warp_wait(tfull_bar(acc), (uint32_t(it) >> 1) & 1u, wc, kErrEpilogueWait, lane)) break;
             tc_fence_after();
             const uint32_t t_row = tmem_base + (uint32_t(q * 32) << 16) + acc * kBlockN;
             for (int c = 0; c < t.count; c += 32) {
-                const int place = t.p0 + c + lane;
-                const int my_row = c + lane < t.count ? out_row(p, place) : -1;
                 uint32_t v[32];
                 tmem_ld_32cols(t_row + uint32_t(c), v);
                 tmem_ld_wait();
@@ -335,21 +301,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
 #pragma unroll
-                for (int j = 0; j < 32; ++j) box[j * kTurnPitch + lane] = none ? 0.0f : __uint_as_float(v[j]);
+                for (int j = 0; j < 32; ++j) box[j * kTurnPitch + lane] = __uint_as_float(v[j]);
                 __syncwarp();
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int row = __shfl_sync(0xffffffffu, my_row, i * 8 + sub);
-                    if (unsigned(row) >= unsigned(p.out_rows) || have <= 0) continue;
+                    const int row = t.p0 + c + i * 8 + sub;
+                    if (c + i * 8 + sub >= t.count || have <= 0) continue;
                     const float4* src = reinterpret_cast<const float4*>(box + (i * 8 + sub) * kTurnPitch + c8);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const int n = min(4, have - 4 * h);
                         if (n <= 0) break;
-                        float4 f = src[h], b = make_float4(0, 0, 0, 0);
-                        if (p.base) b = base_four(p, row, col + 4 * h, n);
-                        f = make_float4(fmaf(f.x, scale, b.x), fmaf(f.y, scale, b.y), fmaf(f.z, scale, b.z), fmaf(f.w, scale, b.w));
-                        store_four(p, row, col + 4 * h, n, f);
+                        store_four(p, row, col + 4 * h, n, src[h]);
                     }
                 }
                 __syncwarp();
@@ -399,45 +362,14 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 1);
     static_assert((2 * S + 1) * 8 + 4 <= int(kBarBytes), "barrier area");
     __shared__ int found[3];  // group, first place, places
-    __shared__ int sums[kThreads / 32];
+    __shared__ int sums[kFewThreads / 32];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = splits > 1 ? cluster_ctarank() : 0;
     const uint32_t unit = blockIdx.x / uint32_t(splits);
     const int m0 = int(unit % uint32_t(p.num_m)) * 128, wanted = int(unit / uint32_t(p.num_m));  // block of rows
 
-    // The block's group: blocks counted through the groups until the wanted one is passed.
-    const int seen = p.groups + (p.all_rows ? 1 : 0);
-    if (threadIdx.x == 0) found[0] = -1;
-    __syncthreads();
-    int before = 0;
-    for (int g0 = 0; g0 < seen && before <= wanted; g0 += kThreads) {
-        const int g = g0 + int(threadIdx.x);
-        int b = 0, e = 0;
-        if (threadIdx.x < kThreads && g < seen) group_span(p.offsets, p.groups, p.rows, g, b, e);
-        const int blocks = (e - b + N - 1) / N;
-        int s = blocks;
-#pragma unroll
-        for (int d = 1; d < 32; d *= 2) {
-            const int u = __shfl_up_sync(0xffffffffu, s, d);
-            if (lane >= d) s += u;
-        }
-        if (lane == 31 && warp < kThreads / 32) sums[warp] = s;
-        __syncthreads();
-        int at = before + s - blocks, all = 0;
-        for (int w = 0; w < kThreads / 32; ++w) {
-            if (w < warp) at += sums[w];
-            all += sums[w];
-        }
-        if (blocks > 0 && at <= wanted && wanted < at + blocks) {
-            found[0] = g;
-            found[1] = b + (wanted - at) * N;
-            found[2] = min(N, e - found[1]);
-        }
-        before += all;
-        __syncthreads();
-    }
-    __syncthreads();
+    find_block(p.offsets, p.groups, p.rows, p.all_rows != 0, N, wanted, found, sums);
     const int group = found[0], p0 = found[1], count = found[2];
     if (group < 0) return;  // (every CTA of the cluster: the grid is made for the most blocks there can be)
     const bool none = group == p.groups;
@@ -464,7 +396,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     if (warp == 0) {
         auto load_w = [&](int kb, uint32_t s) {
             const uint32_t sa = smem0 + s * F::kStageBytes;
-            const int k0 = (p.half ? kb % p.w_blocks : kb) * kBlockK;
+            const int k0 = kb * kBlockK;
             if (W_MN) {
                 for (int c = 0; c < p.w_boxes; ++c) tma_load_box(sa + c * kMnChunk, &map_w, full_bar(s), m0 + 64 * c, k0, group);
             } else {
@@ -537,7 +469,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                 }
 #pragma unroll
                 for (int r = 0; r < kRows; ++r)
-                    pick.copy(smem0 + s * F::kStageBytes + kStageA, r, src[r] + kb * kBlockK, there[r] ? p.x_cols - kb * kBlockK : 0);
+                    pick.copy(smem0 + s * F::kStageBytes + kStageA, r, src[r] + kb * kBlockK, there[r] ? p.reduce - kb * kBlockK : 0);
                 cp_async_commit();
                 if (fills - handed == kUnderWay) {
                     cp_async_wait<kUnderWay>();
@@ -567,7 +499,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             }
         tc_fence_before();
     }
-    grid_dependency_wait();  // (base and the result may be what the kernel before this one works on)
+    grid_dependency_wait();  // (the result may be what the kernel before this one works on)
     if (splits > 1) cluster_sync();  // every part stands
     else __syncthreads();
     const float scale = none ? 0.0f : p.scale ? __ldg(p.scale + group) : p.scale_all;
@@ -614,9 +546,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             const int row = out_row(p, p0 + e / 32);
             if (unsigned(row) >= unsigned(p.out_rows)) continue;
             const int have = min(4, p.own - col);
-            float4 f = sum[u], b = make_float4(0, 0, 0, 0);
-            if (p.base && have > 0) b = base_four(p, row, col, have);
-            f = make_float4(fmaf(f.x, scale, b.x), fmaf(f.y, scale, b.y), fmaf(f.z, scale, b.z), fmaf(f.w, scale, b.w));
+            const float4 f = make_float4(sum[u].x * scale, sum[u].y * scale, sum[u].z * scale, sum[u].w * scale);
             if (have > 0 && p.out) store_four(p, row, col, have, f);
             if (p.split_out && col < p.split_half) {
                 const float w[4] = {f.x, f.y, f.z, f.w};
@@ -648,7 +578,7 @@ cudaError_t launch_few(const CUtensorMap& mw, Params p, const GroupedDesc& d, in
     const void* shape = reinterpret_cast<const void*>(grouped_few_shape_kernel);
     cudaError_t e = ctas_per_sm(shape, kFewThreads, Few<N>::kSmem, &per_sm);
     // CTAs of a cluster: as many as two an SM allow, with four K-blocks each
-    while (e == cudaSuccess && !d.half && splits < 8 && likely * splits * 2 <= 2 * num_sms && p.num_k >= 8 * splits) {
+    while (e == cudaSuccess && splits < 8 && likely * splits * 2 <= 2 * num_sms && p.num_k >= 8 * splits) {
         e = clusters_at_a_time(shape, kFewThreads, Few<N>::kSmem, 2 * splits, &clusters);
         if (e != cudaSuccess || likely > clusters) break;
         splits *= 2;
@@ -701,16 +631,14 @@ std::string grouped_check(const GroupedDesc& d) {
     if (!d.x.at || !d.w || (!d.out.at && !d.split_out)) return "null pointer";
     if (off(d.x.at, 16) || off(d.w, 16) || off(d.out.at, 16) || off(d.split_out, 16)) return "operand pointers must be 16-byte aligned";
     if (d.x.ld % 8 || d.ldw % 8 || d.w_apart % 8 || d.out.ld % 8) return "leading dimensions must be multiples of 8 elements";
-    const int64_t x_cols = d.half ? 2 * d.half : d.reduce, inner = d.own_contiguous ? d.own : d.reduce, outer = d.own_contiguous ? d.reduce : d.own;
-    if (d.x.ld < x_cols || d.ldw < inner || (d.out.at && d.out.ld < d.own)) return "a leading dimension is smaller than a row";
+    const int64_t inner = d.own_contiguous ? d.own : d.reduce, outer = d.own_contiguous ? d.reduce : d.own;
+    if (d.x.ld < d.reduce || d.ldw < inner || (d.out.at && d.out.ld < d.own)) return "a leading dimension is smaller than a row";
     if (d.groups > 1 && d.w_apart < (outer - 1) * d.ldw + inner) return "the groups' weights overlap";
     if (d.x.ld >= (int64_t(1) << 38) || d.ldw >= (int64_t(1) << 38) || d.w_apart >= (int64_t(1) << 38)) return "a leading dimension is too large";
     if (d.x.count < 1 || (!d.x.index && d.x.count < d.rows)) return "x has too few rows";
     if (!d.out.index && d.out.count < d.rows) return "the result has too few rows";
     if (off(d.gathered, 16)) return "the workspace is not 16-byte aligned";
     if (off(d.x.index, 4) || off(d.out.index, 4) || off(d.scale, 4)) return "indexes and scales must be 4-byte aligned";
-    if (d.base && (d.base_type != d.type && d.base_type != TL_TYPE_F32)) return "base must be of x's type or fp32";
-    if (d.base && (off(d.base, type_bytes(d.base_type)) || d.ldbase < d.own)) return "base is not aligned to its elements, or its leading dimension too small";
     return {};
 }
 
@@ -721,15 +649,11 @@ cudaError_t grouped_launch(const GroupedDesc& d, int num_sms, cudaStream_t strea
     p.reduce = int32_t(d.reduce);
     p.own = int32_t(d.own);
     p.groups = int32_t(d.groups);
-    p.half = d.half;
-    const int64_t x_cols = d.half ? 2 * d.half : d.reduce;
-    p.num_k = int32_t((x_cols + kBlockK - 1) / kBlockK);
-    p.w_blocks = int32_t(((d.half ? d.half : d.reduce) + kBlockK - 1) / kBlockK);
+    p.num_k = int32_t((d.reduce + kBlockK - 1) / kBlockK);
     p.offsets = d.offsets;
     p.x = static_cast<const uint16_t*>(d.x.at);
     p.ldx = d.x.ld;
     p.x_rows = int32_t(d.x.count);
-    p.x_cols = int32_t(x_cols);
     p.x_index = d.x.index;
     p.out_index = d.out.index;
     p.out_rows = int32_t(d.out.count);
@@ -737,10 +661,6 @@ cudaError_t grouped_launch(const GroupedDesc& d, int num_sms, cudaStream_t strea
     p.ldout = d.out.ld;
     p.scale = d.scale;
     p.scale_all = d.scale_all;
-    p.base = d.base;
-    p.ldbase = d.ldbase;
-    p.base_f32 = d.base_type == TL_TYPE_F32 ? 1 : 0;
-    p.base_vectors = d.base && !off(d.base, 16) && d.ldbase * int64_t(type_bytes(d.base_type)) % 16 == 0 ? 1 : 0;
     p.split_out = static_cast<uint16_t*>(d.split_out);
     p.split_half = d.split_half;
     p.fp16 = d.type == TL_TYPE_F16 ? 1 : 0;
@@ -758,11 +678,10 @@ cudaError_t grouped_launch(const GroupedDesc& d, int num_sms, cudaStream_t strea
 
     const int64_t mean = (d.rows + d.groups - 1) / d.groups;
     cudaError_t e;
-    if (d.own > kBlockM && !d.split_out && (mean > 64 || d.half)) {
+    if (d.own > kBlockM && !d.split_out && !d.all_rows && !d.out.index && mean > 64) {
         p.num_m = int32_t((d.own + 255) / 256);
         p.idesc = idesc_16(256, d.own_contiguous, false, p.fp16 != 0);
-        const int64_t seen = d.groups + (d.all_rows ? 1 : 0);
-        const int64_t tiles = (d.rows / kBlockN + std::min(seen, d.rows)) * p.num_m;
+        const int64_t tiles = (d.rows / kBlockN + std::min(d.groups, d.rows)) * p.num_m;
         if (tiles > INT32_MAX) {
             if (why) *why = "too many tiles";
             return cudaErrorInvalidValue;
@@ -771,11 +690,11 @@ cudaError_t grouped_launch(const GroupedDesc& d, int num_sms, cudaStream_t strea
         RowsOperand x = d.x;
         if (x.index) {
             if (!d.gathered) return cudaErrorInvalidValue;
-            const cudaError_t g = pick_rows_launch(d.x, d.rows, x_cols, d.gathered, stream);
+            const cudaError_t g = pick_rows_launch(d.x, d.rows, d.reduce, d.gathered, stream);
             if (g != cudaSuccess) return g;
-            x = {d.gathered, picked_ld(x_cols), d.rows, nullptr};
+            x = {d.gathered, picked_ld(d.reduce), d.rows, nullptr};
         }
-        if (!rows_map(&mx, d.type, x, x_cols, kBoxRows, why)) return cudaErrorInvalidValue;
+        if (!rows_map(&mx, d.type, x, d.reduce, kBoxRows, why)) return cudaErrorInvalidValue;
         auto run = [&](auto kern) { return launch_in_clusters(kern, dim3(grid), kThreads, 2, kPairSmem, false, stream, mw, mx, p); };
         e = d.own_contiguous ? run(grouped_kernel<true>) : run(grouped_kernel<false>);
     } else {

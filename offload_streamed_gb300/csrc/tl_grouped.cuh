@@ -117,6 +117,44 @@ __device__ __forceinline__ void group_span(const int32_t* offsets, int groups, i
     end = g == groups ? rows : min(max(offsets[g + 1], begin), rows);
 }
 
+// The block of at most `size` rows of one group that is the `wanted`-th of all
+// groups' (with all_rows, of the rows behind them, too): found = group, first place
+// and places; the group is -1 if there are fewer.  Every thread of the CTA takes
+// part; sums holds an int for each warp.
+__device__ __forceinline__ void find_block(const int32_t* offsets, int groups, int rows, bool all_rows, int size, int wanted, int* found, int* sums) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, seen = groups + (all_rows ? 1 : 0);
+    if (threadIdx.x == 0) found[0] = -1;
+    __syncthreads();
+    int before = 0;
+    for (int g0 = 0; g0 < seen && before <= wanted; g0 += blockDim.x) {
+        const int g = g0 + int(threadIdx.x);
+        int b = 0, e = 0;
+        if (g < seen) group_span(offsets, groups, rows, g, b, e);
+        const int blocks = (e - b + size - 1) / size;
+        int s = blocks;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int u = __shfl_up_sync(0xffffffffu, s, d);
+            if (lane >= d) s += u;
+        }
+        if (lane == 31) sums[warp] = s;
+        __syncthreads();
+        int at = before + s - blocks, all = 0;
+        for (int w = 0; w < warps; ++w) {
+            if (w < warp) at += sums[w];
+            all += sums[w];
+        }
+        if (blocks > 0 && at <= wanted && wanted < at + blocks) {
+            found[0] = g;
+            found[1] = b + (wanted - at) * size;
+            found[2] = min(size, e - found[1]);
+        }
+        before += all;
+        __syncthreads();
+    }
+    __syncthreads();
+}
+
 // ---- rows picked up ------------------------------------------------------------------
 
 // 128 threads pick up rows 16 bytes at a time by cp.async (TMA's gathers of four rows

@@ -20,7 +20,7 @@ struct RowsOperand {
 int64_t picked_ld(int64_t cols);
 cudaError_t pick_rows_launch(const RowsOperand& x, int64_t rows, int64_t cols, void* out, cudaStream_t stream);
 
-// out[row(p), own] = scale[g] sum_k x[row(p), k] w[g](k, own) (+ base)
+// out[row(p), own] = scale[g] sum_k x[row(p), k] w[g](k, own)
 struct GroupedDesc {
     int64_t rows = 0, reduce = 0, own = 0, groups = 0;
     int32_t type = 0;  // TL_TYPE_BF16 or TL_TYPE_F16, of x, w and out
@@ -29,21 +29,16 @@ struct GroupedDesc {
     const void* w = nullptr;
     int64_t ldw = 0, w_apart = 0;
     bool own_contiguous = true;  // w[g] is [reduce, own]; else [own, reduce]
-    // Not 0: x's columns are two parts of `half` (16, 32, 64 or 128), and both
-    // are multiplied with the same `reduce` <= half weights.
-    int32_t half = 0;
     RowsOperand out;                // at is written
-    const float* scale = nullptr;   // [groups]; nullptr: scale_all
+    // From here on for own <= 128 (as an indexed out).  all_rows: rows behind the last group are written, too, as zeros.
+    bool all_rows = false;
+    const float* scale = nullptr;  // [groups]; nullptr: scale_all
     float scale_all = 1.0f;
-    const void* base = nullptr;     // rows as out's; nullptr: none
-    int64_t ldbase = 0;
-    int32_t base_type = 0;
-    bool all_rows = false;          // rows behind the last group are written, too: base, or zeros
-    // Not nullptr (own <= 128): the unrounded result, too, as two parts of split_half
+    // Not nullptr: the unrounded result, too, as two parts of split_half
     // columns whose sum it is to twice the type's digits; [rows, 2 split_half], by place.
     void* split_out = nullptr;
     int32_t split_half = 0;
-    void* gathered = nullptr;  // workspace for an indexed x's rows, [rows, picked_ld] (all but `half` and small `own` need it)
+    void* gathered = nullptr;  // workspace for an indexed x's rows, [rows, picked_ld] (own > 128 needs it)
     bool early = false;  // the kernel ahead writes x alone: w may be read before it has completed
     int32_t* err = nullptr;
 };

@@ -11,7 +11,8 @@
 // Order by expert.  A stable counting sort, whose places depend on nothing but
 // the ids: each CTA counts its entries by expert; then each sums all CTAs' counts
 // (those before its own apart), and its warps, whose entries lie one after
-// another, rank theirs 32 at a time by the lanes of equal id.  Counting is fused
+// another, rank theirs 32 at a time by the lanes of equal id, which a ballot for
+// each bit of the ids gives (one instruction for it, match.any, took longer).  Counting is fused
 // into the choice, so a call is two launches, or one where a single CTA does it.
 #include "tl_launch.h"
 #include "tl_route.h"
@@ -41,6 +42,16 @@ struct Sort {
 };
 
 __device__ __forceinline__ int bin_of(int id, int groups) { return unsigned(id) < unsigned(groups) ? id : groups; }
+
+// The lanes that hold the same b (0 .. 2^bits - 1) as this one.
+__device__ __forceinline__ unsigned lanes_of(int b, int bits) {
+    unsigned same = 0xffffffffu;
+    for (int i = 0; i < bits; ++i) {
+        const unsigned set = __ballot_sync(0xffffffffu, (b >> i) & 1);
+        same &= (b >> i) & 1 ? set : ~set;
+    }
+    return same;
+}
 
 // Exclusive sum over the CTA's threads; *all is the total.
 __device__ int scan_cta(int v, int* scratch, int* all) {
@@ -77,10 +88,11 @@ __device__ void place_entries(const Sort& p, int first, int len, int cta, int ct
     const int span = (len + kSortThreads - 1) / kSortThreads * 32;
     const int from = first + min(len, warp * span), to = first + min(len, (warp + 1) * span);
     int* mine = at + warp * bins;
+    const int bits = 32 - __clz(bins);  // (bins itself stands for a lane without an entry)
     for (int i = from; i < to; i += 32) {
-        const int b = i + lane < to ? bin_of(p.ids[i + lane], p.groups) : -1;
-        const unsigned same = __match_any_sync(0xffffffffu, b);
-        if (b >= 0 && (same & ((1u << lane) - 1)) == 0) mine[b] += __popc(same);
+        const int b = i + lane < to ? bin_of(p.ids[i + lane], p.groups) : bins;
+        const unsigned same = lanes_of(b, bits);
+        if (b < bins && (same & ((1u << lane) - 1)) == 0) mine[b] += __popc(same);
         __syncwarp();
     }
     __syncthreads();
@@ -88,6 +100,7 @@ __device__ void place_entries(const Sort& p, int first, int len, int cta, int ct
     for (int g = warp; g < bins; g += kSortWarps) {
         int before = 0, total = 0;
         if (ctas > 1) {
+#pragma unroll 5
             for (int c = lane; c < ctas; c += 32) {
                 const int v = __ldcg(p.counts + int64_t(g) * ctas + c);
                 total += v;
@@ -121,12 +134,12 @@ __device__ void place_entries(const Sort& p, int first, int len, int cta, int ct
     }
     __syncthreads();
     for (int i = from; i < to; i += 32) {
-        const int b = i + lane < to ? bin_of(p.ids[i + lane], p.groups) : -1;
-        const unsigned same = __match_any_sync(0xffffffffu, b), earlier = same & ((1u << lane) - 1);
+        const int b = i + lane < to ? bin_of(p.ids[i + lane], p.groups) : bins;
+        const unsigned same = lanes_of(b, bits), earlier = same & ((1u << lane) - 1);
         int place = 0;
-        if (b >= 0) place = start[b] + mine[b] + __popc(earlier);
+        if (b < bins) place = start[b] + mine[b] + __popc(earlier);
         __syncwarp();
-        if (b >= 0) {
+        if (b < bins) {
             if (earlier == 0) mine[b] += __popc(same);
             p.slots[i + lane] = b < p.groups ? place : -1;
             p.rows[place] = (i + lane) / p.k;
@@ -216,6 +229,20 @@ __device__ __forceinline__ float warp_max(float v) {
     return v;
 }
 
+// A lane's keys, largest first: a network of V (V - 1) / 2 comparisons at most, in which
+// neighbours are exchanged.
+template <int V>
+__device__ __forceinline__ void sort_keys(uint32_t (&key)[V]) {
+#pragma unroll
+    for (int round = 0; round < V; ++round)
+#pragma unroll
+        for (int i = round & 1; i + 1 < V; i += 2) {
+            const uint32_t a = key[i], b = key[i + 1];
+            key[i] = max(a, b);
+            key[i + 1] = min(a, b);
+        }
+}
+
 struct Choice {
     const void* logits;
     int64_t ld;
@@ -254,12 +281,19 @@ __global__ void __launch_bounds__(kSortThreads) route_kernel(const Choice c, con
             }
             sum = warp_sum(sum);
         }
-        // lane j keeps the j-th best
+        // lane j keeps the j-th best.  Few keys with their indexes are sorted first, and
+        // the winner's lane moves up by one; others' are looked through again.
+        constexpr bool kSorted = sizeof(T) == 2 && V <= 8;
         uint32_t won = 0;
         int id = -1;
         uint32_t local = 0;
+        if constexpr (kSorted) {
+            sort_keys(key);
+            local = key[0];
+        } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) local = max(local, key[i]);
+            for (int i = 0; i < V; ++i) local = max(local, key[i]);
+        }
         for (int j = 0; j < k; ++j) {
             const uint32_t m = __reduce_max_sync(0xffffffffu, local);
             if (m == 0) break;
@@ -279,7 +313,13 @@ __global__ void __launch_bounds__(kSortThreads) route_kernel(const Choice c, con
                 won = m;
                 id = e;
             }
-            if ((e & 31) == lane) {  // remove the first of the lane's that holds it
+            if constexpr (kSorted) {
+                const bool it = local == m;
+#pragma unroll
+                for (int i = 0; i + 1 < V; ++i) key[i] = it ? key[i + 1] : key[i];
+                key[V - 1] = it ? 0 : key[V - 1];
+                local = key[0];
+            } else if ((e & 31) == lane) {  // remove the first of the lane's that holds it
                 bool here = true;
                 local = 0;
 #pragma unroll
