@@ -179,9 +179,9 @@ __global__ void __launch_bounds__(kFewThreads) expand_few_kernel(const FewArgs p
 
 // ---- base + s h . b for many rows ------------------------------------------------
 
-// A CTA takes 128 rows of one adapter and 128 columns; bytes bound it, so what
-// counts is how many of base are asked for at a time: all of a thread's before the
-// product, and by as many CTAs as fit.  The product is short (2 x 16 .. 128) and its
+// A CTA takes 128 rows of one adapter and, one after another, some tiles of 128
+// columns; bytes bound it, so what counts is how many of base are asked for at a
+// time: all of a thread's before the product, and by as many CTAs as fit.  The product is short (2 x 16 .. 128) and its
 // operands are in shared memory; mma.sync leaves its sums in registers, in which a
 // row's 16-byte vector is one thread's: column 8 c + 2 j + e of each 32 is
 // column 2 c + e of the j-th MMA's eight.
@@ -201,7 +201,7 @@ struct ExpandArgs {
     int32_t base_f32, base_vectors;
     uint16_t* out;
     int64_t ldout;
-    int32_t tiles;  // of columns
+    int32_t tiles, per, shares;  // tiles of columns, those of a CTA, CTAs for a block of rows
 };
 
 __device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
@@ -234,128 +234,134 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const ExpandA
     using E = Expand<CONTIG, HALF>;
     extern __shared__ __align__(16) uint8_t expand_smem[];
     __shared__ int found[3], sums[kExpandThreads / 32];
-    const int tile = int(blockIdx.x % unsigned(p.tiles)), wanted = int(blockIdx.x / unsigned(p.tiles));
+    const int first = int(blockIdx.x % unsigned(p.shares)) * p.per, wanted = int(blockIdx.x / unsigned(p.shares));
     gr::find_block(p.offsets, p.groups, p.rows, true, kExpandRows, wanted, found, sums);
     const int group = found[0], p0 = found[1], count = found[2];
     if (group < 0) return;
     const bool none = group == p.groups;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     const int row0 = (warp & 3) * 32, col0 = (warp >> 2) * 64;  // of the warp: 32 x 64
-    const int n0 = tile * kExpandCols;
 
     // what this thread adds to: rows g and g + 8 of two blocks of 16, a vector of each 32 columns
     int rows[4];
-    uint4 base[4][2];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = row0 + i * 8 + g;
         rows[i] = r < count ? __ldg(p.index + p0 + r) : -1;
         if (unsigned(rows[i]) >= unsigned(p.rows)) rows[i] = -1;
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int col = n0 + col0 + j * 32 + c * 8;
-            base[i][j] = make_uint4(0, 0, 0, 0);
-            if (p.base_vectors && rows[i] >= 0 && col + 8 <= p.own)
-                base[i][j] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.base) + int64_t(rows[i]) * p.ldbase + col);
-        }
-
-    float acc[2][8][4];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) acc[i][j][k] = 0;
+    const float scale = none ? 0.0f : p.scale ? __ldg(p.scale + group) : p.scale_all;
+    const uint32_t sh = smem_addr(expand_smem), sw = sh + kExpandRows * E::kPitchH;
     if (!none) {
-        const uint32_t sh = smem_addr(expand_smem), sw = sh + kExpandRows * E::kPitchH;
         constexpr int kVecH = HALF / 4;  // 16-byte vectors of h's row
         for (int v = threadIdx.x; v < kExpandRows * kVecH; v += kExpandThreads) {
             const int r = v / kVecH, k = v % kVecH;
             gr::cp_async16(sh + uint32_t(r) * E::kPitchH + uint32_t(k) * 16u, p.h + int64_t(p0 + min(r, count - 1)) * (2 * HALF) + k * 8, 16);
         }
         gr::cp_async_commit();
-        const uint16_t* w = p.w + int64_t(group) * p.w_apart;
-        if constexpr (CONTIG) {
-            for (int v = threadIdx.x; v < HALF * 16; v += kExpandThreads) {
-                const int k = v / 16, q = v % 16, col = n0 + q * 8;
-                uint4 u = make_uint4(0, 0, 0, 0);
-                if (k < p.rank && col < p.own) u = load_eight(w + int64_t(k) * p.ldw + col, p.own - col);
-                uint8_t* at = expand_smem + kExpandRows * E::kPitchH + k * E::kPitchW + (q / 4 * 32 + q % 4 * 2) * 2;
-                *reinterpret_cast<uint32_t*>(at) = u.x;
-                *reinterpret_cast<uint32_t*>(at + 16) = u.y;
-                *reinterpret_cast<uint32_t*>(at + 32) = u.z;
-                *reinterpret_cast<uint32_t*>(at + 48) = u.w;
-            }
-        } else {
-            constexpr int kVecW = HALF / 8;
-            for (int v = threadIdx.x; v < kExpandCols * kVecW; v += kExpandThreads) {
-                const int col = v / kVecW, k = v % kVecW * 8;
-                uint4 u = make_uint4(0, 0, 0, 0);
-                if (n0 + col < p.own && k < p.rank) u = load_eight(w + int64_t(n0 + col) * p.ldw + k, p.rank - k);
-                *reinterpret_cast<uint4*>(expand_smem + kExpandRows * E::kPitchH + col * E::kPitchW + k * 2) = u;
-            }
-        }
-        gr::cp_async_wait<0>();
-        __syncthreads();
-        // (a lane's row of the four 8 x 8 parts that an ldmatrix takes)
-        const int part = lane >> 3, in = lane & 7;
-#pragma unroll 1
-        for (int ks = 0; ks < HALF / 16; ++ks) {
-            uint32_t a[2][2][4];  // [part of h][block of 16 rows]
-#pragma unroll
-            for (int hl = 0; hl < 2; ++hl)
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    ldmatrix4(sh + uint32_t(row0 + i * 16 + (part & 1) * 8 + in) * E::kPitchH + uint32_t(hl * HALF + ks * 16 + (part >> 1) * 8) * 2u, a[hl][i]);
-#pragma unroll
-            for (int j = 0; j < 8; j += 2) {  // MMAs' columns j * 8 .., j of each four in one 32
-                uint32_t b[4];
-                const int q = j / 4 * 32, t = j % 4 + (part >> 1);
-                if constexpr (CONTIG)
-                    ldmatrix4_trans(sw + uint32_t(ks * 16 + (part & 1) * 8 + in) * E::kPitchW + uint32_t(col0 + q + t * 8) * 2u, b);
-                else
-                    ldmatrix4(sw + uint32_t(col0 + q + 8 * (in >> 1) + 2 * t + (in & 1)) * E::kPitchW + uint32_t(ks * 16 + (part & 1) * 8) * 2u, b);
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int hl = 0; hl < 2; ++hl) {
-                        mma16816<FP16>(acc[i][j], a[hl][i], b[0], b[1]);
-                        mma16816<FP16>(acc[i][j + 1], a[hl][i], b[2], b[3]);
-                    }
-            }
-        }
     }
-    const float scale = none ? 0.0f : p.scale ? __ldg(p.scale + group) : p.scale_all;
+#pragma unroll 1
+    for (int tile = first; tile < min(p.tiles, first + p.per); ++tile) {
+        const int n0 = tile * kExpandCols;
+        uint4 base[4][2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int col = n0 + col0 + j * 32 + c * 8, have = p.own - col;
-            if (rows[i] < 0 || have <= 0) continue;
-            float b[8];
-            eight_values(base[i][j], FP16, b);
-            if (p.base && (!p.base_vectors || have < 8)) {
-                const int64_t at = int64_t(rows[i]) * p.ldbase + col;
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (k < have) b[k] = p.base_f32 ? static_cast<const float*>(p.base)[at + k] : value16(static_cast<const uint16_t*>(p.base)[at + k], FP16);
+            for (int j = 0; j < 2; ++j) {
+                const int col = n0 + col0 + j * 32 + c * 8;
+                base[i][j] = make_uint4(0, 0, 0, 0);
+                if (p.base_vectors && rows[i] >= 0 && col + 8 <= p.own)
+                    base[i][j] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.base) + int64_t(rows[i]) * p.ldbase + col);
             }
-            uint32_t o[4];
+
+        float acc[2][8][4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float* f = acc[i >> 1][j * 4 + k] + (i & 1) * 2;
-                o[k] = gr::round16x2(fmaf(f[0], scale, b[2 * k]), fmaf(f[1], scale, b[2 * k + 1]), FP16);
-            }
-            uint16_t* dst = p.out + int64_t(rows[i]) * p.ldout + col;
-            if (have >= 8) {
-                *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) acc[i][j][k] = 0;
+        if (!none) {
+            if (tile != first) __syncthreads();  // (the tile before has been multiplied)
+            const uint16_t* w = p.w + int64_t(group) * p.w_apart;
+            if constexpr (CONTIG) {
+                for (int v = threadIdx.x; v < HALF * 16; v += kExpandThreads) {
+                    const int k = v / 16, q = v % 16, col = n0 + q * 8;
+                    uint4 u = make_uint4(0, 0, 0, 0);
+                    if (k < p.rank && col < p.own) u = load_eight(w + int64_t(k) * p.ldw + col, p.own - col);
+                    uint8_t* at = expand_smem + kExpandRows * E::kPitchH + k * E::kPitchW + (q / 4 * 32 + q % 4 * 2) * 2;
+                    *reinterpret_cast<uint32_t*>(at) = u.x;
+                    *reinterpret_cast<uint32_t*>(at + 16) = u.y;
+                    *reinterpret_cast<uint32_t*>(at + 32) = u.z;
+                    *reinterpret_cast<uint32_t*>(at + 48) = u.w;
+                }
             } else {
-                for (int k = 0; k < have; ++k) dst[k] = uint16_t(o[k / 2] >> (16 * (k & 1)));
+                constexpr int kVecW = HALF / 8;
+                for (int v = threadIdx.x; v < kExpandCols * kVecW; v += kExpandThreads) {
+                    const int col = v / kVecW, k = v % kVecW * 8;
+                    uint4 u = make_uint4(0, 0, 0, 0);
+                    if (n0 + col < p.own && k < p.rank) u = load_eight(w + int64_t(n0 + col) * p.ldw + k, p.rank - k);
+                    *reinterpret_cast<uint4*>(expand_smem + kExpandRows * E::kPitchH + col * E::kPitchW + k * 2) = u;
+                }
+            }
+            gr::cp_async_wait<0>();
+            __syncthreads();
+            // (a lane's row of the four 8 x 8 parts that an ldmatrix takes)
+            const int part = lane >> 3, in = lane & 7;
+#pragma unroll 1
+            for (int ks = 0; ks < HALF / 16; ++ks) {
+                uint32_t a[2][2][4];  // [part of h][block of 16 rows]
+#pragma unroll
+                for (int hl = 0; hl < 2; ++hl)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        ldmatrix4(sh + uint32_t(row0 + i * 16 + (part & 1) * 8 + in) * E::kPitchH + uint32_t(hl * HALF + ks * 16 + (part >> 1) * 8) * 2u, a[hl][i]);
+#pragma unroll
+                for (int j = 0; j < 8; j += 2) {  // MMAs' columns j * 8 .., j of each four in one 32
+                    uint32_t b[4];
+                    const int q = j / 4 * 32, t = j % 4 + (part >> 1);
+                    if constexpr (CONTIG)
+                        ldmatrix4_trans(sw + uint32_t(ks * 16 + (part & 1) * 8 + in) * E::kPitchW + uint32_t(col0 + q + t * 8) * 2u, b);
+                    else
+                        ldmatrix4(sw + uint32_t(col0 + q + 8 * (in >> 1) + 2 * t + (in & 1)) * E::kPitchW + uint32_t(ks * 16 + (part & 1) * 8) * 2u, b);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int hl = 0; hl < 2; ++hl) {
+                            mma16816<FP16>(acc[i][j], a[hl][i], b[0], b[1]);
+                            mma16816<FP16>(acc[i][j + 1], a[hl][i], b[2], b[3]);
+                        }
+                }
             }
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int col = n0 + col0 + j * 32 + c * 8, have = p.own - col;
+                if (rows[i] < 0 || have <= 0) continue;
+                float b[8];
+                eight_values(base[i][j], FP16, b);
+                if (p.base && (!p.base_vectors || have < 8)) {
+                    const int64_t at = int64_t(rows[i]) * p.ldbase + col;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (k < have) b[k] = p.base_f32 ? static_cast<const float*>(p.base)[at + k] : value16(static_cast<const uint16_t*>(p.base)[at + k], FP16);
+                }
+                uint32_t o[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float* f = acc[i >> 1][j * 4 + k] + (i & 1) * 2;
+                    o[k] = gr::round16x2(fmaf(f[0], scale, b[2 * k]), fmaf(f[1], scale, b[2 * k + 1]), FP16);
+                }
+                uint16_t* dst = p.out + int64_t(rows[i]) * p.ldout + col;
+                if (have >= 8) {
+                    *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+                } else {
+                    for (int k = 0; k < have; ++k) dst[k] = uint16_t(o[k / 2] >> (16 * (k & 1)));
+                }
+            }
+    }
 }
 
 bool off(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
@@ -434,7 +440,7 @@ GroupedDesc shrink(const AdapterDesc& d, const Workspace& w, bool backward) {
 }
 
 // y (or dx) of all rows: base + s h . b, or base + dh . a^T.
-cudaError_t expand(const AdapterDesc& d, const Workspace& w, bool backward, cudaStream_t stream) {
+cudaError_t expand(const AdapterDesc& d, const Workspace& w, bool backward, int num_sms, cudaStream_t stream) {
     ExpandArgs p{};
     p.rows = int32_t(d.tokens);
     p.own = int32_t(backward ? d.K : d.n);
@@ -456,7 +462,12 @@ cudaError_t expand(const AdapterDesc& d, const Workspace& w, bool backward, cuda
     p.ldout = backward ? d.lddx : d.ldy;
     p.tiles = (p.own + kExpandCols - 1) / kExpandCols;
     // whole blocks of rows, and one of each group (and of the rows behind them) that has a row
-    const int64_t ctas = (d.tokens / kExpandRows + std::min(d.adapters + 1, d.tokens)) * p.tiles;
+    const int64_t blocks = d.tokens / kExpandRows + std::min(d.adapters + 1, d.tokens);
+    // tiles of a CTA: what it finds and loads once counts less with more of them, as
+    // long as there are four CTAs for an SM (8192 x 8192, rank 16, us with 1 / 4 tiles: see the table's case)
+    p.per = int32_t(std::max<int64_t>(1, std::min<int64_t>(8, blocks * p.tiles / (4 * std::max(1, num_sms)))));
+    p.shares = (p.tiles + p.per - 1) / p.per;
+    const int64_t ctas = blocks * p.shares;
     if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
     auto run = [&](auto contig, auto half) {
         constexpr bool CONTIG = decltype(contig)::value;
@@ -603,7 +614,7 @@ cudaError_t adapter_forward_launch(const AdapterDesc& d, int num_sms, cudaStream
     const Workspace w(d.workspace, d.tokens, d.rank, d.adapters);
     cudaError_t e = sort_rows(d, w, stream);
     if (e == cudaSuccess) e = grouped_launch(shrink(d, w, false), num_sms, stream, why);
-    if (e == cudaSuccess) e = expand(d, w, false, stream);
+    if (e == cudaSuccess) e = expand(d, w, false, num_sms, stream);
     return e;
 }
 
@@ -613,7 +624,7 @@ cudaError_t adapter_backward_launch(const AdapterDesc& d, int num_sms, cudaStrea
     if (d.tokens > 0) {
         e = sort_rows(d, w, stream);
         if (e == cudaSuccess) e = grouped_launch(shrink(d, w, true), num_sms, stream, why);
-        if (e == cudaSuccess && d.dx) e = expand(d, w, true, stream);
+        if (e == cudaSuccess && d.dx) e = expand(d, w, true, num_sms, stream);
     }
     if (e == cudaSuccess && d.da) e = grouped_dw_launch(gradient(d, w, false), num_sms, stream, why);
     if (e == cudaSuccess && d.da) e = grouped_dw_launch(gradient(d, w, true), num_sms, stream, why);

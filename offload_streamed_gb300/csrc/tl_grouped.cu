@@ -336,31 +336,37 @@ __global__ void __launch_bounds__(kThreads, 1)
 constexpr int kFewThreads = kThreads + 32;
 constexpr size_t kFewSmem = 112 * 1024;  // of a CTA: two share an SM
 
+// A stage is N rows of x and what there is of the weight: where own is small, less
+// than the 16 KiB that the MMA reads (what it finds past them makes rows of the
+// result that are not stored), which therefore have to be there after the last stage.
+constexpr int kFewMostStages = 8;
 template <int N>
 struct Few {
-    static constexpr uint32_t kStageBytes = kStageA + uint32_t(N) * 128;
+    static constexpr uint32_t kRowBytes = uint32_t(N) * 128;
     static constexpr uint32_t kFixed = kBarBytes + 1024;
-    static constexpr int kStages = int((kFewSmem - kFixed) / kStageBytes);
-    static constexpr size_t kSmem = size_t(kStages) * kStageBytes + kFixed;
     static constexpr uint32_t kCols = N <= 32 ? 32 : N;
-    static_assert(kStages >= 3 && size_t(N) * 128 * 4 <= size_t(kStages) * kStageBytes, "the parts fit the stages");
+    static constexpr uint32_t stage(uint32_t w_bytes) { return kRowBytes + (w_bytes + 1023) / 1024 * 1024; }
+    static constexpr int stages(uint32_t w_bytes) {
+        const int s = int((kFewSmem - kFixed - (kStageA - (w_bytes + 1023) / 1024 * 1024)) / stage(w_bytes));
+        return s < kFewMostStages ? s : kFewMostStages;
+    }
+    static_assert(stages(kStageA) >= 3 && size_t(N) * 128 * 4 + kFixed <= kFewSmem, "the parts fit the stages");
 };
 
 template <bool W_MN, int N>
 __global__ void __launch_bounds__(kFewThreads, 2)
-    grouped_few_kernel(const __grid_constant__ CUtensorMap map_w, const Params p, int splits, int per) {
+    grouped_few_kernel(const __grid_constant__ CUtensorMap map_w, const Params p, int splits, int per, uint32_t S, uint32_t stage) {
     using F = Few<N>;
     const SharedWaitCtx wc{p.err, p.timeout_ns};
-    constexpr int S = F::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S * F::kStageBytes);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kFewSmem - F::kFixed);
     const uint32_t bar0 = smem_addr(bars), smem0 = smem_addr(smem);
     auto full_bar = [&](uint32_t s) { return bar0 + 8u * s; };
-    auto empty_bar = [&](uint32_t s) { return bar0 + 8u * (S + s); };
-    const uint32_t done_bar = bar0 + 8u * (2 * S);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 1);
-    static_assert((2 * S + 1) * 8 + 4 <= int(kBarBytes), "barrier area");
+    auto empty_bar = [&](uint32_t s) { return bar0 + 8u * (kFewMostStages + s); };
+    const uint32_t done_bar = bar0 + 8u * (2 * kFewMostStages);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kFewMostStages + 1);
+    static_assert((2 * kFewMostStages + 1) * 8 + 4 <= int(kBarBytes), "barrier area");
     __shared__ int found[3];  // group, first place, places
     __shared__ int sums[kFewThreads / 32];
 
@@ -377,7 +383,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
 
     if (threadIdx.x == 0) {
         tma_prefetch_map(&map_w);
-        for (int s = 0; s < S; ++s) {
+        for (uint32_t s = 0; s < S; ++s) {
             mbar_init(full_bar(s), 1 + kPickWarps);
             mbar_init(empty_bar(s), 1);
         }
@@ -395,7 +401,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
 
     if (warp == 0) {
         auto load_w = [&](int kb, uint32_t s) {
-            const uint32_t sa = smem0 + s * F::kStageBytes;
+            const uint32_t sa = smem0 + s * stage + F::kRowBytes;
             const int k0 = kb * kBlockK;
             if (W_MN) {
                 for (int c = 0; c < p.w_boxes; ++c) tma_load_box(sa + c * kMnChunk, &map_w, full_bar(s), m0 + 64 * c, k0, group);
@@ -403,8 +409,6 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                 tma_load_box(sa, &map_w, full_bar(s), k0, m0, group);
             }
         };
-        // The weight is there before the kernel ahead of this one began
-        // (GroupedDesc::early).
         uint32_t fills = 0;
         if (lane == 0) {
             for (int kb = kb0; kb < kb1; ++kb, ++fills) {
@@ -413,7 +417,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                 mbar_arrive_expect_tx(full_bar(s), p.w_bytes);
                 load_w(kb, s);
             }
-            const uint32_t outstanding = fills < uint32_t(S) ? fills : uint32_t(S);
+            const uint32_t outstanding = fills < S ? fills : S;
             for (uint32_t j = 0; j < outstanding; ++j) {
                 const uint32_t f = fills - 1 - j;
                 wait_bounded(full_bar(f % S), (f / S) & 1u, wc, kErrDrainWait, false);
@@ -427,19 +431,18 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                 const uint32_t s = fills % S;
                 if (!wait_bounded(full_bar(s), (fills / S) & 1u, wc, kErrMmaWaitFull)) break;
                 tc_fence_after();
-                const uint32_t sa = smem0 + s * F::kStageBytes;
-                block_mmas<W_MN, false>(p, kb, kb == kb0, tmem_base, sa, sa + kStageA, idesc);
+                const uint32_t sa = smem0 + s * stage + F::kRowBytes;
+                block_mmas<W_MN, false>(p, kb, kb == kb0, tmem_base, sa, sa - F::kRowBytes, idesc);
                 umma_commit(empty_bar(s));
             }
             umma_commit(done_bar);
             wait_bounded(done_bar, 0, wc, kErrDrainWait, false);
         }
     } else if (warp >= kFirstEpilogueWarp && warp < kThreads / 32) {
-        // These warps pick up the rows first, which the kernel ahead of this one may make.
-        grid_dependency_wait();
+        // these warps pick up the rows first
         {
             const Picker pick(int(threadIdx.x) - 32 * kFirstEpilogueWarp);
-            constexpr int kRows = (N + kPickRows - 1) / kPickRows, kUnderWay = S - 1 < 4 ? S - 1 : 4;
+            constexpr int kRows = (N + kPickRows - 1) / kPickRows, kUnderWay = 2;  // (fewer than the stages)
             const uint16_t* src[kRows];
             bool there[kRows];
 #pragma unroll
@@ -469,7 +472,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                 }
 #pragma unroll
                 for (int r = 0; r < kRows; ++r)
-                    pick.copy(smem0 + s * F::kStageBytes + kStageA, r, src[r] + kb * kBlockK, there[r] ? p.reduce - kb * kBlockK : 0);
+                    pick.copy(smem0 + s * stage, r, src[r] + kb * kBlockK, there[r] ? p.reduce - kb * kBlockK : 0);
                 cp_async_commit();
                 if (fills - handed == kUnderWay) {
                     cp_async_wait<kUnderWay>();
@@ -499,7 +502,6 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             }
         tc_fence_before();
     }
-    grid_dependency_wait();  // (the result may be what the kernel before this one works on)
     if (splits > 1) cluster_sync();  // every part stands
     else __syncthreads();
     const float scale = none ? 0.0f : p.scale ? __ldg(p.scale + group) : p.scale_all;
@@ -576,18 +578,18 @@ cudaError_t launch_few(const CUtensorMap& mw, Params p, const GroupedDesc& d, in
     const int64_t likely = std::max<int64_t>(1, std::min(blocks, (d.rows + N - 1) / N + std::min(seen, d.rows) / 2)) * p.num_m;
     int splits = 1, per_sm = 0, clusters = 0;
     const void* shape = reinterpret_cast<const void*>(grouped_few_shape_kernel);
-    cudaError_t e = ctas_per_sm(shape, kFewThreads, Few<N>::kSmem, &per_sm);
+    cudaError_t e = ctas_per_sm(shape, kFewThreads, kFewSmem, &per_sm);
     // CTAs of a cluster: as many as two an SM allow, with four K-blocks each
     while (e == cudaSuccess && splits < 8 && likely * splits * 2 <= 2 * num_sms && p.num_k >= 8 * splits) {
-        e = clusters_at_a_time(shape, kFewThreads, Few<N>::kSmem, 2 * splits, &clusters);
+        e = clusters_at_a_time(shape, kFewThreads, kFewSmem, 2 * splits, &clusters);
         if (e != cudaSuccess || likely > clusters) break;
         splits *= 2;
     }
     if (e != cudaSuccess) return e;
     if (units * splits > INT32_MAX) return cudaErrorInvalidConfiguration;
     const int per = (p.num_k + splits - 1) / splits;
-    return launch_in_clusters(grouped_few_kernel<W_MN, N>, dim3(unsigned(units * splits)), kFewThreads, splits, Few<N>::kSmem, d.early, stream, mw,
-                              p, splits, per);
+    return launch_in_clusters(grouped_few_kernel<W_MN, N>, dim3(unsigned(units * splits)), kFewThreads, splits, kFewSmem, false, stream, mw,
+                              p, splits, per, uint32_t(Few<N>::stages(p.w_bytes)), Few<N>::stage(p.w_bytes));
 }
 
 // A sorted copy of indexed rows: rows outside the matrix as zeros.

@@ -39,7 +39,6 @@ struct GroupedDesc {
     void* split_out = nullptr;
     int32_t split_half = 0;
     void* gathered = nullptr;  // workspace for an indexed x's rows, [rows, picked_ld] (own > 128 needs it)
-    bool early = false;  // the kernel ahead writes x alone: w may be read before it has completed
     int32_t* err = nullptr;
 };
 std::string grouped_check(const GroupedDesc& d);

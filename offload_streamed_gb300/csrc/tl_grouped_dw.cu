@@ -240,24 +240,23 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_dw_kernel(const __grid_co
 
 // ---- narrow gradients --------------------------------------------------------
 
-// The rows of a block that a picking thread copies, of one operand.
+// The rows of a block that a picking thread copies, of one operand: numbers, so that
+// the next block's can be on their way.
 struct BlockRows {
-    const uint16_t* src[kBlockK / kPickRows];
-    bool there[kBlockK / kPickRows];
-    __device__ __forceinline__ void find(const uint16_t* at, int64_t ld, int rows, const int32_t* index, int p, int end) {
+    int row[kBlockK / kPickRows];
+    __device__ __forceinline__ void find(const int32_t* index, int p, int end) {
 #pragma unroll
         for (int i = 0; i < kBlockK / kPickRows; ++i) {
-            const int place = p + kPickRows * i, row = place < end ? (index ? __ldg(index + place) : place) : -1;
-            there[i] = unsigned(row) < unsigned(rows);
-            src[i] = at + (there[i] ? row * ld : 0);
+            const int place = p + kPickRows * i;
+            row[i] = place < end ? (index ? __ldg(index + place) : place) : -1;
         }
     }
-    // columns col .. col + 63 of `cols`, to the box at `box`
-    __device__ __forceinline__ void copy(const Picker& pick, uint32_t box, int col, int cols) const {
+    // columns col .. col + 63 of `cols`, to the box at `box`; a row outside the matrix as zeros
+    __device__ __forceinline__ void copy(const Picker& pick, uint32_t box, const uint16_t* at, int64_t ld, int rows, int col, int cols) const {
 #pragma unroll
         for (int i = 0; i < kBlockK / kPickRows; ++i) {
-            const int have = there[i] ? cols - col : 0;
-            pick.copy(box, i, src[i] + (have > 0 ? col : 0), have);
+            const int have = unsigned(row[i]) < unsigned(rows) ? cols - col : 0;
+            pick.copy(box, i, at + (have > 0 ? row[i] * ld + col : 0), have);
         }
     }
 };
@@ -265,7 +264,8 @@ struct BlockRows {
 constexpr int kNarrowThreads = kThreads + 32;  // the ninth warp as in tl_grouped.cu
 constexpr size_t kNarrowSmem = 112 * 1024;     // of a CTA: two share an SM
 constexpr int kNarrowMostStages = 8;
-constexpr int kNarrowUnderWay = 1;  // blocks that a picking thread has under way: fewer than the stages, which are two at least
+// Blocks that a picking thread has under way behind the one handed over: fewer than the stages.
+constexpr int kNarrowUnderWay = 2;
 constexpr uint32_t kNarrowFixed = kBarBytes + 1024;
 __host__ __device__ constexpr uint32_t narrow_stage(int n) { return kStageA + uint32_t((n + 63) / 64) * kMnChunk; }
 constexpr int narrow_stages(int n) {
@@ -346,8 +346,8 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
             const Picker pick(int(threadIdx.x) - 32 * kFirstEpilogueWarp);
             const int boxes = (p.n + 63) / 64;
             BlockRows x, dy, nx, ny;
-            x.find(p.x, p.ldx, p.x_rows, p.x_index, begin + kb0 * kBlockK + pick.row, end);
-            dy.find(p.dy, p.lddy, p.dy_rows, p.dy_index, begin + kb0 * kBlockK + pick.row, end);
+            x.find(p.x_index, begin + kb0 * kBlockK + pick.row, end);
+            dy.find(p.dy_index, begin + kb0 * kBlockK + pick.row, end);
             uint32_t fills = 0, handed = 0;
             auto hand_over = [&] {
                 fence_proxy_async_shared();
@@ -358,8 +358,8 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
             bool go = true;
             for (int kb = kb0; kb < kb1; ++kb, ++fills) {
                 const uint32_t s = fills % uint32_t(S);
-                nx.find(p.x, p.ldx, p.x_rows, p.x_index, begin + (kb + 1) * kBlockK + pick.row, end);
-                ny.find(p.dy, p.lddy, p.dy_rows, p.dy_index, begin + (kb + 1) * kBlockK + pick.row, end);
+                nx.find(p.x_index, begin + (kb + 1) * kBlockK + pick.row, end);
+                ny.find(p.dy_index, begin + (kb + 1) * kBlockK + pick.row, end);
                 if (!warp_test(empty_bar(s), ((fills / uint32_t(S)) & 1u) ^ 1u)) {
                     cp_async_wait<0>();
                     while (handed < fills) hand_over();
@@ -369,10 +369,10 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
                     break;
                 }
                 const uint32_t sa = smem0 + s * stage, sb = sa + kStageA;
-                for (int c = 0; c < 2; ++c) x.copy(pick, sa + c * kMnChunk, m0 + 64 * c, p.m_dim);
-                for (int c = 0; c < boxes; ++c) dy.copy(pick, sb + c * kMnChunk, 64 * c, p.dy_cols);
+                for (int c = 0; c < 2; ++c) x.copy(pick, sa + c * kMnChunk, p.x, p.ldx, p.x_rows, m0 + 64 * c, p.m_dim);
+                for (int c = 0; c < boxes; ++c) dy.copy(pick, sb + c * kMnChunk, p.dy, p.lddy, p.dy_rows, 64 * c, p.dy_cols);
                 cp_async_commit();
-                if (fills - handed == kNarrowUnderWay) {
+                if (S > kNarrowUnderWay && fills - handed == kNarrowUnderWay) {  // (else before the next wait)
                     cp_async_wait<kNarrowUnderWay>();
                     hand_over();
                 }

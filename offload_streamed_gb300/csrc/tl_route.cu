@@ -252,8 +252,25 @@ struct Choice {
     int32_t per;  // tokens of a CTA
 };
 
+// A token's logits, V a lane (-inf past the last), as they lie in memory: lane e % 32 has
+// logit e or, vectors of V, lane e / V.
+template <typename T, int V, bool VECTORS>
+__device__ __forceinline__ void load_logits(const T* row, int experts, T (&v)[V]) {
+    const int lane = threadIdx.x & 31;
+    if constexpr (VECTORS) {
+        if (lane * V < experts) {
+            const Vec<T, V> u = *reinterpret_cast<const Vec<T, V>*>(row + lane * V);
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[i] = u.v[i];
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = !VECTORS && i * 32 + lane < experts ? row[i * 32 + lane] : from_f32<T>(-INFINITY);
+}
+
 // V logits a lane.  Writes ids and weights of a CTA's tokens and its counts; alone: places the entries too.
-template <typename T, int V>
+template <typename T, int V, bool VECTORS>
 __global__ void __launch_bounds__(kSortThreads) route_kernel(const Choice c, const Sort p, int32_t* ids, const bool alone) {
     extern __shared__ int sort_smem[];
     grid_dependents_go();
@@ -261,14 +278,14 @@ __global__ void __launch_bounds__(kSortThreads) route_kernel(const Choice c, con
     for (int b = threadIdx.x; b <= experts; b += kSortThreads) sort_smem[b] = 0;
     __syncthreads();
     const int first = int(blockIdx.x) * c.per, last = min(c.tokens, first + c.per);
+    const T* logits = static_cast<const T*>(c.logits);
+    T next[V];  // the next token's, on their way
+    if (first + warp < last) load_logits<T, V, VECTORS>(logits + int64_t(first + warp) * c.ld, experts, next);
     for (int t = first + warp; t < last; t += kSortWarps) {
-        const T* row = static_cast<const T*>(c.logits) + int64_t(t) * c.ld;
         uint32_t key[V], top = 0;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int e = i * 32 + lane;
-            key[i] = e < experts ? key_of<T>(row[e], e) : 0;
-        }
+        for (int i = 0; i < V; ++i) key[i] = key_of<T>(next[i], VECTORS ? lane * V + i : i * 32 + lane);
+        if (t + kSortWarps < last) load_logits<T, V, VECTORS>(logits + int64_t(t + kSortWarps) * c.ld, experts, next);
         float sum = 0, best = 0;
         if (!c.normalize) {
 #pragma unroll
@@ -407,54 +424,62 @@ __global__ void __launch_bounds__(kBackThreads) route_backward_kernel(const T* l
 
 // ---- the sum of the experts' answers ------------------------------------------
 
-// `lanes` threads (a power of two) share a token's row, a vector of N elements
-// each; the grid's second dimension walks the row's further vectors.
-constexpr int kCombineThreads = 256;
-template <typename T, int N>
+// `lanes` threads (a power of two) share a token's row, kVectors vectors of N elements
+// each; the grid's second dimension walks the row's further vectors.  B entries at
+// a time: their rows are all asked for before one is used.
+constexpr int kCombineThreads = 256, kVectors = 2;
+template <typename T, int N, int B>
 __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const T* y, int64_t ldy, const int32_t* slots, const float* weights, T* out,
                                                                   int64_t ldo, int tokens, int k, int rows, int vectors, int lanes) {
     const int64_t t = int64_t(blockIdx.x) * (kCombineThreads / lanes) + threadIdx.x / lanes;
-    const int v = int(blockIdx.y) * lanes + int(threadIdx.x % lanes);
-    if (t >= tokens || v >= vectors) return;
+    const int v0 = int(blockIdx.y) * lanes * kVectors + int(threadIdx.x % lanes);
+    if (t >= tokens || v0 >= vectors) return;
     using L = Lanes<N>;
-    constexpr int M = N == 1 ? 1 : N / 2, kBatch = 4;
-    L sum[M];
+    constexpr int M = N == 1 ? 1 : N / 2;
+    L sum[kVectors][M];
 #pragma unroll
-    for (int i = 0; i < M; ++i) sum[i] = splat<L>(0.0f);
-    for (int j0 = 0; j0 < k; j0 += kBatch) {
-        Vec<T, N> u[kBatch];
-        float w[kBatch];
+    for (int q = 0; q < kVectors; ++q)
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-            w[j] = 0;
-            if (j0 + j < k) {
-                const int s = slots[t * k + j0 + j];
-                const bool there = unsigned(s) < unsigned(rows);
-                if (there) {
-                    u[j] = *reinterpret_cast<const Vec<T, N>*>(y + int64_t(s) * ldy + int64_t(v) * N);
-                    w[j] = weights ? weights[t * k + j0 + j] : 1.0f;
+        for (int i = 0; i < M; ++i) sum[q][i] = splat<L>(0.0f);
+    for (int j0 = 0; j0 < k; j0 += B) {
+        Vec<T, N> u[B][kVectors];
+        float w[B];
+#pragma unroll
+        for (int j = 0; j < B; ++j) {
+            const int s = j0 + j < k ? slots[t * k + j0 + j] : -1;
+            const bool there = unsigned(s) < unsigned(rows);
+            w[j] = there ? (weights ? weights[t * k + j0 + j] : 1.0f) : 0.0f;
+#pragma unroll
+            for (int q = 0; q < kVectors; ++q) {
+                if (there && v0 + q * lanes < vectors) {
+                    u[j][q] = *reinterpret_cast<const Vec<T, N>*>(y + int64_t(s) * ldy + int64_t(v0 + q * lanes) * N);
                 } else {  // a missing answer adds nothing, whatever its weight
 #pragma unroll
-                    for (int i = 0; i < N; ++i) u[j].v[i] = from_f32<T>(0.0f);
+                    for (int i = 0; i < N; ++i) u[j][q].v[i] = from_f32<T>(0.0f);
                 }
             }
         }
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j)
-            if (j0 + j < k) {
-                L a[M];
-                unpack(u[j], a);
+        for (int j = 0; j < B; ++j)
 #pragma unroll
-                for (int i = 0; i < M; ++i) sum[i] = fma(a[i], splat<L>(w[j]), sum[i]);
+            for (int q = 0; q < kVectors; ++q) {
+                L a[M];
+                unpack(u[j][q], a);
+#pragma unroll
+                for (int i = 0; i < M; ++i) sum[q][i] = fma(a[i], splat<L>(w[j]), sum[q][i]);
             }
     }
-    Vec<T, N> o;
-    pack(sum, o);
-    *reinterpret_cast<Vec<T, N>*>(out + t * ldo + int64_t(v) * N) = o;
+#pragma unroll
+    for (int q = 0; q < kVectors; ++q) {
+        if (v0 + q * lanes >= vectors) break;
+        Vec<T, N> o;
+        pack(sum[q], o);
+        *reinterpret_cast<Vec<T, N>*>(out + t * ldo + int64_t(v0 + q * lanes) * N) = o;
+    }
 }
 
-// A CTA's `lanes` threads walk a token's row once for each of its entries: dout
-// comes from memory the first time and from the first-level cache after that.
+// `lanes` threads walk a token's row, four of its entries at a time: dout is read
+// once for four, from memory the first time.
 template <typename T, int N>
 __global__ void __launch_bounds__(kCombineThreads) combine_backward_kernel(const T* dout, int64_t lddout, const T* y, int64_t ldy,
                                                                            const int32_t* slots, const float* weights, T* dy, int64_t lddy,
@@ -463,39 +488,52 @@ __global__ void __launch_bounds__(kCombineThreads) combine_backward_kernel(const
     const int64_t t = int64_t(blockIdx.x) * (kCombineThreads / lanes) + threadIdx.x / lanes;
     const int first = int(threadIdx.x % lanes), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     using L = Lanes<N>;
-    constexpr int M = N == 1 ? 1 : N / 2;
+    constexpr int M = N == 1 ? 1 : N / 2, B = 4;
     const bool mine = t < tokens;  // (whole warps: lanes is 32 at least)
-    for (int j = 0; j < k; ++j) {
-        L dot[M];
+    for (int j0 = 0; j0 < k; j0 += B) {
+        L dot[B];
+        int at[B];
+        float w[B];
 #pragma unroll
-        for (int i = 0; i < M; ++i) dot[i] = splat<L>(0.0f);
-        const int s = mine ? slots[t * k + j] : -1;
-        if (unsigned(s) < unsigned(rows)) {
-            const float w = weights ? weights[t * k + j] : 1.0f;
-#pragma unroll 2
+        for (int j = 0; j < B; ++j) {
+            dot[j] = splat<L>(0.0f);
+            at[j] = mine && j0 + j < k ? slots[t * k + j0 + j] : -1;
+            if (unsigned(at[j]) >= unsigned(rows)) at[j] = -1;
+            w[j] = at[j] >= 0 && weights ? weights[t * k + j0 + j] : 1.0f;
+        }
+        if (mine)
             for (int v = first; v < vectors; v += lanes) {
                 L g[M];
+                Vec<T, N> u[B];
                 unpack(*reinterpret_cast<const Vec<T, N>*>(dout + t * lddout + int64_t(v) * N), g);
                 if (dweights) {
-                    L a[M];
-                    unpack(*reinterpret_cast<const Vec<T, N>*>(y + int64_t(s) * ldy + int64_t(v) * N), a);
 #pragma unroll
-                    for (int i = 0; i < M; ++i) dot[i] = fma(g[i], a[i], dot[i]);
+                    for (int j = 0; j < B; ++j)
+                        if (at[j] >= 0) u[j] = *reinterpret_cast<const Vec<T, N>*>(y + int64_t(at[j]) * ldy + int64_t(v) * N);
                 }
 #pragma unroll
-                for (int i = 0; i < M; ++i) g[i] = mul(g[i], splat<L>(w));
-                Vec<T, N> o;
-                pack(g, o);
-                *reinterpret_cast<Vec<T, N>*>(dy + int64_t(s) * lddy + int64_t(v) * N) = o;
-            }
-        }
-        if (dweights) {
-            float f = 0;
+                for (int j = 0; j < B; ++j)
+                    if (at[j] >= 0) {
+                        if (dweights) {
+                            L a[M];
+                            unpack(u[j], a);
 #pragma unroll
-            for (int i = 0; i < M; ++i) f += total(dot[i]);
-            f = warp_sum(f);
-            if (lane == 0) part[j][warp] = f;
-        }
+                            for (int i = 0; i < M; ++i) dot[j] = fma(g[i], a[i], dot[j]);
+                        }
+                        L f[M];
+#pragma unroll
+                        for (int i = 0; i < M; ++i) f[i] = mul(g[i], splat<L>(w[j]));
+                        Vec<T, N> o;
+                        pack(f, o);
+                        *reinterpret_cast<Vec<T, N>*>(dy + int64_t(at[j]) * lddy + int64_t(v) * N) = o;
+                    }
+            }
+        if (dweights)
+#pragma unroll
+            for (int j = 0; j < B; ++j) {
+                const float f = warp_sum(total(dot[j]));
+                if (lane == 0 && j0 + j < k) part[j0 + j][warp] = f;
+            }
     }
     if (!dweights) return;
     __syncthreads();
@@ -552,13 +590,16 @@ cudaError_t route_typed(const RouteDesc& d, cudaStream_t stream) {
     const Choice c{d.logits, d.ld, d.weights, int32_t(d.tokens), d.normalize ? 1 : 0, per};
     const size_t smem = alone ? place_smem(d.groups) : size_t(d.groups + 1) * 4;
     auto run = [&](auto kern) { return launch(kern, grid, smem, false, stream, c, s, d.ids, alone); };
+    // vectors of a lane, where rows are whole ones on their boundaries (16-bit logits: their order needs the index in the key)
+    const auto whole = [&](int v) { return sizeof(T) == 2 && d.groups % v == 0 && d.ld % v == 0 && !off(d.logits, sizeof(T) * v); };
+    constexpr bool V = sizeof(T) == 2;
     cudaError_t e;
-    if (d.groups <= 32) e = run(route_kernel<T, 1>);
-    else if (d.groups <= 64) e = run(route_kernel<T, 2>);
-    else if (d.groups <= 128) e = run(route_kernel<T, 4>);
-    else if (d.groups <= 256) e = run(route_kernel<T, 8>);
-    else if (d.groups <= 512) e = run(route_kernel<T, 16>);
-    else e = run(route_kernel<T, 32>);
+    if (d.groups <= 32) e = run(route_kernel<T, 1, false>);
+    else if (d.groups <= 64) e = whole(2) ? run(route_kernel<T, 2, V>) : run(route_kernel<T, 2, false>);
+    else if (d.groups <= 128) e = whole(4) ? run(route_kernel<T, 4, V>) : run(route_kernel<T, 4, false>);
+    else if (d.groups <= 256) e = whole(8) ? run(route_kernel<T, 8, V>) : run(route_kernel<T, 8, false>);
+    else if (d.groups <= 512) e = run(route_kernel<T, 16, false>);
+    else e = run(route_kernel<T, 32, false>);
     if (e != cudaSuccess || alone) return e;
     return launch(sort_place_kernel, grid, place_smem(d.groups), true, stream, s);
 }
@@ -581,11 +622,12 @@ bool whole_vectors(const CombineDesc& d, bool backward) {
 template <typename T, int N>
 cudaError_t combine_vectors(const CombineDesc& d, bool backward, cudaStream_t stream) {
     const int64_t vectors = (d.cols + N - 1) / N;
-    const int lanes = row_lanes(vectors, kCombineThreads), tokens = kCombineThreads / lanes;
+    const int lanes = row_lanes(backward ? vectors : (vectors + kVectors - 1) / kVectors, kCombineThreads), tokens = kCombineThreads / lanes;
     dim3 grid(unsigned((d.tokens + tokens - 1) / tokens));
     if (!backward) {
-        grid.y = unsigned((vectors + lanes - 1) / lanes);
-        combine_kernel<T, N><<<grid, kCombineThreads, 0, stream>>>(static_cast<const T*>(d.y), d.ldy, d.slots, d.weights, static_cast<T*>(d.out), d.ldout,
+        grid.y = unsigned((vectors + lanes * kVectors - 1) / (lanes * kVectors));
+        const auto kern = d.k <= 2 ? combine_kernel<T, N, 2> : combine_kernel<T, N, 4>;
+        kern<<<grid, kCombineThreads, 0, stream>>>(static_cast<const T*>(d.y), d.ldy, d.slots, d.weights, static_cast<T*>(d.out), d.ldout,
                                                                    int(d.tokens), int(d.k), int(d.rows), int(vectors), lanes);
     } else {
         combine_backward_kernel<T, N><<<grid, kCombineThreads, 0, stream>>>(static_cast<const T*>(d.dout), d.lddout, static_cast<const T*>(d.y), d.ldy, d.slots,
