@@ -79,48 +79,62 @@ __device__ int scan_cta(int v, int* scratch, int* all) {
 }
 
 // The places of entries first .. first + len - 1, `cta` of `ctas`.  at: [warps][groups + 1],
-// start: [groups + 1].  With one CTA there are no counts to read.
+// start: [2 (groups + 1)].  With one CTA there are no counts to read.
 __device__ void place_entries(const Sort& p, int first, int len, int cta, int ctas, int* at, int* start, int* scratch) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, bins = p.groups + 1;
     for (int i = threadIdx.x; i < kSortWarps * bins; i += kSortThreads) at[i] = 0;
-    __syncthreads();
-    // how many of each group a warp has
-    const int span = (len + kSortThreads - 1) / kSortThreads * 32;
-    const int from = first + min(len, warp * span), to = first + min(len, (warp + 1) * span);
-    int* mine = at + warp * bins;
-    const int bits = 32 - __clz(bins);  // (bins itself stands for a lane without an entry)
-    for (int i = from; i < to; i += 32) {
-        const int b = i + lane < to ? bin_of(p.ids[i + lane], p.groups) : bins;
-        const unsigned same = lanes_of(b, bits);
-        if (b < bins && (same & ((1u << lane) - 1)) == 0) mine[b] += __popc(same);
-        __syncwarp();
-    }
-    __syncthreads();
-    // all entries of a group, and those in CTAs before this one
-    for (int g = warp; g < bins; g += kSortWarps) {
-        int before = 0, total = 0;
-        if (ctas > 1) {
+    // all entries of a group in start, those in CTAs before this one in the second half of it
+    int* before = start + bins;
+    if (ctas > 1)
+        for (int g = warp; g < bins; g += kSortWarps) {
+            int earlier = 0, total = 0;
 #pragma unroll 5
             for (int c = lane; c < ctas; c += 32) {
                 const int v = __ldcg(p.counts + int64_t(g) * ctas + c);
                 total += v;
-                before += c < cta ? v : 0;
+                earlier += c < cta ? v : 0;
             }
-        } else {
-            total = at[lane * bins + g];
+            total = __reduce_add_sync(0xffffffffu, total);
+            earlier = __reduce_add_sync(0xffffffffu, earlier);
+            if (lane == 0) {
+                start[g] = total;
+                before[g] = earlier;
+            }
         }
-        total = __reduce_add_sync(0xffffffffu, total);
-        before = __reduce_add_sync(0xffffffffu, before);
-        // where a warp's entries of the group begin, from the group's first in this CTA on
-        const int v = at[lane * bins + g];
-        int s = v;
+    __syncthreads();
+    // how many of each group a warp has, and each entry's rank among them; those of
+    // the first rounds stay in registers
+    constexpr int kKept = 8;
+    const int span = (len + kSortThreads - 1) / kSortThreads * 32, rounds = span / 32;
+    const int from = first + min(len, warp * span), to = first + min(len, (warp + 1) * span);
+    int* mine = at + warp * bins;
+    const int bits = 32 - __clz(bins);  // (bins itself stands for a lane without an entry)
+    auto rank_of = [&](int i, int& bin) {
+        bin = i + lane < to ? bin_of(p.ids[i + lane], p.groups) : bins;
+        const unsigned same = lanes_of(bin, bits), earlier = same & ((1u << lane) - 1);
+        const int rank = bin < bins ? mine[bin] + __popc(earlier) : 0;
+        __syncwarp();
+        if (bin < bins && earlier == 0) mine[bin] += __popc(same);
+        __syncwarp();
+        return rank;
+    };
+    int rank[kKept], bin[kKept];
 #pragma unroll
-        for (int d = 1; d < 32; d *= 2) {
-            const int u = __shfl_up_sync(0xffffffffu, s, d);
-            if (lane >= d) s += u;
+    for (int r = 0; r < kKept; ++r)
+        if (r < rounds) rank[r] = rank_of(from + 32 * r, bin[r]);
+    int other;
+    for (int r = kKept; r < rounds; ++r) rank_of(from + 32 * r, other);
+    __syncthreads();
+    // where each warp's entries of a group begin, from the group's first in this CTA on
+    for (int g = threadIdx.x; g < bins; g += kSortThreads) {
+        int s = ctas > 1 ? before[g] : 0;
+#pragma unroll 8
+        for (int w = 0; w < kSortWarps; ++w) {
+            const int v = at[w * bins + g];
+            at[w * bins + g] = s;
+            s += v;
         }
-        at[lane * bins + g] = s - v + before;
-        if (lane == 0) start[g] = total;
+        if (ctas == 1) start[g] = s;
     }
     __syncthreads();
     int all;
@@ -133,18 +147,21 @@ __device__ void place_entries(const Sort& p, int first, int len, int cta, int ct
         if (g == 0) p.offsets[p.groups] = all;
     }
     __syncthreads();
-    for (int i = from; i < to; i += 32) {
-        const int b = i + lane < to ? bin_of(p.ids[i + lane], p.groups) : bins;
-        const unsigned same = lanes_of(b, bits), earlier = same & ((1u << lane) - 1);
-        int place = 0;
-        if (b < bins) place = start[b] + mine[b] + __popc(earlier);
+    auto put = [&](int i, int b, int in_warp) {
+        if (b >= bins) return;
+        const int place = start[b] + in_warp;
+        p.slots[i + lane] = b < p.groups ? place : -1;
+        p.rows[place] = (i + lane) / p.k;
+    };
+#pragma unroll
+    for (int r = 0; r < kKept; ++r)
+        if (r < rounds) put(from + 32 * r, bin[r], bin[r] < bins ? mine[bin[r]] + rank[r] : 0);
+    if (rounds > kKept) {  // (the kept rounds count again, behind the warp's begin, which then grows)
         __syncwarp();
-        if (b < bins) {
-            if (earlier == 0) mine[b] += __popc(same);
-            p.slots[i + lane] = b < p.groups ? place : -1;
-            p.rows[place] = (i + lane) / p.k;
+        for (int r = 0; r < rounds; ++r) {
+            const int k = rank_of(from + 32 * r, other);
+            if (r >= kKept) put(from + 32 * r, other, k);
         }
-        __syncwarp();
     }
 }
 
@@ -575,7 +592,7 @@ cudaError_t launch(void (*kern)(P...), unsigned grid, size_t smem, bool early, c
     return cudaLaunchKernelEx(&cfg, kern, P(args)...);
 }
 
-size_t place_smem(int64_t groups) { return size_t(kSortWarps + 1) * size_t(groups + 1) * 4; }
+size_t place_smem(int64_t groups) { return size_t(kSortWarps + 2) * size_t(groups + 1) * 4; }
 
 Sort sort_of(const RouteDesc& d, int64_t per) {
     return Sort{d.ids, d.slots, d.rows, d.offsets, d.counts, int32_t(d.tokens * d.k), int32_t(d.k), int32_t(d.groups), int32_t(per)};

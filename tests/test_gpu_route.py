@@ -77,7 +77,7 @@ def test_route_takes_strides_and_no_tokens(tl):
     assert w.shape == (0, 5) and rows.shape == (0,) and offsets.tolist() == [0] * 41
 
 
-@pytest.mark.parametrize("T,k,groups", [(1, 1, 1), (17, 3, 5), (8192, 1, 64), (8193, 1, 3), (3000, 4, 1024), (200000, 2, 37)])
+@pytest.mark.parametrize("T,k,groups", [(1, 1, 1), (17, 3, 5), (8192, 1, 64), (8193, 1, 3), (3000, 4, 1024), (200000, 2, 37), (700000, 2, 9)])
 def test_group_rows(tl, T, k, groups):
     g = torch.Generator().manual_seed(T)
     ids = torch.randint(-2, groups + 2, (T, k), generator=g, dtype=torch.int32)
