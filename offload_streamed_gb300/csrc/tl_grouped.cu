@@ -130,11 +130,12 @@ __device__ __forceinline__ Tile find_tile(const Params& p, const int* first, int
     return t;
 }
 
-constexpr int kBoxRows = 32;  // of x
+constexpr int kBoxRows = 32;  // of x, in boxes for few rows (with one box of 128 for more: each load costs the issuing thread)
 
 template <bool W_MN>
 __global__ void __launch_bounds__(kThreads, 1)
-    grouped_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, const Params p) {
+    grouped_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_x_few,
+                   const Params p) {
     const SharedWaitCtx wc{p.err, p.timeout_ns};
     constexpr int S = kPairStages;
     extern __shared__ uint8_t smem_raw[];
@@ -218,8 +219,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int tile = int(cluster_id_x()); ok && tile < tiles; tile += step) {
                 const Tile t = tile_at(tile);
                 const int m0 = t.m * 256 + int(rank) * kBlockM, half_n = t.n / 2, row0 = t.p0 + int(rank) * half_n;
-                const int boxes = (half_n + kBoxRows - 1) / kBoxRows;
-                const uint32_t bytes = 2u * (p.w_bytes + uint32_t(boxes * kBoxRows) * 128u);
+                const int boxes = half_n > kBlockM / 2 ? 0 : (half_n + kBoxRows - 1) / kBoxRows;
+                const uint32_t bytes = 2u * (p.w_bytes + uint32_t(boxes ? boxes * kBoxRows : kBlockM) * 128u);
                 for (int kb = 0; kb < p.num_k; ++kb, ++fills) {
                     const uint32_t s = fills % S;
                     if (!wait_bounded(empty_bar(s), ((fills / S) & 1u) ^ 1u, wc, kErrProducerWait)) {
@@ -236,7 +237,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tma_load_box_pair(sa, &map_w, fb, k0, m0, t.g);
                     }
                     // (rows past the tile's last are others or zeros: their results are not stored)
-                    for (int c = 0; c < boxes; ++c) tma_load_2d_pair(sb + c * kBoxRows * 128, &map_x, fb, kb * kBlockK, row0 + c * kBoxRows);
+                    if (boxes == 0) tma_load_2d_pair(sb, &map_x, fb, kb * kBlockK, row0);
+                    for (int c = 0; c < boxes; ++c) tma_load_2d_pair(sb + c * kBoxRows * 128, &map_x_few, fb, kb * kBlockK, row0 + c * kBoxRows);
                 }
             }
         }
@@ -696,8 +698,9 @@ cudaError_t grouped_launch(const GroupedDesc& d, int num_sms, cudaStream_t strea
             if (g != cudaSuccess) return g;
             x = {d.gathered, picked_ld(d.reduce), d.rows, nullptr};
         }
-        if (!rows_map(&mx, d.type, x, d.reduce, kBoxRows, why)) return cudaErrorInvalidValue;
-        auto run = [&](auto kern) { return launch_in_clusters(kern, dim3(grid), kThreads, 2, kPairSmem, false, stream, mw, mx, p); };
+        CUtensorMap few;
+        if (!rows_map(&mx, d.type, x, d.reduce, kBlockM, why) || !rows_map(&few, d.type, x, d.reduce, kBoxRows, why)) return cudaErrorInvalidValue;
+        auto run = [&](auto kern) { return launch_in_clusters(kern, dim3(grid), kThreads, 2, kPairSmem, false, stream, mw, mx, few, p); };
         e = d.own_contiguous ? run(grouped_kernel<true>) : run(grouped_kernel<false>);
     } else {
         p.num_m = int32_t((d.own + kBlockM - 1) / kBlockM);
