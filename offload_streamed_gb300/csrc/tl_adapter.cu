@@ -28,7 +28,11 @@ using gr::round16;
 using gr::value16;
 
 constexpr int kFewThreads = 256;
-constexpr int64_t kFewRows = 64;
+constexpr int64_t kFewRows = 256, kFewWork = 4096;
+// Rows too few to sort: each reads an adapter's weights for itself.  8192 x 8192, us in
+// a graph, this way against sorted: rank 16 of 64, 65 rows 19 / 69, 256 rows 36 / 72;
+// of 2, 256 rows 33 / 44; rank 64, 64 rows 56 / 109; rank 128, 32 rows 89 / 115.
+bool few_rows(int64_t tokens, int64_t rank) { return tokens <= kFewRows && tokens * rank <= kFewWork; }
 
 struct FewArgs {
     int32_t tokens, K, n, rank, adapters, fp16;
@@ -90,13 +94,24 @@ __global__ void __launch_bounds__(kFewThreads) shrink_few_kernel(const FewArgs p
         const uint16_t* x = p.x + int64_t(t) * p.ldx;
         const uint16_t* a = p.a + int64_t(id) * p.a_apart + 8 * v;
         const int have = p.rank - 8 * v;
-#pragma unroll 8
-        for (int k = k0 + first; k < k1; k += together) {
-            float f[8];
-            eight_values(load_eight(a + int64_t(k) * p.lda, have), p.fp16, f);
-            const float w = value16(x[k], p.fp16);
+        constexpr int kAhead = 8;  // loads under way
+        for (int k = k0 + first; k < k1; k += kAhead * together) {
+            uint4 u[kAhead];
+            uint16_t w[kAhead];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) acc[j] = fmaf(w, f[j], acc[j]);
+            for (int q = 0; q < kAhead; ++q) {
+                const bool there = k + q * together < k1;
+                u[q] = there ? load_eight(a + int64_t(k + q * together) * p.lda, have) : make_uint4(0, 0, 0, 0);
+                w[q] = there ? x[k + q * together] : uint16_t(0);
+            }
+#pragma unroll
+            for (int q = 0; q < kAhead; ++q) {
+                float f[8];
+                eight_values(u[q], p.fp16, f);
+                const float v = value16(w[q], p.fp16);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) acc[j] = fmaf(v, f[j], acc[j]);
+            }
         }
     }
 #pragma unroll
@@ -464,7 +479,7 @@ cudaError_t expand(const AdapterDesc& d, const Workspace& w, bool backward, int 
     // whole blocks of rows, and one of each group (and of the rows behind them) that has a row
     const int64_t blocks = d.tokens / kExpandRows + std::min(d.adapters + 1, d.tokens);
     // tiles of a CTA: what it finds and loads once counts less with more of them, as
-    // long as there are four CTAs for an SM (8192 x 8192, rank 16, us with 1 / 4 tiles: see the table's case)
+    // long as there are four CTAs for an SM (8192 x 8192, rank 16, us with 1 / 7: 74 / 67)
     p.per = int32_t(std::max<int64_t>(1, std::min<int64_t>(8, blocks * p.tiles / (4 * std::max(1, num_sms)))));
     p.shares = (p.tiles + p.per - 1) / p.per;
     const int64_t ctas = blocks * p.shares;
@@ -575,7 +590,7 @@ cudaError_t few_forward(const AdapterDesc& d, int num_sms, cudaStream_t stream) 
 
 size_t adapter_workspace(int64_t tokens, int64_t rank, int64_t adapters) {
     if (tokens < 0 || tokens > INT32_MAX / 2 || rank < 1 || rank > kAdapterMaxRank || adapters < 1 || adapters > kMaxGroups) return 0;
-    const size_t few = size_t(std::min(tokens, kFewRows)) * kFewSplits * size_t(kAdapterMaxRank) * 4;
+    const size_t few = few_rows(tokens, rank) ? size_t(tokens) * kFewSplits * size_t((rank + 7) / 8 * 8) * 4 : 0;
     return std::max<size_t>(256, std::max(few, Workspace(nullptr, tokens, rank, adapters).bytes));
 }
 
@@ -610,7 +625,7 @@ std::string adapter_check(const AdapterDesc& d, bool backward) {
 
 cudaError_t adapter_forward_launch(const AdapterDesc& d, int num_sms, cudaStream_t stream, std::string* why) {
     if (d.tokens == 0) return cudaSuccess;
-    if (d.tokens <= kFewRows) return few_forward(d, num_sms, stream);
+    if (few_rows(d.tokens, d.rank)) return few_forward(d, num_sms, stream);
     const Workspace w(d.workspace, d.tokens, d.rank, d.adapters);
     cudaError_t e = sort_rows(d, w, stream);
     if (e == cudaSuccess) e = grouped_launch(shrink(d, w, false), num_sms, stream, why);
