@@ -449,7 +449,6 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             bool there[kRows];
 #pragma unroll
             for (int r = 0; r < kRows; ++r) {
-                // (past the last row: that row again, whose results are not stored)
                 const int place = p0 + min(pick.row + kPickRows * r, count - 1), row = p.x_index ? __ldg(p.x_index + place) : place;
                 there[r] = unsigned(row) < unsigned(p.x_rows);
                 src[r] = p.x + (there[r] ? row * p.ldx : 0);
@@ -474,7 +473,8 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                 }
 #pragma unroll
                 for (int r = 0; r < kRows; ++r)
-                    pick.copy(smem0 + s * stage, r, src[r] + kb * kBlockK, there[r] ? p.reduce - kb * kBlockK : 0);
+                    // (past the last row: what the stage held before, whose results are not stored)
+                    if (kPickRows * r < count) pick.copy(smem0 + s * stage, r, src[r] + kb * kBlockK, there[r] ? p.reduce - kb * kBlockK : 0);
                 cp_async_commit();
                 if (fills - handed == kUnderWay) {
                     cp_async_wait<kUnderWay>();
@@ -682,7 +682,7 @@ cudaError_t grouped_launch(const GroupedDesc& d, int num_sms, cudaStream_t strea
 
     const int64_t mean = (d.rows + d.groups - 1) / d.groups;
     cudaError_t e;
-    if (d.own > kBlockM && !d.split_out && !d.all_rows && !d.out.index && mean > 64) {
+    if (d.own > kBlockM && !d.split_out && !d.all_rows && !d.out.index && mean > 16) {
         p.num_m = int32_t((d.own + 255) / 256);
         p.idesc = idesc_16(256, d.own_contiguous, false, p.fp16 != 0);
         const int64_t tiles = (d.rows / kBlockN + std::min(d.groups, d.rows)) * p.num_m;
@@ -705,7 +705,8 @@ cudaError_t grouped_launch(const GroupedDesc& d, int num_sms, cudaStream_t strea
     } else {
         p.num_m = int32_t((d.own + kBlockM - 1) / kBlockM);
         p.idesc = idesc_16(128, d.own_contiguous, false, p.fp16 != 0);
-        const int64_t want = 2 * mean;
+        // room for half as many again as the mean: groups differ, and a second block reads the weight again
+        const int64_t want = mean + mean / 2;
         auto run = [&](auto mn) {
             constexpr bool MN = decltype(mn)::value;
             if (want <= 16) return launch_few<MN, 16>(mw, p, d, num_sms, stream);
