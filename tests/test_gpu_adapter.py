@@ -59,7 +59,7 @@ def test_ranks(tl, T, r, base):
 
 
 @pytest.mark.parametrize("T,K,n,R,runs", [(3, 1, 1, 1, 1), (70, 7, 300, 3, 2), (130, 300, 7, 2, 50), (33, 65, 129, 40, 1),
-                                          (1000, 513, 1030, 3, 300), (2000, 72, 64, 900, 2), (64, 4099, 2056, 64, 1)])
+                                          (1000, 513, 1030, 3, 300), (2000, 72, 64, 900, 2), (3000, 72, 136, 1024, 3), (64, 4099, 2056, 64, 1)])
 def test_odd_sizes(tl, T, K, n, R, runs):
     both(tl, *case(T, K, n, 16, R, F16, runs), base_dtype=F16)
 

@@ -150,6 +150,24 @@ def test_indices_and_offsets_outside(tl):
     torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("most", [40, 3])
+def test_as_many_groups_as_there_may_be(tl, most):
+    g = torch.Generator().manual_seed(most)
+    both(tl, torch.randint(0, most, (1024,), generator=g).tolist(), 72, 136, BF16, True)
+
+
+def test_many_rows_and_none_in_a_group(tl):
+    """Offsets that hold nothing, where the sizes alone ask for the kernels of many rows."""
+    x, w, dy = normal(1, 300, 64), normal(2, 2, 64, 264), normal(3, 300, 264)
+    off = torch.zeros(3, dtype=torch.int32, device="cuda")
+    y = torch.full((300, 264), 7.0, dtype=BF16, device="cuda")
+    s, err = torch.cuda.current_stream().cuda_stream, tl.tiled_linear_operator_error_word()
+    tl.tiled_linear_grouped_forward(300, 64, 264, 2, 0, x.data_ptr(), 64, 300, None, w.data_ptr(), 264, 64 * 264, off.data_ptr(), y.data_ptr(), 264, None, 0, err, s)
+    assert (y == 7).all()
+    assert not tl.grouped_linear_backward(x, dy, w, off)[1].any()
+    tl.check_operators()
+
+
 def test_no_rows(tl):
     x, w, off = normal(1, 0, 64), normal(2, 3, 64, 200), torch.zeros(4, dtype=torch.int32, device="cuda")
     assert tl.grouped_linear(x, w, off).shape == (0, 200)
