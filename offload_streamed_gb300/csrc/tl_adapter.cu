@@ -199,7 +199,10 @@ __global__ void __launch_bounds__(kFewThreads) expand_few_kernel(const FewArgs p
 // time: all of a thread's before the product, and by as many CTAs as fit.  The product is short (2 x 16 .. 128) and its
 // operands are in shared memory; mma.sync leaves its sums in registers, in which a
 // row's 16-byte vector is one thread's: column 8 c + 2 j + e of each 32 is
-// column 2 c + e of the j-th MMA's eight.
+// column 2 c + e of the j-th MMA's eight.  8192 rows, us: 4096 columns, rank 16, 37 (3.6
+// TB/s), rank 64 about 55; 8192 columns, rank 16, 67 (4.0 TB/s).  The grouped product's
+// kernel with base added in its epilogue took 228 and 456; CTAs of 64 rows and 128
+// threads, four an SM, 40 and 69.
 constexpr int kExpandThreads = 256, kExpandRows = 128, kExpandCols = 128;
 
 struct ExpandArgs {
