@@ -16,7 +16,7 @@
 //                      share the reduction and add their parts in a fixed order.
 //                      Indexed rows are picked up where they lie.
 //
-// What bounds them: the tensor cores and their power for many rows (16384 rows of one
+// What bounds them: the tensor cores for many rows (16384 rows of one
 // group, 8192 x 4096: 677 us, 1.62 PFLOP/s; of eight groups through an index 806, 60 to
 // 80 of it the copy), the weights' bytes for few (32 rows of 8 groups, 8192 x 4096:
 // 86 us, 6.2 TB/s).

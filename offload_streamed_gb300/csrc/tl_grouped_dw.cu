@@ -21,7 +21,7 @@
 // PFLOP/s), with few rows the writing of dw (512 rows, 64 groups, 2048 x 2048: 163 us for
 // 537 MB, which a memset takes 138 for; eight storing warps instead of four: the same).  The
 // narrow one has 48 KB a CTA of x under way: 8192 x 16 of four adapters from 8192 rows, 68 us for
-// 134 MB, half of memory's rate; with stages handed over one by one it took 92.
+// 134 MB, a quarter of memory's rate (92 while the next block's rows were not on their way).
 #include "tl_grouped.cuh"
 
 #include <algorithm>

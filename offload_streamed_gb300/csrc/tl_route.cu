@@ -16,9 +16,9 @@
 // launches, or one where a single CTA does it.
 //
 // 65536 x 256 bf16, top 8: 58 us in a graph for 6 of bytes.  The choice is 38 of them,
-// bound by its instructions (some 400 a token; the next token's logits are on their way
-// meanwhile, without which it took 47); the order about 20, three passes' latency (its
-// counts' loads are issued together: with four threads a group instead of a warp 73).
+// bound by its instructions (some 400 a token; with scalar loads, and the next token's
+// not under way meanwhile, it took 47); the order about 20, its passes' latency (the
+// counts' loads of a warp are issued together; four threads a group instead took 73).
 #include "tl_launch.h"
 #include "tl_route.h"
 #include "tl_types.cuh"
@@ -579,8 +579,8 @@ bool off(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n
 
 int route_per(int64_t tokens) { return int(std::max<int64_t>(kSortWarps, (tokens + kSortCtas - 1) / kSortCtas)); }
 int group_per(int64_t entries) { return int(std::max<int64_t>(2 * kSortThreads, (entries + kSortCtas - 1) / kSortCtas)); }
-// One CTA does all: a second launch costs more than the further rounds (8192 entries
-// by 8 groups: 7 us, of which the second launch alone would take about half).
+// One CTA does all: no second launch, and the further rounds are few (8192 entries by 8
+// groups: 7 us; two launches for as many tokens of 64 experts 9).
 constexpr int64_t kAloneTokens = 128, kAloneEntries = 8192;
 
 template <typename... P, typename... A>
