@@ -694,7 +694,8 @@ cudaError_t grouped_launch(const GroupedDesc& d, int num_sms, cudaStream_t strea
         p.num_m = int32_t((d.own + 255) / 256);
         p.idesc = idesc_16(256, d.own_contiguous, false, p.fp16 != 0);
         const int64_t tiles = (d.rows / kBlockN + std::min(d.groups, d.rows)) * p.num_m;
-        if (tiles > INT32_MAX) {
+        // (whatever the offsets hold, a CTA's count of the tiles stays in 32 bits)
+        if (d.groups * ((d.rows + kBlockN - 1) / kBlockN) * p.num_m > INT32_MAX) {
             if (why) *why = "too many tiles";
             return cudaErrorInvalidValue;
         }
