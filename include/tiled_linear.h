@@ -748,11 +748,14 @@ tl_status tiled_linear_grouped_dw(int64_t R, int64_t K, int64_t n, int64_t group
  * id = ids[t] (none where that is outside 0..adapters-1), a [adapters][K, r] and
  * b [adapters][r, n] (r 1..128), s = scale_dev[id] (or `scale` where that is NULL):
  *   h[t] = x[t] . a[id]  [T, r] (kept for the backward)    y[t] = base[t] + s h[t] . b[id]
- * and without an adapter h = 0, y = base.  y is made from the unrounded h (in two
- * parts, so that infinite weights give NaN where they would give infinities).  All of
+ * and without an adapter h = 0, y = base.  y is made from the h before it is rounded
+ * to its type, which may leave that type's range: of many rows in two parts of the
+ * type, whose sum keeps 16 (bf16) or 22 (fp16: to 2^-39 of the row's largest) of fp32's
+ * 24 digits (infinite weights give NaN where they would give infinities).  All of
  * `type` (bf16 or fp16) but base [T, n], which may be fp32 (base_type) or NULL for
  * zeros: the shared projection's own result, however it was computed.  y may be base.
- * Backward, with dh = s dy . b^T:
+ * Backward, with dh = s dy . b^T, in two parts likewise (fp16, in da: to 2^-38 of the
+ * adapter's largest):
  *   dx = base + dh . a^T   base [T, K]: the shared projection's part; dx may be base
  *   da[id] = sum x[t]^T dh[t],   db[id] = s sum h[t]^T dy[t]     zeros without rows
  * dx, or da and db both, may be NULL where not wanted.

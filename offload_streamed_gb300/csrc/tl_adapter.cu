@@ -4,8 +4,9 @@
 // bytes of x, is a product whose weight depends on the row (tl_grouped.cu), and
 // y = base + s h . b, bound by those of base and y, a kernel of its own
 // (expand_kernel).  h goes from one to the other in two parts of the type's digits, whose sum is the unrounded h to
-// twice those digits: rounding it to one would err as much as rounding y does.  The
-// same holds for dh = s dy . b^T in the backward pass.
+// twice those digits: rounding it to one would err as much as rounding y does.  fp16's
+// are scaled by a power of two for each place (unit_of in tl_grouped.cuh), so that an h outside fp16's
+// range passes like any other.  The same holds for dh = s dy . b^T in the backward pass.
 //
 // Few rows: nothing is sorted; a CTA takes a row and a share of the reduction
 // (first launch) or of the columns (second), on the CUDA cores, since each weight
@@ -210,6 +211,7 @@ struct ExpandArgs {
     const int32_t* offsets;
     const int32_t* index;  // the row of each place
     const uint16_t* h;     // [rows, 2 half], by place
+    const float* units;    // of h's rows (fp16)
     const uint16_t* w;
     int64_t ldw, w_apart;
     const float* scale;
@@ -270,6 +272,11 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const ExpandA
     }
     const float scale = none ? 0.0f : p.scale ? __ldg(p.scale + group) : p.scale_all;
     const uint32_t sh = smem_addr(expand_smem), sw = sh + kExpandRows * E::kPitchH;
+    __shared__ float unit[kExpandRows];
+    if constexpr (FP16) {
+        if (int(threadIdx.x) < kExpandRows) unit[threadIdx.x] = int(threadIdx.x) < count ? __ldg(p.units + p0 + int(threadIdx.x)) : 0.0f;
+        __syncthreads();
+    }
     if (!none) {
         constexpr int kVecH = HALF / 4;  // 16-byte vectors of h's row
         for (int v = threadIdx.x; v < kExpandRows * kVecH; v += kExpandThreads) {
@@ -367,10 +374,11 @@ __global__ void __launch_bounds__(kExpandThreads, 2) expand_kernel(const ExpandA
                         if (k < have) b[k] = p.base_f32 ? static_cast<const float*>(p.base)[at + k] : value16(static_cast<const uint16_t*>(p.base)[at + k], FP16);
                 }
                 uint32_t o[4];
+                const float u = FP16 ? unit[row0 + i * 8 + g] : 1.0f;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const float* f = acc[i >> 1][j * 4 + k] + (i & 1) * 2;
-                    o[k] = gr::round16x2(fmaf(f[0], scale, b[2 * k]), fmaf(f[1], scale, b[2 * k + 1]), FP16);
+                    o[k] = gr::round16x2(fmaf(f[0] * u, scale, b[2 * k]), fmaf(f[1] * u, scale, b[2 * k + 1]), FP16);
                 }
                 uint16_t* dst = p.out + int64_t(rows[i]) * p.ldout + col;
                 if (have >= 8) {
@@ -391,6 +399,7 @@ constexpr int kFewSplits = 16;
 struct Workspace {
     int32_t *slots, *rows, *offsets, *counts;
     uint16_t* split;  // [tokens, 2 half], by place
+    float* units;     // fp16: of the split's rows
     size_t bytes;
     Workspace(void* base, int64_t tokens, int64_t rank, int64_t adapters) {
         uintptr_t at = reinterpret_cast<uintptr_t>(base);
@@ -403,6 +412,7 @@ struct Workspace {
         rows = static_cast<int32_t*>(take(size_t(tokens) * 4));
         offsets = static_cast<int32_t*>(take(size_t(adapters + 1) * 4));
         counts = static_cast<int32_t*>(take(route_workspace(tokens, 1, adapters)));
+        units = reinterpret_cast<float*>(slots);  // (the sort's slots are nobody's; its launches have ended by then)
         split = static_cast<uint16_t*>(take(size_t(tokens) * 4 * size_t(half_of(rank))));
         bytes = size_t(at - reinterpret_cast<uintptr_t>(base));
     }
@@ -454,6 +464,7 @@ GroupedDesc shrink(const AdapterDesc& d, const Workspace& w, bool backward) {
     }
     g.split_out = w.split;
     g.split_half = half_of(d.rank);
+    if (d.type == TL_TYPE_F16) g.split_units = w.units;
     return g;
 }
 
@@ -467,6 +478,7 @@ cudaError_t expand(const AdapterDesc& d, const Workspace& w, bool backward, int 
     p.offsets = w.offsets;
     p.index = w.rows;
     p.h = w.split;
+    p.units = w.units;
     p.w = static_cast<const uint16_t*>(backward ? d.a : d.b);
     p.ldw = backward ? d.lda : d.ldb;
     p.w_apart = backward ? d.a_apart : d.b_apart;
@@ -520,6 +532,7 @@ GroupedDwDesc gradient(const AdapterDesc& d, const Workspace& w, bool of_b) {
         g.x.at = d.x;
         g.x.ld = d.ldx;
         g.half = half_of(d.rank);
+        if (d.type == TL_TYPE_F16) g.dy_units = w.units;
         g.dy = {w.split, 2 * g.half, d.tokens, nullptr};  // by place
         g.dw = d.da;
         g.lddw = d.ldda;

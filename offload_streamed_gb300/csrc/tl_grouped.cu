@@ -50,6 +50,7 @@ struct Params {
     float scale_all;
     uint16_t* split_out;
     int32_t split_half;
+    float* split_units;
     int32_t fp16;
     int32_t all_rows;
     uint32_t idesc;  // without N
@@ -79,13 +80,29 @@ __device__ __forceinline__ void store_four(const Params& p, int64_t row, int col
     }
 }
 
-// The unrounded result of place p as two parts: what rounding keeps and what it takes off,
-// rounded in its turn (an infinity leaves nothing).
+// The unrounded result of a place, of which each lane of a warp has four columns, as two
+// parts: what rounding keeps and what it takes off, rounded in its turn (an infinity leaves
+// nothing).  Rounded to the type at once it would err as much as the rounding of what is
+// made of it; two parts keep 16 (bf16) or 22 digits of fp32's 24, for half the bytes and
+// none of the instructions of a third.
 __device__ __forceinline__ void store_split(const Params& p, int64_t place, int col, const float (&f)[4]) {
+    float to_units = 1.0f;
+    if (p.split_units) {
+        uint32_t most = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t size = __float_as_uint(f[j]) & 0x7fffffffu;
+            if (col + j < p.own && size < 0x7f800000u) most = max(most, size);
+        }
+        const float unit = unit_of(__reduce_max_sync(0xffffffffu, most));
+        if (col == 0) p.split_units[place] = unit;
+        to_units = reciprocal_of_unit(unit);
+    }
+    if (col >= p.split_half) return;
     uint16_t hi[4], lo[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const float v = col + j < p.own ? f[j] : 0.0f;
+        const float v = col + j < p.own ? f[j] * to_units : 0.0f;
         hi[j] = round16(v, p.fp16);
         const float rest = v - value16(hi[j], p.fp16);
         lo[j] = round16(isfinite(rest) ? rest : 0.0f, p.fp16);
@@ -557,7 +574,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             const int have = min(4, p.own - col);
             const float4 f = make_float4(sum[u].x * scale, sum[u].y * scale, sum[u].z * scale, sum[u].w * scale);
             if (have > 0 && p.out) store_four(p, row, col, have, f);
-            if (p.split_out && col < p.split_half) {
+            if (p.split_out) {  // (a warp has a row: all of its 128 columns, m0 being 0)
                 const float w[4] = {f.x, f.y, f.z, f.w};
                 store_split(p, p0 + e / 32, col, w);
             }
@@ -647,7 +664,8 @@ std::string grouped_check(const GroupedDesc& d) {
     if (d.x.count < 1 || (!d.x.index && d.x.count < d.rows)) return "x has too few rows";
     if (!d.out.index && d.out.count < d.rows) return "the result has too few rows";
     if (off(d.gathered, 16)) return "the workspace is not 16-byte aligned";
-    if (off(d.x.index, 4) || off(d.out.index, 4) || off(d.scale, 4)) return "indexes and scales must be 4-byte aligned";
+    if (off(d.x.index, 4) || off(d.out.index, 4) || off(d.scale, 4) || off(d.split_units, 4)) return "indexes and scales must be 4-byte aligned";
+    if (d.split_out && (d.own > d.split_half || d.split_half > kBlockM)) return "a result in two parts has 128 columns at most";
     return {};
 }
 
@@ -672,6 +690,7 @@ cudaError_t grouped_launch(const GroupedDesc& d, int num_sms, cudaStream_t strea
     p.scale_all = d.scale_all;
     p.split_out = static_cast<uint16_t*>(d.split_out);
     p.split_half = d.split_half;
+    p.split_units = d.split_units;
     p.fp16 = d.type == TL_TYPE_F16 ? 1 : 0;
     p.all_rows = d.all_rows ? 1 : 0;
     p.err = d.err;

@@ -178,9 +178,10 @@ struct Picker {
     }
     // Row row + 16 i of a box at `box`: from `src` on (the row's first element of the
     // box's columns), `cols` of which are there (none: zeros).
+    __device__ __forceinline__ uint32_t at(uint32_t box, int i) const { return box + dst + uint32_t(i) * (kPickRows * 128u); }
     __device__ __forceinline__ void copy(uint32_t box, int i, const uint16_t* src, int cols) const {
         const int have = min(max(cols - 8 * chunk, 0), 8);
-        cp_async16(box + dst + uint32_t(i) * (kPickRows * 128u), src + (have ? 8 * chunk : 0), uint32_t(have) * 2u);
+        cp_async16(at(box, i), src + (have ? 8 * chunk : 0), uint32_t(have) * 2u);
     }
 };
 
@@ -195,6 +196,20 @@ __device__ __forceinline__ uint32_t round16x2(float lo, float hi, bool fp16) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
+
+// ---- fp16's units --------------------------------------------------------------------
+
+// Two parts hold twice fp16's digits only well within its range, so they are those of a
+// number in units of a power of two of the place, which puts the largest of its finite
+// numbers (`most`, the bits of its magnitude) into [2^14, 2^15): 2^-22 of a number and 2^-39 of
+// the place's largest are lost, whatever their sizes.  (bf16 has fp32's range and needs none.)  A unit is at
+// least 2^-126, so that its reciprocal is a normal number; a place without a number but
+// 0 has that one, and so does not count where units are compared.
+__device__ __forceinline__ float unit_of(uint32_t most) { return __uint_as_float(uint32_t(max(int(most >> 23) - 14, 1)) << 23); }
+__device__ __forceinline__ float reciprocal_of_unit(float unit) { return __uint_as_float((254u << 23) - __float_as_uint(unit)); }
+// Part of a place from its unit to a larger one.  (Below 2^-60 no finite part is left of
+// any; an infinite one stays infinite.)
+__device__ __forceinline__ float between_units(float unit, float reciprocal) { return fmaxf(unit * reciprocal, 0x1p-60f); }
 
 }  // namespace gr
 

@@ -34,10 +34,12 @@ struct GroupedDesc {
     bool all_rows = false;
     const float* scale = nullptr;  // [groups]; nullptr: scale_all
     float scale_all = 1.0f;
-    // Not nullptr: the unrounded result, too, as two parts of split_half
+    // Not nullptr (own <= 128): the unrounded result, too, as two parts of split_half
     // columns whose sum it is to twice the type's digits; [rows, 2 split_half], by place.
+    // fp16's parts are of the result in units of split_units[place], a power of two.
     void* split_out = nullptr;
     int32_t split_half = 0;
+    float* split_units = nullptr;  // [rows], by place; fp16 only
     void* gathered = nullptr;  // workspace for an indexed x's rows, [rows, picked_ld] (own > 128 needs it)
     int32_t* err = nullptr;
 };
@@ -51,6 +53,7 @@ struct GroupedDwDesc {
     const int32_t* offsets = nullptr;
     RowsOperand x, dy;
     int32_t half = 0;  // not 0: dy's columns are two parts of `half`, which are added (n_dim <= half)
+    const float* dy_units = nullptr;  // [rows], by place: what dy's two parts are in units of, powers of two; nullptr: ones
     void* dw = nullptr;
     int64_t lddw = 0, dw_apart = 0;
     void* gathered = nullptr;  // workspace for an indexed x's rows, [rows, picked_ld] (n_dim > 128 needs it)

@@ -1527,7 +1527,8 @@ def adapter_linear(x, a, b, ids, base=None, scale=1.0):
     the device (one outside 0..adapters-1: no adapter, h = 0 and y = base).  base
     [T, n] (x's dtype or fp32; None for zeros) is the shared projection's result,
     streamed, in 8 bits or any other; scale: one number, or fp32 [adapters].  h, kept
-    for the backward, is rounded to x's dtype, y is made from the unrounded one."""
+    for the backward, is rounded to x's dtype (infinite where it leaves it), y is made
+    from the one before that."""
     where, _ = "adapter_linear", _t()
     kind, kept, xa, aa, ba, ip, sa, (T, K, n, r, adapters) = _adapter_args(x, a, b, ids, scale, where)
     bt, bp, ldbase = _adapter_base(base, (T, n), x, where)

@@ -1,0 +1,116 @@
+"""Adapters in fp16 whose h, and whose dh in the backward, leave fp16's range or reach its subnormal numbers while the
+results do not: against 64 bits, element by element, within bounds of an intermediate result that keeps its digits.
+
+Two parts of a number whose place's largest lies in [2^14, 2^15): what the first rounds off is at most 2^-11 of it, and of
+that the second again 2^-11, or half a subnormal step, 2^-25: 2^-22 of the number and 2^-39 of the place's largest.  In da
+places of different sizes meet at the largest's unit, where either part may lose 2^-25 once more: 2^-39 twice, and once
+for the place's own, of the largest of all: 3 * 2^-39."""
+import pytest
+import torch
+
+import rows_reference
+from rows_reference import adapter, adapter_backward, check
+from test_gpu_adapter import both, case, normal, owners, tl  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+
+
+def by_place(ref, before, dtype):
+    size = ref.abs() + before
+    return before + 2.0 ** -22 * size + 2.0 ** -39 * size.amax(1, keepdim=True)
+
+
+def by_adapter(ref, before, dtype):
+    size = ref.abs() + before
+    return before + 2.0 ** -22 * size + 3 * 2.0 ** -39 * (size.max() if size.numel() else 0.0)
+
+
+def checked(monkeypatch, names, got, refs, skip=()):
+    """refs: () -> (value, bound) of each result, with the intermediate's error by place, or in da by adapter."""
+    monkeypatch.setattr(rows_reference, "between", by_place)
+    values = list(refs())
+    if "da" in names:
+        monkeypatch.setattr(rows_reference, "between", by_adapter)
+        values[names.index("da")] = refs()[names.index("da")]
+    for name, g, (ref, bound) in zip(names, got, values):
+        if name not in skip:
+            assert ref.abs().max() < 65504, f"{name} does not fit the type: {ref.abs().max()}"
+            check(name, g, ref, bound)
+
+
+def scaled(seed, size, *shape):
+    """Normal values of a size given for all, or for each row."""
+    return (normal(seed, *shape, dtype=F32) * size).to(F16)
+
+
+# sizes of x, a, b for the forward, and of x, h, dy, a, b for the backward
+SIZES = {"large": ((100.0, 60.0, 1e-3), (1e-3, 1e-2, 2000.0, 1e-3, 4.0)), "small": ((1e-2, 1e-4, 30.0), (100.0, 1.0, 1e-4, 30.0, 1e-3))}
+SHAPES = [(256, 264, 392, 16, 5), (257, 264, 392, 16, 5), (40, 264, 392, 128, 3), (300, 200, 136, 24, 3), (700, 264, 392, 64, 2), (300, 72, 1030, 128, 4),
+          (2000, 136, 264, 32, 1)]
+
+
+@pytest.mark.parametrize("T,K,n,r,R", SHAPES)
+@pytest.mark.parametrize("size", SIZES)
+def test_forward(tl, monkeypatch, size, T, K, n, r, R):  # noqa: F811
+    sx, sa, sb = SIZES[size][0]
+    x, a, b = scaled(1, sx, T, K), scaled(2, sa, R, K, r), scaled(3, sb, R, r, n)
+    ids, scale = owners(4, T, R, 3), torch.exp(0.3 * normal(5, R, dtype=F32))
+    y, h = tl.adapter_linear(x, a, b, ids, scale=scale)
+    # (h is returned in its own type: infinite where it leaves it)
+    checked(monkeypatch, ("y", "h"), (y, h), lambda: adapter(x, a, b, ids, None, scale), skip=("h",) if size == "large" else ())
+    if size == "large":
+        assert torch.isinf(h).any()
+    tl.check_operators()
+
+
+@pytest.mark.parametrize("T,K,n,r,R", SHAPES)
+@pytest.mark.parametrize("size", SIZES)
+def test_backward(tl, monkeypatch, size, T, K, n, r, R):  # noqa: F811
+    sx, sh, sg, sa, sb = SIZES[size][1]
+    x, h, dy = scaled(1, sx, T, K), scaled(2, sh, T, r), scaled(3, sg, T, n)
+    a, b, ids = scaled(4, sa, R, K, r), scaled(5, sb, R, r, n), owners(6, T, R, 3)
+    dy[::3] = 0  # (rows that pass nothing back)
+    scale = torch.exp(0.3 * normal(7, R, dtype=F32))
+    got = tl.adapter_linear_backward(x, h, dy, a, b, ids, scale=scale)
+    checked(monkeypatch, ("dx", "da", "db"), got, lambda: adapter_backward(x, h, dy, a, b, ids, None, scale))
+    tl.check_operators()
+
+
+@pytest.mark.parametrize("T", [200, 600, 3000])
+def test_rows_of_different_sizes(tl, monkeypatch, T):  # noqa: F811
+    """Six decades within an adapter: a place keeps its own digits in y and dx, and da those of its largest."""
+    K, n, r, R = 264, 392, 16, 2
+    g = torch.Generator(device="cuda").manual_seed(9)
+    size = 10.0 ** (6 * torch.rand(T, 1, generator=g, device="cuda") - 4)
+    x, a, b, ids = scaled(1, 10 * size, T, K), scaled(2, 1.0, R, K, r), scaled(3, 1e-2, R, r, n), owners(4, T, R, 3)
+    y, h = tl.adapter_linear(x, a, b, ids)
+    checked(monkeypatch, ("y", "h"), (y, h), lambda: adapter(x, a, b, ids, None, [1.0] * R))
+    dy, x, h = scaled(5, size, T, n), scaled(6, 0.1, T, K), scaled(7, 0.1, T, r)
+    got = tl.adapter_linear_backward(x, h, dy, a, b, ids, scale=0.25)
+    checked(monkeypatch, ("dx", "da", "db"), got, lambda: adapter_backward(x, h, dy, a, b, ids, None, [0.25] * R))
+    tl.check_operators()
+
+
+@pytest.mark.parametrize("base", [None, F16, F32])
+@pytest.mark.parametrize("r", [1, 8, 24, 32, 64, 100, 128])
+@pytest.mark.parametrize("T", [20, 300])
+def test_ranks(tl, monkeypatch, T, r, base):  # noqa: F811
+    monkeypatch.setattr(rows_reference, "between", by_adapter)
+    both(tl, *case(T, 264, 392, r, 5, F16), base_dtype=base)
+
+
+def test_an_infinite_row_stays_one(tl):  # noqa: F811
+    """A row of infinities changes no bit of the others' y and dx, and none of the other adapters' gradients."""
+    T, K, n, r, R = 400, 136, 264, 16, 3
+    x, a, b, ids, scale = case(T, K, n, r, R, F16)
+    h, dy = normal(8, T, r, dtype=F16), normal(9, T, n, dtype=F16)
+    good = *tl.adapter_linear(x, a, b, ids, scale=scale), *tl.adapter_linear_backward(x, h, dy, a, b, ids, scale=scale)
+    row = (ids == 1).nonzero()[7, 0]
+    x[row], dy[row] = float("inf"), float("inf")
+    bad = *tl.adapter_linear(x, a, b, ids, scale=scale), *tl.adapter_linear_backward(x, h, dy, a, b, ids, scale=scale)
+    keep = torch.arange(T, device="cuda") != row
+    for i in (0, 1, 2):
+        assert torch.equal(good[i][keep], bad[i][keep]) and not torch.isfinite(bad[i][row]).any(), i
+    for i in (3, 4):
+        assert torch.equal(good[i][[0, 2]], bad[i][[0, 2]]) and not torch.isfinite(bad[i][1]).all(), i
