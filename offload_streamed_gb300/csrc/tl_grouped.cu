@@ -104,6 +104,7 @@ __device__ __forceinline__ void store_split(const Params& p, int64_t place, int 
     for (int j = 0; j < 4; ++j) {
         const float v = col + j < p.own ? f[j] * to_units : 0.0f;
         hi[j] = round16(v, p.fp16);
+        if (!p.fp16 && isfinite(v) && (hi[j] & 0x7fffu) == 0x7f80u) --hi[j];  // (past bf16's largest number: that one, and the rest)
         const float rest = v - value16(hi[j], p.fp16);
         lo[j] = round16(isfinite(rest) ? rest : 0.0f, p.fp16);
     }

@@ -114,3 +114,23 @@ def test_an_infinite_row_stays_one(tl):  # noqa: F811
         assert torch.equal(good[i][keep], bad[i][keep]) and not torch.isfinite(bad[i][row]).any(), i
     for i in (3, 4):
         assert torch.equal(good[i][[0, 2]], bad[i][[0, 2]]) and not torch.isfinite(bad[i][1]).all(), i
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("T", [20, 300])
+def test_bf16_at_the_end_of_its_range(tl, T, sign):  # noqa: F811
+    """h and dh finite in 32 bits, but past the largest bf16 by more than half a step: 2^127 (2 - 2^-7 + 1.5 2^-8)."""
+    r = 16
+    big, rest = 2.0 ** 64 * (2 - 2.0 ** -7), 2.0 ** 64 * 1.5 * 2.0 ** -8
+    x = torch.full((T, 8), sign * 2.0 ** 63, device="cuda").to(BF16)
+    a = torch.zeros(1, 8, r, device="cuda").to(BF16)
+    a[:, 0], a[:, 1] = big, rest
+    b = torch.full((1, r, 8), 2.0 ** -120, device="cuda").to(BF16)
+    ids = torch.zeros(T, dtype=torch.int32, device="cuda")
+    ref = sign * 2.0 ** 63 * (big + rest) * r * 2.0 ** -120
+    y, h = tl.adapter_linear(x, a, b, ids)
+    assert ((y.double() - ref).abs() <= 2.0 ** -7 * abs(ref)).all() and torch.isinf(h).all()
+    # the same as dh = dy . b^T, with the factors turned
+    dx, da, db = tl.adapter_linear_backward((x[:, :2] * 2.0 ** -100).contiguous(), torch.zeros_like(h), x, b[:, :, :2].transpose(1, 2).contiguous(),
+                                            a.transpose(1, 2).contiguous(), ids)
+    assert ((dx.double() - ref).abs() <= 2.0 ** -7 * abs(ref)).all() and not db.any()
