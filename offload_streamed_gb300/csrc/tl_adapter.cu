@@ -25,6 +25,7 @@ namespace {
 
 using gr::grid_dependency_wait;
 using gr::grid_dependents_go;
+using gr::load_eight;
 using gr::round16;
 using gr::value16;
 
@@ -57,15 +58,6 @@ struct FewArgs {
     int32_t padded, splits, per;
 };
 
-// Eight elements, of which `have` are there.
-__device__ __forceinline__ uint4 load_eight(const uint16_t* p, int have) {
-    if (have >= 8) return __ldg(reinterpret_cast<const uint4*>(p));
-    uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        if (j < have) w[j / 2] |= uint32_t(p[j]) << (16 * (j & 1));
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
 __device__ __forceinline__ void eight_values(const uint4& u, bool fp16, float (&f)[8]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll

@@ -620,7 +620,7 @@ cudaError_t launch_few(const CUtensorMap& mw, Params p, const GroupedDesc& d, in
 // A sorted copy of indexed rows: rows outside the matrix as zeros.
 constexpr int kPickCopyThreads = 256;
 __global__ void __launch_bounds__(kPickCopyThreads) pick_rows_kernel(const uint16_t* x, int64_t ldx, int x_rows, const int32_t* index, int rows,
-                                                                     int vectors, int lanes, uint16_t* out, int64_t ldo) {
+                                                                     int cols, int lanes, uint16_t* out, int64_t ldo) {
     // `lanes` threads (a power of two) walk a row; four vectors of each under way
     const int64_t p = int64_t(blockIdx.x) * (kPickCopyThreads / lanes) + threadIdx.x / lanes;
     if (p >= rows) return;
@@ -628,8 +628,11 @@ __global__ void __launch_bounds__(kPickCopyThreads) pick_rows_kernel(const uint1
     const bool there = unsigned(row) < unsigned(x_rows);
     const uint4* src = reinterpret_cast<const uint4*>(x + (there ? row * ldx : 0));
     uint4* dst = reinterpret_cast<uint4*>(out + p * ldo);
+    const int whole = cols / 8, first = int(threadIdx.x % lanes);
 #pragma unroll 4
-    for (int v = int(threadIdx.x % lanes); v < vectors; v += lanes) dst[v] = there ? __ldg(src + v) : make_uint4(0, 0, 0, 0);
+    for (int v = first; v < whole; v += lanes) dst[v] = there ? __ldg(src + v) : make_uint4(0, 0, 0, 0);
+    if (first == whole % lanes && cols % 8)  // (behind a row's end is not the row's)
+        dst[whole] = there ? load_eight(reinterpret_cast<const uint16_t*>(src + whole), cols % 8) : make_uint4(0, 0, 0, 0);
 }
 
 }  // namespace
@@ -637,12 +640,12 @@ __global__ void __launch_bounds__(kPickCopyThreads) pick_rows_kernel(const uint1
 int64_t picked_ld(int64_t cols) { return (cols + 7) / 8 * 8; }
 
 cudaError_t pick_rows_launch(const RowsOperand& x, int64_t rows, int64_t cols, void* out, cudaStream_t stream) {
-    const int64_t vectors = picked_ld(cols) / 8;  // (x's rows hold as many: their distance is a multiple of 8)
+    const int64_t vectors = picked_ld(cols) / 8;
     int lanes = 32;
     while (lanes < kPickCopyThreads && lanes * 4 < vectors) lanes *= 2;
     const int per = kPickCopyThreads / lanes;
     pick_rows_kernel<<<unsigned((rows + per - 1) / per), kPickCopyThreads, 0, stream>>>(static_cast<const uint16_t*>(x.at), x.ld, int(x.count), x.index,
-                                                                                     int(rows), int(vectors), lanes, static_cast<uint16_t*>(out), picked_ld(cols));
+                                                                                     int(rows), int(cols), lanes, static_cast<uint16_t*>(out), picked_ld(cols));
     return cudaGetLastError();
 }
 

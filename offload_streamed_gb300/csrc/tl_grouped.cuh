@@ -185,6 +185,16 @@ struct Picker {
     }
 };
 
+// Eight elements, of which `have` are there.
+__device__ __forceinline__ uint4 load_eight(const uint16_t* p, int have) {
+    if (have >= 8) return __ldg(reinterpret_cast<const uint4*>(p));
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (j < have) w[j / 2] |= uint32_t(p[j]) << (16 * (j & 1));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 __device__ __forceinline__ uint16_t round16(float v, bool fp16) {
     return fp16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
