@@ -460,6 +460,11 @@ GroupedDesc shrink(const AdapterDesc& d, const Workspace& w, bool backward) {
     return g;
 }
 
+// Whole blocks of rows, and one of each adapter (and of the rows behind them) that has a row.
+int64_t expand_blocks(const AdapterDesc& d) { return d.tokens / kExpandRows + std::min(d.adapters + 1, d.tokens); }
+int64_t expand_tiles(int64_t cols) { return (cols + kExpandCols - 1) / kExpandCols; }
+constexpr int64_t kExpandMost = 8;  // tiles of a CTA
+
 // y (or dx) of all rows: base + s h . b, or base + dh . a^T.
 cudaError_t expand(const AdapterDesc& d, const Workspace& w, bool backward, int num_sms, cudaStream_t stream) {
     ExpandArgs p{};
@@ -482,15 +487,13 @@ cudaError_t expand(const AdapterDesc& d, const Workspace& w, bool backward, int 
     p.base_vectors = d.base && !p.base_f32 && !off(d.base, 16) && d.ldbase % 8 == 0 ? 1 : 0;
     p.out = static_cast<uint16_t*>(backward ? d.dx : d.y);
     p.ldout = backward ? d.lddx : d.ldy;
-    p.tiles = (p.own + kExpandCols - 1) / kExpandCols;
-    // whole blocks of rows, and one of each group (and of the rows behind them) that has a row
-    const int64_t blocks = d.tokens / kExpandRows + std::min(d.adapters + 1, d.tokens);
+    p.tiles = int32_t(expand_tiles(p.own));
+    const int64_t blocks = expand_blocks(d);
     // tiles of a CTA: what it finds and loads once counts less with more of them, as
     // long as there are four CTAs for an SM (8192 x 8192, rank 16, us with 1 / 7: 74 / 67)
-    p.per = int32_t(std::max<int64_t>(1, std::min<int64_t>(8, blocks * p.tiles / (4 * std::max(1, num_sms)))));
+    p.per = int32_t(std::max<int64_t>(1, std::min<int64_t>(kExpandMost, blocks * p.tiles / (4 * std::max(1, num_sms)))));
     p.shares = (p.tiles + p.per - 1) / p.per;
     const int64_t ctas = blocks * p.shares;
-    if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
     auto run = [&](auto contig, auto half) {
         constexpr bool CONTIG = decltype(contig)::value;
         constexpr int HALF = decltype(half)::value;
@@ -621,6 +624,7 @@ std::string adapter_check(const AdapterDesc& d, bool backward) {
         const int64_t ldout = backward ? d.lddx : d.ldy, cols = backward ? d.K : d.n;
         if (out && (off(out, 16) || ldout % 8 || ldout < cols)) return "the result is not 16-byte aligned, or its leading dimension no multiple of 8 or too small";
         if (off(d.scale, 4)) return "scales must be 4-byte aligned";
+        if (out && expand_blocks(d) * ((expand_tiles(cols) + kExpandMost - 1) / kExpandMost) > INT32_MAX) return "too many tiles";
         if (d.base && d.base_type != d.type && d.base_type != TL_TYPE_F32) return "base must be of x's type or fp32";
         if (d.base && (off(d.base, type_bytes(d.base_type)) || d.ldbase < cols)) return "base is not aligned to its elements, or its leading dimension too small";
     }

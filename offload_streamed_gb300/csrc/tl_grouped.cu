@@ -595,23 +595,35 @@ __global__ void __launch_bounds__(kFewThreads, 2) grouped_few_shape_kernel() {}
 
 bool off(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
 
+// Rows of a group in the mean decide.  Forward, 2048 x 2048, us, few / many: 64 groups of
+// 32 rows 124 / 107, of 64 rows 179 / 119; 8192 x 4096, 8 groups of 32 117 / 123, of 17
+// - / 116 and of 16 105 / -.
+int64_t mean_rows(const GroupedDesc& d) { return (d.rows + d.groups - 1) / d.groups; }
+bool by_pairs(const GroupedDesc& d) { return d.own > kBlockM && !d.split_out && !d.all_rows && !d.out.index && mean_rows(d) > 16; }
+// Rows of a block of few: room for half as many again as the mean, since groups differ, and a
+// second block reads the weight again.
+int few_size(const GroupedDesc& d) {
+    const int64_t want = mean_rows(d) + mean_rows(d) / 2;
+    return want <= 16 ? 16 : want <= 32 ? 32 : want <= 64 ? 64 : 128;
+}
+// The most blocks of rows there can be: whole ones, and one of each group that has a row.
+int64_t few_blocks(const GroupedDesc& d) { return d.rows / few_size(d) + std::min(d.groups + (d.all_rows ? 1 : 0), d.rows); }
+
 template <bool W_MN, int N>
 cudaError_t launch_few(const CUtensorMap& mw, Params p, const GroupedDesc& d, int num_sms, cudaStream_t stream) {
-    // the most blocks of rows there can be: whole ones, and one of each group that has a row
     const int64_t seen = d.groups + (d.all_rows ? 1 : 0);
-    const int64_t blocks = d.rows / N + std::min(seen, d.rows), units = blocks * p.num_m;
+    const int64_t blocks = few_blocks(d), units = blocks * p.num_m;
     const int64_t likely = std::max<int64_t>(1, std::min(blocks, (d.rows + N - 1) / N + std::min(seen, d.rows) / 2)) * p.num_m;
     int splits = 1, per_sm = 0, clusters = 0;
     const void* shape = reinterpret_cast<const void*>(grouped_few_shape_kernel);
     cudaError_t e = ctas_per_sm(shape, kFewThreads, kFewSmem, &per_sm);
     // CTAs of a cluster: as many as two an SM allow, with four K-blocks each
-    while (e == cudaSuccess && splits < 8 && likely * splits * 2 <= 2 * num_sms && p.num_k >= 8 * splits) {
+    while (e == cudaSuccess && splits < 8 && likely * splits * 2 <= 2 * num_sms && p.num_k >= 8 * splits && units * splits * 2 <= INT32_MAX) {
         e = clusters_at_a_time(shape, kFewThreads, kFewSmem, 2 * splits, &clusters);
         if (e != cudaSuccess || likely > clusters) break;
         splits *= 2;
     }
     if (e != cudaSuccess) return e;
-    if (units * splits > INT32_MAX) return cudaErrorInvalidConfiguration;
     const int per = (p.num_k + splits - 1) / splits;
     return launch_in_clusters(grouped_few_kernel<W_MN, N>, dim3(unsigned(units * splits)), kFewThreads, splits, kFewSmem, false, stream, mw,
                               p, splits, per, uint32_t(Few<N>::stages(p.w_bytes)), Few<N>::stage(p.w_bytes));
@@ -670,6 +682,9 @@ std::string grouped_check(const GroupedDesc& d) {
     if (off(d.gathered, 16)) return "the workspace is not 16-byte aligned";
     if (off(d.x.index, 4) || off(d.out.index, 4) || off(d.scale, 4) || off(d.split_units, 4)) return "indexes and scales must be 4-byte aligned";
     if (d.split_out && (d.own > d.split_half || d.split_half > kBlockM)) return "a result in two parts has 128 columns at most";
+    // (of pairs: whatever the offsets hold, a CTA's count of the tiles stays in 32 bits)
+    const int64_t tiles = by_pairs(d) ? d.groups * ((d.rows + kBlockN - 1) / kBlockN) * ((d.own + 255) / 256) : few_blocks(d) * ((d.own + kBlockM - 1) / kBlockM);
+    if (tiles > INT32_MAX) return "too many tiles";
     return {};
 }
 
@@ -708,20 +723,11 @@ cudaError_t grouped_launch(const GroupedDesc& d, int num_sms, cudaStream_t strea
     p.w_boxes = d.own <= 64 ? 1 : 2;
     p.w_bytes = d.own_contiguous ? uint32_t(p.w_boxes) * kMnChunk : box_rows * 128u;
 
-    // Rows of a group in the mean decide.  Forward, 2048 x 2048, us, few / many: 64 groups of
-    // 32 rows 124 / 107, of 64 rows 179 / 119; 8192 x 4096, 8 groups of 32 117 / 123, of 17
-    // - / 116 and of 16 105 / -.
-    const int64_t mean = (d.rows + d.groups - 1) / d.groups;
     cudaError_t e;
-    if (d.own > kBlockM && !d.split_out && !d.all_rows && !d.out.index && mean > 16) {
+    if (by_pairs(d)) {
         p.num_m = int32_t((d.own + 255) / 256);
         p.idesc = idesc_16(256, d.own_contiguous, false, p.fp16 != 0);
         const int64_t tiles = (d.rows / kBlockN + std::min(d.groups, d.rows)) * p.num_m;
-        // (whatever the offsets hold, a CTA's count of the tiles stays in 32 bits)
-        if (d.groups * ((d.rows + kBlockN - 1) / kBlockN) * p.num_m > INT32_MAX) {
-            if (why) *why = "too many tiles";
-            return cudaErrorInvalidValue;
-        }
         const unsigned grid = 2 * unsigned(std::min<int64_t>(tiles, std::max(1, num_sms / 2)));
         RowsOperand x = d.x;
         if (x.index) {
@@ -737,14 +743,14 @@ cudaError_t grouped_launch(const GroupedDesc& d, int num_sms, cudaStream_t strea
     } else {
         p.num_m = int32_t((d.own + kBlockM - 1) / kBlockM);
         p.idesc = idesc_16(128, d.own_contiguous, false, p.fp16 != 0);
-        // room for half as many again as the mean: groups differ, and a second block reads the weight again
-        const int64_t want = mean + mean / 2;
         auto run = [&](auto mn) {
             constexpr bool MN = decltype(mn)::value;
-            if (want <= 16) return launch_few<MN, 16>(mw, p, d, num_sms, stream);
-            if (want <= 32) return launch_few<MN, 32>(mw, p, d, num_sms, stream);
-            if (want <= 64) return launch_few<MN, 64>(mw, p, d, num_sms, stream);
-            return launch_few<MN, 128>(mw, p, d, num_sms, stream);
+            switch (few_size(d)) {
+                case 16: return launch_few<MN, 16>(mw, p, d, num_sms, stream);
+                case 32: return launch_few<MN, 32>(mw, p, d, num_sms, stream);
+                case 64: return launch_few<MN, 64>(mw, p, d, num_sms, stream);
+                default: return launch_few<MN, 128>(mw, p, d, num_sms, stream);
+            }
         };
         e = d.own_contiguous ? run(std::true_type{}) : run(std::false_type{});
     }

@@ -536,6 +536,8 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
 // Asked about, never launched (see tl_fp8.cu).
 __global__ void __launch_bounds__(kNarrowThreads, 2) narrow_shape_kernel() {}
 
+bool narrow(const GroupedDwDesc& d) { return d.half || d.n_dim <= 128; }
+
 bool off(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
 
 }  // namespace
@@ -562,6 +564,8 @@ std::string grouped_dw_check(const GroupedDwDesc& d) {
     if (d.x.count < 1 || d.dy.count < 1 || (!d.x.index && d.x.count < d.rows) || (!d.dy.index && d.dy.count < d.rows)) return "x or dy has too few rows";
     if (off(d.gathered, 16)) return "the workspace is not 16-byte aligned";
     if (off(d.x.index, 4) || off(d.dy.index, 4) || off(d.scale, 4) || off(d.dy_units, 4)) return "indexes and scales must be 4-byte aligned";
+    const int64_t tiles = narrow(d) ? (d.m_dim + 127) / 128 * d.groups : (d.m_dim + 255) / 256 * ((d.n_dim + 255) / 256);  // of all groups, or of one
+    if (tiles > INT32_MAX) return "too many tiles";
     return {};
 }
 
@@ -602,7 +606,7 @@ cudaError_t grouped_dw_launch(const GroupedDwDesc& d, int num_sms, cudaStream_t 
     p.err = d.err;
     p.timeout_ns = 2000000000ull;
     cudaError_t e;
-    if (d.half || d.n_dim <= 128) {
+    if (narrow(d)) {
         p.num_m = int32_t((d.m_dim + 127) / 128);
         p.n = d.half ? 2 * d.half : int32_t((d.n_dim + 15) / 16 * 16);
         p.idesc = idesc_16(128, true, true, p.fp16 != 0);
@@ -612,13 +616,12 @@ cudaError_t grouped_dw_launch(const GroupedDwDesc& d, int num_sms, cudaStream_t 
         int splits = 1, per_sm = 0, clusters = 0;
         const void* shape = reinterpret_cast<const void*>(narrow_shape_kernel);
         e = ctas_per_sm(shape, kNarrowThreads, smem, &per_sm);
-        while (e == cudaSuccess && splits < 8 && units * splits * 2 <= 2 * num_sms && blocks >= 4 * splits) {
+        while (e == cudaSuccess && splits < 8 && units * splits * 2 <= 2 * num_sms && blocks >= 4 * splits && units * splits * 2 <= INT32_MAX) {
             e = clusters_at_a_time(shape, kNarrowThreads, smem, 2 * splits, &clusters);
             if (e != cudaSuccess || units > clusters) break;
             splits *= 2;
         }
         if (e != cudaSuccess) return e;
-        if (units * splits > INT32_MAX) return cudaErrorInvalidConfiguration;
         e = launch_in_clusters(d.dy_units ? grouped_dw_narrow_kernel<true> : grouped_dw_narrow_kernel<false>, dim3(unsigned(units * splits)), kNarrowThreads,
                                splits, smem, false, stream, p, splits, stages);
     } else {
