@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
     } else {
         // quads of neighbours: rows of the result of 128 or `width` elements
         const int of_row = p.transposed ? 32 : width / 4, quads = (p.transposed ? width : 128) * of_row;
-        const float scale = p.scale ? __ldg(p.scale + g) : p.scale_all;
+        const float scale = begin == end ? 0.0f : p.scale ? __ldg(p.scale + g) : p.scale_all;  // (nothing's sum is zero, scaled by whatever)
         const int out_rows = p.transposed ? p.n_dim : p.m_dim - m0, out_cols = p.transposed ? p.m_dim - m0 : p.n_dim;
         uint16_t* out = p.dw + int64_t(g) * p.dw_apart + (p.transposed ? int64_t(m0) : int64_t(m0) * p.lddw);
         for (int e = int(rank) * kThreads + int(threadIdx.x); e < quads; e += splits * kThreads) {

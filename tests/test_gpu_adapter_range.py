@@ -134,3 +134,18 @@ def test_bf16_at_the_end_of_its_range(tl, T, sign):  # noqa: F811
     dx, da, db = tl.adapter_linear_backward((x[:, :2] * 2.0 ** -100).contiguous(), torch.zeros_like(h), x, b[:, :, :2].transpose(1, 2).contiguous(),
                                             a.transpose(1, 2).contiguous(), ids)
     assert ((dx.double() - ref).abs() <= 2.0 ** -7 * abs(ref)).all() and not db.any()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_scales_of_adapters_without_rows(tl, dtype):  # noqa: F811
+    """A sum of nothing is zero, whatever its adapter's scale."""
+    for T in (20, 300):
+        x, a, b, ids, _ = case(T, 72, 136, 16, 4, dtype)
+        ids[ids == 2] = -1
+        scale = torch.tensor([1.0, 0.5, float("inf"), 2.0], device="cuda")
+        h, dy = normal(8, T, 16, dtype=dtype), normal(9, T, 136, dtype=dtype)
+        good = tl.adapter_linear_backward(x, h, dy, a, b, ids, scale=scale.clamp(max=2.0))
+        for bad in (float("inf"), float("nan")):
+            scale[2] = bad
+            got = tl.adapter_linear_backward(x, h, dy, a, b, ids, scale=scale)
+            assert all(torch.equal(p, q) for p, q in zip(good, got)) and not got[1][2].any() and not got[2][2].any()
