@@ -1450,6 +1450,8 @@ def _grouped_args(x, w, offsets, rows, where: str):
     if rows is not None:
         R = rows.shape[0] if rows.dim() == 1 else -1
         rp = _int32(rows, (R,), x.device, where, "rows")
+        if R > 0 and x.shape[0] == 0:
+            _refuse(where, "x has no rows")
     return kind, (xk, wk), (xp, ldx, x.shape[0], rp), (wp, ldw, apart), op, (R, K, n, groups)
 
 

@@ -32,3 +32,16 @@ def test_nothing_behind_a_row_is_read(tl, K, tokens):  # noqa: F811
     for work in works:
         assert work.any() and not (work == MARK).any()
     tl.check_operators()
+
+
+def test_backward_refuses_before_it_begins(tl, monkeypatch):  # noqa: F811
+    """What one of the backward's two products refuses is refused before the other is enqueued."""
+    begun, real = [], tl.tiled_linear_grouped_dx
+    monkeypatch.setattr(tl, "tiled_linear_grouped_dx", lambda *a: (begun.append(1), real(*a)))
+    off, rows = offsets_of([3, 5]), torch.zeros(8, dtype=torch.int32, device="cuda")
+    x, w, dy = normal(1, 4, 64), normal(2, 2, 64, 136), normal(3, 8, 136)
+    with pytest.raises(tl.TiledLinearError) as e:
+        tl.grouped_linear_backward(x[:0], dy, w, off, rows)
+    assert e.value.status == tl.TL_ERR_INVALID and not begun
+    tl.grouped_linear_backward(x, dy, w, off, rows)
+    assert begun
