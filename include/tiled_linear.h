@@ -753,10 +753,11 @@ tl_status tiled_linear_grouped_dw(int64_t R, int64_t K, int64_t n, int64_t group
  * type, whose sum keeps 16 (bf16) or 22 (fp16: to 2^-39 of the row's largest) of fp32's
  * 24 digits (infinite weights give NaN where they would give infinities).  All of
  * `type` (bf16 or fp16) but base [T, n], which may be fp32 (base_type) or NULL for
- * zeros: the shared projection's own result, however it was computed.  y may be base.
+ * zeros: the shared projection's own result, however it was computed.  y may be base
+ * (of its type and leading dimension), and dx likewise.
  * Backward, with dh = s dy . b^T, in two parts likewise (fp16, in da: to 2^-38 of the
  * adapter's largest):
- *   dx = base + dh . a^T   base [T, K]: the shared projection's part; dx may be base
+ *   dx = base + dh . a^T   base [T, K]: the shared projection's part
  *   da[id] = sum x[t]^T dh[t],   db[id] = s sum h[t]^T dy[t]     zeros without rows
  * dx, or da and db both, may be NULL where not wanted.
  * Leading dimensions and distances (of base: any) are multiples of 8 elements,

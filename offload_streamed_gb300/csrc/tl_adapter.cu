@@ -624,6 +624,8 @@ std::string adapter_check(const AdapterDesc& d, bool backward) {
         const int64_t ldout = backward ? d.lddx : d.ldy, cols = backward ? d.K : d.n;
         if (out && (off(out, 16) || ldout % 8 || ldout < cols)) return "the result is not 16-byte aligned, or its leading dimension no multiple of 8 or too small";
         if (off(d.scale, 4)) return "scales must be 4-byte aligned";
+        if (d.base && d.base == out && (d.base_type != d.type || (d.tokens > 1 && d.ldbase != ldout)))
+            return "base lies where the result does, but is of another type or leading dimension";
         if (out && expand_blocks(d) * ((expand_tiles(cols) + kExpandMost - 1) / kExpandMost) > INT32_MAX) return "too many tiles";
         if (d.base && d.base_type != d.type && d.base_type != TL_TYPE_F32) return "base must be of x's type or fp32";
         if (d.base && (off(d.base, type_bytes(d.base_type)) || d.ldbase < cols)) return "base is not aligned to its elements, or its leading dimension too small";

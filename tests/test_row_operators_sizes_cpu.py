@@ -34,3 +34,10 @@ def test_too_many_adapter_tiles(tl):  # noqa: F811
     refused(tl, tl.tiled_linear_adapter_forward, A, A_GOOD, dict(wide, ldy=1 << 30), tl.TL_ERR_INVALID, "too many tiles")
     wide = dict(T=1 << 29, K=n, r=8, adapters=2, ldx=1 << 30, a_apart=1 << 33, ldbase=1 << 30, lddx=1 << 30, da_apart=1 << 33, bytes=1 << 60)
     refused(tl, tl.tiled_linear_adapter_backward, AB, AB_GOOD, wide, tl.TL_ERR_INVALID, "too many tiles")
+
+
+def test_base_under_the_result(tl):  # noqa: F811
+    """The result may lie where base does only where each element of the one is that of the other."""
+    for kw in (dict(base_type=2), dict(ldbase=72), dict(T=1, base_type=2)):
+        refused(tl, tl.tiled_linear_adapter_forward, A, A_GOOD, kw, tl.TL_ERR_INVALID, "base")
+        refused(tl, tl.tiled_linear_adapter_backward, AB, AB_GOOD, kw, tl.TL_ERR_INVALID, "base")
