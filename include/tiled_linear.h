@@ -755,7 +755,7 @@ tl_status tiled_linear_grouped_dw(int64_t R, int64_t K, int64_t n, int64_t group
  * `type` (bf16 or fp16) but base [T, n], which may be fp32 (base_type) or NULL for
  * zeros: the shared projection's own result, however it was computed.  y may be base
  * (of its type and leading dimension), and dx likewise.
- * Backward, with dh = s dy . b^T, in two parts likewise (fp16, in da: to 2^-38 of the
+ * Backward, with dh = s dy . b^T, in two parts likewise (fp16, in da: to 2^-37 of the
  * adapter's largest):
  *   dx = base + dh . a^T   base [T, K]: the shared projection's part
  *   da[id] = sum x[t]^T dh[t],   db[id] = s sum h[t]^T dy[t]     zeros without rows

@@ -8,10 +8,11 @@
 // are scaled by a power of two for each place (unit_of in tl_grouped.cuh), so that an h outside fp16's
 // range passes like any other.  The same holds for dh = s dy . b^T in the backward pass.
 //
-// Few rows: nothing is sorted; a CTA takes a row and a share of the reduction
+// Few rows, in the forward: nothing is sorted; a CTA takes a row and a share of the reduction
 // (first launch) or of the columns (second), on the CUDA cores, since each weight
 // is met by about one row and bytes bound it.  The second launch asks for its
-// weights while the first still runs.
+// weights while the first still runs.  (The backward sorts any number of rows: da and db
+// are sums over an adapter's.)
 #include "tl_adapter.h"
 #include "tl_route.h"
 
@@ -33,7 +34,8 @@ constexpr int kFewThreads = 256;
 constexpr int64_t kFewRows = 256, kFewWork = 4096;
 // Rows too few to sort: each reads an adapter's weights for itself.  8192 x 8192, us in
 // a graph, this way against sorted: rank 16 of 64, 65 rows 19 / 69, 256 rows 36 / 72;
-// of 2, 256 rows 33 / 44; rank 64, 64 rows 56 / 109; rank 128, 32 rows 89 / 115.
+// of 2, 256 rows 33 / 44; rank 64, 64 rows 56 / 109; rank 128, 32 rows 89 / 115.  The
+// limit is below the crossover, which has not been measured.
 bool few_rows(int64_t tokens, int64_t rank) { return tokens <= kFewRows && tokens * rank <= kFewWork; }
 
 struct FewArgs {

@@ -96,7 +96,7 @@ __device__ __forceinline__ void umma_16(uint32_t d, uint64_t a, uint64_t b, uint
     else umma_bf16(d, a, b, idesc, accumulate);
 }
 
-// Whether a phase has completed, by lane 0's look; if so, as every lane sees it.
+// Whether a phase has completed, as every lane of the warp sees it.
 __device__ __forceinline__ bool warp_test(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
@@ -162,9 +162,10 @@ __device__ __forceinline__ void find_block(const int32_t* offsets, int groups, i
 // take some 36 clocks each, whoever issues them: 14 bytes a clock and SM): eight threads for 128 bytes of a row, sixteen rows at
 // a time, into the image that a TMA load of a box with 128-byte swizzle leaves.
 // What they wrote is handed to the tensor cores by a proxy fence of each thread
-// after its copies have landed and an arrival of each warp: a stage when four
-// further ones are under way, or all of them before a wait for a free stage, which
-// would otherwise keep from the tensor cores what that wait depends on.
+// after its copies have landed and an arrival of each warp: a stage when two
+// further ones are under way (the widest shapes have two or three stages in all), or all
+// of them before a wait for a free stage, which would otherwise keep from the tensor
+// cores what that wait depends on.
 // For single CTAs alone: the arrival at the other CTA of a pair would need release
 // semantics in the cluster for each stage, which took longer than the stage's MMAs
 // (8192 x 8192 x 4096 in eight groups, 2 rows a token: 3.0 ms, against 1.2 with

@@ -15,10 +15,10 @@
 // each bit of the ids gives.  Counting is fused into the choice, so a call is two
 // launches, or one where a single CTA does it.
 //
-// 65536 x 256 bf16, top 8: 58 us in a graph for 6 of bytes.  The choice is 38 of them,
-// bound by its instructions (some 400 a token; with scalar loads, and the next token's
-// not under way meanwhile, it took 47); the order about 20, its passes' latency (the
-// counts' loads of a warp are issued together; four threads a group instead took 73).
+// 65536 x 256 bf16, top 8: 55 us among other calls, 50 repeated in a graph, for 6 of bytes.  The
+// choice is about two thirds of it, bound by its instructions (some 400 a token; with scalar
+// loads, and the next token's not under way meanwhile, it took 47 instead of 38); the order
+// the rest, its passes' latency (the counts' loads of a warp are issued together).
 #include "tl_launch.h"
 #include "tl_route.h"
 #include "tl_types.cuh"

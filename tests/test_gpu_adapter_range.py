@@ -149,3 +149,29 @@ def test_scales_of_adapters_without_rows(tl, dtype):  # noqa: F811
             scale[2] = bad
             got = tl.adapter_linear_backward(x, h, dy, a, b, ids, scale=scale)
             assert all(torch.equal(p, q) for p, q in zip(good, got)) and not got[1][2].any() and not got[2][2].any()
+
+
+def test_same_bits_again_and_in_a_graph(tl):  # noqa: F811
+    """Inputs of other sizes in a captured call: the units are found anew, and the bits are those of a call by itself."""
+    T, K, n, r, R = 600, 264, 392, 32, 3
+    _, a, b, _, scale = case(1, K, n, r, R, F16)
+    inputs = []
+    for s, size in enumerate((1.0, 300.0, 1e-4)):
+        inputs.append((scaled(s, size, T, K), scaled(10 + s, size, T, n), scaled(20 + s, 1.0, T, r), owners(s, T, R, 5)))
+
+    def call(x, dy, h, ids):
+        return *tl.adapter_linear(x, a, b, ids, scale=scale), *tl.adapter_linear_backward(x, h, dy, a, b, ids, scale=scale)
+
+    want = [call(*i) for i in inputs]
+    held = [t.clone() for t in inputs[0]]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call(*held)
+    for i in (1, 2, 0, 2, 1):
+        for t, s in zip(held, inputs[i]):
+            t.copy_(s)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(out, want[i])), i
+        assert all(torch.equal(p, q) for p, q in zip(call(*inputs[i]), want[i])), i
+    tl.check_operators()
