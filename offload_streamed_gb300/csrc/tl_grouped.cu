@@ -618,7 +618,7 @@ cudaError_t launch_few(const CUtensorMap& mw, Params p, const GroupedDesc& d, in
     const void* shape = reinterpret_cast<const void*>(grouped_few_shape_kernel);
     cudaError_t e = ctas_per_sm(shape, kFewThreads, kFewSmem, &per_sm);
     // CTAs of a cluster: as many as two an SM allow, with four K-blocks each
-    while (e == cudaSuccess && splits < 8 && likely * splits * 2 <= 2 * num_sms && p.num_k >= 8 * splits && units * splits * 2 <= INT32_MAX) {
+    while (e == cudaSuccess && splits < 8 && likely * splits * 2 <= 2 * num_sms && p.num_k >= 8 * splits) {
         e = clusters_at_a_time(shape, kFewThreads, kFewSmem, 2 * splits, &clusters);
         if (e != cudaSuccess || likely > clusters) break;
         splits *= 2;

@@ -616,7 +616,7 @@ cudaError_t grouped_dw_launch(const GroupedDwDesc& d, int num_sms, cudaStream_t 
         int splits = 1, per_sm = 0, clusters = 0;
         const void* shape = reinterpret_cast<const void*>(narrow_shape_kernel);
         e = ctas_per_sm(shape, kNarrowThreads, smem, &per_sm);
-        while (e == cudaSuccess && splits < 8 && units * splits * 2 <= 2 * num_sms && blocks >= 4 * splits && units * splits * 2 <= INT32_MAX) {
+        while (e == cudaSuccess && splits < 8 && units * splits * 2 <= 2 * num_sms && blocks >= 4 * splits) {
             e = clusters_at_a_time(shape, kNarrowThreads, smem, 2 * splits, &clusters);
             if (e != cudaSuccess || units > clusters) break;
             splits *= 2;
